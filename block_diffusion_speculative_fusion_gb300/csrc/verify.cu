@@ -342,11 +342,11 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    const int y = s_y;
+    const int y = min(s_y, V - 1);   // past V only for a row of -inf alone, which has no law
     const double Z = s_Z, u = u_final[b];
     int flags = j.flags;
     if (Z > 0.0 && (fabs(s_clo / Z - u) < 1e-6 || fabs(s_chi / Z - u) < 1e-6)) flags |= 2;  // CDF_BOUNDARY
-    if (degenerate) flags |= 4;                                                           // DEGENERATE
+    if (degenerate || !(Z > 0.0)) flags |= 4;                                             // DEGENERATE
     bonus[b] = y;
     if (flags_out) flags_out[b] = (uint8_t)flags;
     if (probs) probs[(size_t)b * (2 * n_max + 1) + 2 * n_max] = (float)Z;
@@ -445,8 +445,9 @@ sample_stats_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const fl
     const float at = fmaf(zxt, k2, -pt.m), ad = fmaf(zxd, k2, -pd.m);   // as in the row sums
     const double rt = ((double)zxt * k2d - (double)pt.m) - (double)at;
     const double rd = ((double)zxd * k2d - (double)pd.m) - (double)ad;
-    const double px = (double)ex2_ftz(at) * (1.0 + rt * 0.6931471805599453) / (double)pt.s;
-    const double qx = (double)ex2_ftz(ad) * (1.0 + rd * 0.6931471805599453) / (double)pd.s;
+    // (a logit of -inf, as a grammar mask leaves it, has probability 0; its residual has no value)
+    const double px = zxt == -CUDART_INF_F ? 0.0 : (double)ex2_ftz(at) * (1.0 + rt * 0.6931471805599453) / (double)pt.s;
+    const double qx = zxd == -CUDART_INF_F ? 0.0 : (double)ex2_ftz(ad) * (1.0 + rd * 0.6931471805599453) / (double)pd.s;
     s_px[i - 1] = (float)px;
     s_qx[i - 1] = (float)qx;
     // q(x) = 0: the candidate was not drawn from q (infinite ratio, flagged)
