@@ -61,6 +61,14 @@ class TreeDims(ctypes.Structure):
     _fields_ = [(n, c_i32) for n in ("B", "n", "V", "dtype", "K", "budget")]
 
 
+class RulesDims(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("B", "n_rows", "V", "dtype", "hist_max", "n_bias")]
+
+
+class PagesDims(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("B", "page_size", "max_pages", "num_pages")]
+
+
 _SIGS = {
     "dflash_last_error": (ctypes.c_char_p, []),
     "dflash_last_launch_count": (ctypes.c_int, []),
@@ -92,6 +100,11 @@ _SIGS = {
     "dflash_draft_select_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(VerifyDims)]),
     "dflash_draft_select": (ctypes.c_int, [ctypes.POINTER(VerifyDims), ctypes.c_float, c_p, c_p, c_p, c_p, c_p,
                                            c_p, c_p, c_p, c_p, ctypes.c_size_t, c_p]),
+    # dims, logits, cand, n_draft, hist, hist_len, prompt_len, repetition, presence, frequency, bias_tok,
+    # bias_val, mask, mask_on, out, stream
+    "dflash_logits_rules": (ctypes.c_int, [ctypes.POINTER(RulesDims)] + [c_p] * 15),
+    "dflash_pages_resize": (ctypes.c_int, [ctypes.POINTER(PagesDims)] + [c_p] * 9),
+    "dflash_slot_map": (ctypes.c_int, [ctypes.POINTER(PagesDims), c_i32] + [c_p] * 8),
     "dflash_block_attn_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(AttnDims)]),
     "dflash_block_attn": (ctypes.c_int, [ctypes.POINTER(AttnDims), c_p, c_p, c_p, c_p, c_p, c_p, c_p,
                                          ctypes.c_float, c_p, c_p, ctypes.c_size_t, c_p]),
@@ -190,6 +203,22 @@ def _opt(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
 
 def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(device: torch.device, fn, *args) -> None:
+    """Call ``fn(*args, stream)`` with ``device`` current and its current stream."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(device))
+    _check(rc)
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if isinstance(t, torch.Tensor) and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 _WS: Dict[Tuple[int, int], torch.Tensor] = {}
@@ -486,6 +515,108 @@ def ddtree_verify_greedy(target_logits: torch.Tensor, node_token: torch.Tensor, 
         _dev(o["bonus"], "bonus", torch.int64), _dev(o["commit_len"], "commit_len", torch.int32),
         _opt(o.get("path"), "path", torch.int32), _opt(o.get("out_tokens"), "out_tokens", torch.int64),
         w.data_ptr(), w.numel(), _stream(dev)))
+    return o
+
+
+# ---------------------------------------------------------------------------
+# rules on the verify rows' logits
+# ---------------------------------------------------------------------------
+def logits_rules(logits: torch.Tensor, cand: Optional[torch.Tensor] = None, n_draft: Optional[torch.Tensor] = None,
+                 hist: Optional[torch.Tensor] = None, hist_len: Optional[torch.Tensor] = None,
+                 prompt_len: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                 presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                 bias_tok: Optional[torch.Tensor] = None, bias_val: Optional[torch.Tensor] = None,
+                 mask: Optional[torch.Tensor] = None, mask_on: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Penalties, biases and grammar masks on logits [B, R, V]
+    (``dflash_logits_rules``); row r's history is hist[b, :hist_len[b]] and
+    cand[b, 1 .. r]. hist [B, H], cand [B, R] int64; hist_len, prompt_len,
+    n_draft [B] int32; repetition, presence, frequency [B] float32; bias_tok
+    [B, n] int64 with bias_val [B, n] float32; mask [B, R, ceil(V / 32)] int32,
+    bit 1 = allowed, for the sequences with mask_on[b] != 0 (uint8; None: all).
+    Returns ``out`` (a new tensor, whose rows past n_draft[b] are then zero, if
+    not given); ``out=logits`` works in place."""
+    _dev(logits, "logits")
+    B, R, V = logits.shape
+    dev = logits.device
+    if (hist is None) != (hist_len is None):
+        raise ValueError("hist and hist_len come together")
+    if (bias_tok is None) != (bias_val is None):
+        raise ValueError("bias_tok and bias_val come together")
+    H = 0 if hist is None else hist.shape[1]
+    nb = 0 if bias_tok is None else bias_tok.shape[1]
+    _same_device(dev, cand=cand, n_draft=n_draft, hist=hist, hist_len=hist_len, prompt_len=prompt_len,
+                 repetition=repetition, presence=presence, frequency=frequency, bias_tok=bias_tok,
+                 bias_val=bias_val, mask=mask, mask_on=mask_on, out=out)
+    if out is None:
+        out = torch.empty_like(logits) if n_draft is None else torch.zeros_like(logits)
+    dims = RulesDims(B, R, V, _dtype_code(logits), H, nb)
+    _launch(dev, lib().dflash_logits_rules, ctypes.byref(dims), logits.data_ptr(),
+            _opt(cand, "cand", torch.int64, (B, R)), _opt(n_draft, "n_draft", torch.int32, (B,)),
+            _opt(hist, "hist", torch.int64, (B, H)), _opt(hist_len, "hist_len", torch.int32, (B,)),
+            _opt(prompt_len, "prompt_len", torch.int32, (B,)), _opt(repetition, "repetition", torch.float32, (B,)),
+            _opt(presence, "presence", torch.float32, (B,)), _opt(frequency, "frequency", torch.float32, (B,)),
+            _opt(bias_tok, "bias_tok", torch.int64, (B, nb)), _opt(bias_val, "bias_val", torch.float32, (B, nb)),
+            _opt(mask, "mask", torch.int32, (B, R, (V + 31) // 32)), _opt(mask_on, "mask_on", torch.uint8, (B,)),
+            _dev(out, "out", logits.dtype, (B, R, V)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# block tables and slot maps
+# ---------------------------------------------------------------------------
+def pages_resize(length: torch.Tensor, page_table: torch.Tensor, n_pages: torch.Tensor, free_pages: torch.Tensor,
+                 n_free: torch.Tensor, page_size: int, out: Optional[dict] = None) -> dict:
+    """Grow or shrink every sequence's row of the block table to length[b]
+    tokens (``dflash_pages_resize``). length, n_pages [B], page_table [B,
+    max_pages], free_pages [num_pages], n_free [1], all int32; page_table and
+    free_pages are changed in place. Returns n_pages [B] and n_free [1] int32
+    (tensors other than the inputs), short [B] uint8."""
+    _dev(page_table, "page_table", torch.int32)
+    B, max_pages = page_table.shape
+    dev = page_table.device
+    o = out if out is not None else {}
+    if "n_pages" not in o:
+        o["n_pages"] = torch.empty(B, dtype=torch.int32, device=dev)
+    if "n_free" not in o:
+        o["n_free"] = torch.empty(1, dtype=torch.int32, device=dev)
+    if "short" not in o:
+        o["short"] = torch.empty(B, dtype=torch.uint8, device=dev)
+    _same_device(dev, length=length, n_pages=n_pages, free_pages=free_pages, n_free=n_free)
+    _same_device(dev, **o)
+    num_pages = free_pages.shape[0]
+    dims = PagesDims(B, int(page_size), max_pages, num_pages)
+    _launch(dev, lib().dflash_pages_resize, ctypes.byref(dims), _dev(length, "length", torch.int32, (B,)),
+            page_table.data_ptr(), _dev(n_pages, "n_pages", torch.int32, (B,)),
+            _dev(free_pages, "free_pages", torch.int32, (num_pages,)), _dev(n_free, "n_free", torch.int32, (1,)),
+            _dev(o["n_pages"], "out n_pages", torch.int32, (B,)), _dev(o["n_free"], "out n_free", torch.int32, (1,)),
+            _dev(o["short"], "short", torch.uint8, (B,)))
+    return o
+
+
+def slot_map(start_pos: torch.Tensor, n_rows: torch.Tensor, page_table: torch.Tensor, page_size: int, num_pages: int,
+             rows_max: int, out: Optional[dict] = None) -> dict:
+    """Slot map of the ragged batch of rows start_pos[b] .. start_pos[b] +
+    n_rows[b] - 1 (``dflash_slot_map``). Returns cu_rows [B + 1], row_seq and
+    positions [rows_max] int32, slots [rows_max] int64 (-1 past the last row)."""
+    _dev(page_table, "page_table", torch.int32)
+    B, max_pages = page_table.shape
+    dev = page_table.device
+    o = out if out is not None else {}
+    if "cu_rows" not in o:
+        o["cu_rows"] = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    for name, dt in (("row_seq", torch.int32), ("positions", torch.int32), ("slots", torch.int64)):
+        if name not in o:
+            o[name] = torch.empty(max(int(rows_max), 0), dtype=dt, device=dev)
+    _same_device(dev, start_pos=start_pos, n_rows=n_rows)
+    _same_device(dev, **o)
+    dims = PagesDims(B, int(page_size), max_pages, int(num_pages))
+    _launch(dev, lib().dflash_slot_map, ctypes.byref(dims), int(rows_max),
+            _dev(start_pos, "start_pos", torch.int32, (B,)), _dev(n_rows, "n_rows", torch.int32, (B,)),
+            page_table.data_ptr(), _dev(o["cu_rows"], "cu_rows", torch.int32, (B + 1,)),
+            _dev(o["row_seq"], "row_seq", torch.int32, (rows_max,)),
+            _dev(o["positions"], "positions", torch.int32, (rows_max,)),
+            _dev(o["slots"], "slots", torch.int64, (rows_max,)))
     return o
 
 

@@ -449,6 +449,97 @@ int dflash_ddtree_verify_greedy(const dflash_tree_dims* d, const void* target_lo
   return ok(1);
 }
 
+// ------------------------------------------------------------- logit rules ---
+int dflash_logits_rules(const dflash_rules_dims* d, const void* logits, const int64_t* cand, const int32_t* n_draft,
+                        const int64_t* hist, const int32_t* hist_len, const int32_t* prompt_len,
+                        const float* repetition, const float* presence, const float* frequency,
+                        const int64_t* bias_tok, const float* bias_val, const int32_t* mask, const uint8_t* mask_on,
+                        void* out, dflash_stream_t stream) {
+  CallRange range_("dflash_logits_rules");
+  if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
+  if (d->B < 1 || d->n_rows < 1 || d->V < 1 || d->hist_max < 0 || d->n_bias < 0)
+    return fail(DFLASH_ERR_INVALID_ARG, "bad dims B=%d n_rows=%d V=%d hist_max=%d n_bias=%d", d->B, d->n_rows, d->V,
+                d->hist_max, d->n_bias);
+  if (bad_dtype(d->dtype)) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", d->dtype);
+  if (d->n_rows > dflash::kRulesMaxRows)
+    return fail(DFLASH_ERR_UNSUPPORTED, "n_rows=%d > %d", d->n_rows, dflash::kRulesMaxRows);
+  if (d->hist_max >= 1 << dflash::kRulesCountBits)
+    return fail(DFLASH_ERR_UNSUPPORTED, "hist_max=%d > %d", d->hist_max, (1 << dflash::kRulesCountBits) - 1);
+  if (d->n_bias >= 1 << dflash::kRulesBiasBits)
+    return fail(DFLASH_ERR_UNSUPPORTED, "n_bias=%d > %d", d->n_bias, (1 << dflash::kRulesBiasBits) - 1);
+  if (d->B > 65535) return fail(DFLASH_ERR_UNSUPPORTED, "B=%d > 65535", d->B);
+  if (d->V > 1 << 30) return fail(DFLASH_ERR_UNSUPPORTED, "V=%d too large", d->V);
+  if (!logits || !out || (d->hist_max > 0 && (!hist || !hist_len)) || (d->n_bias > 0 && (!bias_tok || !bias_val)))
+    return fail(DFLASH_ERR_INVALID_ARG, "logits_rules: a required pointer is NULL");
+  const size_t el = d->dtype == DFLASH_BF16 ? 2 : 4;
+  const size_t bytes = (size_t)d->B * d->n_rows * d->V * el;
+  const uintptr_t in0 = (uintptr_t)logits, out0 = (uintptr_t)out;
+  if (in0 % el || out0 % el) return fail(DFLASH_ERR_INVALID_ARG, "logits_rules: logits or out is not aligned to its type");
+  if (in0 != out0 && in0 < out0 + bytes && out0 < in0 + bytes)
+    return fail(DFLASH_ERR_INVALID_ARG, "logits_rules: out overlaps logits without being it");
+  dflash::RulesArgs a{};
+  a.B = d->B; a.n_rows = d->n_rows; a.V = d->V; a.dtype = d->dtype; a.hist_max = d->hist_max; a.n_bias = d->n_bias;
+  a.logits = logits; a.cand = cand; a.n_draft = n_draft;
+  a.hist = d->hist_max > 0 ? hist : nullptr; a.hist_len = hist_len; a.prompt_len = prompt_len;
+  a.repetition = repetition; a.presence = presence; a.frequency = frequency;
+  a.bias_tok = bias_tok; a.bias_val = bias_val; a.mask = mask; a.mask_on = mask_on;
+  a.out = out;
+  a.stream = (cudaStream_t)stream;
+  cudaError_t e = dflash::launch_rules(a, kPlanSms);
+  if (e != cudaSuccess) return cuda_fail(e, "logits_rules launch");
+  return ok(1);
+}
+
+// -------------------------------------------------- block tables, slot maps ---
+static int check_pages_dims(const dflash_pages_dims* d) {
+  if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
+  if (d->B < 1 || d->page_size < 1 || d->max_pages < 1 || d->num_pages < 1)
+    return fail(DFLASH_ERR_INVALID_ARG, "bad dims B=%d page_size=%d max_pages=%d num_pages=%d", d->B, d->page_size,
+                d->max_pages, d->num_pages);
+  if (d->B > dflash::kPagesMaxB) return fail(DFLASH_ERR_UNSUPPORTED, "B=%d > %d", d->B, dflash::kPagesMaxB);
+  if ((long)d->B * d->max_pages > 0x7fffffffL) return fail(DFLASH_ERR_UNSUPPORTED, "B*max_pages > 2^31 - 1");
+  return DFLASH_OK;
+}
+
+int dflash_pages_resize(const dflash_pages_dims* d, const int32_t* length, int32_t* page_table,
+                        const int32_t* n_pages, int32_t* free_pages, const int32_t* n_free, int32_t* n_pages_out,
+                        int32_t* n_free_out, uint8_t* short_seq, dflash_stream_t stream) {
+  CallRange range_("dflash_pages_resize");
+  int rc = check_pages_dims(d);
+  if (rc) return rc;
+  if (!length || !page_table || !n_pages || !free_pages || !n_free || !n_pages_out || !n_free_out)
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_resize: a required pointer is NULL");
+  if (n_pages_out == n_pages || n_free_out == n_free || n_pages_out == length)
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_resize: n_pages_out and n_free_out must not alias an input");
+  dflash::PagesArgs a{};
+  a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
+  a.length = length; a.page_table = page_table; a.n_pages = n_pages; a.free_pages = free_pages; a.n_free = n_free;
+  a.n_pages_out = n_pages_out; a.n_free_out = n_free_out; a.short_ = short_seq;
+  a.stream = (cudaStream_t)stream;
+  cudaError_t e = dflash::launch_pages_resize(a, kPlanSms);
+  if (e != cudaSuccess) return cuda_fail(e, "pages_resize launch");
+  return ok(1);
+}
+
+int dflash_slot_map(const dflash_pages_dims* d, int32_t rows_max, const int32_t* start_pos, const int32_t* n_rows,
+                    const int32_t* page_table, int32_t* cu_rows, int32_t* row_seq, int32_t* positions, int64_t* slots,
+                    dflash_stream_t stream) {
+  CallRange range_("dflash_slot_map");
+  int rc = check_pages_dims(d);
+  if (rc) return rc;
+  if (rows_max < 1 || rows_max > 1 << 30) return fail(DFLASH_ERR_INVALID_ARG, "rows_max=%d outside [1, 2^30]", rows_max);
+  if (!start_pos || !n_rows || !page_table || !cu_rows || !row_seq || !positions || !slots)
+    return fail(DFLASH_ERR_INVALID_ARG, "slot_map: a required pointer is NULL");
+  dflash::SlotArgs a{};
+  a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages; a.rows_max = rows_max;
+  a.start_pos = start_pos; a.n_rows = n_rows; a.page_table = page_table;
+  a.cu_rows = cu_rows; a.row_seq = row_seq; a.positions = positions; a.slots = slots;
+  a.stream = (cudaStream_t)stream;
+  cudaError_t e = dflash::launch_slot_map(a, kPlanSms);
+  if (e != cudaSuccess) return cuda_fail(e, "slot_map launch");
+  return ok(1);
+}
+
 // --------------------------------------------------------------- attention ---
 static int check_attn_dims(const dflash_attn_dims* d) {
   if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");

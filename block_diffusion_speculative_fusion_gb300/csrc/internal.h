@@ -174,6 +174,59 @@ cudaError_t launch_ddtree_build(const TreeArgs& a);
 size_t ddtree_verify_ws_bytes(int B, int budget, int V, int dtype, int num_sms);
 cudaError_t launch_ddtree_verify(const TreeArgs& a);
 
+// ----------------------------------------------------------- logit rules ---
+constexpr int kRulesMaxRows = 256;
+constexpr int kRulesCountBits = 18;   // of a token's word: its occurrences in the output
+constexpr int kRulesBiasBits = 11;    // its bias entry
+struct RulesArgs {
+  int B, n_rows, V, dtype, hist_max, n_bias;
+  const void* logits;          // [B, n_rows, V]
+  const int64_t* cand;         // [B, n_rows] or null
+  const int32_t* n_draft;      // [B] or null
+  const int64_t* hist;         // [B, hist_max] or null
+  const int32_t* hist_len;     // [B]
+  const int32_t* prompt_len;   // [B] or null
+  const float* repetition;     // [B] or null
+  const float* presence;       // [B] or null
+  const float* frequency;      // [B] or null
+  const int64_t* bias_tok;     // [B, n_bias]
+  const float* bias_val;       // [B, n_bias]
+  const int32_t* mask;         // [B, n_rows, ceil(V / 32)] or null
+  const uint8_t* mask_on;      // [B] or null
+  void* out;                   // [B, n_rows, V]; may be logits
+  cudaStream_t stream;
+};
+cudaError_t launch_rules(const RulesArgs& a, int num_sms);
+
+// ------------------------------------------------ block tables, slot maps ---
+constexpr int kPagesMaxB = 4096;
+struct PagesArgs {
+  int B, page_size, max_pages, num_pages;
+  const int32_t* length;       // [B] tokens to hold
+  int32_t* page_table;         // [B, max_pages]
+  const int32_t* n_pages;      // [B]
+  int32_t* free_pages;         // [num_pages]
+  const int32_t* n_free;       // [1]
+  int32_t* n_pages_out;        // [B]
+  int32_t* n_free_out;         // [1]
+  uint8_t* short_;             // [B] or null
+  cudaStream_t stream;
+};
+cudaError_t launch_pages_resize(const PagesArgs& a, int num_sms);
+struct SlotArgs {
+  int B, page_size, max_pages, num_pages, rows_max;
+  const int32_t* start_pos;    // [B]
+  const int32_t* n_rows;       // [B]
+  const int32_t* page_table;   // [B, max_pages]
+  int32_t* cu_rows;            // [B + 1]
+  int32_t* row_seq;            // [rows_max]
+  int32_t* positions;          // [rows_max]
+  int64_t* slots;              // [rows_max]
+  int vec;                     // the row arrays take 16-byte stores
+  cudaStream_t stream;
+};
+cudaError_t launch_slot_map(const SlotArgs& a, int num_sms);
+
 // ------------------------------------------------------------- attention ---
 struct AttnArgs {
   int B, n_q, n_kv, Hq, Hkv, D, page_size, max_pages, num_pages, max_ctx, dtype;

@@ -505,6 +505,117 @@ int dflash_ddtree_verify_greedy(const dflash_tree_dims* dims, const void* target
                                 void* workspace, size_t ws_bytes, dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* Rules on the verify rows' logits                                           */
+/* ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B;         /* sequences */
+  int32_t n_rows;    /* rows per sequence (n_max + 1 of a verify; 1 for plain decoding), <= 256 */
+  int32_t V;         /* vocabulary */
+  int32_t dtype;     /* type of the logits */
+  int32_t hist_max;  /* row stride of hist, 0 .. 262143 (0: no history) */
+  int32_t n_bias;    /* row stride of bias_tok / bias_val, 0 .. 2047 (0: no biases) */
+} dflash_rules_dims;
+
+/*
+ * Penalties for repeated tokens, sparse biases and grammar masks on the logits
+ * that a verify call then reads. The pages have no counterpart: it is the
+ * request's sampling parameters that a server applies to the target's law
+ * before the greedy rule ([SGLang] 3) or the sampled rule ([SpecDec] 3).
+ *
+ * Row r of sequence b predicts the token after the committed ones and the
+ * candidates cand[b, 1 .. r] (cand[b, 0], the anchor, is the last committed
+ * token), so its history grows along the row index. With
+ *   c(v) = occurrences of v in hist[b, prompt_len[b] .. hist_len[b]) and cand[b, 1 .. r]
+ *   seen(v) = c(v) > 0, or v is in hist[b, 0 .. prompt_len[b])
+ * every logit z of token v becomes
+ *   z <- seen(v) ? (z > 0 ? z / repetition[b] : z * repetition[b]) : z
+ *   z <- z - frequency[b] * c(v) - presence[b] * [c(v) > 0]
+ *   z <- z + (the value of the last entry of v in bias_tok[b], 0 if none)
+ *   z <- -inf if bit v of the row's mask is 0
+ * in fp32, rounded to dtype once. A logit that none of these changes keeps its
+ * bits; a masked one is -inf whatever it held (NaN included). A row whose mask
+ * forbids every token is all -inf: the greedy rule takes token 0 there, the
+ * sampled rule a token in [0, V) with DFLASH_FLAG_DEGENERATE.
+ *
+ * logits [B, n_rows, V]; out [B, n_rows, V]: a second buffer, or logits itself
+ *   (then only the logits that change are written); no other overlap
+ * cand [B, n_rows] int64 or NULL (the rows' histories are then the committed one)
+ * n_draft [B] int32 or NULL: rows 0 .. n_draft[b] (clamped to [0, n_rows - 1])
+ *   are written, the rest of out is left as it was; NULL: every row
+ * hist [B, hist_max] int64 or NULL; hist_len [B] int32 (with hist);
+ *   prompt_len [B] int32 or NULL (0); lengths are clamped to [0, hist_max] and
+ *   [0, hist_len[b]]
+ * repetition (> 0), presence, frequency [B] float or NULL (1, 0, 0)
+ * bias_tok [B, n_bias] int64, bias_val [B, n_bias] float (both or neither)
+ * mask [B, n_rows, ceil(V / 32)] int32 or NULL: token v is bit v % 32 of word
+ *   v / 32, 1 = allowed; mask_on [B] uint8 or NULL (every sequence): sequences
+ *   with 0 are not masked and their words not read
+ * Tokens of cand, hist and bias_tok outside [0, V) count for nothing (-1 pads a
+ * list). No workspace; repeated calls give identical bits.
+ */
+int dflash_logits_rules(const dflash_rules_dims* dims, const void* logits, const int64_t* cand,
+                        const int32_t* n_draft, const int64_t* hist, const int32_t* hist_len,
+                        const int32_t* prompt_len, const float* repetition, const float* presence,
+                        const float* frequency, const int64_t* bias_tok, const float* bias_val,
+                        const int32_t* mask, const uint8_t* mask_on, void* out, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Block tables and slot maps                                                 */
+/* ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t B;          /* sequences (rows of the table), <= 4096 */
+  int32_t page_size;  /* tokens per page */
+  int32_t max_pages;  /* row stride of page_table; B * max_pages < 2^31 */
+  int32_t num_pages;  /* pages of the pools, and entries of free_pages */
+} dflash_pages_dims;
+
+/*
+ * Resizes every sequence's row of the block table to hold length[b] tokens
+ * ([SGLang] 5.1: headroom reserved before the draft, the part that the verify
+ * did not commit given back after it; 0 ends a sequence, a new one starts with
+ * n_pages[b] = 0). Sequence b needs ceil(length[b] / page_size) pages:
+ *   - pages past that are given back: appended to the free list in sequence
+ *     order, first page first. Their table entries stay as they are (entries
+ *     past a context are not read).
+ *   - missing pages are taken from the end of the list so extended, sequence by
+ *     sequence, and written to the next entries of the row. A sequence gets all
+ *     of them or none: none if they, with those asked for by the sequences
+ *     before it, exceed the list.
+ * A length that a table row cannot hold leaves its sequence as it is.
+ *
+ * length [B] int32 (negative: 0); page_table [B, max_pages] int32, in and out
+ * n_pages [B] int32  pages that each row holds (clamped to [0, max_pages])
+ * free_pages [num_pages] int32, in and out: the first n_free[0] entries are free
+ * n_pages_out [B], n_free_out [1] int32: the new counts; must not alias n_pages
+ *   and n_free, so that the call can be repeated with the same result
+ * short_seq [B] uint8 or NULL: 1 where the pages asked for were not given
+ * No page may appear twice among the free list and the rows' first n_pages
+ * entries (pages are not counted by reference). No workspace.
+ */
+int dflash_pages_resize(const dflash_pages_dims* dims, const int32_t* length, int32_t* page_table,
+                        const int32_t* n_pages, int32_t* free_pages, const int32_t* n_free,
+                        int32_t* n_pages_out, int32_t* n_free_out, uint8_t* short_seq, dflash_stream_t stream);
+
+/*
+ * Slot map of a ragged batch of rows ([SGLang] 5.1, req_to_token): sequence b
+ * has n_rows[b] rows at positions start_pos[b] .., and the batch is the rows of
+ * sequence 0, then of sequence 1, and so on. With T = sum of n_rows (at most
+ * rows_max: rows past it are cut off)
+ *   cu_rows [B + 1] int32   first row of each sequence; cu_rows[B] = T
+ *   row_seq, positions [rows_max] int32   sequence and position of each row
+ *   slots [rows_max] int64   page_table[b][p / page_size] * page_size +
+ *                            p % page_size, or -1 if position p has no page
+ *                            (negative, past max_pages, or an entry outside
+ *                            [0, num_pages))
+ * and -1 in all three for the rows T .. rows_max - 1, so that a captured graph
+ * of rows_max rows writes nothing for them. rows_max in [1, 2^30]; negative
+ * n_rows count as 0. No workspace.
+ */
+int dflash_slot_map(const dflash_pages_dims* dims, int32_t rows_max, const int32_t* start_pos,
+                    const int32_t* n_rows, const int32_t* page_table, int32_t* cu_rows, int32_t* row_seq,
+                    int32_t* positions, int64_t* slots, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Diagnostics                                                                */
 /* ------------------------------------------------------------------------- */
 /*

@@ -553,3 +553,113 @@ def ddtree_walk_greedy(target_logits, node_token, node_parent, n_nodes):
         acc[b] = a
         out_tokens[b, a] = bonus[b]
     return dict(accept_len=acc, commit_len=acc + 1, bonus=bonus, path=path, out_tokens=out_tokens)
+
+
+# ---------------------------------------------------------------------------
+# rules on the verify rows' logits; block tables and slot maps
+# ---------------------------------------------------------------------------
+def logits_rules(logits, cand=None, n_draft=None, hist=None, hist_len=None, prompt_len=None, repetition=None,
+                 presence=None, frequency=None, bias_tok=None, bias_val=None, mask=None, mask_on=None, out=None):
+    """Penalties, biases and grammar masks, token by token. Returns (out,
+    size): ``out`` [B, R, V] in float64 (rows past n_draft[b] as given, or 0)
+    and the sum of the magnitudes of the terms of each value (for error bounds)."""
+    z = _f64(logits)
+    B, R, V = z.shape
+    res = np.zeros_like(z) if out is None else _f64(out).copy()
+    size = np.zeros_like(z)
+    for b in range(B):
+        theta = 1.0 if repetition is None else float(repetition[b])
+        pi = 0.0 if presence is None else float(presence[b])
+        phi = 0.0 if frequency is None else float(frequency[b])
+        prompt, count = set(), {}
+        if hist is not None:
+            n = min(max(int(hist_len[b]), 0), hist.shape[1])
+            p = 0 if prompt_len is None else min(max(int(prompt_len[b]), 0), n)
+            for i in range(n):
+                t = int(hist[b, i])
+                if 0 <= t < V:
+                    if i < p:
+                        prompt.add(t)
+                    else:
+                        count[t] = count.get(t, 0) + 1
+        bias = {}
+        if bias_tok is not None:
+            for t, v in zip(bias_tok[b], bias_val[b]):
+                if 0 <= int(t) < V:
+                    bias[int(t)] = float(v)          # the last entry of a token counts
+        nd = R - 1 if n_draft is None else min(max(int(n_draft[b]), 0), R - 1)
+        for r in range(nd + 1):
+            if r >= 1 and cand is not None and 0 <= int(cand[b, r]) < V:
+                count[int(cand[b, r])] = count.get(int(cand[b, r]), 0) + 1
+            row = z[b, r].copy()
+            mag = np.abs(row)
+            for t in prompt | set(count):
+                row[t] = row[t] / theta if row[t] > 0 else row[t] * theta
+                mag[t] = abs(row[t])
+            for t, c in count.items():
+                row[t] -= phi * c + pi
+                mag[t] += abs(phi) * c + abs(pi)
+            for t, v in bias.items():
+                row[t] += v
+                mag[t] += abs(v)
+            if mask is not None and (mask_on is None or mask_on[b]):
+                words = np.asarray(mask[b, r]).astype(np.int64) & 0xFFFFFFFF
+                for t in range(V):
+                    if not (int(words[t // 32]) >> (t % 32)) & 1:
+                        row[t] = -np.inf
+            res[b, r] = row
+            size[b, r] = mag
+    return res, size
+
+
+def pages_resize(length, page_table, n_pages, free_pages, n_free, page_size):
+    """Block tables resized to lengths: returns page_table, n_pages, free_pages,
+    n_free, short. All frees come first, then the sequences take in order."""
+    table = [list(map(int, r)) for r in page_table]
+    free = list(map(int, free_pages))
+    max_pages = len(table[0])
+    held = [min(max(int(n), 0), max_pages) for n in n_pages]
+    stack = free[:int(n_free)]
+    asked = []
+    short = []
+    for b, n in enumerate(length):
+        k = -(-max(int(n), 0) // page_size)
+        short.append(int(k > max_pages))
+        asked.append(held[b] if k > max_pages else k)
+    now = list(held)
+    for b, k in enumerate(asked):
+        if k < held[b]:
+            stack.extend(table[b][k:held[b]])
+            now[b] = k
+    free = stack + free[len(stack):]
+    pool, before = len(stack), 0
+    for b, k in enumerate(asked):
+        want = max(0, k - held[b])
+        before += want
+        if want and before > pool:
+            short[b] = 1
+        elif want:
+            for i in range(want):
+                table[b][held[b] + i] = stack.pop()
+            now[b] = k
+    return (np.array(table, dtype=np.int32), np.array(now, dtype=np.int32), np.array(free, dtype=np.int32),
+            len(stack), np.array(short, dtype=np.uint8))
+
+
+def slot_map(start_pos, n_rows, page_table, page_size, num_pages, rows_max):
+    """cu_rows, row_seq, positions, slots of the ragged batch of rows."""
+    cu, seq, pos, slot = [0], [], [], []
+    max_pages = len(page_table[0])
+    for b in range(len(n_rows)):
+        for j in range(max(int(n_rows[b]), 0)):
+            if len(seq) == rows_max:
+                break
+            p = int(start_pos[b]) + j
+            page = int(page_table[b][p // page_size]) if 0 <= p < max_pages * page_size else -1
+            seq.append(b)
+            pos.append(p)
+            slot.append(page * page_size + p % page_size if 0 <= page < num_pages else -1)
+        cu.append(len(seq))
+    pad = [-1] * (rows_max - len(seq))
+    return (np.array(cu, dtype=np.int32), np.array(seq + pad, dtype=np.int32), np.array(pos + pad, dtype=np.int32),
+            np.array(slot + pad, dtype=np.int64))
