@@ -205,20 +205,34 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _launch(device: torch.device, fn, *args) -> None:
-    """Call ``fn(*args, stream)`` with ``device`` current and its current stream."""
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(device))
+def _arg(t: Optional[torch.Tensor], name: str, dev: int, dtype: torch.dtype, shape: Tuple[int, ...]):
+    """Device pointer of a contiguous tensor of this dtype and shape on CUDA
+    device ``dev`` (None stays None); raises what ``_dev`` raises otherwise.
+    The checks of a small call cost more host time than its launch, so the
+    valid case takes the fewest attribute reads."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+# the stream handle without a Stream object, where this torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _launch(dev: int, fn, *args) -> None:
+    """``fn(*args, stream)`` with CUDA device ``dev`` current, on its current stream."""
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream(device))
-    _check(rc)
-
-
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if isinstance(t, torch.Tensor) and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
+    if rc != OK:
+        raise DflashError(rc, last_error())
 
 
 _WS: Dict[Tuple[int, int], torch.Tensor] = {}
@@ -538,27 +552,27 @@ def logits_rules(logits: torch.Tensor, cand: Optional[torch.Tensor] = None, n_dr
     not given); ``out=logits`` works in place."""
     _dev(logits, "logits")
     B, R, V = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     if (hist is None) != (hist_len is None):
         raise ValueError("hist and hist_len come together")
     if (bias_tok is None) != (bias_val is None):
         raise ValueError("bias_tok and bias_val come together")
     H = 0 if hist is None else hist.shape[1]
     nb = 0 if bias_tok is None else bias_tok.shape[1]
-    _same_device(dev, cand=cand, n_draft=n_draft, hist=hist, hist_len=hist_len, prompt_len=prompt_len,
-                 repetition=repetition, presence=presence, frequency=frequency, bias_tok=bias_tok,
-                 bias_val=bias_val, mask=mask, mask_on=mask_on, out=out)
     if out is None:
         out = torch.empty_like(logits) if n_draft is None else torch.zeros_like(logits)
-    dims = RulesDims(B, R, V, _dtype_code(logits), H, nb)
-    _launch(dev, lib().dflash_logits_rules, ctypes.byref(dims), logits.data_ptr(),
-            _opt(cand, "cand", torch.int64, (B, R)), _opt(n_draft, "n_draft", torch.int32, (B,)),
-            _opt(hist, "hist", torch.int64, (B, H)), _opt(hist_len, "hist_len", torch.int32, (B,)),
-            _opt(prompt_len, "prompt_len", torch.int32, (B,)), _opt(repetition, "repetition", torch.float32, (B,)),
-            _opt(presence, "presence", torch.float32, (B,)), _opt(frequency, "frequency", torch.float32, (B,)),
-            _opt(bias_tok, "bias_tok", torch.int64, (B, nb)), _opt(bias_val, "bias_val", torch.float32, (B, nb)),
-            _opt(mask, "mask", torch.int32, (B, R, (V + 31) // 32)), _opt(mask_on, "mask_on", torch.uint8, (B,)),
-            _dev(out, "out", logits.dtype, (B, R, V)))
+    seq = (B,)
+    _launch(dev, lib().dflash_logits_rules, ctypes.byref(RulesDims(B, R, V, _dtype_code(logits), H, nb)),
+            logits.data_ptr(), _arg(cand, "cand", dev, torch.int64, (B, R)),
+            _arg(n_draft, "n_draft", dev, torch.int32, seq), _arg(hist, "hist", dev, torch.int64, (B, H)),
+            _arg(hist_len, "hist_len", dev, torch.int32, seq), _arg(prompt_len, "prompt_len", dev, torch.int32, seq),
+            _arg(repetition, "repetition", dev, torch.float32, seq),
+            _arg(presence, "presence", dev, torch.float32, seq),
+            _arg(frequency, "frequency", dev, torch.float32, seq),
+            _arg(bias_tok, "bias_tok", dev, torch.int64, (B, nb)),
+            _arg(bias_val, "bias_val", dev, torch.float32, (B, nb)),
+            _arg(mask, "mask", dev, torch.int32, (B, R, (V + 31) // 32)),
+            _arg(mask_on, "mask_on", dev, torch.uint8, seq), _arg(out, "out", dev, logits.dtype, (B, R, V)))
     return out
 
 
@@ -574,23 +588,21 @@ def pages_resize(length: torch.Tensor, page_table: torch.Tensor, n_pages: torch.
     (tensors other than the inputs), short [B] uint8."""
     _dev(page_table, "page_table", torch.int32)
     B, max_pages = page_table.shape
-    dev = page_table.device
+    dev = page_table.get_device()
     o = out if out is not None else {}
     if "n_pages" not in o:
-        o["n_pages"] = torch.empty(B, dtype=torch.int32, device=dev)
+        o["n_pages"] = torch.empty_like(n_pages)
     if "n_free" not in o:
-        o["n_free"] = torch.empty(1, dtype=torch.int32, device=dev)
+        o["n_free"] = torch.empty_like(n_free)
     if "short" not in o:
-        o["short"] = torch.empty(B, dtype=torch.uint8, device=dev)
-    _same_device(dev, length=length, n_pages=n_pages, free_pages=free_pages, n_free=n_free)
-    _same_device(dev, **o)
-    num_pages = free_pages.shape[0]
-    dims = PagesDims(B, int(page_size), max_pages, num_pages)
-    _launch(dev, lib().dflash_pages_resize, ctypes.byref(dims), _dev(length, "length", torch.int32, (B,)),
-            page_table.data_ptr(), _dev(n_pages, "n_pages", torch.int32, (B,)),
-            _dev(free_pages, "free_pages", torch.int32, (num_pages,)), _dev(n_free, "n_free", torch.int32, (1,)),
-            _dev(o["n_pages"], "out n_pages", torch.int32, (B,)), _dev(o["n_free"], "out n_free", torch.int32, (1,)),
-            _dev(o["short"], "short", torch.uint8, (B,)))
+        o["short"] = torch.empty(B, dtype=torch.uint8, device=page_table.device)
+    num_pages = len(free_pages)
+    i32 = torch.int32
+    _launch(dev, lib().dflash_pages_resize, ctypes.byref(PagesDims(B, page_size, max_pages, num_pages)),
+            _arg(length, "length", dev, i32, (B,)), page_table.data_ptr(), _arg(n_pages, "n_pages", dev, i32, (B,)),
+            _arg(free_pages, "free_pages", dev, i32, (num_pages,)), _arg(n_free, "n_free", dev, i32, (1,)),
+            _arg(o["n_pages"], "out n_pages", dev, i32, (B,)), _arg(o["n_free"], "out n_free", dev, i32, (1,)),
+            _arg(o["short"], "short", dev, torch.uint8, (B,)))
     return o
 
 
@@ -601,22 +613,23 @@ def slot_map(start_pos: torch.Tensor, n_rows: torch.Tensor, page_table: torch.Te
     positions [rows_max] int32, slots [rows_max] int64 (-1 past the last row)."""
     _dev(page_table, "page_table", torch.int32)
     B, max_pages = page_table.shape
-    dev = page_table.device
+    dev = page_table.get_device()
+    i32, device = torch.int32, page_table.device
+    rows = (max(rows_max, 0),)
     o = out if out is not None else {}
     if "cu_rows" not in o:
-        o["cu_rows"] = torch.empty(B + 1, dtype=torch.int32, device=dev)
-    for name, dt in (("row_seq", torch.int32), ("positions", torch.int32), ("slots", torch.int64)):
-        if name not in o:
-            o[name] = torch.empty(max(int(rows_max), 0), dtype=dt, device=dev)
-    _same_device(dev, start_pos=start_pos, n_rows=n_rows)
-    _same_device(dev, **o)
-    dims = PagesDims(B, int(page_size), max_pages, int(num_pages))
-    _launch(dev, lib().dflash_slot_map, ctypes.byref(dims), int(rows_max),
-            _dev(start_pos, "start_pos", torch.int32, (B,)), _dev(n_rows, "n_rows", torch.int32, (B,)),
-            page_table.data_ptr(), _dev(o["cu_rows"], "cu_rows", torch.int32, (B + 1,)),
-            _dev(o["row_seq"], "row_seq", torch.int32, (rows_max,)),
-            _dev(o["positions"], "positions", torch.int32, (rows_max,)),
-            _dev(o["slots"], "slots", torch.int64, (rows_max,)))
+        o["cu_rows"] = torch.empty(B + 1, dtype=i32, device=device)
+    if "row_seq" not in o:
+        o["row_seq"] = torch.empty(rows, dtype=i32, device=device)
+    if "positions" not in o:
+        o["positions"] = torch.empty(rows, dtype=i32, device=device)
+    if "slots" not in o:
+        o["slots"] = torch.empty(rows, dtype=torch.int64, device=device)
+    _launch(dev, lib().dflash_slot_map, ctypes.byref(PagesDims(B, page_size, max_pages, num_pages)), rows_max,
+            _arg(start_pos, "start_pos", dev, i32, (B,)), _arg(n_rows, "n_rows", dev, i32, (B,)),
+            page_table.data_ptr(), _arg(o["cu_rows"], "cu_rows", dev, i32, (B + 1,)),
+            _arg(o["row_seq"], "row_seq", dev, i32, rows), _arg(o["positions"], "positions", dev, i32, rows),
+            _arg(o["slots"], "slots", dev, torch.int64, rows))
     return o
 
 

@@ -468,7 +468,7 @@ int dflash_logits_rules(const dflash_rules_dims* d, const void* logits, const in
   if (d->n_bias >= 1 << dflash::kRulesBiasBits)
     return fail(DFLASH_ERR_UNSUPPORTED, "n_bias=%d > %d", d->n_bias, (1 << dflash::kRulesBiasBits) - 1);
   if (d->B > 65535) return fail(DFLASH_ERR_UNSUPPORTED, "B=%d > 65535", d->B);
-  if (d->V > 1 << 30) return fail(DFLASH_ERR_UNSUPPORTED, "V=%d too large", d->V);
+  if (d->V > 1 << 25) return fail(DFLASH_ERR_UNSUPPORTED, "V=%d > 2^25", d->V);
   if (!logits || !out || (d->hist_max > 0 && (!hist || !hist_len)) || (d->n_bias > 0 && (!bias_tok || !bias_val)))
     return fail(DFLASH_ERR_INVALID_ARG, "logits_rules: a required pointer is NULL");
   const size_t el = d->dtype == DFLASH_BF16 ? 2 : 4;
@@ -485,7 +485,7 @@ int dflash_logits_rules(const dflash_rules_dims* d, const void* logits, const in
   a.bias_tok = bias_tok; a.bias_val = bias_val; a.mask = mask; a.mask_on = mask_on;
   a.out = out;
   a.stream = (cudaStream_t)stream;
-  cudaError_t e = dflash::launch_rules(a, kPlanSms);
+  cudaError_t e = dflash::launch_rules(a);
   if (e != cudaSuccess) return cuda_fail(e, "logits_rules launch");
   return ok(1);
 }

@@ -196,7 +196,7 @@ struct RulesArgs {
   void* out;                   // [B, n_rows, V]; may be logits
   cudaStream_t stream;
 };
-cudaError_t launch_rules(const RulesArgs& a, int num_sms);
+cudaError_t launch_rules(const RulesArgs& a);
 
 // ------------------------------------------------ block tables, slot maps ---
 constexpr int kPagesMaxB = 4096;

@@ -12,31 +12,67 @@
 // in fp32, rounded to the I/O type once; a token that no rule touches keeps
 // its bits.
 //
-// Bound: one read and one write of the rows. A CTA owns a chunk of the
-// vocabulary of one sequence, for all its rows: it gathers the history's counts
-// and the bias entries of its tokens once, in shared memory (one word a token),
-// and streams the rows past them. Few tokens have a rule: one bit a token tells
-// a 16-byte vector that none of its tokens has, and such a vector is copied. A
-// vector that the mask forbids whole is written without being read; in place,
-// a vector without a rule is neither read nor written.
+// Bound: one read and one write of the rows. A CTA owns 256 16-byte vectors of
+// the vocabulary of one sequence, one a thread, for all its rows. Without lists
+// it streams them through registers, four rows in flight a thread, with the
+// mask alone: a vector that the mask forbids whole is written without being
+// read, and in place a vector without a masked token is neither read nor
+// written. With lists the rows pass through shared memory, four at a time in
+// two stages (cp.async keeps up to 32 KB a CTA in flight whatever the threads
+// do); between a stage's arrival and its way out the CTA mends the tokens that
+// have a rule, of which there are few: one (token, row) pair a thread, out of a
+// list compacted in shared memory.
+//
+// What is known of the tokens, two words each, comes from the history, which
+// the CTAs of a cluster of up to eight read once between them: each adds its
+// part of it to the tokens' owners (distributed shared memory) while the first
+// rows are on their way.
 #include "common.cuh"
 #include "internal.h"
+#include "stream.cuh"
+#include "tma.cuh"
 
 namespace dflash {
 
 namespace rules {
-constexpr int kThreads = 256;
-// the word of a token in shared memory
-constexpr uint32_t kCountMask = (1u << kRulesCountBits) - 1;            // occurrences in the output
-constexpr int kBiasShift = kRulesCountBits;                             // last bias entry of the token, plus one
-constexpr uint32_t kBiasMask = (1u << kRulesBiasBits) - 1;
-constexpr uint32_t kCand = 1u << 30;                                    // the token is among the candidates
-constexpr uint32_t kPrompt = 1u << 31;                                  // the token is in the prompt
-static_assert(kRulesCountBits + kRulesBiasBits <= 30, "token word");
+constexpr int kVecs = 256;            // vectors of a CTA's chunk
+constexpr int kRowsInFlight = 4;         // rows of a stage
+constexpr int kStages = 2;
+constexpr int kCtasPerSm = 4;            // 54 KB of shared memory each
+constexpr int kMaxCluster = 8;
+// a token's word: occurrences in the output, and
+constexpr uint32_t kCountMask = (1u << kRulesCountBits) - 1;
+constexpr uint32_t kCand = 1u << 30;     // the token is among the candidates
+constexpr uint32_t kPrompt = 1u << 31;   // the token is in the prompt
+static_assert(kRulesCountBits <= 30, "token word");
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Address of this CTA's shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t at_rank(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void red_add(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_or(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_max(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 }  // namespace rules
 
 struct RulesParams {
-  int R, V, H, nb, W, chunk, in_place;
+  int R, V, H, nb, W, in_place;
+  int lists;   // penalties or biases are given
   const int64_t* cand;
   const int32_t* n_draft;
   const int64_t* hist;
@@ -58,29 +94,6 @@ __device__ __forceinline__ uint4 ld_rows16(const void* p) {
   return r;
 }
 
-// Element j (a run-time index) of a 16-byte vector, read and replaced.
-__device__ __forceinline__ uint32_t vec_word(const uint4& u, int i) {
-  return i < 2 ? (i == 0 ? u.x : u.y) : (i == 2 ? u.z : u.w);
-}
-__device__ __forceinline__ void set_vec_word(uint4& u, int i, uint32_t w) {
-  u.x = i == 0 ? w : u.x;
-  u.y = i == 1 ? w : u.y;
-  u.z = i == 2 ? w : u.z;
-  u.w = i == 3 ? w : u.w;
-}
-template <typename T> __device__ __forceinline__ float vec_get(const uint4& u, int j);
-template <> __device__ __forceinline__ float vec_get<float>(const uint4& u, int j) { return __uint_as_float(vec_word(u, j)); }
-template <> __device__ __forceinline__ float vec_get<bf16>(const uint4& u, int j) {
-  const uint32_t w = vec_word(u, j >> 1);
-  return (j & 1) ? bf16_hi(w) : bf16_lo(w);
-}
-template <typename T> __device__ __forceinline__ void vec_set(uint4& u, int j, float v);
-template <> __device__ __forceinline__ void vec_set<float>(uint4& u, int j, float v) { set_vec_word(u, j, __float_as_uint(v)); }
-template <> __device__ __forceinline__ void vec_set<bf16>(uint4& u, int j, float v) {
-  const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v)), w = vec_word(u, j >> 1);
-  set_vec_word(u, j >> 1, (j & 1) ? (w & 0xffffu) | (h << 16) : (w & 0xffff0000u) | h);
-}
-
 // Element j of a 16-byte vector set to -inf where bit j of `ok` is 0.
 template <typename T> __device__ __forceinline__ void forbid16(uint4& u, uint32_t ok);
 template <> __device__ __forceinline__ void forbid16<float>(uint4& u, uint32_t ok) {
@@ -93,8 +106,10 @@ template <> __device__ __forceinline__ void forbid16<bf16>(uint4& u, uint32_t ok
   uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (!((ok >> (2 * q)) & 1)) w[q] = (w[q] & 0xffff0000u) | 0xff80u;
-    if (!((ok >> (2 * q + 1)) & 1)) w[q] = (w[q] & 0xffffu) | 0xff800000u;
+    // the two bits spread over their halves of the word
+    const uint32_t lo = (uint32_t)((int)(ok << (31 - 2 * q)) >> 31), hi = (uint32_t)((int)(ok << (30 - 2 * q)) >> 31);
+    const uint32_t m = __byte_perm(lo, hi, 0x7610);
+    w[q] = (w[q] & m) | (0xff80ff80u & ~m);
   }
 }
 
@@ -106,166 +121,300 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* a, int at, int n, in
   return x & ((1u << n) - 1);
 }
 
+// Shared memory of a CTA: the stages, then what is known of the tokens.
 template <typename T>
-__global__ void __launch_bounds__(rules::kThreads)
+struct RulesSmem {
+  static constexpr int C = rules::kVecs * VecTraits<T>::N;   // tokens of a chunk
+  // vectors start where the row's address is a multiple of 16 bytes, up to a
+  // vector less one token past the chunk's start: the words reach that far
+  static constexpr int CW = C + VecTraits<T>::N;
+  uint4 stage[rules::kStages][rules::kRowsInFlight][rules::kVecs];
+  uint32_t word[CW];       // occurrences
+  uint32_t entry[CW];      // the last bias entry plus one; then its value's bits
+  uint16_t list[CW];       // the tokens that have a rule
+  int32_t cand[kRulesMaxRows];
+  int n;                   // length of list
+};
+
+// EVEN: logits and out start on 16 bytes and V is a multiple of a vector, so
+// that every row's vectors start at the chunk's first token.
+template <typename T, bool EVEN>
+__global__ void __launch_bounds__(rules::kVecs, rules::kCtasPerSm)
 rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParams p) {
   using namespace rules;
   constexpr int N = VecTraits<T>::N;
+  constexpr int U = kRowsInFlight;
   constexpr uint32_t kAll = (1u << N) - 1;
-  extern __shared__ uint32_t sm[];
-  uint32_t* word = sm;                       // [chunk] what is known of each token
-  uint32_t* rule = sm + p.chunk;             // [chunk / 32] bit: some row changes the token
-  __shared__ int32_t s_cand[kRulesMaxRows];
+  constexpr int C = RulesSmem<T>::C, CW = RulesSmem<T>::CW;
+  extern __shared__ uint4 rules_smem[];
+  RulesSmem<T>& sm = *reinterpret_cast<RulesSmem<T>*>(rules_smem);
+  // clusters of low tokens, which text repeats most, start first: they mend most
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int c0 = blockIdx.x * p.chunk, c1 = min(p.V, c0 + p.chunk), len = c1 - c0;
+  const int chunk = blockIdx.z * gridDim.x + blockIdx.x;
+  const int c0 = chunk * C;                  // past V in the CTAs that fill up a cluster
+  if (p.lists) {
+    for (int i = tid; i < CW; i += kVecs) sm.word[i] = sm.entry[i] = 0;
+    if (tid == 0) sm.n = 0;
+    __syncthreads();
+    cluster_arrive();                        // (with the wait below: the cluster's words are zero)
+  }
   const int nd = p.n_draft ? min(max(p.n_draft[b], 0), p.R - 1) : p.R - 1;
-
   const float theta = p.repetition ? p.repetition[b] : 1.f;
   const float phi = p.frequency ? p.frequency[b] : 0.f;
   const float pi = p.presence ? p.presence[b] : 0.f;
+  const int n_hist = p.hist ? min(max(p.hist_len[b], 0), p.H) : 0;
+  const int n_prompt = p.prompt_len ? min(max(p.prompt_len[b], 0), n_hist) : 0;
   const bool penal = theta != 1.f || phi != 0.f || pi != 0.f;
   const bool any = penal || p.nb > 0;
   const bool masked = p.mask != nullptr && (p.mask_on == nullptr || p.mask_on[b] != 0);
-
-  if (any) {
-    for (int i = tid; i < p.chunk + p.chunk / 32; i += kThreads) sm[i] = 0;
-    for (int i = tid; i < p.R; i += kThreads) {
-      const int64_t t = (p.cand && penal && i >= 1 && i <= nd) ? p.cand[(size_t)b * p.R + i] : -1;
-      s_cand[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
-    }
-    __syncthreads();
-    // the last entry of a token's biases counts
-    for (int i = tid; i < p.nb; i += kThreads) {
-      const int64_t t = p.bias_tok[(size_t)b * p.nb + i] - c0;
-      if (t >= 0 && t < len) {
-        atomicMax(&word[t], (uint32_t)(i + 1) << kBiasShift);
-        atomicOr(&rule[t >> 5], 1u << (t & 31));
-      }
-    }
-    __syncthreads();
-    if (penal) {
-      const int n = p.hist ? min(max(p.hist_len[b], 0), p.H) : 0;
-      const int np = p.prompt_len ? min(max(p.prompt_len[b], 0), n) : 0;
-      const int64_t* h = p.hist + (size_t)b * p.H;
-      auto note = [&](int64_t tok, int i) {
-        const int64_t t = tok - c0;
-        if (t >= 0 && t < len) {
-          if (i < np) atomicOr(&word[t], kPrompt);
-          else atomicAdd(&word[t], 1u);
-          atomicOr(&rule[t >> 5], 1u << (t & 31));
-        }
-      };
-      for (int i = tid; i < n; i += kThreads) note(h[i], i);
-      for (int i = 1 + tid; i <= nd; i += kThreads) {
-        const int t = s_cand[i] - c0;
-        if (t >= 0 && t < len) {
-          atomicOr(&word[t], kCand);
-          atomicOr(&rule[t >> 5], 1u << (t & 31));
-        }
-      }
-    }
-    __syncthreads();
-  }
-
-  // what row r makes of logit z of token e
-  auto apply = [&](float z, int e, int r) -> float {
-    const uint32_t w = word[e - c0];
+  const T* z0 = logits + (size_t)b * p.R * p.V;
+  T* o0 = out + (size_t)b * p.R * p.V;
+  const uint32_t* m0 = masked ? p.mask + (size_t)b * p.R * p.W : nullptr;
+  // both buffers' rows have to start their vectors at the same token
+  const bool vec = EVEN || ((reinterpret_cast<uintptr_t>(z0) ^ reinterpret_cast<uintptr_t>(o0)) & 15) == 0;
+  // tokens of row r before its first vector
+  auto head = [&](int r) -> int {
+    if (EVEN) return 0;
+    return (int)(((16u - (unsigned)(reinterpret_cast<uintptr_t>(z0 + (size_t)r * p.V) & 15u)) & 15u) / sizeof(T));
+  };
+  // what row r makes of logit z of token c0 + i
+  auto apply = [&](float z, int i, int r) -> float {
+    const uint32_t w = sm.word[i];
     int c = (int)(w & kCountMask);
-    if (w & kCand)
-      for (int i = 1; i <= r; ++i) c += s_cand[i] == e ? 1 : 0;
+    if (w & kCand)                           // (a candidate further on does not count yet)
+      for (int k = 1; k <= r; ++k) c += sm.cand[k] == c0 + i ? 1 : 0;
     if (c > 0 || (w & kPrompt)) z = z > 0.f ? __fdiv_rn(z, theta) : z * theta;
     if (c > 0) z = __fsub_rn(__fsub_rn(z, __fmul_rn(phi, (float)c)), pi);
-    const uint32_t j = (w >> kBiasShift) & kBiasMask;
-    if (j) z += p.bias_val[(size_t)b * p.nb + j - 1];
-    return z;
+    const uint32_t v = sm.entry[i];
+    return v ? z + __uint_as_float(v) : z;
   };
-  // whether row r changes token e at all (a candidate further on does not count yet)
-  auto touched = [&](int e, int r) -> bool {
-    const uint32_t w = word[e - c0];
-    if (w & ~kCand) return true;
-    for (int i = 1; i <= r; ++i)
-      if (s_cand[i] == e) return true;
-    return false;
+  auto one = [&](int e, int r) {             // a token that no vector holds
+    const size_t at = (size_t)r * p.V + e;
+    const bool good = !m0 || ((m0[(size_t)r * p.W + (e >> 5)] >> (e & 31)) & 1);
+    const int i = e - c0;
+    const bool ruled = any && (sm.word[i] | sm.entry[i]) != 0;
+    if (p.in_place && good && !ruled) return;
+    T v = from_f32<T>(-CUDART_INF_F);
+    if (good) v = ruled ? from_f32<T>(apply(to_f32(z0[at]), i, r)) : z0[at];
+    o0[at] = v;
   };
-
-  constexpr int U = 4;
-  for (int r = 0; r <= nd; ++r) {
-    const size_t row = (size_t)b * p.R + r;
-    const T* z = logits + row * p.V;
-    T* o = out + row * p.V;
-    const uint32_t* mk = masked ? p.mask + row * p.W : nullptr;
-    auto one = [&](int e) {
-      const bool ok = !mk || ((mk[e >> 5] >> (e & 31)) & 1);
-      const bool rl = any && ((rule[(e - c0) >> 5] >> ((e - c0) & 31)) & 1);
-      if (p.in_place && ok && !rl) return;
-      T v = from_f32<T>(-CUDART_INF_F);
-      if (ok) {
-        v = z[e];
-        if (rl && touched(e, r)) v = from_f32<T>(apply(to_f32(v), e, r));
-      }
-      o[e] = v;
-    };
-    // both rows have to start a vector at the same token
-    const uintptr_t az = reinterpret_cast<uintptr_t>(z + c0), ao = reinterpret_cast<uintptr_t>(o + c0);
-    int head = len, nvec = 0;
-    if (((az ^ ao) & 15) == 0) {
-      head = min(len, (int)(((16u - (unsigned)(az & 15u)) & 15u) / sizeof(T)));
-      nvec = (len - head) / N;
+  // the tokens of a row before its first vector and after its last (EVEN: none),
+  // or all of them where the buffers' vectors do not meet
+  auto scalars = [&](int r) {
+    if (EVEN) return;
+    if (!vec) {
+      for (int e = c0 + tid; e < min(p.V, c0 + C); e += kVecs) one(e, r);
+    } else if (tid < N) {
+      const int h = min(head(r), p.V);
+      if (c0 == 0 && tid < h) one(tid, r);
+      const int k = (p.V - h) / N, e = h + k * N + tid;
+      if (k / kVecs == chunk && e < p.V) one(e, r);
     }
-    const int a0 = c0 + head;
-    for (int e = c0 + tid; e < a0; e += kThreads) one(e);
-    for (int e = a0 + nvec * N + tid; e < c1; e += kThreads) one(e);
-    for (int v0 = tid; v0 < nvec; v0 += U * kThreads) {
-      uint32_t ok[U], rl[U];
+  };
+  // whether row r has a vector for this thread, the mask words (byte, if EVEN)
+  // that hold its allowed bits, and the bits: bit j is token j's
+  auto has_vec = [&](int r) { return r <= nd && vec && head(r) + c0 + tid * N + N <= p.V; };
+  auto mask_words = [&](int r) -> uint32_t {
+    if (!m0 || !has_vec(r)) return 0xffffffffu;
+    const int e = head(r) + c0 + tid * N;
+    if constexpr (EVEN) return reinterpret_cast<const uint8_t*>(m0 + (size_t)r * p.W)[e / 8];
+    return bits_at(m0 + (size_t)r * p.W, e, N, p.W);
+  };
+  auto allowed = [&](uint32_t words, int r) -> uint32_t {
+    if (!has_vec(r)) return 0;
+    return (EVEN && N < 8 ? words >> (tid * N & 7) : words) & kAll;
+  };
+  auto at_vec = [&](int r) -> size_t { return (size_t)r * p.V + (head(r) + c0 + tid * N); };
+
+  if (!any) {
+    if (p.lists) cluster_wait();
+    if (c0 >= p.V) return;
+    for (int r0 = 0; r0 <= nd; r0 += U) {
+      uint32_t ok[U];
       uint4 x[U];
 #pragma unroll
+      for (int u = 0; u < U; ++u) ok[u] = mask_words(r0 + u);
+#pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kThreads, e = a0 + v * N;
-        ok[u] = v >= nvec ? 0u : (mk ? bits_at(mk, e, N, p.W) : kAll);
+        ok[u] = allowed(ok[u], r0 + u);
+        if (ok[u] && !(p.in_place && ok[u] == kAll)) x[u] = ld_rows16(z0 + at_vec(r0 + u));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kThreads, e = a0 + v * N;
-        rl[u] = any && v < nvec ? bits_at(rule, e - c0, N, p.chunk / 32) : 0u;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (ok[u] && !(p.in_place && ok[u] == kAll && !rl[u])) x[u] = ld_rows16(z + e);
+        if (!has_vec(r0 + u) || (p.in_place && ok[u] == kAll)) continue;
+        if (m0) forbid16<T>(x[u], ok[u]);
+        *reinterpret_cast<uint4*>(o0 + at_vec(r0 + u)) = x[u];
       }
+      for (int u = 0; u < U && r0 + u <= nd; ++u) scalars(r0 + u);
+    }
+    return;
+  }
+
+  bool plain = false;                        // in place: the thread's vector has no rule (once that is known)
+  // requests the thread's vectors of group g's rows, whose mask words have been
+  // read before; returns their allowed bits, a byte a row
+  uint32_t words[U];
+  auto read_mask = [&](int g) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * kThreads, e = a0 + v * N;
-        if (v >= nvec || (p.in_place && ok[u] == kAll && !rl[u])) continue;
-        uint32_t todo = rl[u] & ok[u];
-        while (todo) {
-          const int j = __ffs(todo) - 1;
-          todo &= todo - 1;
-          if (touched(e + j, r)) vec_set<T>(x[u], j, apply(vec_get<T>(x[u], j), e + j, r));
-        }
-        if (ok[u] != kAll) forbid16<T>(x[u], ok[u]);
-        *reinterpret_cast<uint4*>(o + e) = x[u];
-      }
+    for (int u = 0; u < U; ++u) words[u] = mask_words(g * U + u);
+  };
+  auto fetch = [&](int g) -> uint32_t {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t ok = allowed(words[u], g * U + u);
+      bits |= ok << (8 * u);
+      if (ok && !(plain && ok == kAll)) cp_async16(&sm.stage[g % kStages][u][tid], z0 + at_vec(g * U + u));
+    }
+    cp_async_commit();
+    return bits;
+  };
+  read_mask(0);
+  uint32_t ok_now = fetch(0);
+  read_mask(1);
+  uint32_t ok_next = fetch(1);
+  read_mask(2);
+
+  for (int i = tid; i < p.R; i += kVecs) {
+    const int64_t t = (p.cand && penal && i >= 1 && i <= nd) ? p.cand[(size_t)b * p.R + i] : -1;
+    sm.cand[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
+  }
+  __syncthreads();
+  cluster_wait();
+  {
+    uint32_t cs;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
+    const uint32_t rank = cluster_rank();
+    const int64_t first = (int64_t)(chunk - (int)rank) * C;      // the cluster's first token
+    const int span = (int)cs * C;
+    // f at the token's word in its owner, and in the chunk before, whose vectors may reach it
+    auto note = [&](int64_t tok, auto&& f) {
+      const int64_t v = tok - first;
+      if (tok < 0 || tok >= p.V || v < 0 || v >= span + N) return;
+      const int owner = (int)v / C, off = (int)v % C;
+      if (v < span) f((uint32_t)owner, off);
+      if (!EVEN && off < N && owner >= 1) f((uint32_t)(owner - 1), off + C);
+    };
+    const int step = (int)cs * kVecs, i0 = (int)rank * kVecs + tid;
+    for (int i = i0; i < p.nb; i += step)    // the last entry of a token's biases counts
+      note(p.bias_tok[(size_t)b * p.nb + i], [&](uint32_t k, int off) { red_max(at_rank(&sm.entry[off], k), (uint32_t)i + 1); });
+    if (penal) {
+      const int64_t* h = p.hist + (size_t)b * p.H;
+#pragma unroll 4
+      for (int i = i0; i < n_hist; i += step)
+        note(h[i], [&](uint32_t k, int off) {
+          const uint32_t a = at_rank(&sm.word[off], k);
+          if (i < n_prompt) red_or(a, kPrompt);
+          else red_add(a, 1u);
+        });
+      for (int i = 1 + i0; i <= nd; i += step)
+        note(sm.cand[i], [&](uint32_t k, int off) { red_or(at_rank(&sm.word[off], k), kCand); });
     }
   }
+  cluster_arrive();
+  cluster_wait();                            // every part of the lists is in
+  if (c0 >= p.V) return;                     // (the whole CTA)
+  for (int i = tid; i < (CW + 31) / 32 * 32; i += kVecs) {
+    const uint32_t j = i < CW ? sm.entry[i] : 0;
+    const bool ruled = i < CW && (sm.word[i] | j) != 0;
+    if (j) sm.entry[i] = __float_as_uint(p.bias_val[(size_t)b * p.nb + j - 1]);
+    const unsigned m = __ballot_sync(0xffffffffu, ruled);
+    int at = 0;
+    if ((tid & 31) == 0 && m) at = atomicAdd(&sm.n, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0);
+    if (ruled) sm.list[at + __popc(m & ((1u << (tid & 31)) - 1))] = (uint16_t)i;
+  }
+  __syncthreads();
+  const int n = sm.n;
+  if (EVEN && p.in_place) {
+    plain = true;
+#pragma unroll
+    for (int j = 0; j < N; ++j) plain = plain && (sm.word[tid * N + j] | sm.entry[tid * N + j]) == 0;
+  }
+
+  // pairs (row, list entry) kVecs apart
+  const int dr = n ? kVecs / n : 0, di = n ? kVecs % n : 0;
+  const int r_first = n ? tid / n : 0, k_first = n ? tid % n : 0;
+  for (int g = 0; g * U <= nd; ++g) {
+    cp_async_wait_one();                     // group g is here (group g + 1 may be on its way)
+    __syncthreads();
+    if (n) {
+      const int rows = min(U, nd + 1 - g * U);
+      for (int u = r_first, k = k_first; u < rows;) {
+        const int i = sm.list[k], r = g * U + u;
+        // the token's place among the chunk's vectors; the tail of a row is in none
+        const int off = i - head(r);
+        if (EVEN || (vec && off >= 0 && off < C && c0 + i - off % N + N <= p.V)) {
+          T* z = reinterpret_cast<T*>(sm.stage[g % kStages][u]) + off;
+          *z = from_f32<T>(apply(to_f32(*z), i, r));
+        }
+        u += dr;
+        k += di;
+        if (k >= n) {
+          k -= n;
+          ++u;
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = g * U + u;
+      const uint32_t ok = (ok_now >> (8 * u)) & 0xffu;
+      if (!has_vec(r) || (plain && ok == kAll)) continue;
+      uint4 x = sm.stage[g % kStages][u][tid];
+      if (m0) forbid16<T>(x, ok);
+      *reinterpret_cast<uint4*>(o0 + at_vec(r)) = x;
+    }
+    for (int u = 0; u < U && g * U + u <= nd; ++u) scalars(g * U + u);
+    ok_now = ok_next;
+    ok_next = fetch(g + 2);
+    read_mask(g + 3);
+  }
+  cp_async_wait_all();
+}
+
+template <typename T, bool EVEN>
+static cudaError_t launch_rules_e(const RulesArgs& a, const RulesParams& p) {
+  constexpr int C = RulesSmem<T>::C;
+  const int nch = (a.V + C - 1) / C;
+  // the largest cluster that the chunks fill; without lists there is nothing to share
+  int cs = 1;
+  if (p.lists)
+    while (cs < rules::kMaxCluster && cs < nch) cs *= 2;
+  const size_t smem = p.lists ? sizeof(RulesSmem<T>) : 0;
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.ensure(rules_kernel<T, EVEN>, sizeof(RulesSmem<T>));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs, a.B, (nch + cs - 1) / cs);
+  cfg.blockDim = dim3(rules::kVecs);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cs;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rules_kernel<T, EVEN>, (const T*)a.logits, (T*)a.out, p);
 }
 
 template <typename T>
-static cudaError_t launch_rules_t(const RulesArgs& a, int num_sms) {
+static cudaError_t launch_rules_t(const RulesArgs& a) {
   RulesParams p{};
   p.R = a.n_rows; p.V = a.V; p.H = a.hist_max; p.nb = a.n_bias; p.W = (a.V + 31) / 32;
   p.in_place = a.out == a.logits;
+  p.lists = a.n_bias > 0 || a.repetition || a.presence || a.frequency;
   p.cand = a.cand; p.n_draft = a.n_draft; p.hist = a.hist; p.hist_len = a.hist_len; p.prompt_len = a.prompt_len;
   p.repetition = a.repetition; p.presence = a.presence; p.frequency = a.frequency;
   p.bias_tok = a.bias_tok; p.bias_val = a.bias_val; p.mask = (const uint32_t*)a.mask; p.mask_on = a.mask_on;
-  // the largest chunk that still gives every SM two CTAs: each chunk's CTA reads the whole history
-  p.chunk = 8192;
-  while (p.chunk > 1024 && (long)a.B * ((a.V + p.chunk - 1) / p.chunk) < 2L * num_sms) p.chunk /= 2;
-  const size_t smem = (size_t)(p.chunk + p.chunk / 32) * sizeof(uint32_t);
-  rules_kernel<T><<<dim3((a.V + p.chunk - 1) / p.chunk, a.B), rules::kThreads, smem, a.stream>>>(
-      (const T*)a.logits, (T*)a.out, p);
-  return cudaGetLastError();
+  auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  const bool even = a.V % VecTraits<T>::N == 0 && aligned(a.logits) && aligned(a.out);
+  return even ? launch_rules_e<T, true>(a, p) : launch_rules_e<T, false>(a, p);
 }
 
-cudaError_t launch_rules(const RulesArgs& a, int num_sms) {
-  return a.dtype == 0 ? launch_rules_t<float>(a, num_sms) : launch_rules_t<bf16>(a, num_sms);
-}
+cudaError_t launch_rules(const RulesArgs& a) { return a.dtype == 0 ? launch_rules_t<float>(a) : launch_rules_t<bf16>(a); }
 
 }  // namespace dflash
