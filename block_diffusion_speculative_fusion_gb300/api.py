@@ -69,6 +69,14 @@ class PagesDims(ctypes.Structure):
     _fields_ = [(n, c_i32) for n in ("B", "page_size", "max_pages", "num_pages")]
 
 
+class Fp8QuantDims(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("T", "K", "dtype", "block_rows")]
+
+
+class Fp8GemmDims(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("T", "N", "K", "out_dtype")]
+
+
 _SIGS = {
     "dflash_last_error": (ctypes.c_char_p, []),
     "dflash_last_launch_count": (ctypes.c_int, []),
@@ -105,6 +113,14 @@ _SIGS = {
     "dflash_logits_rules": (ctypes.c_int, [ctypes.POINTER(RulesDims)] + [c_p] * 15),
     "dflash_pages_resize": (ctypes.c_int, [ctypes.POINTER(PagesDims)] + [c_p] * 9),
     "dflash_slot_map": (ctypes.c_int, [ctypes.POINTER(PagesDims), c_i32] + [c_p] * 8),
+    "dflash_fp8_quant": (ctypes.c_int, [ctypes.POINTER(Fp8QuantDims)] + [c_p] * 4),
+    "dflash_fp8_gemm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Fp8GemmDims)]),
+    "dflash_fp8_gemm": (ctypes.c_int, [ctypes.POINTER(Fp8GemmDims)] + [c_p] * 7 + [ctypes.c_size_t, c_p]),
+    "dflash_materialize_fp8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(CtxKvDims)]),
+    # dims, hidden, commit_len, start_pos, W_f, W_f_scale, b_f, W_kv, W_kv_scale, k_norm_w, eps, theta, k_pools,
+    # v_pools, page_table, new_len, workspace, ws_bytes, stream
+    "dflash_materialize_ctx_kv_fp8": (ctypes.c_int, [ctypes.POINTER(CtxKvDims)] + [c_p] * 9 +
+                                      [ctypes.c_float, ctypes.c_float] + [c_p] * 5 + [ctypes.c_size_t, c_p]),
     "dflash_block_attn_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(AttnDims)]),
     "dflash_block_attn": (ctypes.c_int, [ctypes.POINTER(AttnDims), c_p, c_p, c_p, c_p, c_p, c_p, c_p,
                                          ctypes.c_float, c_p, c_p, ctypes.c_size_t, c_p]),
@@ -749,3 +765,96 @@ def materialize_ctx_kv(hidden: torch.Tensor, commit_len: torch.Tensor, start_pos
         _dev(page_table, "page_table", torch.int32, (B, max_pages)), _opt(new_len, "new_len", torch.int32, (B,)),
         w.data_ptr(), w.numel(), _stream(hidden.device))
     _check(rc)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point with a scale per 128 values
+# ---------------------------------------------------------------------------
+_E4M3 = torch.float8_e4m3fn
+
+
+def fp8_quant(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
+              scale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x [T, K] in e4m3 with one float32 scale per ``block_rows`` x 128 values
+    (``dflash_fp8_quant``): block_rows 1 for activations, 128 for weights.
+    Returns q [T, K] float8_e4m3fn and scale [ceil(T / block_rows),
+    ceil(K / 128)]; x is about q * scale. K is a multiple of 16."""
+    _dev(x, "x")
+    T, K = x.shape
+    dev = x.get_device()
+    shape = (-(-T // block_rows) if block_rows > 0 else T, -(-K // 128))
+    if q is None:
+        q = torch.empty((T, K), dtype=_E4M3, device=x.device)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _launch(dev, lib().dflash_fp8_quant, ctypes.byref(Fp8QuantDims(T, K, _dtype_code(x), block_rows)), x.data_ptr(),
+            _arg(q, "q", dev, _E4M3, (T, K)), _arg(scale, "scale", dev, torch.float32, shape))
+    return q, scale
+
+
+def fp8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+             bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+             out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x w^T + bias of e4m3 operands with block scales (``dflash_fp8_gemm``).
+    x [T, K], w [N, K] float8_e4m3fn; x_scale [T, ceil(K / 128)], w_scale
+    [ceil(N / 128), ceil(K / 128)] float32; bias [N] and the result [T, N] in
+    ``out_dtype`` (bfloat16 or float32)."""
+    _dev(x, "x", _E4M3)
+    T, K = x.shape
+    N = w.shape[0]
+    dev = x.get_device()
+    if out is not None:
+        out_dtype = out.dtype
+    else:
+        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
+    groups = -(-K // 128)
+    w_ws = ws if ws is not None else workspace(x.device, WS_COUNTER_BYTES, slot=3)
+    _launch(dev, lib().dflash_fp8_gemm, ctypes.byref(Fp8GemmDims(T, N, K, _dtype_code(out))), x.data_ptr(),
+            _arg(x_scale, "x_scale", dev, torch.float32, (T, groups)), _arg(w, "w", dev, _E4M3, (N, K)),
+            _arg(w_scale, "w_scale", dev, torch.float32, (-(-N // 128), groups)),
+            _arg(bias, "bias", dev, out_dtype, (N,)), _arg(out, "out", dev, out_dtype, (T, N)),
+            w_ws.data_ptr(), w_ws.numel())
+    return out
+
+
+def materialize_ctx_kv_fp8(hidden: torch.Tensor, commit_len: torch.Tensor, start_pos: torch.Tensor,
+                           W_f: torch.Tensor, W_f_scale: torch.Tensor, b_f: Optional[torch.Tensor],
+                           W_kv: torch.Tensor, W_kv_scale: torch.Tensor, k_norm_w: Optional[torch.Tensor],
+                           rms_eps: float, rope_theta: float, k_pools: Sequence[torch.Tensor],
+                           v_pools: Sequence[torch.Tensor], page_table: torch.Tensor,
+                           new_len: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> None:
+    """``materialize_ctx_kv`` with e4m3 weights (``dflash_materialize_ctx_kv_fp8``):
+    W_f [d, m*d] and W_kv [L, 2, Hkv*D, d] float8_e4m3fn with the scales of
+    ``fp8_quant(..., block_rows=128)`` over W_f and over W_kv.view(-1, d)."""
+    _dev(hidden, "hidden", torch.bfloat16)
+    B, rows_max, md = hidden.shape
+    dev = hidden.get_device()
+    d = W_f.shape[0]
+    m = md // d
+    L, two, HD, d2 = W_kv.shape
+    if two != 2 or d2 != d or m * d != md:
+        raise ValueError("inconsistent hidden / W_f / W_kv shapes")
+    if len(k_pools) != L or len(v_pools) != L:
+        raise ValueError("need one K and one V pool per draft layer")
+    num_pages, page, Hkv, D = k_pools[0].shape
+    if Hkv * D != HD:
+        raise ValueError("pool head layout does not match W_kv")
+    max_pages = page_table.shape[1]
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    dims = CtxKvDims(B, rows_max, m, d, L, Hkv, D, page, max_pages, num_pages, BF16)
+    need = lib().dflash_materialize_fp8_workspace_size(ctypes.byref(dims))
+    if need == 0:
+        raise DflashError(ERR_INVALID_ARG, last_error())
+    w = ws if ws is not None else workspace(hidden.device, need, slot=4)
+    pool = (num_pages, page, Hkv, D)
+    kp = (c_p * L)(*[_arg(t, f"k_pools[{i}]", dev, bf, pool) for i, t in enumerate(k_pools)])
+    vp = (c_p * L)(*[_arg(t, f"v_pools[{i}]", dev, bf, pool) for i, t in enumerate(v_pools)])
+    groups = -(-d // 128)
+    _launch(dev, lib().dflash_materialize_ctx_kv_fp8, ctypes.byref(dims), hidden.data_ptr(),
+            _arg(commit_len, "commit_len", dev, i32, (B,)), _arg(start_pos, "start_pos", dev, i32, (B,)),
+            _arg(W_f, "W_f", dev, _E4M3, (d, md)), _arg(W_f_scale, "W_f_scale", dev, f32, (groups, -(-md // 128))),
+            _arg(b_f, "b_f", dev, bf, (d,)), _arg(W_kv, "W_kv", dev, _E4M3, (L, 2, HD, d)),
+            _arg(W_kv_scale, "W_kv_scale", dev, f32, (-(-L * 2 * HD // 128), groups)),
+            _arg(k_norm_w, "k_norm_w", dev, bf, (L, D)), rms_eps, rope_theta, ctypes.cast(kp, c_p),
+            ctypes.cast(vp, c_p), _arg(page_table, "page_table", dev, i32, (B, max_pages)),
+            _arg(new_len, "new_len", dev, i32, (B,)), w.data_ptr(), w.numel())

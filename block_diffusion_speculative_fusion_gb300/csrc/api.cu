@@ -673,4 +673,117 @@ int dflash_materialize_ctx_kv(const dflash_ctx_kv_dims* d, const void* hidden, c
   return ok(launches);
 }
 
+// -------------------------------------- 8-bit product with block scales ---
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int dflash_fp8_quant(const dflash_fp8_quant_dims* d, const void* x, void* q, float* scale, dflash_stream_t stream) {
+  CallRange range_("dflash_fp8_quant");
+  if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
+  if (d->T < 0 || d->K < 1) return fail(DFLASH_ERR_INVALID_ARG, "bad dims T=%d K=%d", d->T, d->K);
+  if (bad_dtype(d->dtype)) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", d->dtype);
+  if (d->block_rows != 1 && d->block_rows != 128)
+    return fail(DFLASH_ERR_INVALID_ARG, "block_rows=%d is not 1 or 128", d->block_rows);
+  if (d->K % 16) return fail(DFLASH_ERR_UNSUPPORTED, "K=%d is not a multiple of 16", d->K);
+  if (d->T > 1 << 23) return fail(DFLASH_ERR_UNSUPPORTED, "T=%d > 2^23", d->T);
+  if (d->T == 0) return ok(0);
+  if (!x || !q || !scale) return fail(DFLASH_ERR_INVALID_ARG, "fp8_quant: a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(q)) return fail(DFLASH_ERR_INVALID_ARG, "fp8_quant: x or q is not 16-byte aligned");
+  dflash::Fp8QuantArgs a{};
+  a.T = d->T; a.K = d->K; a.dtype = d->dtype; a.block_rows = d->block_rows;
+  a.x = x; a.q = q; a.scale = scale;
+  a.stream = (cudaStream_t)stream;
+  cudaError_t e = dflash::launch_fp8_quant(a, false);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8_quant launch");
+  return ok(1);
+}
+
+static int check_fp8_gemm_dims(const dflash_fp8_gemm_dims* d) {
+  if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
+  if (d->T < 0 || d->N < 1 || d->K < 1) return fail(DFLASH_ERR_INVALID_ARG, "bad dims T=%d N=%d K=%d", d->T, d->N, d->K);
+  if (bad_dtype(d->out_dtype)) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", d->out_dtype);
+  if (d->K % 16) return fail(DFLASH_ERR_UNSUPPORTED, "K=%d is not a multiple of 16", d->K);
+  if (d->T > 1 << 23 || d->N > 1 << 23 || d->K > 1 << 23)
+    return fail(DFLASH_ERR_UNSUPPORTED, "T=%d, N=%d or K=%d > 2^23", d->T, d->N, d->K);
+  if (((long)d->T + 127) / 128 * (((long)d->N + 127) / 128) > 1L << 27)
+    return fail(DFLASH_ERR_UNSUPPORTED, "T=%d x N=%d has too many tiles", d->T, d->N);
+  return DFLASH_OK;
+}
+
+size_t dflash_fp8_gemm_workspace_size(const dflash_fp8_gemm_dims* d) {
+  return check_fp8_gemm_dims(d) == DFLASH_OK ? DFLASH_WS_COUNTER_BYTES : 0;
+}
+
+int dflash_fp8_gemm(const dflash_fp8_gemm_dims* d, const void* x, const float* x_scale, const void* w,
+                    const float* w_scale, const void* bias, void* out, void* workspace, size_t ws_bytes,
+                    dflash_stream_t stream) {
+  CallRange range_("dflash_fp8_gemm");
+  int rc = check_fp8_gemm_dims(d);
+  if (rc) return rc;
+  if (d->T == 0) return ok(0);
+  if (!x || !x_scale || !w || !w_scale || !out) return fail(DFLASH_ERR_INVALID_ARG, "fp8_gemm: a required pointer is NULL");
+  if (!aligned16(x) || !aligned16(w)) return fail(DFLASH_ERR_INVALID_ARG, "fp8_gemm: x or w is not 16-byte aligned");
+  rc = check_ws(workspace, ws_bytes, DFLASH_WS_COUNTER_BYTES);
+  if (rc) return rc;
+  dflash::Fp8GemmArgs a{};
+  a.T = d->T; a.N = d->N; a.K = d->K; a.out_dtype = d->out_dtype;
+  a.x = x; a.x_scale = x_scale; a.w = w; a.w_scale = w_scale; a.bias = bias; a.out = out;
+  a.err = (int*)workspace + kMaxCounters;
+  a.stream = (cudaStream_t)stream;
+  cudaError_t e = dflash::launch_fp8_gemm(a, false);
+  if (e != cudaSuccess) return cuda_fail(e, "fp8_gemm launch");
+  return ok(1);
+}
+
+static int check_mat_fp8_dims(const dflash_ctx_kv_dims* d) {
+  int rc = check_mat_dims(d);
+  if (rc) return rc;
+  if (d->dtype != DFLASH_BF16) return fail(DFLASH_ERR_UNSUPPORTED, "materialize_fp8: dtype %d is not bf16", d->dtype);
+  if (d->d % 16) return fail(DFLASH_ERR_UNSUPPORTED, "d=%d is not a multiple of 16", d->d);
+  return DFLASH_OK;
+}
+
+size_t dflash_materialize_fp8_workspace_size(const dflash_ctx_kv_dims* d) {
+  if (check_mat_fp8_dims(d) != DFLASH_OK) return 0;
+  return DFLASH_WS_COUNTER_BYTES + dflash::mat_fp8_ws_bytes(d->B, d->rows_max, d->m, d->d, d->L, d->Hkv, d->D);
+}
+
+int dflash_materialize_ctx_kv_fp8(const dflash_ctx_kv_dims* d, const void* hidden, const int32_t* commit_len,
+                                  const int32_t* start_pos, const void* W_f, const float* W_f_scale, const void* b_f,
+                                  const void* W_kv, const float* W_kv_scale, const void* k_norm_w, float rms_eps,
+                                  float rope_theta, void* const* k_pools, void* const* v_pools,
+                                  const int32_t* page_table, int32_t* new_len, void* workspace, size_t ws_bytes,
+                                  dflash_stream_t stream) {
+  CallRange range_("dflash_materialize_ctx_kv_fp8");
+  int rc = check_mat_fp8_dims(d);
+  if (rc) return rc;
+  if (!hidden || !commit_len || !start_pos || !W_f || !W_f_scale || !W_kv || !W_kv_scale || !k_pools || !v_pools ||
+      !page_table)
+    return fail(DFLASH_ERR_INVALID_ARG, "materialize_fp8: a required pointer is NULL");
+  if (!aligned16(W_f) || !aligned16(W_kv))
+    return fail(DFLASH_ERR_INVALID_ARG, "materialize_fp8: W_f or W_kv is not 16-byte aligned");
+  if (new_len && new_len == start_pos) return fail(DFLASH_ERR_INVALID_ARG, "new_len must not alias start_pos");
+  if (rope_theta < 0.f || !(rms_eps >= 0.f)) return fail(DFLASH_ERR_INVALID_ARG, "bad rope_theta or rms_eps");
+  rc = check_ws(workspace, ws_bytes, dflash_materialize_fp8_workspace_size(d));
+  if (rc) return rc;
+  dflash::MatArgs a{};
+  a.B = d->B; a.rows_max = d->rows_max; a.m = d->m; a.d = d->d; a.L = d->L; a.Hkv = d->Hkv; a.D = d->D;
+  a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages; a.dtype = d->dtype;
+  a.hidden = hidden; a.commit_len = commit_len; a.start_pos = start_pos; a.W_f = W_f; a.b_f = b_f;
+  a.W_kv = W_kv; a.k_norm_w = k_norm_w; a.rms_eps = rms_eps; a.rope_theta = rope_theta;
+  for (int l = 0; l < d->L; ++l) {
+    if (!k_pools[l] || !v_pools[l]) return fail(DFLASH_ERR_INVALID_ARG, "pool pointer of layer %d is NULL", l);
+    a.pools.k[l] = k_pools[l];
+    a.pools.v[l] = v_pools[l];
+  }
+  a.page_table = page_table; a.new_len = new_len;
+  a.counters = (int32_t*)workspace;
+  a.err = (int*)workspace + kMaxCounters;
+  a.scratch = (char*)workspace + DFLASH_WS_COUNTER_BYTES;
+  a.stream = (cudaStream_t)stream;
+  int launches = 0;
+  cudaError_t e = dflash::launch_materialize_fp8(a, W_f_scale, W_kv_scale, &launches);
+  if (e != cudaSuccess) return cuda_fail(e, "materialize_fp8 launch");
+  return ok(launches);
+}
+
 }  // extern "C"

@@ -1,0 +1,546 @@
+// 8-bit floating point (e4m3) with a scale for every 128 values: quantisation
+// of rows and weight blocks, and the product of such operands on tcgen05.
+//
+//   s = max(amax / 448, 2^-126),  q = e4m3(x * (1 / s))   amax over 1 x 128 (rows)
+//                                                         or 128 x 128 (weights)
+//   out[t][n] = sum_g xs[t][g] ws[n / 128][g] (sum_{k in group g} xq[t][k] wq[n][k]) + bias[n]
+//
+// One e4m3 value of a group is its largest, so a group's inner sum needs no
+// more than the tensor core's fp32; the groups' sums meet in fp32 registers,
+// each multiplied by its own scales (the scales are arbitrary fp32 numbers, so
+// they cannot ride in the MMA, which takes powers of two per 32 values).
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+#include "tma.cuh"
+
+namespace dflash {
+
+namespace f8 {
+constexpr int G = 128;                    // values per scale, and the k-block
+constexpr float kMax = 448.f;             // largest finite e4m3
+constexpr float kMinScale = 1.17549435e-38f;
+}  // namespace f8
+
+// ---------------------------------------------------------------------------
+// Quantisation. Bound: one read and one write. A warp takes whole groups (16
+// bytes a lane: two bf16 groups or one fp32 group at once), four at a time, and
+// finds the largest magnitude by shuffles.
+// ---------------------------------------------------------------------------
+template <typename T> constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+// NaN is passed over here and kept by the conversion.
+template <typename T> __device__ __forceinline__ float vec_absmax(const uint4& u) {
+  return vec_max<T>(make_uint4(u.x & kAbs<T>, u.y & kAbs<T>, u.z & kAbs<T>, u.w & kAbs<T>));
+}
+__device__ __forceinline__ float f8_scale(float amax) { return fmaxf(__fdiv_rn(amax, f8::kMax), f8::kMinScale); }
+
+// The vector's values times 1 / scale (a division each would bound the kernel by
+// its instructions: 138 us instead of 82 for 8190 x 20480 bf16), four e4m3 to a word.
+template <typename T> __device__ __forceinline__ void f8_store(uint8_t* dst, const uint4& u, float r) {
+  constexpr int N = VecTraits<T>::N;
+  float f[N];
+  unpack16<T>(u, f);
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int j = 0; j < N; j += 4) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[j] * r, f[j + 1] * r), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[j + 2] * r, f[j + 3] * r), __NV_SATFINITE, __NV_E4M3);
+    w[j / 4] = lo | (hi << 16);
+  }
+  if constexpr (N == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+f8_quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale, int T_rows,
+                     const int32_t* __restrict__ T_dev, int K) {
+  wait_for_prior_grid();   // in the materialisation's chain the rows come from the kernel before
+  dependents_may_launch();
+  constexpr int N = VecTraits<T>::N;
+  constexpr int LPG = f8::G / N;           // lanes of a group
+  constexpr int GPW = 32 / LPG;            // groups of a warp's load
+  constexpr int U = 4;
+  const int rows = T_dev ? min(*T_dev, T_rows) : T_rows;
+  const int groups = (K + f8::G - 1) / f8::G;
+  const long total = (long)rows * groups;
+  const int lane = threadIdx.x & 31, sub = lane / LPG, at = (lane % LPG) * N;
+  const long warps = (long)gridDim.x * (blockDim.x >> 5);
+  for (long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w * (U * GPW) < total; w += warps) {
+    uint4 v[U];
+    size_t off[U];
+    long gi[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      gi[u] = (w * U + u) * GPW + sub;
+      v[u] = make_uint4(0, 0, 0, 0);
+      off[u] = ~(size_t)0;
+      if (gi[u] < total) {
+        const long t = gi[u] / groups;
+        const int k = (int)(gi[u] - t * groups) * f8::G + at;
+        if (k < K) {                       // K is a multiple of 16: a vector is inside or outside
+          off[u] = (size_t)t * K + k;
+          v[u] = ld_stream16(x + off[u]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float m = vec_absmax<T>(v[u]);
+#pragma unroll
+      for (int o = LPG / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float s = f8_scale(m);
+      if (off[u] != ~(size_t)0) f8_store<T>(q + off[u], v[u], __frcp_rn(s));
+      if (at == 0 && gi[u] < total) scale[gi[u]] = s;
+    }
+  }
+}
+
+// One CTA per 128 x 128 block, a warp 16 of its rows, held in registers between
+// the search for the largest magnitude and the conversion.
+template <typename T>
+__global__ void __launch_bounds__(256)
+f8_quant_blocks_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale, int T_rows, int K) {
+  constexpr int N = VecTraits<T>::N;
+  constexpr int LPG = f8::G / N, RPL = 32 / LPG;   // rows of a warp's load
+  constexpr int L = 16 / RPL;
+  __shared__ float s_max[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k = blockIdx.x * f8::G + (lane % LPG) * N;
+  const int t0 = blockIdx.y * f8::G + warp * 16 + lane / LPG;
+  uint4 v[L];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int t = t0 + i * RPL;
+    v[i] = t < T_rows && k < K ? ld_stream16(x + (size_t)t * K + k) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < L; ++i) m = fmaxf(m, vec_absmax<T>(v[i]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_max[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, s_max[i]);
+  const float s = f8_scale(m), r = __frcp_rn(s);
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int t = t0 + i * RPL;
+    if (t < T_rows && k < K) f8_store<T>(q + (size_t)t * K + k, v[i], r);
+  }
+  if (threadIdx.x == 0) scale[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+template <typename T>
+static cudaError_t launch_f8_quant_t(const Fp8QuantArgs& a, bool dependent) {
+  const int groups = (a.K + f8::G - 1) / f8::G;
+  if (a.block_rows == f8::G) {
+    const dim3 grid(groups, (a.T + f8::G - 1) / f8::G);
+    f8_quant_blocks_kernel<T><<<grid, 256, 0, a.stream>>>((const T*)a.x, (uint8_t*)a.q, a.scale, a.T, a.K);
+    return cudaGetLastError();
+  }
+  // 32 fp32 or 64 bf16 groups a CTA pass; eight CTAs fill an SM
+  const long per = 8L * 4 * (32 / (f8::G / VecTraits<T>::N));
+  const long need = ((long)a.T * groups + per - 1) / per;
+  const int grid = (int)std::max(1L, std::min(need, 8L * 152));
+  if (dependent)
+    return launch_dependent(f8_quant_rows_kernel<T>, dim3(grid), dim3(256), 0, a.stream, (const T*)a.x, (uint8_t*)a.q,
+                            a.scale, a.T, a.T_dev, a.K);
+  f8_quant_rows_kernel<T><<<grid, 256, 0, a.stream>>>((const T*)a.x, (uint8_t*)a.q, a.scale, a.T, a.T_dev, a.K);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent) {
+  return a.dtype == 0 ? launch_f8_quant_t<float>(a, dependent) : launch_f8_quant_t<bf16>(a, dependent);
+}
+
+// ---------------------------------------------------------------------------
+// Product. A tile is 128 rows of x (the MMA's M, one TMEM lane each) by BN
+// weight rows (N); a k-block is one group of 128 values, one 128-byte swizzle
+// atom a row, and its four MMAs (K = 32 each) write a TMEM accumulator of their
+// own. Eight warps take each accumulator out of TMEM and add it, times the
+// group's scales, to the tile's sums in registers, while the MMAs of the next
+// groups go on in the other accumulators. With the rows in the lanes a thread
+// needs one scale a group (its row's times the weight block's), and the sums
+// cost one multiply-add each.
+//
+// Few tiles (decode: the weights' bytes bound it) are split over K among the
+// CTAs of a cluster of up to eight; each leaves its sums in its shared memory,
+// and every CTA adds its part of the tile over the cluster in rank order
+// (distributed shared memory: no workspace, no atomics, the same bits each
+// time). Many tiles go round persistent CTAs, one per SM.
+//
+// Warps 0 - 7 sum, warp 8 issues the TMA loads, warp 9 the MMAs. Every wait is
+// bounded as in the bf16 GEMM: one that gives up records a code, the CTA drains
+// its copies and MMAs, frees its TMEM and returns.
+// ---------------------------------------------------------------------------
+namespace f8 {
+constexpr int BM = 128;
+constexpr int A_BYTES = BM * G;           // 16 KB
+constexpr int RING_BYTES = 196608;        // 4 stages of 48 KB (BN = 256) or 6 of 32 KB
+constexpr int THREADS = 320;
+constexpr int SUM_WARPS = 8;
+constexpr int SMEM_BYTES = RING_BYTES + 1024 + 512;
+constexpr int MAX_CLUSTER = 8;
+
+template <int BN> struct Cfg {
+  static constexpr int STAGE = A_BYTES + BN * G;
+  static constexpr int STAGES = RING_BYTES / STAGE;
+  static constexpr int BUFS = 512 / BN;   // TMEM accumulators
+  static constexpr int COLS = BN / 2;     // a summing thread's columns
+  static constexpr int RED_LD = BN + 4;   // floats: a quarter warp's rows fall on distinct banks
+};
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0), fp32 D, both K-major.
+__device__ __forceinline__ uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Bounded wait that also gives up when another role of the CTA has. A k-block's
+// waits are short (a copy, four MMAs, one read-out), so the clock is looked at
+// after every attempt; the attempts themselves suspend the thread.
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                int code, unsigned long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      if (err) atomicCAS(err, 0, code);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ uint32_t ctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+// Four consecutive outputs of a row from column n on.
+template <typename O>
+__device__ __forceinline__ void store_out4(O* row, int n, int N, float4 v, const O* bias, bool vec) {
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  if (vec && n + 4 <= N) {
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (bias) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = to_f32(bias[n + j]);
+    }
+    if constexpr (sizeof(O) == 4) {
+      *reinterpret_cast<float4*>(row + n) = make_float4(f[0] + b[0], f[1] + b[1], f[2] + b[2], f[3] + b[3]);
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0] + b[0], f[1] + b[1]);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2] + b[2], f[3] + b[3]);
+      *reinterpret_cast<uint2*>(row + n) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < N) row[n + j] = from_f32<O>(f[j] + (bias ? to_f32(bias[n + j]) : 0.f));
+}
+}  // namespace f8
+
+struct Fp8GemmParams {
+  const float* xs;        // [T, groups]
+  const float* ws;        // [ceil(N / 128), groups]
+  const void* bias;       // [N] or null
+  void* out;              // [T, N]
+  const int32_t* T_dev;   // or null
+  int T, N, groups, splits, box_m, vec;
+  int* err;
+  unsigned long long wait_ns;
+};
+
+template <int BN, typename O>
+__global__ void __launch_bounds__(f8::THREADS, 1)
+f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+               const Fp8GemmParams p) {
+  using namespace f8;
+  using C = Cfg<BN>;
+  wait_for_prior_grid();   // as a dependent launch: the rows come from the kernel before
+  dependents_may_launch();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);   // [STAGES]
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;    // [BUFS]
+  uint64_t* tempty = tfull + C::BUFS;
+  uint64_t* mma_done = tempty + C::BUFS;
+  uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
+  int* consumed_sm = reinterpret_cast<int*>(tmem_base_sm + 2);
+
+  const int T = p.T_dev ? min(*p.T_dev, p.T) : p.T;
+  const int nt = (p.N + BN - 1) / BN;
+  const int tiles = nt * ((T + BM - 1) / BM);
+  const int S = p.splits;
+  const int rank = S > 1 ? (int)ctarank() : 0;
+  const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
+  if (first >= tiles) return;             // (every CTA of the cluster)
+  const int kb0 = (int)((long)rank * p.groups / S), kb1 = (int)((long)(rank + 1) * p.groups / S);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int producer_issued = 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < C::BUFS; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], SUM_WARPS);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    *consumed_sm = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(tmem_base_sm, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_base_sm;
+
+  if (warp == 8) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t bytes = (uint32_t)(p.box_m * G + BN * G);
+      const uint64_t once = l2_policy_evict_first();
+      const bool stream_w = T <= BM;      // each weight is read by one tile alone
+      for (int tile = first; ok && tile < tiles; tile += step) {
+        const int m0 = tile / nt * BM, n0 = tile % nt * BN;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_or_give_up(&empty[stage], phase ^ 1u, abort_flag, p.err, 21, p.wait_ns)) { ok = false; break; }
+          uint8_t* sa = smem + stage * C::STAGE;
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          if (stream_w) tma_load_2d_hint(sa + A_BYTES, &wmap, &full[stage], kb * G, n0, once);
+          else tma_load_2d(sa + A_BYTES, &wmap, &full[stage], kb * G, n0);
+          tma_load_2d(sa, &xmap, &full[stage], kb * G, m0);
+          ++producer_issued;
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------ MMA issuer ------------------------------
+    if (lane == 0) {
+      int stage = 0, buf = 0, consumed = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_e4m3(BM, BN);
+      for (int tile = first; ok && tile < tiles; tile += step)
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_or_give_up(&tempty[buf], buf_phase ^ 1u, abort_flag, p.err, 22, p.wait_ns) ||
+              !wait_or_give_up(&full[stage], phase, abort_flag, p.err, 23, p.wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * C::STAGE);
+          const uint64_t adesc = sdesc_sw128(sa), bdesc = sdesc_sw128(sa + A_BYTES);
+          const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
+#pragma unroll
+          for (int j = 0; j < G / 32; ++j)   // 32 bytes of K per instruction
+            mma_e4m3(d_tmem, adesc + (uint64_t)(j * 2), bdesc + (uint64_t)(j * 2), idesc, j > 0 ? 1u : 0u);
+          tc_commit(&empty[stage]);
+          tc_commit(&tfull[buf]);
+          ++consumed;
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+          if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1u; }
+        }
+      *consumed_sm = consumed;
+      // every MMA issued by this thread has completed before TMEM is released
+      tc_commit(mma_done);
+      mbar_wait_bounded(mma_done, 0, p.err, 24);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------ sums (warps 0 - 7) ------------------------------
+    const int quarter = warp & 3, half = warp >> 2;   // TMEM lanes [32 q, 32 q + 32) belong to warp q mod 4
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < tiles; tile += step) {
+      const int m0 = tile / nt * BM, n0 = tile % nt * BN + half * C::COLS;
+      const int row = m0 + quarter * 32 + lane;
+      const bool live = row < T && n0 < p.N;
+      const float* xs = p.xs + (size_t)(live ? row : 0) * p.groups;
+      const float* ws = p.ws + (size_t)(live ? n0 / G : 0) * p.groups;
+      float acc[C::COLS];
+#pragma unroll
+      for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
+      float s_next = live ? __ldg(xs + kb0) * __ldg(ws + kb0) : 0.f;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const float s = s_next;
+        if (kb + 1 < kb1 && live) s_next = __ldg(xs + kb + 1) * __ldg(ws + kb + 1);
+        // a warp-wide decision: the TMEM loads below are warp-collective
+        if (!__all_sync(0xffffffffu, wait_or_give_up(&tfull[buf], buf_phase, abort_flag, p.err, 25, p.wait_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + half * C::COLS);
+#pragma unroll
+        for (int c0 = 0; c0 < C::COLS; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(tbase + (uint32_t)c0, r);
+          tmem_ld_wait();
+          if (c0 + 32 == C::COLS) {       // the accumulator is read out: the MMAs may have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[buf]);
+          }
+#pragma unroll
+          for (int q = 0; q < 32; ++q) acc[c0 + q] = fmaf(__uint_as_float(r[q]), s, acc[c0 + q]);
+        }
+        if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1u; }
+      }
+      if (!ok) break;
+      if (S == 1) {
+        if (live) {
+          O* o = (O*)p.out + (size_t)row * p.N;
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 4)
+            store_out4<O>(o, n0 + c, p.N, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]), (const O*)p.bias,
+                          p.vec != 0);
+        }
+      } else if (row < T) {
+        // the ring is idle: its last copies have been multiplied. The tile's sums go there
+        float* red = reinterpret_cast<float*>(smem) + (size_t)(quarter * 32 + lane) * C::RED_LD + half * C::COLS;
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 4)
+          *reinterpret_cast<float4*>(red + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (S > 1) {
+    cluster_sync();
+    const int m0 = first / nt * BM, n0 = first % nt * BN;   // a cluster has one tile
+    const int rows = min(BM, T - m0), cells = rows * (BN / 4);
+    const uint32_t red = smem_u32(smem);
+    for (int i = rank * THREADS + (int)threadIdx.x; i < cells; i += S * THREADS) {
+      const int r = i / (BN / 4), c = (i % (BN / 4)) * 4;
+      if (n0 + c >= p.N) continue;
+      const uint32_t at = red + (uint32_t)(r * C::RED_LD + c) * 4u;
+      float4 v = ld_peer(at, 0);
+      for (int k = 1; k < S; ++k) {
+        const float4 y = ld_peer(at, (uint32_t)k);
+        v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+      }
+      store_out4<O>((O*)p.out + (size_t)(m0 + r) * p.N, n0 + c, p.N, v, (const O*)p.bias, p.vec != 0);
+    }
+    cluster_sync();                       // no CTA leaves while a peer reads its sums
+  }
+  // After an abort, copies issued but never consumed may still be in flight:
+  // wait for them (bounded) so that none lands after this CTA has exited.
+  if (warp == 8 && lane == 0 && *abort_flag)
+    for (int i = *consumed_sm; i < producer_issued; ++i)
+      mbar_wait_bounded(&full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.err, 26);
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// Tile width and split over K. `waves` of whole tiles on 152 SMs: the wide tile
+// reads each row of x half as often, the narrow one wastes less of a last wave;
+// below one wave of narrow tiles, K is split until the SMs are used.
+struct Fp8Plan { int BN, S; };
+static Fp8Plan fp8_plan(int T, int N, int groups) {
+  const long mt = (T + f8::BM - 1) / f8::BM;
+  const long t256 = mt * ((N + 255) / 256), t128 = mt * ((N + 127) / 128);
+  if (t128 > 76) return 2 * ((t256 + 151) / 152) <= (t128 + 151) / 152 ? Fp8Plan{256, 1} : Fp8Plan{128, 1};
+  int S = 1;
+  while (S * 2 <= f8::MAX_CLUSTER && t128 * S * 2 <= 152 && S * 2 <= groups) S *= 2;
+  return Fp8Plan{128, S};
+}
+
+template <int BN, typename O>
+static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent) {
+  using namespace f8;
+  Fp8GemmParams p{};
+  p.xs = a.x_scale; p.ws = a.w_scale; p.bias = a.bias; p.out = a.out; p.T_dev = a.T_dev;
+  p.T = a.T; p.N = a.N; p.groups = (a.K + G - 1) / G; p.splits = S;
+  p.box_m = std::min(BM, (a.T + 7) / 8 * 8);
+  p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && ((size_t)a.N * sizeof(O)) % (4 * sizeof(O)) == 0;
+  p.err = a.err; p.wait_ns = wait_limit_ns();
+  CUtensorMap xmap, wmap;
+  const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.T}, wd[2] = {(uint64_t)a.K, (uint64_t)a.N};
+  const uint64_t strides[1] = {(uint64_t)a.K};
+  const uint32_t xb[2] = {G, (uint32_t)p.box_m}, wb[2] = {G, BN};
+  if (!encode_tensor_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a.x), xd, strides, xb,
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tensor_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(a.w), wd, strides, wb,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorNotSupported;
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.ensure(f8_gemm_kernel<BN, O>, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const long tiles = (long)((a.T + BM - 1) / BM) * ((a.N + BN - 1) / BN);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(S > 1 ? tiles * S : std::min(tiles, 152L)));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (S > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = S;
+    at[n].val.clusterDim.y = 1;
+    at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, O>, xmap, wmap, p);
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dependent) {
+  const Fp8Plan plan = fp8_plan(a.T, a.N, (a.K + f8::G - 1) / f8::G);
+  if (a.out_dtype == 0)
+    return plan.BN == 256 ? launch_f8_gemm_t<256, float>(a, plan.S, dependent)
+                          : launch_f8_gemm_t<128, float>(a, plan.S, dependent);
+  return plan.BN == 256 ? launch_f8_gemm_t<256, bf16>(a, plan.S, dependent)
+                        : launch_f8_gemm_t<128, bf16>(a, plan.S, dependent);
+}
+
+}  // namespace dflash

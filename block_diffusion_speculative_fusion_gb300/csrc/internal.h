@@ -249,6 +249,30 @@ struct AttnArgs {
 size_t attn_ws_bytes(int B, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size, int dtype);
 cudaError_t launch_block_attn(const AttnArgs& a, int* launches);
 
+// -------------------------------------- 8-bit product with block scales ---
+struct Fp8QuantArgs {
+  int T, K, dtype, block_rows;   // block_rows 1 or 128
+  const int32_t* T_dev;          // rows in use (device), or null: all T
+  const void* x;                 // [T, K]
+  void* q;                       // [T, K] e4m3
+  float* scale;                  // [ceil(T / block_rows), ceil(K / 128)]
+  cudaStream_t stream;
+};
+cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent);
+struct Fp8GemmArgs {
+  int T, N, K, out_dtype;
+  const int32_t* T_dev;          // rows in use (device), or null: all T
+  const void* x;                 // [T, K] e4m3
+  const float* x_scale;          // [T, ceil(K / 128)]
+  const void* w;                 // [N, K] e4m3
+  const float* w_scale;          // [ceil(N / 128), ceil(K / 128)]
+  const void* bias;              // [N] of out_dtype, or null
+  void* out;                     // [T, N]
+  int* err;                      // the workspace's error word
+  cudaStream_t stream;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dependent);
+
 // ----------------------------------------------------------- materialise ---
 constexpr int kMaxLayers = 16;
 struct MatPools {
@@ -283,6 +307,9 @@ struct MatPlan {
 MatPlan mat_plan(int B, int rows_max, int m, int d, int L, int Hkv, int D, int dtype);
 size_t mat_ws_bytes(const MatPlan& p, int dtype);
 cudaError_t launch_materialize(const MatArgs& a, int* launches);
+// With W_f and W_kv in e4m3 and their 128 x 128 block scales (dtype bf16).
+size_t mat_fp8_ws_bytes(int B, int rows_max, int m, int d, int L, int Hkv, int D);
+cudaError_t launch_materialize_fp8(const MatArgs& a, const float* W_f_scale, const float* W_kv_scale, int* launches);
 
 // tcgen05 GEMM: part[seg][t][n] = sum over one K segment of X[t][k] W[n][k], bf16 in, fp32 out.
 namespace tcplan {

@@ -568,6 +568,94 @@ static cudaError_t launch_mat_t(const MatArgs& a, int* launches) {
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// The same chain with 8-bit weights: the gathered rows and h_ctx are quantised
+// (one scale per row and 128 values), the GEMMs are the 8-bit product with its
+// sums finished in one kernel, so the epilogue reads a single partial.
+//   gather -> quantise X -> product 1 (+ b_f, h_ctx in bf16) -> quantise h_ctx
+//   -> product 2 (fp32) -> epilogue
+// ---------------------------------------------------------------------------
+struct MatFp8Layout {
+  size_t rope, slots, X, Xq, xs, h, hq, hs, part, total;
+};
+static MatFp8Layout mat_fp8_layout(int B, int rows_max, int m, int d, int L, int Hkv, int D) {
+  const size_t T = (size_t)B * rows_max, K1 = (size_t)m * d, N2 = (size_t)L * 2 * Hkv * D;
+  MatFp8Layout o;
+  size_t s = align_up(sizeof(int32_t) * (64 + 2 * T + B + 1));
+  auto take = [&](size_t bytes) {
+    const size_t at = s;
+    s += align_up(bytes);
+    return at;
+  };
+  o.rope = take(sizeof(float2) * T * 128);
+  o.slots = take(sizeof(long long) * T);
+  o.X = take(T * K1 * 2);
+  o.Xq = take(T * K1);
+  o.xs = take(T * ((K1 + 127) / 128) * 4);
+  o.h = take(T * d * 2);
+  o.hq = take(T * d);
+  o.hs = take(T * (((size_t)d + 127) / 128) * 4);
+  o.part = take(T * N2 * 4);
+  o.total = s;
+  return o;
+}
+size_t mat_fp8_ws_bytes(int B, int rows_max, int m, int d, int L, int Hkv, int D) {
+  return mat_fp8_layout(B, rows_max, m, d, L, Hkv, D).total;
+}
+
+cudaError_t launch_materialize_fp8(const MatArgs& a, const float* W_f_scale, const float* W_kv_scale, int* launches) {
+  const int T_max = a.B * a.rows_max, K1 = a.m * a.d, N2 = a.L * 2 * a.Hkv * a.D;
+  const MatFp8Layout lay = mat_fp8_layout(a.B, a.rows_max, a.m, a.d, a.L, a.Hkv, a.D);
+  char* ws = (char*)a.scratch;
+  int32_t* meta = (int32_t*)ws;
+  int32_t* row_b = meta + 64;
+  int32_t* row_j = row_b + T_max;
+  RopeFreq inv_freq;
+  for (int i = 0; i < 128; ++i)
+    inv_freq.f[i] = i < a.D / 2 && a.rope_theta > 0.f ? std::exp(-(2.0 * i / a.D) * std::log((double)a.rope_theta)) : 0.0;
+  float2* rope = a.rope_theta > 0.f ? (float2*)(ws + lay.rope) : nullptr;
+  long long* slots = (long long*)(ws + lay.slots);
+  float* part = (float*)(ws + lay.part);
+  cudaStream_t st = a.stream;
+  const int gs = 4 * 152;
+  mat_gather_kernel<<<gs, 256, 0, st>>>(a.commit_len, a.start_pos, a.B, a.rows_max, (const uint8_t*)a.hidden,
+                                        (uint8_t*)(ws + lay.X), (size_t)K1 * 2, meta, row_b, row_j, a.new_len, 0, a.d,
+                                        K1, N2, a.d, inv_freq, rope, a.D / 2, a.page_table, a.page_size, a.max_pages,
+                                        a.num_pages, slots, a.err);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto quant = [&](size_t x, size_t q, size_t scale, int K) {
+    Fp8QuantArgs g{};
+    g.T = T_max; g.K = K; g.dtype = 1; g.block_rows = 1; g.T_dev = meta;
+    g.x = ws + x; g.q = ws + q; g.scale = (float*)(ws + scale); g.stream = st;
+    return launch_fp8_quant(g, true);
+  };
+  auto product = [&](size_t x, size_t xs, const void* w, const float* w_scale, const void* bias, void* out, int N, int K,
+                     int out_dtype) {
+    Fp8GemmArgs g{};
+    g.T = T_max; g.N = N; g.K = K; g.out_dtype = out_dtype; g.T_dev = meta;
+    g.x = ws + x; g.x_scale = (const float*)(ws + xs); g.w = w; g.w_scale = w_scale; g.bias = bias; g.out = out;
+    g.err = a.err; g.stream = st;
+    return launch_fp8_gemm(g, true);
+  };
+  if ((e = quant(lay.X, lay.Xq, lay.xs, K1)) != cudaSuccess) return e;
+  if ((e = product(lay.Xq, lay.xs, a.W_f, W_f_scale, a.b_f, ws + lay.h, a.d, K1, 1)) != cudaSuccess) return e;
+  if ((e = quant(lay.h, lay.hq, lay.hs, a.d)) != cudaSuccess) return e;
+  if ((e = product(lay.hq, lay.hs, a.W_kv, W_kv_scale, nullptr, part, N2, a.d, 0)) != cudaSuccess) return e;
+  if (a.D == 128) {
+    e = launch_dependent(mat_epilogue_d128_kernel<bf16>, dim3(kEpiCtasPerSm * 152), dim3(256), 0, st, part, 1, meta,
+                         slots, (const bf16*)a.k_norm_w, a.rms_eps, rope, a.pools, T_max, a.L, a.Hkv, a.d);
+  } else {
+    const size_t esmem = sizeof(float) * 8 * (size_t)a.D;
+    e = launch_dependent(mat_epilogue_kernel<bf16>, dim3(gs), dim3(256), esmem, st, part, 1, meta, row_b, row_j,
+                         a.start_pos, a.page_table, (const bf16*)a.k_norm_w, a.rms_eps, rope, a.pools, T_max, a.L,
+                         a.Hkv, a.D, a.page_size, a.max_pages, a.num_pages, a.d);
+  }
+  if (e != cudaSuccess) return e;
+  *launches = 6;
+  return cudaGetLastError();
+}
+
 cudaError_t launch_materialize(const MatArgs& a, int* launches) {
   return a.dtype == 0 ? launch_mat_t<float>(a, launches) : launch_mat_t<bf16>(a, launches);
 }

@@ -505,6 +505,73 @@ int dflash_ddtree_verify_greedy(const dflash_tree_dims* dims, const void* target
                                 void* workspace, size_t ws_bytes, dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* 8-bit floating point with a scale per 128 values                           */
+/* ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t T;           /* rows, >= 0 (0: nothing is done) */
+  int32_t K;           /* columns, a multiple of 16 */
+  int32_t dtype;       /* type of x */
+  int32_t block_rows;  /* rows that share a scale: 1 (activations) or 128 (weights) */
+} dflash_fp8_quant_dims;
+
+/*
+ * x [T, K] in e4m3 (4 exponent and 3 mantissa bits, no infinity, largest value
+ * 448), with one scale per block of block_rows x 128 values (the last block of
+ * a row or column may be smaller):
+ *   scale = max(amax / 448, 2^-126), amax = largest magnitude of the block
+ *   q = x * (1 / scale), rounded to the nearest e4m3 (ties to even), at most 448
+ * in fp32, each step correctly rounded. q [T, K] one byte each; scale [ceil(T / block_rows), ceil(K / 128)]
+ * float. A NaN becomes e4m3's NaN; in a block with an infinity the scale is
+ * infinite, so that the block's products are NaN.
+ * x and q 16-byte aligned. No workspace.
+ */
+int dflash_fp8_quant(const dflash_fp8_quant_dims* dims, const void* x, void* q, float* scale,
+                     dflash_stream_t stream);
+
+typedef struct {
+  int32_t T;          /* rows of x, >= 0 (0: nothing is done) */
+  int32_t N;          /* rows of w: columns of out */
+  int32_t K;          /* shared dimension, a multiple of 16 */
+  int32_t out_dtype;  /* type of out and bias */
+} dflash_fp8_gemm_dims;
+
+/*
+ * out = x w^T + bias of e4m3 operands with block scales:
+ *   out[t][n] = bias[n] + sum_g x_scale[t][g] * w_scale[n / 128][g] *
+ *                               sum_{k = 128 g}^{128 g + 127} x[t][k] * w[n][k]
+ * with fp32 sums, rounded to out_dtype once.
+ * x [T, K], w [N, K] e4m3, 16-byte aligned; x_scale [T, ceil(K / 128)],
+ * w_scale [ceil(N / 128), ceil(K / 128)] float (dflash_fp8_quant with
+ * block_rows 1 and 128); bias [N] or NULL; out [T, N]. Repeated calls give
+ * identical bits. The workspace holds the error word only (a bounded wait that
+ * ran out): calls may share one.
+ */
+size_t dflash_fp8_gemm_workspace_size(const dflash_fp8_gemm_dims* dims);
+int dflash_fp8_gemm(const dflash_fp8_gemm_dims* dims, const void* x, const float* x_scale, const void* w,
+                    const float* w_scale, const void* bias, void* out, void* workspace, size_t ws_bytes,
+                    dflash_stream_t stream);
+
+/*
+ * dflash_materialize_ctx_kv with W_f and W_kv in e4m3 (half the bytes that
+ * bound a decode-sized commit). dims->dtype is DFLASH_BF16 and types every
+ * other tensor.
+ * W_f [d, m*d], W_kv [L, 2, Hkv*D, d] e4m3, 16-byte aligned; W_f_scale
+ * [ceil(d / 128), ceil(m*d / 128)], W_kv_scale [ceil(L*2*Hkv*D / 128),
+ * ceil(d / 128)] float: the scales of dflash_fp8_quant with block_rows 128 over
+ * W_f and over W_kv as one matrix of L*2*Hkv*D rows. The committed rows of
+ * hidden, and h_ctx once rounded to bf16, are quantised by the call
+ * (block_rows 1). Every other argument as dflash_materialize_ctx_kv; m*d and d
+ * are multiples of 16.
+ */
+size_t dflash_materialize_fp8_workspace_size(const dflash_ctx_kv_dims* dims);
+int dflash_materialize_ctx_kv_fp8(const dflash_ctx_kv_dims* dims, const void* hidden, const int32_t* commit_len,
+                                  const int32_t* start_pos, const void* W_f, const float* W_f_scale,
+                                  const void* b_f, const void* W_kv, const float* W_kv_scale,
+                                  const void* k_norm_w, float rms_eps, float rope_theta, void* const* k_pools,
+                                  void* const* v_pools, const int32_t* page_table, int32_t* new_len,
+                                  void* workspace, size_t ws_bytes, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Rules on the verify rows' logits                                           */
 /* ------------------------------------------------------------------------- */
 typedef struct {

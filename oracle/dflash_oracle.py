@@ -663,3 +663,48 @@ def slot_map(start_pos, n_rows, page_table, page_size, num_pages, rows_max):
     pad = [-1] * (rows_max - len(seq))
     return (np.array(cu, dtype=np.int32), np.array(seq + pad, dtype=np.int32), np.array(pos + pad, dtype=np.int32),
             np.array(slot + pad, dtype=np.int64))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating point with a scale per 128 values
+# ---------------------------------------------------------------------------
+def e4m3_round(v):
+    """Nearest value of the e4m3 grid (ties to even), magnitude at most 448."""
+    v = _f64(v)
+    a = np.abs(v)
+    _, e = np.frexp(a)                     # a = m 2^e, m in [0.5, 1)
+    step = np.exp2(np.maximum(e - 1, -6) - 3.0)
+    with np.errstate(invalid="ignore"):
+        return np.sign(v) * np.minimum(np.rint(a / step) * step, 448.0)
+
+
+def fp8_quant(x, block_rows=1):
+    """(values on the e4m3 grid, float32 scales) of x [T, K]; scale, its
+    reciprocal and the products are fp32 ones, as the definition has them."""
+    x = np.asarray(x, dtype=np.float32)
+    T, K = x.shape
+    G, S = -(-K // 128), -(-T // block_rows)
+    scale = np.zeros((S, G), dtype=np.float32)
+    q = np.zeros((T, K))
+    for i in range(S):
+        rows = slice(i * block_rows, (i + 1) * block_rows)
+        for g in range(G):
+            blk = x[rows, g * 128:(g + 1) * 128]
+            s = max(np.float32(np.abs(blk).max()) / np.float32(448), np.float32(2.0 ** -126))
+            scale[i, g] = s
+            with np.errstate(invalid="ignore"):
+                q[rows, g * 128:(g + 1) * 128] = e4m3_round(blk * (np.float32(1) / np.float32(s)))
+    return q, scale
+
+
+def fp8_spread(scale, block_rows, T, K):
+    """Scales over the elements they belong to."""
+    return np.repeat(np.repeat(_f64(scale), block_rows, 0)[:T], 128, 1)[:, :K]
+
+
+def fp8_gemm(x, x_scale, w, w_scale, bias=None):
+    """(out, size): the product in float64, and the sum of its terms' magnitudes."""
+    xd = _f64(x) * fp8_spread(x_scale, 1, *x.shape)
+    wd = _f64(w) * fp8_spread(w_scale, 128, *w.shape)
+    b = 0.0 if bias is None else _f64(bias)
+    return xd @ wd.T + b, np.abs(xd) @ np.abs(wd).T + np.abs(b)
