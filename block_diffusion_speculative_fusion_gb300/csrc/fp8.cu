@@ -163,7 +163,7 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent) {
 // Product. A tile is 128 rows of x (the MMA's M, one TMEM lane each) by BN
 // weight rows (N); a k-block is one group of 128 values, one 128-byte swizzle
 // atom a row, and its four MMAs (K = 32 each) write a TMEM accumulator of their
-// own. Eight warps take each accumulator out of TMEM and add it, times the
+// own. Sixteen warps take each accumulator out of TMEM and add it, times the
 // group's scales, to the tile's sums in registers, while the MMAs of the next
 // groups go on in the other accumulators. With the rows in the lanes a thread
 // needs one scale a group (its row's times the weight block's), and the sums
@@ -175,7 +175,7 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent) {
 // (distributed shared memory: no workspace, no atomics, the same bits each
 // time). Many tiles go round persistent CTAs, one per SM.
 //
-// Warps 0 - 7 sum, warp 8 issues the TMA loads, warp 9 the MMAs. Every wait is
+// Warps 0 - 15 sum, 16 and 17 issue the MMAs, 18 and 19 the TMA loads. Every wait is
 // bounded as in the bf16 GEMM: one that gives up records a code, the CTA drains
 // its copies and MMAs, frees its TMEM and returns.
 // ---------------------------------------------------------------------------
@@ -183,17 +183,25 @@ namespace f8 {
 constexpr int BM = 128;
 constexpr int A_BYTES = BM * G;           // 16 KB
 constexpr int RING_BYTES = 196608;        // 4 stages of 48 KB (BN = 256) or 6 of 32 KB
-constexpr int THREADS = 320;
-constexpr int SUM_WARPS = 8;
-constexpr int SMEM_BYTES = RING_BYTES + 1024 + 512;
-constexpr int MAX_CLUSTER = 8;
+constexpr int SUM_WARPS = 16;
+constexpr int MMA_WARPS = 2, TMA_WARPS = 2;
+constexpr int THREADS = 32 * (SUM_WARPS + MMA_WARPS + TMA_WARPS);
+constexpr int BUFS = 4, BUF_N = 128;      // TMEM accumulators of 128 columns
+// Scales of the last groups, written by the rows' producer: 128 of x, then the
+// weight blocks'. It writes a group's when its stage is free, STAGES groups ahead
+// of the MMAs, which in turn run up to BUFS groups ahead of the sums.
+constexpr int SCALE_SLOTS = 16, SCALE_LD = BM + 4;
+constexpr int SMEM_BYTES = RING_BYTES + 4 * SCALE_SLOTS * SCALE_LD + 1024 + 512;
 
 template <int BN> struct Cfg {
   static constexpr int STAGE = A_BYTES + BN * G;
   static constexpr int STAGES = RING_BYTES / STAGE;
-  static constexpr int BUFS = 512 / BN;   // TMEM accumulators
-  static constexpr int COLS = BN / 2;     // a summing thread's columns
+  static constexpr int PARTS = BN / BUF_N;   // accumulators that a k-block fills
+  static constexpr int COLS = BN / 4;     // a summing thread's columns
   static constexpr int RED_LD = BN + 4;   // floats: a quarter warp's rows fall on distinct banks
+  static_assert(STAGES + BUFS < SCALE_SLOTS, "scale slots");
+  static constexpr bool WIDE = BN > BUF_N;   // never split over K
+  static constexpr int LD = WIDE ? 16 : 32;  // TMEM columns of a load: with 64 sums a thread has registers for 16
 };
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -208,22 +216,46 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// Bounded wait that also gives up when another role of the CTA has. A k-block's
-// waits are short (a copy, four MMAs, one read-out), so the clock is looked at
-// after every attempt; the attempts themselves suspend the thread.
-__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err,
-                                                int code, unsigned long long limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > limit_ns) {
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// One lane of the (converged) warp, the same at every use of the returned flag.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// Bounded wait of a whole (converged) warp, which also gives up when another
+// warp of the CTA has. The usual short wait is spun through (a suspended attempt
+// wakes late), a longer one suspends. One that took longer than the limit counts
+// as run out even if its phase came at last. The limit is counted in SM cycles,
+// two to a nanosecond (1.9 to 2.1 at full clock): the global timer ticks too
+// seldom for a limit below a few microseconds.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code,
+                                          unsigned long long limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const long long t0 = clock64();
+  for (int i = 0;; ++i) {
+    const bool done = __all_sync(0xffffffffu, i < 32 ? mbar_test(bar, parity) : mbar_try_wait(bar, parity));
+    if (!done && (i & 3) != 3) continue;
+    if (__any_sync(0xffffffffu, (unsigned long long)(clock64() - t0) / 2 > limit_ns)) {
       *abort_flag = 1;
-      if (err) atomicCAS(err, 0, code);
+      if (err && (threadIdx.x & 31) == 0) atomicCAS(err, 0, code);
       return false;
     }
+    if (done) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
   }
-  return true;
 }
 __device__ __forceinline__ uint32_t ctarank() {
   uint32_t r;
@@ -243,6 +275,32 @@ __device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
       : "memory");
   return v;
 }
+// Pairs of fp32 in a 64-bit register: one instruction multiplies and adds both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float4 four(uint64_t a, uint64_t b) {
+  float4 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(a));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.z), "=f"(v.w) : "l"(b));
+  return v;
+}
+// Scales kb .. kb + 3 of a row, 0 past the last group or row.
+__device__ __forceinline__ float4 scale4(const float* scale, int row, int rows, int kb, int groups, int vec) {
+  if (row >= rows || kb >= groups) return make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* s = scale + (size_t)row * groups + kb;
+  if (vec) return __ldg(reinterpret_cast<const float4*>(s));
+  return make_float4(__ldg(s), kb + 1 < groups ? __ldg(s + 1) : 0.f, kb + 2 < groups ? __ldg(s + 2) : 0.f,
+                     kb + 3 < groups ? __ldg(s + 3) : 0.f);
+}
+__device__ __forceinline__ float of4(const float4& v, int i) { return i < 2 ? (i == 0 ? v.x : v.y) : (i == 2 ? v.z : v.w); }
 // Four consecutive outputs of a row from column n on.
 template <typename O>
 __device__ __forceinline__ void store_out4(O* row, int n, int N, float4 v, const O* bias, bool vec) {
@@ -275,7 +333,8 @@ struct Fp8GemmParams {
   const void* bias;       // [N] or null
   void* out;              // [T, N]
   const int32_t* T_dev;   // or null
-  int T, N, groups, splits, box_m, vec;
+  int T, N, groups, splits, box_m, vec, wblocks;
+  int vec_xs, vec_ws;     // rows of scales take 16-byte loads
   int* err;
   unsigned long long wait_ns;
 };
@@ -290,140 +349,179 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   dependents_may_launch();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);   // [STAGES]
+  float* scales = reinterpret_cast<float*>(smem + RING_BYTES);       // [SCALE_SLOTS][SCALE_LD]
+  uint64_t* full = reinterpret_cast<uint64_t*>(scales + SCALE_SLOTS * SCALE_LD);   // [STAGES]
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;    // [BUFS]
-  uint64_t* tempty = tfull + C::BUFS;
-  uint64_t* mma_done = tempty + C::BUFS;
+  uint64_t* tempty = tfull + BUFS;
+  uint64_t* mma_done = tempty + BUFS;
   uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
-  int* consumed_sm = reinterpret_cast<int*>(tmem_base_sm + 2);
 
   const int T = p.T_dev ? min(*p.T_dev, p.T) : p.T;
   const int nt = (p.N + BN - 1) / BN;
   const int tiles = nt * ((T + BM - 1) / BM);
-  const int S = p.splits;
+  const int S = C::WIDE ? 1 : p.splits;
   const int rank = S > 1 ? (int)ctarank() : 0;
   const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
   if (first >= tiles) return;             // (every CTA of the cluster)
   const int kb0 = (int)((long)rank * p.groups / S), kb1 = (int)((long)(rank + 1) * p.groups / S);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int producer_issued = 0;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&full[s], TMA_WARPS);
+      mbar_init(&empty[s], C::PARTS);
     }
-    for (int a = 0; a < C::BUFS; ++a) {
+    for (int a = 0; a < BUFS; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], SUM_WARPS);
+      mbar_init(&tempty[a], SUM_WARPS / C::PARTS);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, MMA_WARPS);
     *abort_flag = 0;
-    *consumed_sm = 0;
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(tmem_base_sm, 512);
+  if (warp == 0) tmem_alloc(tmem_base_sm, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_base_sm;
 
-  if (warp == 8) {
-    // ------------------------------ TMA producer ------------------------------
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      const uint32_t bytes = (uint32_t)(p.box_m * G + BN * G);
-      const uint64_t once = l2_policy_evict_first();
-      const bool stream_w = T <= BM;      // each weight is read by one tile alone
-      for (int tile = first; ok && tile < tiles; tile += step) {
-        const int m0 = tile / nt * BM, n0 = tile % nt * BN;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_or_give_up(&empty[stage], phase ^ 1u, abort_flag, p.err, 21, p.wait_ns)) { ok = false; break; }
-          uint8_t* sa = smem + stage * C::STAGE;
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          if (stream_w) tma_load_2d_hint(sa + A_BYTES, &wmap, &full[stage], kb * G, n0, once);
-          else tma_load_2d(sa + A_BYTES, &wmap, &full[stage], kb * G, n0);
-          tma_load_2d(sa, &xmap, &full[stage], kb * G, m0);
-          ++producer_issued;
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+  // The issuing warps run converged and let one lane issue: what the TMA and MMA
+  // instructions take then sits in uniform registers. Barriers, commits and copies
+  // cost an issuer some 400 cycles of latency a round all the same, as much as
+  // the tensor core needs for an accumulator, so there are two of each kind.
+  if (warp >= SUM_WARPS + MMA_WARPS) {
+    // ------------------------------ TMA producers: weights, rows ------------------------------
+    const bool leader = elect_one(), rows = warp > SUM_WARPS + MMA_WARPS;
+    int stage = 0;
+    int issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t bytes = (uint32_t)(rows ? p.box_m * G : BN * G);
+    const uint64_t once = l2_policy_evict_first();
+    const bool stream_w = !rows && T <= BM;   // each weight is read by one tile alone
+    // The rows' producer also brings the scales: four groups of its rows at a time
+    // (16 bytes a row; one group at a time, by every summing warp, cost the L1 32
+    // lines a warp and group and took longer than the MMAs), read four groups ahead.
+    float4 cur[5], nxt[5];                  // rows lane + 32 i; weight block `lane` of the tile
+    for (int tile = first; ok && tile < tiles; tile += step) {
+      const int y = rows ? tile / nt * BM : tile % nt * BN;
+      auto fetch = [&](int kb) {            // groups kb .. kb + 3 (kb a multiple of 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nxt[i] = scale4(p.xs, y + 32 * i + lane, T, kb, p.groups, p.vec_xs);
+        nxt[4] = scale4(p.ws, lane < C::PARTS ? tile % nt * C::PARTS + lane : p.wblocks, p.wblocks, kb, p.groups, p.vec_ws);
+      };
+      if (rows) fetch(kb0 & ~3);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (rows && (kb == kb0 || kb % 4 == 0)) {
+#pragma unroll
+          for (int i = 0; i < 5; ++i) cur[i] = nxt[i];
+          fetch((kb & ~3) + 4);
         }
+        if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, 21, p.wait_ns)) { ok = false; break; }
+        if (rows) {
+          float* sc = scales + issued % SCALE_SLOTS * SCALE_LD;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[32 * i + lane] = of4(cur[i], kb % 4);
+          if (lane < C::PARTS) sc[BM + lane] = of4(cur[4], kb % 4);
+          __syncwarp();
+        }
+        uint8_t* dst = smem + stage * C::STAGE + (rows ? 0 : A_BYTES);
+        if (leader) {
+          mbar_arrive_expect_tx(&full[stage], bytes);
+          if (stream_w) tma_load_2d_hint(dst, &wmap, &full[stage], kb * G, y, once);
+          else tma_load_2d(dst, rows ? &xmap : &wmap, &full[stage], kb * G, y);
+        }
+        ++issued;
+        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
       }
     }
+    // After an abort copies may still be in flight: wait for the last one of every
+    // stage (bounded) so that none lands after the CTA has exited. A stage that the
+    // other producer left unissued never completes, and when that wait has run out
+    // all copies have landed.
+    if (lane == 0 && *abort_flag)
+      for (int i = max(0, issued - C::STAGES); i < issued; ++i)
+        if (!mbar_wait_bounded(&full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.err, 26)) break;
     __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------ MMA issuer ------------------------------
-    if (lane == 0) {
-      int stage = 0, buf = 0, consumed = 0;
-      uint32_t phase = 0, buf_phase = 0;
-      bool ok = true;
-      const uint32_t idesc = idesc_e4m3(BM, BN);
-      for (int tile = first; ok && tile < tiles; tile += step)
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!wait_or_give_up(&tempty[buf], buf_phase ^ 1u, abort_flag, p.err, 22, p.wait_ns) ||
-              !wait_or_give_up(&full[stage], phase, abort_flag, p.err, 23, p.wait_ns)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * C::STAGE);
-          const uint64_t adesc = sdesc_sw128(sa), bdesc = sdesc_sw128(sa + A_BYTES);
-          const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BN);
+  } else if (warp >= SUM_WARPS) {
+    // ------------------------------ MMA issuers ------------------------------
+    // They take the accumulators in turn; each accumulator is filled by the MMAs of
+    // one group alone, so these need no order among themselves.
+    const bool leader = elect_one();
+    bool ok = true;
+    const uint32_t idesc = idesc_e4m3(BM, BUF_N);
+    const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
+    int n = 0;                              // groups of all tiles so far
+    for (int tile = first; ok && tile < tiles; tile += step)
+      for (int kb = kb0; ok && kb < kb1; ++kb, ++n)
 #pragma unroll
-          for (int j = 0; j < G / 32; ++j)   // 32 bytes of K per instruction
-            mma_e4m3(d_tmem, adesc + (uint64_t)(j * 2), bdesc + (uint64_t)(j * 2), idesc, j > 0 ? 1u : 0u);
-          tc_commit(&empty[stage]);
-          tc_commit(&tfull[buf]);
-          ++consumed;
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
-          if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1u; }
+        for (int part = 0; part < C::PARTS; ++part) {
+          const int u = n * C::PARTS + part;
+          if (u % MMA_WARPS != warp - SUM_WARPS) continue;
+          const int stage = n % C::STAGES, buf = u % BUFS;
+          if (!warp_wait(&tempty[buf], ((uint32_t)(u / BUFS) & 1u) ^ 1u, abort_flag, p.err, 22, p.wait_ns) ||
+              !warp_wait(&full[stage], (uint32_t)(n / C::STAGES) & 1u, abort_flag, p.err, 23, p.wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          // (the address field counts 16 bytes, and the ring stays below its 2^14 of them)
+          const uint64_t adesc = desc0 + (uint64_t)(stage * (C::STAGE / 16));
+          const uint64_t bdesc = adesc + (A_BYTES + part * BUF_N * G) / 16;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(buf * BUF_N);
+          if (leader) {
+#pragma unroll
+            for (int j = 0; j < G / 32; ++j)   // 32 bytes of K per instruction
+              mma_e4m3(d_tmem, adesc + (uint64_t)(j * 2), bdesc + (uint64_t)(j * 2), idesc, j > 0 ? 1u : 0u);
+            tc_commit(&tfull[buf]);
+            tc_commit(&empty[stage]);
+          }
         }
-      *consumed_sm = consumed;
-      // every MMA issued by this thread has completed before TMEM is released
-      tc_commit(mma_done);
-      mbar_wait_bounded(mma_done, 0, p.err, 24);
-    }
+    // every MMA issued by this thread has completed before TMEM is released
+    if (leader) tc_commit(mma_done);
     __syncwarp();
   } else {
-    // ------------------------------ sums (warps 0 - 7) ------------------------------
-    const int quarter = warp & 3, half = warp >> 2;   // TMEM lanes [32 q, 32 q + 32) belong to warp q mod 4
-    int buf = 0;
-    uint32_t buf_phase = 0;
+    // ------------------------------ sums ------------------------------
+    const int quarter = warp & 3, part = warp >> 2;   // TMEM lanes [32 q, 32 q + 32) belong to warp q mod 4
+    constexpr int PER = BUF_N / C::COLS;              // summing threads across an accumulator
+    int u = part / PER;                               // this thread's accumulators: every PARTS-th
     bool ok = true;
     for (int tile = first; ok && tile < tiles; tile += step) {
-      const int m0 = tile / nt * BM, n0 = tile % nt * BN + half * C::COLS;
-      const int row = m0 + quarter * 32 + lane;
+      const int m0 = tile / nt * BM + quarter * 32, n0 = tile % nt * BN + part * C::COLS;
+      const int row = m0 + lane;
       const bool live = row < T && n0 < p.N;
-      const float* xs = p.xs + (size_t)(live ? row : 0) * p.groups;
-      const float* ws = p.ws + (size_t)(live ? n0 / G : 0) * p.groups;
-      float acc[C::COLS];
+      const bool warp_live = m0 < T && n0 < p.N;      // some lane's sums are wanted
+      uint64_t acc[C::COLS / 2];                      // pairs of fp32 sums
 #pragma unroll
-      for (int c = 0; c < C::COLS; ++c) acc[c] = 0.f;
-      float s_next = live ? __ldg(xs + kb0) * __ldg(ws + kb0) : 0.f;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const float s = s_next;
-        if (kb + 1 < kb1 && live) s_next = __ldg(xs + kb + 1) * __ldg(ws + kb + 1);
-        // a warp-wide decision: the TMEM loads below are warp-collective
-        if (!__all_sync(0xffffffffu, wait_or_give_up(&tfull[buf], buf_phase, abort_flag, p.err, 25, p.wait_ns))) {
+      for (int c = 0; c < C::COLS / 2; ++c) acc[c] = 0;
+      for (int kb = kb0; kb < kb1; ++kb, u += C::PARTS) {
+        const int buf = u % BUFS;
+        if (!warp_wait(&tfull[buf], (uint32_t)(u / BUFS) & 1u, abort_flag, p.err, 25, p.wait_ns)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BN + half * C::COLS);
+        const float* sc = scales + u / C::PARTS % SCALE_SLOTS * SCALE_LD;
+        const float f = sc[quarter * 32 + lane] * sc[BM + part / PER];
+        const uint64_t s = pair(f, f);
+        const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BUF_N + part % PER * C::COLS);
+        auto release = [&]() {                        // the warp has read it out: the MMAs may have it
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(&tempty[buf]);
+        };
+        if (warp_live) {
 #pragma unroll
-        for (int c0 = 0; c0 < C::COLS; c0 += 32) {
-          uint32_t r[32];
-          tmem_ld32(tbase + (uint32_t)c0, r);
-          tmem_ld_wait();
-          if (c0 + 32 == C::COLS) {       // the accumulator is read out: the MMAs may have it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[buf]);
+          for (int c0 = 0; c0 < C::COLS; c0 += C::LD) {
+            uint32_t r[C::LD];
+            if constexpr (C::LD == 32) tmem_ld32(tbase + (uint32_t)c0, r);
+            else tmem_ld16(tbase + (uint32_t)c0, r);
+            tmem_ld_wait();
+            if (c0 + C::LD == C::COLS) release();
+#pragma unroll
+            for (int q = 0; q < C::LD; q += 2)
+              acc[(c0 + q) / 2] = fma2(pair(__uint_as_float(r[q]), __uint_as_float(r[q + 1])), s, acc[(c0 + q) / 2]);
           }
-#pragma unroll
-          for (int q = 0; q < 32; ++q) acc[c0 + q] = fmaf(__uint_as_float(r[q]), s, acc[c0 + q]);
         }
-        if (++buf == C::BUFS) { buf = 0; buf_phase ^= 1u; }
+        else release();
       }
       if (!ok) break;
       if (S == 1) {
@@ -431,21 +529,20 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
           O* o = (O*)p.out + (size_t)row * p.N;
 #pragma unroll
           for (int c = 0; c < C::COLS; c += 4)
-            store_out4<O>(o, n0 + c, p.N, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]), (const O*)p.bias,
-                          p.vec != 0);
+            store_out4<O>(o, n0 + c, p.N, four(acc[c / 2], acc[c / 2 + 1]), (const O*)p.bias, p.vec != 0);
         }
       } else if (row < T) {
         // the ring is idle: its last copies have been multiplied. The tile's sums go there
-        float* red = reinterpret_cast<float*>(smem) + (size_t)(quarter * 32 + lane) * C::RED_LD + half * C::COLS;
+        float* red = reinterpret_cast<float*>(smem) + (size_t)(quarter * 32 + lane) * C::RED_LD + part * C::COLS;
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 4)
-          *reinterpret_cast<float4*>(red + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+          *reinterpret_cast<float4*>(red + c) = four(acc[c / 2], acc[c / 2 + 1]);
       }
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (S > 1) {
+  if (!C::WIDE && S > 1) {
+    __syncthreads();
     cluster_sync();
     const int m0 = first / nt * BM, n0 = first % nt * BN;   // a cluster has one tile
     const int rows = min(BM, T - m0), cells = rows * (BN / 4);
@@ -463,29 +560,34 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
     cluster_sync();                       // no CTA leaves while a peer reads its sums
   }
-  // After an abort, copies issued but never consumed may still be in flight:
-  // wait for them (bounded) so that none lands after this CTA has exited.
-  if (warp == 8 && lane == 0 && *abort_flag)
-    for (int i = *consumed_sm; i < producer_issued; ++i)
-      mbar_wait_bounded(&full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.err, 26);
+  // After an abort, MMAs and copies may still be in flight: wait for the last copy
+  // of every stage and for the MMAs (bounded) so that none lands after this CTA has
+  // exited or its TMEM has been freed.
+  // every accumulator has been read; the MMAs end (bounded) before TMEM is freed
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 0) {
+    if (lane == 0) mbar_wait_bounded(mma_done, 0, p.err, 24);
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
 }
 
-// Tile width and split over K. `waves` of whole tiles on 152 SMs: the wide tile
-// reads each row of x half as often, the narrow one wastes less of a last wave;
-// below one wave of narrow tiles, K is split until the SMs are used.
+// Tile width and split over K. Whole tiles: a wide one takes 1.5 times as long as
+// a narrow one (0.47 against 0.31 us a group), so it is taken where it saves that
+// much in waves (T = 2048, K = 4096, N = 10240: 139 us in 5 waves against 150 in
+// 9; T = 512: 57 in 2 against 54 in 3). Up to half a wave of narrow tiles is split
+// over K as far as the clusters are resident at once (T = 10, K = 20480, N = 4096,
+// 32 tiles: 54 us whole, 31 in two parts, 21 in four, 38 in eight, in three rounds).
 struct Fp8Plan { int BN, S; };
 static Fp8Plan fp8_plan(int T, int N, int groups) {
   const long mt = (T + f8::BM - 1) / f8::BM;
   const long t256 = mt * ((N + 255) / 256), t128 = mt * ((N + 127) / 128);
-  if (t128 > 76) return 2 * ((t256 + 151) / 152) <= (t128 + 151) / 152 ? Fp8Plan{256, 1} : Fp8Plan{128, 1};
-  int S = 1;
-  while (S * 2 <= f8::MAX_CLUSTER && t128 * S * 2 <= 152 && S * 2 <= groups) S *= 2;
-  return Fp8Plan{128, S};
+  const long w256 = (t256 + 151) / 152, w128 = (t128 + 151) / 152;
+  if (t128 > 76) return 3 * w256 < 2 * w128 ? Fp8Plan{256, 1} : Fp8Plan{128, 1};
+  // clusters of 2, 4 and 8 CTAs, one an SM, that the GPCs of a GB300 hold
+  const int S = t128 <= 15 ? 8 : t128 <= 36 ? 4 : 2;
+  return Fp8Plan{128, std::min(S, groups)};
 }
 
 template <int BN, typename O>
@@ -496,6 +598,9 @@ static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent)
   p.T = a.T; p.N = a.N; p.groups = (a.K + G - 1) / G; p.splits = S;
   p.box_m = std::min(BM, (a.T + 7) / 8 * 8);
   p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && ((size_t)a.N * sizeof(O)) % (4 * sizeof(O)) == 0;
+  p.wblocks = (a.N + G - 1) / G;
+  p.vec_xs = p.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.x_scale) & 15) == 0;
+  p.vec_ws = p.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & 15) == 0;
   p.err = a.err; p.wait_ns = wait_limit_ns();
   CUtensorMap xmap, wmap;
   const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.T}, wd[2] = {(uint64_t)a.K, (uint64_t)a.N};
