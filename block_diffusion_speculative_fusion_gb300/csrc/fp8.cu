@@ -200,8 +200,7 @@ template <int BN> struct Cfg {
   static constexpr int COLS = BN / 4;     // a summing thread's columns
   static constexpr int RED_LD = BN + 4;   // floats: a quarter warp's rows fall on distinct banks
   static_assert(STAGES + BUFS < SCALE_SLOTS, "scale slots");
-  static constexpr bool WIDE = BN > BUF_N;   // never split over K
-  static constexpr int LD = WIDE ? 16 : 32;  // TMEM columns of a load: with 64 sums a thread has registers for 16
+  static constexpr int LD = PARTS > 1 ? 16 : 32;   // TMEM columns of a load: with 64 sums a thread has registers for 16
 };
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -301,6 +300,40 @@ __device__ __forceinline__ float4 scale4(const float* scale, int row, int rows, 
                      kb + 3 < groups ? __ldg(s + 3) : 0.f);
 }
 __device__ __forceinline__ float of4(const float4& v, int i) { return i < 2 ? (i == 0 ? v.x : v.y) : (i == 2 ? v.z : v.w); }
+// A 32-byte sector of a row: 8 fp32 or 16 bf16 outputs from column n on, all inside it.
+template <typename O>
+__device__ __forceinline__ void store_sector(O* dst, const uint64_t* acc, const O* bias, int n) {
+  constexpr int V = 32 / sizeof(O);
+  float f[V];
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    const float4 v = four(acc[j / 2], acc[j / 2 + 1]);
+    f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
+  }
+  if (bias) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {          // the sector's bias: two 16-byte loads, the same for all lanes
+      float b[V / 2];
+      unpack16<O>(__ldg(reinterpret_cast<const uint4*>(bias + n) + h), b);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) f[h * (V / 2) + j] += b[j];
+    }
+  }
+  uint32_t w[8];
+  if constexpr (sizeof(O) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 // Four consecutive outputs of a row from column n on.
 template <typename O>
 __device__ __forceinline__ void store_out4(O* row, int n, int N, float4 v, const O* bias, bool vec) {
@@ -335,11 +368,13 @@ struct Fp8GemmParams {
   const int32_t* T_dev;   // or null
   int T, N, groups, splits, box_m, vec, wblocks;
   int vec_xs, vec_ws;     // rows of scales take 16-byte loads
+  int vec32;              // rows of out take 32-byte stores, bias 16-byte loads
   int* err;
   unsigned long long wait_ns;
 };
 
-template <int BN, typename O>
+// SPLIT: the tile's K is divided among the CTAs of a cluster.
+template <int BN, typename O, bool SPLIT>
 __global__ void __launch_bounds__(f8::THREADS, 1)
 f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                const Fp8GemmParams p) {
@@ -361,8 +396,8 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   const int T = p.T_dev ? min(*p.T_dev, p.T) : p.T;
   const int nt = (p.N + BN - 1) / BN;
   const int tiles = nt * ((T + BM - 1) / BM);
-  const int S = C::WIDE ? 1 : p.splits;
-  const int rank = S > 1 ? (int)ctarank() : 0;
+  const int S = SPLIT ? p.splits : 1;
+  const int rank = SPLIT ? (int)ctarank() : 0;
   const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
   if (first >= tiles) return;             // (every CTA of the cluster)
   const int kb0 = (int)((long)rank * p.groups / S), kb1 = (int)((long)(rank + 1) * p.groups / S);
@@ -523,13 +558,21 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         }
         else release();
       }
+      // a split tile's sums go to the ring, which the other half's MMAs may still read
+      if (C::PARTS > 1 && SPLIT) asm volatile("bar.sync 1, %0;" ::"n"(32 * SUM_WARPS) : "memory");
       if (!ok) break;
-      if (S == 1) {
+      if (!SPLIT) {
         if (live) {
           O* o = (O*)p.out + (size_t)row * p.N;
+          constexpr int V = 32 / sizeof(O);           // a whole 32-byte sector a store
+          if (p.vec32 && n0 + C::COLS <= p.N) {
 #pragma unroll
-          for (int c = 0; c < C::COLS; c += 4)
-            store_out4<O>(o, n0 + c, p.N, four(acc[c / 2], acc[c / 2 + 1]), (const O*)p.bias, p.vec != 0);
+            for (int c = 0; c < C::COLS; c += V) store_sector<O>(o + n0 + c, acc + c / 2, (const O*)p.bias, n0 + c);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::COLS; c += 4)
+              store_out4<O>(o, n0 + c, p.N, four(acc[c / 2], acc[c / 2 + 1]), (const O*)p.bias, p.vec != 0);
+          }
         }
       } else if (row < T) {
         // the ring is idle: its last copies have been multiplied. The tile's sums go there
@@ -541,7 +584,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
   }
   tc_fence_before();
-  if (!C::WIDE && S > 1) {
+  if (SPLIT) {
     __syncthreads();
     cluster_sync();
     const int m0 = first / nt * BM, n0 = first % nt * BN;   // a cluster has one tile
@@ -573,34 +616,47 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   }
 }
 
-// Tile width and split over K. Whole tiles: a wide one takes 1.5 times as long as
-// a narrow one (0.47 against 0.31 us a group), so it is taken where it saves that
-// much in waves (T = 2048, K = 4096, N = 10240: 139 us in 5 waves against 150 in
-// 9; T = 512: 57 in 2 against 54 in 3). Up to half a wave of narrow tiles is split
-// over K as far as the clusters are resident at once (T = 10, K = 20480, N = 4096,
-// 32 tiles: 54 us whole, 31 in two parts, 21 in four, 38 in eight, in three rounds).
+// Tile width and split over K: the pair of least estimated time. A round of
+// clusters takes, in nanoseconds, 320 a group for a narrow tile or 500 for a wide
+// one, over the split, and 3000 for its start and end (4500 with the sum over the
+// cluster); a GB300 holds 152, 76, 36 and 15 clusters of 1, 2, 4 and 8 CTAs, one an
+// SM, at once. Measured (narrow against wide, us): 10 x 20480 x 4096 59.6 / 33.4 /
+// 21.2 / 38.9 in 1 / 2 / 4 / 8 parts against 82.7 / 46.1 / 27.9 / 38.1; 271 x 20480
+// x 4096 68.5 / 71.1 / 66.7 / 104.6 against 89.5 / 52.3 / 59.7 / 83.7; 271 x 4096 x
+// 10240 32.9 against 26.3 whole; 16 x 512 x 512 6.1 whole, 7.2 in two.
 struct Fp8Plan { int BN, S; };
 static Fp8Plan fp8_plan(int T, int N, int groups) {
+  static const int kSplit[4] = {1, 2, 4, 8}, kResident[4] = {152, 76, 36, 15};
   const long mt = (T + f8::BM - 1) / f8::BM;
-  const long t256 = mt * ((N + 255) / 256), t128 = mt * ((N + 127) / 128);
-  const long w256 = (t256 + 151) / 152, w128 = (t128 + 151) / 152;
-  if (t128 > 76) return 3 * w256 < 2 * w128 ? Fp8Plan{256, 1} : Fp8Plan{128, 1};
-  // clusters of 2, 4 and 8 CTAs, one an SM, that the GPCs of a GB300 hold
-  const int S = t128 <= 15 ? 8 : t128 <= 36 ? 4 : 2;
-  return Fp8Plan{128, std::min(S, groups)};
+  Fp8Plan best{128, 1};
+  long least = -1;
+  for (int BN = 128; BN <= 256; BN += 128)
+    for (int i = 0; i < 4; ++i) {
+      const int S = kSplit[i];
+      if (S > groups) break;
+      const long rounds = (mt * ((N + BN - 1) / BN) + kResident[i] - 1) / kResident[i];
+      const long ns = rounds * ((BN == 128 ? 320L : 500L) * ((groups + S - 1) / S) + (S == 1 ? 3000 : 4500));
+      if (least < 0 || ns < least) {
+        least = ns;
+        best = Fp8Plan{BN, S};
+      }
+    }
+  return best;
 }
 
-template <int BN, typename O>
+template <int BN, typename O, bool SPLIT>
 static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent) {
   using namespace f8;
   Fp8GemmParams p{};
   p.xs = a.x_scale; p.ws = a.w_scale; p.bias = a.bias; p.out = a.out; p.T_dev = a.T_dev;
   p.T = a.T; p.N = a.N; p.groups = (a.K + G - 1) / G; p.splits = S;
   p.box_m = std::min(BM, (a.T + 7) / 8 * 8);
-  p.vec = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && ((size_t)a.N * sizeof(O)) % (4 * sizeof(O)) == 0;
+  auto aligned = [](const void* q, size_t n) { return reinterpret_cast<uintptr_t>(q) % n == 0; };
+  p.vec = aligned(a.out, 16) && a.N % 4 == 0;
+  p.vec32 = aligned(a.out, 32) && (size_t)a.N * sizeof(O) % 32 == 0 && aligned(a.bias, 16);
   p.wblocks = (a.N + G - 1) / G;
-  p.vec_xs = p.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.x_scale) & 15) == 0;
-  p.vec_ws = p.groups % 4 == 0 && (reinterpret_cast<uintptr_t>(a.w_scale) & 15) == 0;
+  p.vec_xs = p.groups % 4 == 0 && aligned(a.x_scale, 16);
+  p.vec_ws = p.groups % 4 == 0 && aligned(a.w_scale, 16);
   p.err = a.err; p.wait_ns = wait_limit_ns();
   CUtensorMap xmap, wmap;
   const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.T}, wd[2] = {(uint64_t)a.K, (uint64_t)a.N};
@@ -612,7 +668,7 @@ static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent)
                          CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorNotSupported;
   static SmemOptIn opt_in;
-  cudaError_t e = opt_in.ensure(f8_gemm_kernel<BN, O>, SMEM_BYTES);
+  cudaError_t e = opt_in.ensure(f8_gemm_kernel<BN, O, SPLIT>, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const long tiles = (long)((a.T + BM - 1) / BM) * ((a.N + BN - 1) / BN);
   cudaLaunchConfig_t cfg = {};
@@ -636,16 +692,21 @@ static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent)
   }
   cfg.attrs = at;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, O>, xmap, wmap, p);
+  return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, O, SPLIT>, xmap, wmap, p);
+}
+
+template <typename O>
+static cudaError_t launch_f8_gemm_o(const Fp8GemmArgs& a, bool dependent) {
+  const Fp8Plan plan = fp8_plan(a.T, a.N, (a.K + f8::G - 1) / f8::G);
+  if (plan.BN == 256)
+    return plan.S > 1 ? launch_f8_gemm_t<256, O, true>(a, plan.S, dependent)
+                      : launch_f8_gemm_t<256, O, false>(a, 1, dependent);
+  return plan.S > 1 ? launch_f8_gemm_t<128, O, true>(a, plan.S, dependent)
+                    : launch_f8_gemm_t<128, O, false>(a, 1, dependent);
 }
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dependent) {
-  const Fp8Plan plan = fp8_plan(a.T, a.N, (a.K + f8::G - 1) / f8::G);
-  if (a.out_dtype == 0)
-    return plan.BN == 256 ? launch_f8_gemm_t<256, float>(a, plan.S, dependent)
-                          : launch_f8_gemm_t<128, float>(a, plan.S, dependent);
-  return plan.BN == 256 ? launch_f8_gemm_t<256, bf16>(a, plan.S, dependent)
-                        : launch_f8_gemm_t<128, bf16>(a, plan.S, dependent);
+  return a.out_dtype == 0 ? launch_f8_gemm_o<float>(a, dependent) : launch_f8_gemm_o<bf16>(a, dependent);
 }
 
 }  // namespace dflash
