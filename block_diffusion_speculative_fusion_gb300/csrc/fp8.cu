@@ -55,47 +55,48 @@ template <typename T> __device__ __forceinline__ void f8_store(uint8_t* dst, con
   else *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
+// A warp's unit is U vectors a lane of one row, UNIT consecutive values.
+template <typename T> struct QuantUnit {
+  static constexpr int U = 2;
+  static constexpr int VALUES = U * 32 * VecTraits<T>::N;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 6)
 f8_quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale, int T_rows,
                      const int32_t* __restrict__ T_dev, int K) {
   wait_for_prior_grid();   // in the materialisation's chain the rows come from the kernel before
   dependents_may_launch();
   constexpr int N = VecTraits<T>::N;
   constexpr int LPG = f8::G / N;           // lanes of a group
-  constexpr int GPW = 32 / LPG;            // groups of a warp's load
-  constexpr int U = 4;
-  const int rows = T_dev ? min(*T_dev, T_rows) : T_rows;
-  const int groups = (K + f8::G - 1) / f8::G;
-  const long total = (long)rows * groups;
-  const int lane = threadIdx.x & 31, sub = lane / LPG, at = (lane % LPG) * N;
-  const long warps = (long)gridDim.x * (blockDim.x >> 5);
-  for (long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w * (U * GPW) < total; w += warps) {
+  constexpr int U = QuantUnit<T>::U, VALUES = QuantUnit<T>::VALUES;
+  const unsigned rows = T_dev ? min(*T_dev, T_rows) : T_rows;
+  const unsigned groups = (K + f8::G - 1) / f8::G, units = (K + VALUES - 1) / VALUES;
+  const int lane = threadIdx.x & 31;
+  const unsigned long warps = (unsigned long)gridDim.x * (blockDim.x >> 5), total = (unsigned long)rows * units;
+  for (unsigned long w = (unsigned long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < total; w += warps) {
+    // (rows * units fit 32 bits for all but the widest calls)
+    const unsigned t = total >> 32 ? (unsigned)(w / units) : (unsigned)w / units;
+    const int k0 = (int)(w - (unsigned long)t * units) * VALUES + lane * N;
+    const T* src = x + (size_t)t * K;
+    uint8_t* dst = q + (size_t)t * K;
     uint4 v[U];
-    size_t off[U];
-    long gi[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      gi[u] = (w * U + u) * GPW + sub;
-      v[u] = make_uint4(0, 0, 0, 0);
-      off[u] = ~(size_t)0;
-      if (gi[u] < total) {
-        const long t = gi[u] / groups;
-        const int k = (int)(gi[u] - t * groups) * f8::G + at;
-        if (k < K) {                       // K is a multiple of 16: a vector is inside or outside
-          off[u] = (size_t)t * K + k;
-          v[u] = ld_stream16(x + off[u]);
-        }
-      }
+      const int k = k0 + u * 32 * N;       // K is a multiple of 16: a vector is inside or outside
+      v[u] = k < K ? ld_stream16(src + k) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * 32 * N;
       float m = vec_absmax<T>(v[u]);
 #pragma unroll
       for (int o = LPG / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const float s = f8_scale(m);
-      if (off[u] != ~(size_t)0) f8_store<T>(q + off[u], v[u], __frcp_rn(s));
-      if (at == 0 && gi[u] < total) scale[gi[u]] = s;
+      if (k < K) {
+        f8_store<T>(dst + k, v[u], __frcp_rn(s));
+        if (lane % LPG == 0) scale[(size_t)t * groups + k / f8::G] = s;
+      }
     }
   }
 }
@@ -144,10 +145,9 @@ static cudaError_t launch_f8_quant_t(const Fp8QuantArgs& a, bool dependent) {
     f8_quant_blocks_kernel<T><<<grid, 256, 0, a.stream>>>((const T*)a.x, (uint8_t*)a.q, a.scale, a.T, a.K);
     return cudaGetLastError();
   }
-  // 32 fp32 or 64 bf16 groups a CTA pass; eight CTAs fill an SM
-  const long per = 8L * 4 * (32 / (f8::G / VecTraits<T>::N));
-  const long need = ((long)a.T * groups + per - 1) / per;
-  const int grid = (int)std::max(1L, std::min(need, 8L * 152));
+  // a warp per unit, up to what six CTAs an SM hold
+  const long units = (long)a.T * ((a.K + QuantUnit<T>::VALUES - 1) / QuantUnit<T>::VALUES);
+  const int grid = (int)std::max(1L, std::min((units + 7) / 8, 6L * 152));
   if (dependent)
     return launch_dependent(f8_quant_rows_kernel<T>, dim3(grid), dim3(256), 0, a.stream, (const T*)a.x, (uint8_t*)a.q,
                             a.scale, a.T, a.T_dev, a.K);

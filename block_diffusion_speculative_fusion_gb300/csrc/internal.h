@@ -222,7 +222,7 @@ struct SlotArgs {
   int32_t* row_seq;            // [rows_max]
   int32_t* positions;          // [rows_max]
   int64_t* slots;              // [rows_max]
-  int vec;                     // the row arrays take 16-byte stores
+  int vec;                     // the row arrays take 16- and 32-byte stores
   cudaStream_t stream;
 };
 cudaError_t launch_slot_map(const SlotArgs& a, int num_sms);

@@ -18,6 +18,7 @@ namespace dflash {
 namespace pages {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kSegment = 128;            // pages that a warp moves at once
 }  // namespace pages
 
 // Exclusive prefix of one value per thread over the block, and the total.
@@ -96,25 +97,31 @@ pages_resize_kernel(const PagesArgs a) {
   const int pool = (int)min((long long)n_free + all_give, (long long)a.num_pages);
   // (more pages given back than the pool has: the surplus is dropped, not written)
 
-  const int lane = tid & 31;
-  for (int b = blockIdx.x * kWarps + (tid >> 5); b < B; b += gridDim.x * kWarps) {
+  // a warp's unit is kSegment consecutive pages of one sequence, given back or
+  // taken: all loads first (one by one, a whole prompt's 512 pages cost 16 round trips)
+  const int lane = tid & 31, segs = (a.max_pages + kSegment - 1) / kSegment;
+  const long units = (long)B * segs;
+  for (long unit = (long)blockIdx.x * kWarps + (tid >> 5); unit < units; unit += (long)gridDim.x * kWarps) {
+    const int b = (int)(unit / segs), i0 = (int)(unit - (long)b * segs) * kSegment + lane;
     const int h = held(b), k = need(b);
     const int g0 = s_give[b], g = s_give[b + 1] - g0;
     const int w0 = s_want[b], w = s_want[b + 1] - w0;
     int32_t* row = a.page_table + (size_t)b * a.max_pages;
     const bool granted = s_want[b + 1] <= pool;
-    if (lane == 0) {
+    if (i0 == 0) {
       a.n_pages_out[b] = h - g + (granted ? w : 0);
       if (a.short_) a.short_[b] = k < 0 || (w > 0 && !granted);
     }
-    for (int i = lane; i < g; i += 32)
-      if (n_free + g0 + i < a.num_pages) a.free_pages[n_free + g0 + i] = row[k + i];
-    if (w > 0 && granted)
-      for (int i = lane; i < w; i += 32) {
+    const int n = granted ? w : 0;         // a sequence gives or takes, never both
+    int page[kSegment / 32];
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q) {
+      const int i = i0 + 32 * q;
+      if (i < g) page[q] = row[k + i];
+      if (i < n) {
         const int pos = pool - 1 - (w0 + i);
-        int page;
         if (pos < n_free) {
-          page = a.free_pages[pos];
+          page[q] = a.free_pages[pos];
         } else {
           // the last sequence whose pages start at or before this one
           const int f = pos - n_free;
@@ -123,10 +130,16 @@ pages_resize_kernel(const PagesArgs a) {
             const int mid = (lo + hi + 1) >> 1;
             if (s_give[mid] <= f) lo = mid; else hi = mid - 1;
           }
-          page = a.page_table[(size_t)lo * a.max_pages + need(lo) + (f - s_give[lo])];
+          page[q] = a.page_table[(size_t)lo * a.max_pages + need(lo) + (f - s_give[lo])];
         }
-        row[h + i] = page;
       }
+    }
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q) {
+      const int i = i0 + 32 * q;
+      if (i < g && n_free + g0 + i < a.num_pages) a.free_pages[n_free + g0 + i] = page[q];
+      if (i < n) row[h + i] = page[q];
+    }
   }
   if (blockIdx.x == 0) {
     // granted sequences are those whose prefix fits: the largest prefix is what is taken
@@ -140,7 +153,8 @@ pages_resize_kernel(const PagesArgs a) {
 }
 
 cudaError_t launch_pages_resize(const PagesArgs& a, int num_sms) {
-  const int grid = std::min(num_sms, (a.B + pages::kWarps - 1) / pages::kWarps);
+  const long units = (long)a.B * ((a.max_pages + pages::kSegment - 1) / pages::kSegment);
+  const int grid = (int)std::min((long)num_sms, (units + pages::kWarps - 1) / pages::kWarps);
   pages_resize_kernel<<<grid, pages::kThreads, 0, a.stream>>>(a);
   return cudaGetLastError();
 }
@@ -148,11 +162,13 @@ cudaError_t launch_pages_resize(const PagesArgs& a, int num_sms) {
 // ---------------------------------------------------------------------------
 // Slot map of a ragged batch: the rows of all sequences, one after the other.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(pages::kThreads)
+__global__ void __launch_bounds__(pages::kThreads, 3)
 slot_map_kernel(const SlotArgs a) {
   using namespace pages;
-  constexpr int U = 4;                       // consecutive rows per thread: 16-byte stores
-  __shared__ int s_cu[kPagesMaxB + 1];
+  constexpr int U = 4;                       // consecutive rows per thread: 16- and 32-byte stores
+  extern __shared__ int slot_smem[];
+  int* s_cu = slot_smem;                     // [B + 1] first row of each sequence
+  int* s_off = slot_smem + a.B + 1;          // [B] position less row
   const int tid = threadIdx.x, B = a.B, T_max = a.rows_max;
   const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
@@ -162,6 +178,7 @@ slot_map_kernel(const SlotArgs a) {
   for (int b = b0; b < b1; ++b) {
     const int c = (int)min(at, (long long)T_max);
     s_cu[b] = c;
+    s_off[b] = (int)((unsigned)a.start_pos[b] - (unsigned)c);
     if (blockIdx.x == 0) a.cu_rows[b] = c;
     at += max(a.n_rows[b], 0);
   }
@@ -171,53 +188,69 @@ slot_map_kernel(const SlotArgs a) {
     if (blockIdx.x == 0) a.cu_rows[B] = T;
   }
   __syncthreads();
-  for (long t0 = ((long)blockIdx.x * kThreads + tid) * U; t0 < T_max; t0 += (long)gridDim.x * kThreads * U) {
-    int seq[U], pos[U];
-    long long slot[U];
-    int b = 0, end = 0, off = 0;
-    if (t0 < T) {
-      int lo = 0, hi = B - 1;                // the last sequence that starts at or before row t0
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_cu[mid] <= (int)t0) lo = mid; else hi = mid - 1;
+  const int lane = tid & 31;
+  for (long w0 = ((long)blockIdx.x * kThreads + tid - lane) * U; w0 < T_max; w0 += (long)gridDim.x * kThreads * U) {
+    const long t0 = w0 + lane * U;
+    // the last sequence that starts at or before the warp's first row, 32 ways at a
+    // time; the lanes walk on from there
+    int b = 0;
+    if (w0 < T) {
+      int lo = 0, n = B;                     // in [lo, lo + n), s_cu[lo] <= w0
+      while (n > 1) {
+        const int step = (n + 31) / 32, i = lo + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, lane * step < n && s_cu[i] <= (int)w0);
+        const int k = 31 - __clz((int)m);    // bit 0 is set
+        n = min(step, n - k * step);
+        lo += k * step;
       }
       b = lo;
-      end = s_cu[b + 1];
-      off = a.start_pos[b] - s_cu[b];
     }
-    int lp0 = -1;
-    long long base = -1;
+    int seq[U], pos[U];
+    long long slot[U];
+    // first slot of the page that position q of sequence b lies in, -1 without one
+    auto page_slot = [&](int q, int lp) -> long long {
+      if (q < 0 || lp >= a.max_pages) return -1;
+      const int page = a.page_table[(size_t)b * a.max_pages + lp];
+      return page >= 0 && page < a.num_pages ? (long long)page * a.page_size : -1;
+    };
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = (int)t0 + u;
-      seq[u] = -1;
-      pos[u] = -1;
-      slot[u] = -1;
-      if (t < T) {
-        if (t >= end) {
-          do { ++b; } while (s_cu[b + 1] <= t);   // past sequences without rows; t < T ends it
-          end = s_cu[b + 1];
-          off = a.start_pos[b] - s_cu[b];
-          lp0 = -1;
+    for (int u = 0; u < U; ++u) seq[u] = pos[u] = -1, slot[u] = -1;
+    if (t0 < T) {
+      while (s_cu[b + 1] <= (int)t0) ++b;    // past the sequences that end before; t0 < T ends it
+      const int q = (int)((unsigned)s_off[b] + (unsigned)t0), lp = q / a.page_size, in_page = q - lp * a.page_size;
+      if (q >= 0 && (int)t0 + U <= s_cu[b + 1] && U <= a.page_size) {
+        // the usual case: all U rows in one sequence, so in one page or two
+        const long long base = page_slot(q, lp);
+        const long long next = in_page + U > a.page_size ? page_slot(q, lp + 1) : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = in_page + u;
+          const bool over = i >= a.page_size;
+          const long long x = over ? next : base;
+          seq[u] = b;
+          pos[u] = q + u;
+          slot[u] = x >= 0 ? x + (over ? i - a.page_size : i) : -1;
         }
-        seq[u] = b;
-        pos[u] = off + t;
-        const int lp = pos[u] / a.page_size;
-        if (pos[u] >= 0 && lp < a.max_pages) {
-          if (lp != lp0) {
-            const int page = a.page_table[(size_t)b * a.max_pages + lp];
-            base = page >= 0 && page < a.num_pages ? (long long)page * a.page_size : -1;
-            lp0 = lp;
-          }
-          if (base >= 0) slot[u] = base + pos[u] % a.page_size;
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < U && t0 + u < T; ++u) {
+          const int t = (int)t0 + u;
+          while (s_cu[b + 1] <= t) ++b;
+          const int v = (int)((unsigned)s_off[b] + (unsigned)t);
+          const long long base = page_slot(v, v / a.page_size);
+          const long long x = base >= 0 ? base + v % a.page_size : -1;
+#pragma unroll
+          for (int k = 0; k < U; ++k)
+            if (k == u) seq[k] = b, pos[k] = v, slot[k] = x;
         }
       }
     }
     if (a.vec && t0 + U <= T_max) {
       *reinterpret_cast<int4*>(a.row_seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
       *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      reinterpret_cast<longlong2*>(a.slots + t0)[0] = make_longlong2(slot[0], slot[1]);
-      reinterpret_cast<longlong2*>(a.slots + t0)[1] = make_longlong2(slot[2], slot[3]);
+      asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(a.slots + t0), "l"(slot[0]), "l"(slot[1]),
+                   "l"(slot[2]), "l"(slot[3])
+                   : "memory");
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -232,11 +265,11 @@ slot_map_kernel(const SlotArgs a) {
 
 cudaError_t launch_slot_map(const SlotArgs& args, int num_sms) {
   SlotArgs a = args;
-  auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  a.vec = al(a.row_seq) && al(a.positions) && al(a.slots);
+  auto al = [](const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
+  a.vec = al(a.row_seq, 16) && al(a.positions, 16) && al(a.slots, 32);
   const long need = ((long)a.rows_max + 4 * pages::kThreads - 1) / (4 * pages::kThreads);
   const int grid = (int)std::max(1L, std::min((long)num_sms * 3, need));
-  slot_map_kernel<<<grid, pages::kThreads, 0, a.stream>>>(a);
+  slot_map_kernel<<<grid, pages::kThreads, (2 * (size_t)a.B + 1) * sizeof(int), a.stream>>>(a);
   return cudaGetLastError();
 }
 
