@@ -235,6 +235,16 @@ def _arg(t: Optional[torch.Tensor], name: str, dev: int, dtype: torch.dtype, sha
     raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
+def _out(o: dict, name: str, like: torch.Tensor, dev: int, dtype: torch.dtype, shape: Tuple[int, ...]) -> int:
+    """Device pointer of output ``name``: the caller's tensor, checked, or a new
+    one on the device of ``like``."""
+    t = o.get(name)
+    if t is not None:
+        return _arg(t, name, dev, dtype, shape)
+    t = o[name] = torch.empty(shape, dtype=dtype, device=like.device)
+    return t.data_ptr()
+
+
 # the stream handle without a Stream object, where this torch has the call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -606,19 +616,13 @@ def pages_resize(length: torch.Tensor, page_table: torch.Tensor, n_pages: torch.
     B, max_pages = page_table.shape
     dev = page_table.get_device()
     o = out if out is not None else {}
-    if "n_pages" not in o:
-        o["n_pages"] = torch.empty_like(n_pages)
-    if "n_free" not in o:
-        o["n_free"] = torch.empty_like(n_free)
-    if "short" not in o:
-        o["short"] = torch.empty(B, dtype=torch.uint8, device=page_table.device)
     num_pages = len(free_pages)
-    i32 = torch.int32
+    i32, seq = torch.int32, (B,)
     _launch(dev, lib().dflash_pages_resize, ctypes.byref(PagesDims(B, page_size, max_pages, num_pages)),
-            _arg(length, "length", dev, i32, (B,)), page_table.data_ptr(), _arg(n_pages, "n_pages", dev, i32, (B,)),
+            _arg(length, "length", dev, i32, seq), page_table.data_ptr(), _arg(n_pages, "n_pages", dev, i32, seq),
             _arg(free_pages, "free_pages", dev, i32, (num_pages,)), _arg(n_free, "n_free", dev, i32, (1,)),
-            _arg(o["n_pages"], "out n_pages", dev, i32, (B,)), _arg(o["n_free"], "out n_free", dev, i32, (1,)),
-            _arg(o["short"], "short", dev, torch.uint8, (B,)))
+            _out(o, "n_pages", page_table, dev, i32, seq), _out(o, "n_free", page_table, dev, i32, (1,)),
+            _out(o, "short", page_table, dev, torch.uint8, seq))
     return o
 
 
@@ -630,22 +634,13 @@ def slot_map(start_pos: torch.Tensor, n_rows: torch.Tensor, page_table: torch.Te
     _dev(page_table, "page_table", torch.int32)
     B, max_pages = page_table.shape
     dev = page_table.get_device()
-    i32, device = torch.int32, page_table.device
-    rows = (max(rows_max, 0),)
+    i32, rows = torch.int32, (max(rows_max, 0),)
     o = out if out is not None else {}
-    if "cu_rows" not in o:
-        o["cu_rows"] = torch.empty(B + 1, dtype=i32, device=device)
-    if "row_seq" not in o:
-        o["row_seq"] = torch.empty(rows, dtype=i32, device=device)
-    if "positions" not in o:
-        o["positions"] = torch.empty(rows, dtype=i32, device=device)
-    if "slots" not in o:
-        o["slots"] = torch.empty(rows, dtype=torch.int64, device=device)
     _launch(dev, lib().dflash_slot_map, ctypes.byref(PagesDims(B, page_size, max_pages, num_pages)), rows_max,
             _arg(start_pos, "start_pos", dev, i32, (B,)), _arg(n_rows, "n_rows", dev, i32, (B,)),
-            page_table.data_ptr(), _arg(o["cu_rows"], "cu_rows", dev, i32, (B + 1,)),
-            _arg(o["row_seq"], "row_seq", dev, i32, rows), _arg(o["positions"], "positions", dev, i32, rows),
-            _arg(o["slots"], "slots", dev, torch.int64, rows))
+            page_table.data_ptr(), _out(o, "cu_rows", page_table, dev, i32, (B + 1,)),
+            _out(o, "row_seq", page_table, dev, i32, rows), _out(o, "positions", page_table, dev, i32, rows),
+            _out(o, "slots", page_table, dev, torch.int64, rows))
     return o
 
 
@@ -782,14 +777,11 @@ def fp8_quant(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = 
     _dev(x, "x")
     T, K = x.shape
     dev = x.get_device()
-    shape = (-(-T // block_rows) if block_rows > 0 else T, -(-K // 128))
-    if q is None:
-        q = torch.empty((T, K), dtype=_E4M3, device=x.device)
-    if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    o = {"q": q, "scale": scale}
     _launch(dev, lib().dflash_fp8_quant, ctypes.byref(Fp8QuantDims(T, K, _dtype_code(x), block_rows)), x.data_ptr(),
-            _arg(q, "q", dev, _E4M3, (T, K)), _arg(scale, "scale", dev, torch.float32, shape))
-    return q, scale
+            _out(o, "q", x, dev, _E4M3, (T, K)),
+            _out(o, "scale", x, dev, torch.float32, (-(-T // block_rows) if block_rows > 0 else T, -(-K // 128))))
+    return o["q"], o["scale"]
 
 
 def fp8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -803,18 +795,19 @@ def fp8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: t
     T, K = x.shape
     N = w.shape[0]
     dev = x.get_device()
+    groups = -(-K // 128)
     if out is not None:
         out_dtype = out.dtype
-    else:
-        out = torch.empty((T, N), dtype=out_dtype, device=x.device)
-    groups = -(-K // 128)
+    if out_dtype not in _DT:
+        raise TypeError(f"unsupported dtype {out_dtype}; use float32 or bfloat16")
+    o = {"out": out}
     w_ws = ws if ws is not None else workspace(x.device, WS_COUNTER_BYTES, slot=3)
-    _launch(dev, lib().dflash_fp8_gemm, ctypes.byref(Fp8GemmDims(T, N, K, _dtype_code(out))), x.data_ptr(),
+    _launch(dev, lib().dflash_fp8_gemm, ctypes.byref(Fp8GemmDims(T, N, K, _DT[out_dtype])), x.data_ptr(),
             _arg(x_scale, "x_scale", dev, torch.float32, (T, groups)), _arg(w, "w", dev, _E4M3, (N, K)),
             _arg(w_scale, "w_scale", dev, torch.float32, (-(-N // 128), groups)),
-            _arg(bias, "bias", dev, out_dtype, (N,)), _arg(out, "out", dev, out_dtype, (T, N)),
+            _arg(bias, "bias", dev, out_dtype, (N,)), _out(o, "out", x, dev, out_dtype, (T, N)),
             w_ws.data_ptr(), w_ws.numel())
-    return out
+    return o["out"]
 
 
 def materialize_ctx_kv_fp8(hidden: torch.Tensor, commit_len: torch.Tensor, start_pos: torch.Tensor,
