@@ -39,6 +39,7 @@ constexpr int kVecs = 256;            // vectors of a CTA's chunk
 constexpr int kRowsInFlight = 4;         // rows of a stage
 constexpr int kStages = 2;
 constexpr int kCtasPerSm = 4;            // 54 KB of shared memory each
+constexpr int kHistAhead = 4;            // history tokens a thread asks for before the first wait
 constexpr int kMaxCluster = 8;
 // a token's word: occurrences in the output, and
 constexpr uint32_t kCountMask = (1u << kRulesCountBits) - 1;
@@ -129,8 +130,8 @@ struct RulesSmem {
   // vector less one token past the chunk's start: the words reach that far
   static constexpr int CW = C + VecTraits<T>::N;
   uint4 stage[rules::kStages][rules::kRowsInFlight][rules::kVecs];
-  uint32_t word[CW];       // occurrences
-  uint32_t entry[CW];      // the last bias entry plus one; then its value's bits
+  alignas(16) uint32_t word[CW];    // occurrences
+  alignas(16) uint32_t entry[CW];   // the last bias entry plus one; then its value's bits
   uint16_t list[CW];       // the tokens that have a rule
   int32_t cand[kRulesMaxRows];
   int n;                   // length of list
@@ -253,12 +254,11 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
   bool plain = false;                        // in place: the thread's vector has no rule (once that is known)
   // requests the thread's vectors of group g's rows, whose mask words have been
   // read before; returns their allowed bits, a byte a row
-  uint32_t words[U];
-  auto read_mask = [&](int g) {
+  auto read_mask = [&](int g, uint32_t* words) {
 #pragma unroll
     for (int u = 0; u < U; ++u) words[u] = mask_words(g * U + u);
   };
-  auto fetch = [&](int g) -> uint32_t {
+  auto fetch = [&](int g, const uint32_t* words) -> uint32_t {
     uint32_t bits = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -269,22 +269,28 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
     cp_async_commit();
     return bits;
   };
-  read_mask(0);
-  uint32_t ok_now = fetch(0);
-  read_mask(1);
-  uint32_t ok_next = fetch(1);
-  read_mask(2);
-
+  // everything that comes from memory is asked for before anything is waited for
+  uint32_t cs;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
+  const uint32_t rank = cluster_rank();
+  const int step = (int)cs * kVecs, i0 = (int)rank * kVecs + tid;   // the thread's entries of the lists
+  const int64_t* hist = p.hist + (size_t)b * p.H;
+  uint32_t words[U], words1[U];
+  read_mask(0, words);
+  read_mask(1, words1);
+  int64_t ahead[kHistAhead];
+#pragma unroll
+  for (int k = 0; k < kHistAhead; ++k) ahead[k] = penal && i0 + k * step < n_hist ? hist[i0 + k * step] : -1;
   for (int i = tid; i < p.R; i += kVecs) {
     const int64_t t = (p.cand && penal && i >= 1 && i <= nd) ? p.cand[(size_t)b * p.R + i] : -1;
     sm.cand[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
   }
+  uint32_t ok_now = fetch(0, words);
+  uint32_t ok_next = fetch(1, words1);
+  read_mask(2, words);
   __syncthreads();
   cluster_wait();
   {
-    uint32_t cs;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cs));
-    const uint32_t rank = cluster_rank();
     const int64_t first = (int64_t)(chunk - (int)rank) * C;      // the cluster's first token
     const int span = (int)cs * C;
     // f at the token's word in its owner, and in the chunk before, whose vectors may reach it
@@ -295,18 +301,20 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
       if (v < span) f((uint32_t)owner, off);
       if (!EVEN && off < N && owner >= 1) f((uint32_t)(owner - 1), off + C);
     };
-    const int step = (int)cs * kVecs, i0 = (int)rank * kVecs + tid;
+    auto note_hist = [&](int64_t tok, int i) {
+      note(tok, [&](uint32_t k, int off) {
+        const uint32_t a = at_rank(&sm.word[off], k);
+        if (i < n_prompt) red_or(a, kPrompt);
+        else red_add(a, 1u);
+      });
+    };
     for (int i = i0; i < p.nb; i += step)    // the last entry of a token's biases counts
       note(p.bias_tok[(size_t)b * p.nb + i], [&](uint32_t k, int off) { red_max(at_rank(&sm.entry[off], k), (uint32_t)i + 1); });
     if (penal) {
-      const int64_t* h = p.hist + (size_t)b * p.H;
+#pragma unroll
+      for (int k = 0; k < kHistAhead; ++k) note_hist(ahead[k], i0 + k * step);
 #pragma unroll 4
-      for (int i = i0; i < n_hist; i += step)
-        note(h[i], [&](uint32_t k, int off) {
-          const uint32_t a = at_rank(&sm.word[off], k);
-          if (i < n_prompt) red_or(a, kPrompt);
-          else red_add(a, 1u);
-        });
+      for (int i = i0 + kHistAhead * step; i < n_hist; i += step) note_hist(hist[i], i);
       for (int i = 1 + i0; i <= nd; i += step)
         note(sm.cand[i], [&](uint32_t k, int off) { red_or(at_rank(&sm.word[off], k), kCand); });
     }
@@ -314,23 +322,46 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
   cluster_arrive();
   cluster_wait();                            // every part of the lists is in
   if (c0 >= p.V) return;                     // (the whole CTA)
-  for (int i = tid; i < (CW + 31) / 32 * 32; i += kVecs) {
-    const uint32_t j = i < CW ? sm.entry[i] : 0;
-    const bool ruled = i < CW && (sm.word[i] | j) != 0;
-    if (j) sm.entry[i] = __float_as_uint(p.bias_val[(size_t)b * p.nb + j - 1]);
-    const unsigned m = __ballot_sync(0xffffffffu, ruled);
+  // the list: each thread's own tokens (and a thread each for those past the chunk)
+  {
+    const int lane = tid & 31;
+    auto ruled = [&](int i) -> bool {
+      const uint32_t j = sm.entry[i];
+      if (j) sm.entry[i] = __float_as_uint(p.bias_val[(size_t)b * p.nb + j - 1]);
+      return (sm.word[i] | j) != 0;
+    };
+    uint32_t m = 0;
+    if (EVEN) {                              // 16 bytes at once
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const uint4 w = reinterpret_cast<const uint4*>(sm.word)[tid * (N / 4) + q];
+        const uint4 e = reinterpret_cast<const uint4*>(sm.entry)[tid * (N / 4) + q];
+        m |= ((w.x | e.x ? 1u : 0u) | (w.y | e.y ? 2u : 0u) | (w.z | e.z ? 4u : 0u) | (w.w | e.w ? 8u : 0u)) << (4 * q);
+        if (e.x | e.y | e.z | e.w)
+          for (int j = 0; j < 4; ++j) ruled(tid * N + 4 * q + j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) m |= (ruled(tid * N + j) ? 1u : 0u) << j;
+      if (tid < N && ruled(C + tid)) m |= 1u << N;
+    }
+    plain = EVEN && p.in_place && m == 0;
+    int before = __popc(m);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
+    }
     int at = 0;
-    if ((tid & 31) == 0 && m) at = atomicAdd(&sm.n, __popc(m));
-    at = __shfl_sync(0xffffffffu, at, 0);
-    if (ruled) sm.list[at + __popc(m & ((1u << (tid & 31)) - 1))] = (uint16_t)i;
+    if (lane == 31 && before) at = atomicAdd(&sm.n, before);
+    at = __shfl_sync(0xffffffffu, at, 31) + before - __popc(m);
+    for (; m; m &= m - 1) {
+      const int j = __ffs(m) - 1;
+      sm.list[at++] = (uint16_t)(j < N ? tid * N + j : C + tid);
+    }
   }
   __syncthreads();
   const int n = sm.n;
-  if (EVEN && p.in_place) {
-    plain = true;
-#pragma unroll
-    for (int j = 0; j < N; ++j) plain = plain && (sm.word[tid * N + j] | sm.entry[tid * N + j]) == 0;
-  }
 
   // pairs (row, list entry) kVecs apart
   const int dr = n ? kVecs / n : 0, di = n ? kVecs % n : 0;
@@ -368,8 +399,8 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
     }
     for (int u = 0; u < U && g * U + u <= nd; ++u) scalars(g * U + u);
     ok_now = ok_next;
-    ok_next = fetch(g + 2);
-    read_mask(g + 3);
+    ok_next = fetch(g + 2, words);
+    read_mask(g + 3, words);
   }
   cp_async_wait_all();
 }
