@@ -250,6 +250,8 @@ def _mat_case(d, m, L, Hkv, D, commit, start, seed, page=16, k_norm=True, theta=
     (256, 1, 2, 1, 64, [1], [100]),
     (144, 2, 3, 2, 32, [4, 2], [15, 16]),           # groups and blocks that end early
     (512, 1, 2, 2, 128, [16] * 20, list(range(0, 200, 10))),
+    # far fewer rows committed than the call is sized for, tiles of many K/V columns
+    (128, 1, 5, 8, 128, [16, 3] + [0] * 40 + [1] * 30 + [0, 9] * 4, list(range(80))),
 ])
 def test_materialize_fp8(d, m, L, Hkv, D, commit, start):
     _mat_case(d, m, L, Hkv, D, commit, start, seed=d + m, k_norm=D == 128, theta=10000.0 if D != 64 else 0.0)
