@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional, Sequence, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
@@ -262,17 +262,22 @@ def _launch(dev: int, fn, *args) -> None:
 
 
 _WS: Dict[Tuple[int, int], torch.Tensor] = {}
+_WS_OUTGROWN: List[torch.Tensor] = []
 
 
 def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
     """A zero-initialised device workspace of at least ``nbytes`` (cached per
-    device and slot; calls on one stream may share a slot)."""
+    device and slot; calls on one stream may share a slot). One that a larger
+    call outgrows is kept until ``reset_workspaces``: a captured graph may still
+    replay with it."""
     idx = torch.device(device).index
     if idx is None:
         idx = torch.cuda.current_device()
     key = (idx, slot)
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
+        if ws is not None:
+            _WS_OUTGROWN.append(ws)
         ws = torch.zeros(max(nbytes, WS_COUNTER_BYTES), dtype=torch.uint8, device=f"cuda:{idx}")
         _WS[key] = ws
     return ws
@@ -280,6 +285,7 @@ def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
 
 def reset_workspaces():
     _WS.clear()
+    _WS_OUTGROWN.clear()
 
 
 # ---------------------------------------------------------------------------

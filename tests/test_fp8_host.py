@@ -27,6 +27,7 @@ def _p(x=0x10000):
     (api.Fp8QuantDims(4, 128, api.BF16, 64), api.ERR_INVALID_ARG, "block_rows"),
     (api.Fp8QuantDims(4, 120, api.BF16, 1), api.ERR_UNSUPPORTED, "multiple of 16"),
     (api.Fp8QuantDims((1 << 23) + 1, 128, api.BF16, 1), api.ERR_UNSUPPORTED, "2^23"),
+    (api.Fp8QuantDims(4, (1 << 23) + 16, api.BF16, 1), api.ERR_UNSUPPORTED, "2^23"),
 ])
 def test_quant_refusals(L, dims, code, word):
     assert L.dflash_fp8_quant(ctypes.byref(dims), _p(), _p(), _p(), None) == code and word in api.last_error()

@@ -287,3 +287,24 @@ def test_materialize_fp8_follows_the_bf16_materialisation():
         assert torch.equal(a != 0, b != 0) or float(((a != 0) ^ (b != 0)).float().mean()) < 1e-3
         rel = float((a.float() - b.float()).norm() / a.float().norm())
         assert rel < 0.1, rel
+
+
+def test_captured_materialisation_outlives_a_larger_call():
+    # the cached workspace is outgrown after a capture: the graph keeps the one it was captured with
+    api.reset_workspaces()
+    args, pt, pools = _mat_case(128, 2, 1, 2, 128, [3, 0, 5], [0, 7, 30], seed=11)
+    kd, vd = [pools[0].to(DEV)], [pools[1].to(DEV)]
+    table = pt.to(DEV)
+    api.materialize_ctx_kv_fp8(*args, kd, vd, table)
+    ref = kd[0].clone(), vd[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.materialize_ctx_kv_fp8(*args, kd, vd, table)
+    _mat_case(256, 2, 1, 2, 128, [16] * 40, [0] * 40, seed=12)         # a larger workspace
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV) for _ in range(64)]
+    kd[0].zero_()
+    vd[0].zero_()
+    graph.replay()
+    rows = (kd[0] != 0).flatten(2).any(2)
+    assert rows.any() and torch.equal(kd[0][rows], ref[0][rows]) and torch.equal(vd[0][rows], ref[1][rows])
+    assert all(int(j.min()) == 255 for j in junk)
