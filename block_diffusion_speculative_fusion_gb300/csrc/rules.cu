@@ -12,8 +12,9 @@
 // in fp32, rounded to the I/O type once; a token that no rule touches keeps
 // its bits.
 //
-// Bound: one read and one write of the rows. A CTA owns 256 16-byte vectors of
-// the vocabulary of one sequence, one a thread, for all its rows. Without lists
+// Bound: one read and one write of the rows. A CTA owns 2048 tokens of one
+// sequence's vocabulary, a 16-byte vector a thread (bf16) or two (fp32), for all
+// its rows. Without lists
 // it streams them through registers, four rows in flight a thread, with the
 // mask alone: a vector that the mask forbids whole is written without being
 // read, and in place a vector without a masked token is neither read nor
@@ -35,8 +36,8 @@
 namespace dflash {
 
 namespace rules {
-constexpr int kVecs = 256;            // vectors of a CTA's chunk
-constexpr int kRowsInFlight = 4;         // rows of a stage
+constexpr int kVecs = 256;               // threads
+constexpr int kVecsInFlight = 4;         // vectors of a thread in a stage
 constexpr int kStages = 2;
 constexpr int kCtasPerSm = 4;            // 54 KB of shared memory each
 constexpr int kHistAhead = 4;            // history tokens a thread asks for before the first wait
@@ -125,11 +126,13 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* a, int at, int n, in
 // Shared memory of a CTA: the stages, then what is known of the tokens.
 template <typename T>
 struct RulesSmem {
-  static constexpr int C = rules::kVecs * VecTraits<T>::N;   // tokens of a chunk
+  static constexpr int VPT = 8 / VecTraits<T>::N;                  // vectors of a thread in a row
+  static constexpr int UR = rules::kVecsInFlight / VPT;            // rows of a stage
+  static constexpr int C = rules::kVecs * VPT * VecTraits<T>::N;   // tokens of a chunk
   // vectors start where the row's address is a multiple of 16 bytes, up to a
   // vector less one token past the chunk's start: the words reach that far
   static constexpr int CW = C + VecTraits<T>::N;
-  uint4 stage[rules::kStages][rules::kRowsInFlight][rules::kVecs];
+  uint4 stage[rules::kStages][rules::kVecsInFlight][rules::kVecs];   // [row, vector of the thread][thread]
   alignas(16) uint32_t word[CW];    // occurrences
   alignas(16) uint32_t entry[CW];   // the last bias entry plus one; then its value's bits
   uint16_t list[CW];       // the tokens that have a rule
@@ -144,7 +147,7 @@ __global__ void __launch_bounds__(rules::kVecs, rules::kCtasPerSm)
 rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParams p) {
   using namespace rules;
   constexpr int N = VecTraits<T>::N;
-  constexpr int U = kRowsInFlight;
+  constexpr int U = kVecsInFlight, VPT = RulesSmem<T>::VPT, UR = RulesSmem<T>::UR;
   constexpr uint32_t kAll = (1u << N) - 1;
   constexpr int C = RulesSmem<T>::C, CW = RulesSmem<T>::CW;
   extern __shared__ uint4 rules_smem[];
@@ -209,62 +212,69 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
       const int h = min(head(r), p.V);
       if (c0 == 0 && tid < h) one(tid, r);
       const int k = (p.V - h) / N, e = h + k * N + tid;
-      if (k / kVecs == chunk && e < p.V) one(e, r);
+      if (k / (kVecs * VPT) == chunk && e < p.V) one(e, r);
     }
   };
-  // whether row r has a vector for this thread, the mask words (byte, if EVEN)
-  // that hold its allowed bits, and the bits: bit j is token j's
-  auto has_vec = [&](int r) { return r <= nd && vec && head(r) + c0 + tid * N + N <= p.V; };
-  auto mask_words = [&](int r) -> uint32_t {
-    if (!m0 || !has_vec(r)) return 0xffffffffu;
-    const int e = head(r) + c0 + tid * N;
+  // The thread's U vectors of group g: slot u is vector u % VPT of row g * UR + u / VPT.
+  auto row_of = [&](int g, int u) { return g * UR + u / VPT; };
+  auto token_of = [&](int r, int u) { return head(r) + c0 + (tid + u % VPT * kVecs) * N; };   // its first
+  // whether row r has slot u's vector, the mask words (byte, if EVEN) that hold its
+  // allowed bits, and the bits: bit j is token j's
+  auto has_vec = [&](int r, int u) { return r <= nd && vec && token_of(r, u) + N <= p.V; };
+  auto mask_words = [&](int r, int u) -> uint32_t {
+    if (!m0 || !has_vec(r, u)) return 0xffffffffu;
+    const int e = token_of(r, u);
     if constexpr (EVEN) return reinterpret_cast<const uint8_t*>(m0 + (size_t)r * p.W)[e / 8];
     return bits_at(m0 + (size_t)r * p.W, e, N, p.W);
   };
-  auto allowed = [&](uint32_t words, int r) -> uint32_t {
-    if (!has_vec(r)) return 0;
+  auto allowed = [&](uint32_t words, int r, int u) -> uint32_t {
+    if (!has_vec(r, u)) return 0;
     return (EVEN && N < 8 ? words >> (tid * N & 7) : words) & kAll;
   };
-  auto at_vec = [&](int r) -> size_t { return (size_t)r * p.V + (head(r) + c0 + tid * N); };
+  auto at_vec = [&](int r, int u) -> size_t { return (size_t)r * p.V + token_of(r, u); };
 
   if (!any) {
     if (p.lists) cluster_wait();
     if (c0 >= p.V) return;
-    for (int r0 = 0; r0 <= nd; r0 += U) {
+    for (int g = 0; g * UR <= nd; ++g) {
       uint32_t ok[U];
       uint4 x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) ok[u] = mask_words(r0 + u);
+      for (int u = 0; u < U; ++u) ok[u] = mask_words(row_of(g, u), u);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        ok[u] = allowed(ok[u], r0 + u);
-        if (ok[u] && !(p.in_place && ok[u] == kAll)) x[u] = ld_rows16(z0 + at_vec(r0 + u));
+        const int r = row_of(g, u);
+        ok[u] = allowed(ok[u], r, u);
+        if (ok[u] && !(p.in_place && ok[u] == kAll)) x[u] = ld_rows16(z0 + at_vec(r, u));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (!has_vec(r0 + u) || (p.in_place && ok[u] == kAll)) continue;
+        const int r = row_of(g, u);
+        if (!has_vec(r, u) || (p.in_place && ok[u] == kAll)) continue;
         if (m0) forbid16<T>(x[u], ok[u]);
-        *reinterpret_cast<uint4*>(o0 + at_vec(r0 + u)) = x[u];
+        *reinterpret_cast<uint4*>(o0 + at_vec(r, u)) = x[u];
       }
-      for (int u = 0; u < U && r0 + u <= nd; ++u) scalars(r0 + u);
+      for (int r = g * UR; r < (g + 1) * UR && r <= nd; ++r) scalars(r);
     }
     return;
   }
 
-  bool plain = false;                        // in place: the thread's vector has no rule (once that is known)
-  // requests the thread's vectors of group g's rows, whose mask words have been
-  // read before; returns their allowed bits, a byte a row
+  // in place: bit j: the thread's vector j has no rule (once that is known)
+  uint32_t plain = 0;
+  // requests the thread's vectors of group g, whose mask words have been read
+  // before; returns their allowed bits, a byte a vector
   auto read_mask = [&](int g, uint32_t* words) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) words[u] = mask_words(g * U + u);
+    for (int u = 0; u < U; ++u) words[u] = mask_words(row_of(g, u), u);
   };
   auto fetch = [&](int g, const uint32_t* words) -> uint32_t {
     uint32_t bits = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t ok = allowed(words[u], g * U + u);
+      const int r = row_of(g, u);
+      const uint32_t ok = allowed(words[u], r, u);
       bits |= ok << (8 * u);
-      if (ok && !(plain && ok == kAll)) cp_async16(&sm.stage[g % kStages][u][tid], z0 + at_vec(g * U + u));
+      if (ok && !((plain >> (u % VPT) & 1) && ok == kAll)) cp_async16(&sm.stage[g % kStages][u][tid], z0 + at_vec(r, u));
     }
     cp_async_commit();
     return bits;
@@ -322,8 +332,10 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
   cluster_arrive();
   cluster_wait();                            // every part of the lists is in
   if (c0 >= p.V) return;                     // (the whole CTA)
-  // the list: each thread's own tokens (and a thread each for those past the chunk)
+  // the list: eight tokens a thread (and one each of those past the chunk)
   {
+    constexpr int TPT = C / kVecs;
+    static_assert(TPT == 8, "tokens of a thread");
     const int lane = tid & 31;
     auto ruled = [&](int i) -> bool {
       const uint32_t j = sm.entry[i];
@@ -331,21 +343,26 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
       return (sm.word[i] | j) != 0;
     };
     uint32_t m = 0;
-    if (EVEN) {                              // 16 bytes at once
 #pragma unroll
-      for (int q = 0; q < N / 4; ++q) {
-        const uint4 w = reinterpret_cast<const uint4*>(sm.word)[tid * (N / 4) + q];
-        const uint4 e = reinterpret_cast<const uint4*>(sm.entry)[tid * (N / 4) + q];
-        m |= ((w.x | e.x ? 1u : 0u) | (w.y | e.y ? 2u : 0u) | (w.z | e.z ? 4u : 0u) | (w.w | e.w ? 8u : 0u)) << (4 * q);
-        if (e.x | e.y | e.z | e.w)
-          for (int j = 0; j < 4; ++j) ruled(tid * N + 4 * q + j);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j) m |= (ruled(tid * N + j) ? 1u : 0u) << j;
-      if (tid < N && ruled(C + tid)) m |= 1u << N;
+    for (int q = 0; q < TPT / 4; ++q) {      // 16 bytes at once
+      const uint4 w = reinterpret_cast<const uint4*>(sm.word)[tid * (TPT / 4) + q];
+      const uint4 e = reinterpret_cast<const uint4*>(sm.entry)[tid * (TPT / 4) + q];
+      m |= ((w.x | e.x ? 1u : 0u) | (w.y | e.y ? 2u : 0u) | (w.z | e.z ? 4u : 0u) | (w.w | e.w ? 8u : 0u)) << (4 * q);
+      if (e.x | e.y | e.z | e.w)
+        for (int j = 0; j < 4; ++j) ruled(tid * TPT + 4 * q + j);
     }
-    plain = EVEN && p.in_place && m == 0;
+    if (!EVEN && tid < N && ruled(C + tid)) m |= 1u << TPT;
+    if (EVEN && p.in_place)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        uint32_t any_rule = 0;
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const int i = (tid + j * kVecs) * N + q;
+          any_rule |= sm.word[i] | sm.entry[i];   // (an entry turned into a value of 0 changes nothing)
+        }
+        plain |= any_rule ? 0u : 1u << j;
+      }
     int before = __popc(m);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -357,7 +374,7 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
     at = __shfl_sync(0xffffffffu, at, 31) + before - __popc(m);
     for (; m; m &= m - 1) {
       const int j = __ffs(m) - 1;
-      sm.list[at++] = (uint16_t)(j < N ? tid * N + j : C + tid);
+      sm.list[at++] = (uint16_t)(j < TPT ? tid * TPT + j : C + tid);
     }
   }
   __syncthreads();
@@ -366,17 +383,17 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
   // pairs (row, list entry) kVecs apart
   const int dr = n ? kVecs / n : 0, di = n ? kVecs % n : 0;
   const int r_first = n ? tid / n : 0, k_first = n ? tid % n : 0;
-  for (int g = 0; g * U <= nd; ++g) {
+  for (int g = 0; g * UR <= nd; ++g) {
     cp_async_wait_one();                     // group g is here (group g + 1 may be on its way)
     __syncthreads();
     if (n) {
-      const int rows = min(U, nd + 1 - g * U);
+      const int rows = min(UR, nd + 1 - g * UR);
       for (int u = r_first, k = k_first; u < rows;) {
-        const int i = sm.list[k], r = g * U + u;
+        const int i = sm.list[k], r = g * UR + u;
         // the token's place among the chunk's vectors; the tail of a row is in none
         const int off = i - head(r);
         if (EVEN || (vec && off >= 0 && off < C && c0 + i - off % N + N <= p.V)) {
-          T* z = reinterpret_cast<T*>(sm.stage[g % kStages][u]) + off;
+          T* z = reinterpret_cast<T*>(sm.stage[g % kStages][u * VPT]) + off;
           *z = from_f32<T>(apply(to_f32(*z), i, r));
         }
         u += dr;
@@ -390,14 +407,14 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = g * U + u;
+      const int r = row_of(g, u);
       const uint32_t ok = (ok_now >> (8 * u)) & 0xffu;
-      if (!has_vec(r) || (plain && ok == kAll)) continue;
+      if (!has_vec(r, u) || ((plain >> (u % VPT) & 1) && ok == kAll)) continue;
       uint4 x = sm.stage[g % kStages][u][tid];
       if (m0) forbid16<T>(x, ok);
-      *reinterpret_cast<uint4*>(o0 + at_vec(r)) = x;
+      *reinterpret_cast<uint4*>(o0 + at_vec(r, u)) = x;
     }
-    for (int u = 0; u < U && g * U + u <= nd; ++u) scalars(g * U + u);
+    for (int r = g * UR; r < (g + 1) * UR && r <= nd; ++r) scalars(r);
     ok_now = ok_next;
     ok_next = fetch(g + 2, words);
     read_mask(g + 3, words);
