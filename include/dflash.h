@@ -10,6 +10,9 @@
  *   dflash_verify_greedy       the greedy accept rule over the vocabulary
  *   dflash_verify_sample       the min(1, p/q) accept rule with residual resample
  *   dflash_gate                the DLoop block gate c_s >= g
+ * and the operators that a serving program runs around them: rules on the
+ * verify rows' logits, block tables and slot maps of the paged cache, and the
+ * 8-bit quantisation, product and materialisation.
  *
  * Conventions shared by every call:
  *   - Tensor arguments are DEVICE pointers owned by the caller; the library
