@@ -256,6 +256,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
   }
 }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ uint32_t ctarank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -403,7 +409,8 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   const int kb0 = (int)((long)rank * p.groups / S), kb1 = (int)((long)(rank + 1) * p.groups / S);
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  // The producers need the barriers alone: their first loads go out while TMEM is allocated.
+  if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], TMA_WARPS);
       mbar_init(&empty[s], C::PARTS);
@@ -416,11 +423,19 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 0) tmem_alloc(tmem_base_sm, 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_base_sm;
+  uint32_t tmem_base = 0;
+  if (warp >= SUM_WARPS + MMA_WARPS) {
+    if (lane == 0) prefetch_tensor_map(warp > SUM_WARPS + MMA_WARPS ? &xmap : &wmap);
+    named_sync(2, 32 * (TMA_WARPS + 1));
+  } else {
+    if (warp == 0) tmem_alloc(tmem_base_sm, 512);
+    __syncwarp();
+    if (warp == 1) named_sync(2, 32 * (TMA_WARPS + 1));
+    tc_fence_before();
+    named_sync(3, 32 * (SUM_WARPS + MMA_WARPS));
+    tc_fence_after();
+    tmem_base = *tmem_base_sm;
+  }
 
   // The issuing warps run converged and let one lane issue: what the TMA and MMA
   // instructions take then sits in uniform registers. Barriers, commits and copies
@@ -560,7 +575,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         else release();
       }
       // a split tile's sums go to the ring, which the other half's MMAs may still read
-      if (C::PARTS > 1 && SPLIT) asm volatile("bar.sync 1, %0;" ::"n"(32 * SUM_WARPS) : "memory");
+      if (C::PARTS > 1 && SPLIT) named_sync(1, 32 * SUM_WARPS);
       if (!ok) break;
       if (!SPLIT) {
         if (live) {
