@@ -633,16 +633,19 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 }
 
 // Tile width and split over K: the pair of least estimated time. A round of
-// clusters takes, in nanoseconds, 320 a group for a narrow tile or 500 for a wide
-// one, over the split, and 3000 for its start and end (4500 with the sum over the
-// cluster); a GB300 holds 152, 76, 36 and 15 clusters of 1, 2, 4 and 8 CTAs, one an
-// SM, at once. Measured (narrow against wide, us): 10 x 20480 x 4096 59.6 / 33.4 /
-// 21.2 / 38.9 in 1 / 2 / 4 / 8 parts against 82.7 / 46.1 / 27.9 / 38.1; 271 x 20480
-// x 4096 68.5 / 71.1 / 66.7 / 104.6 against 89.5 / 52.3 / 59.7 / 83.7; 271 x 4096 x
-// 10240 32.9 against 26.3 whole; 16 x 512 x 512 6.1 whole, 7.2 in two.
+// clusters takes, in nanoseconds, 390 a group for a narrow tile or 600 for a wide
+// one, over the split, and for its start and end 5500 or 7500 whole, 8000 or 10500
+// with the sum over the cluster; a GB300 holds 152, 76, 36 and 15 clusters of 1, 2,
+// 4 and 8 CTAs, one an SM, at once. The constants are those of least loss over 90
+// measured products of 1 to 2048 rows, 512 to 20480 values and 512 to 32000 columns:
+// the choice is 0.1 % slower than the best of the eight in the mean and 7 % at most.
+// Measured (narrow against wide, us): 10 x 20480 x 4096 61.9 / 30.6 / 20.7 in 1 / 2
+// / 4 parts against 82.3 / 46.1 / 27.7; 10 x 4096 x 10240 15.4 / 22.2 in 1 / 2
+// against 21.5 / 16.3; 271 x 4096 x 10240 32.7 against 24.5 whole.
 struct Fp8Plan { int BN, S; };
 static Fp8Plan fp8_plan(int T, int N, int groups) {
   static const int kSplit[4] = {1, 2, 4, 8}, kResident[4] = {152, 76, 36, 15};
+  static const long kGroup[2] = {390, 600}, kEnds[2][2] = {{5500, 8000}, {7500, 10500}};
   const long mt = (T + f8::BM - 1) / f8::BM;
   Fp8Plan best{128, 1};
   long least = -1;
@@ -651,7 +654,7 @@ static Fp8Plan fp8_plan(int T, int N, int groups) {
       const int S = kSplit[i];
       if (S > groups) break;
       const long rounds = (mt * ((N + BN - 1) / BN) + kResident[i] - 1) / kResident[i];
-      const long ns = rounds * ((BN == 128 ? 320L : 500L) * ((groups + S - 1) / S) + (S == 1 ? 3000 : 4500));
+      const long ns = rounds * (kGroup[BN > 128] * ((groups + S - 1) / S) + kEnds[BN > 128][S > 1]);
       if (least < 0 || ns < least) {
         least = ns;
         best = Fp8Plan{BN, S};

@@ -125,6 +125,12 @@ def test_product_llama8b_fusion_and_projection():
     _check_gemm(271, 10240, 4096, "f32", seed=2)
 
 
+@pytest.mark.parametrize("T,N,K", [(290, 4000, 8016), (300, 2500, 12048),     # wide tiles, split over K
+                                   (20000, 100, 144)])                        # several narrow tiles a CTA
+def test_product_other_tilings(T, N, K):
+    _check_gemm(T, N, K, "bf16" if T < 300 else "f32", seed=T)
+
+
 def test_product_of_a_prefill_on_picked_rows():
     # persistent CTAs over several waves of wide tiles
     T, N, K = 8190, 4096, 1024
