@@ -175,9 +175,16 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent) {
 // (distributed shared memory: no workspace, no atomics, the same bits each
 // time). Many tiles go round persistent CTAs, one per SM.
 //
-// Warps 0 - 15 sum, 16 and 17 issue the MMAs, 18 and 19 the TMA loads. Every wait is
-// bounded as in the bf16 GEMM: one that gives up records a code, the CTA drains
-// its copies and MMAs, frees its TMEM and returns.
+// Warps 0 - 15 sum, 16 and 17 issue the MMAs, 18 the TMA loads, and 19 brings the
+// scales. Every wait is bounded as in the bf16 GEMM: one that gives up records a code,
+// the CTA drains its copies and MMAs, frees its TMEM and returns.
+//
+// Shared memory begins at a constant address (aligned by its declaration, not by
+// code), so that barriers and slots need no registers: 8 % at large sizes, where 64
+// sums and 16 values on their way leave a thread little else. A group takes 240 ns
+// (narrow) or 425 (wide); the MMAs alone, 195 and 335. Measured, bf16: 10 x 20480 x
+// 4096 20 us (84 MB at 4.2 TB/s with the launch), 271 x 4096 x 10240 (fp32) 25, 8190 x
+// 20480 x 4096 525 to 540 (2.6 PFLOP/s).
 // ---------------------------------------------------------------------------
 namespace f8 {
 constexpr int BM = 128;
@@ -187,11 +194,11 @@ constexpr int SUM_WARPS = 16;
 constexpr int MMA_WARPS = 2, TMA_WARPS = 2;
 constexpr int THREADS = 32 * (SUM_WARPS + MMA_WARPS + TMA_WARPS);
 constexpr int BUFS = 4, BUF_N = 128;      // TMEM accumulators of 128 columns
-// Scales of the last groups, written by the rows' producer: 128 of x, then the
-// weight blocks'. It writes a group's when its stage is free, STAGES groups ahead
-// of the MMAs, which in turn run up to BUFS groups ahead of the sums.
+// Scales of the last groups, 128 of x, then the weight blocks'. They are written four
+// groups at once when the first one's stage is free, up to STAGES + 3 groups ahead of
+// the MMAs, which in turn run up to BUFS groups ahead of the sums.
 constexpr int SCALE_SLOTS = 16, SCALE_LD = BM + 4;
-constexpr int SMEM_BYTES = RING_BYTES + 4 * SCALE_SLOTS * SCALE_LD + 1024 + 512;
+constexpr int SMEM_BYTES = RING_BYTES + 4 * SCALE_SLOTS * SCALE_LD + 512;
 
 template <int BN> struct Cfg {
   static constexpr int STAGE = A_BYTES + BN * G;
@@ -199,7 +206,7 @@ template <int BN> struct Cfg {
   static constexpr int PARTS = BN / BUF_N;   // accumulators that a k-block fills
   static constexpr int COLS = BN / 4;     // a summing thread's columns
   static constexpr int RED_LD = BN + 4;   // floats: a quarter warp's rows fall on distinct banks
-  static_assert(STAGES + BUFS < SCALE_SLOTS, "scale slots");
+  static_assert(STAGES + BUFS + 3 < SCALE_SLOTS, "scale slots");
   static constexpr int LD = PARTS > 1 ? 16 : 32;   // TMEM columns of a load: with 64 sums a thread has registers for 16
 };
 
@@ -306,24 +313,31 @@ __device__ __forceinline__ float4 scale4(const float* scale, int row, int rows, 
                      kb + 3 < groups ? __ldg(s + 3) : 0.f);
 }
 __device__ __forceinline__ float of4(const float4& v, int i) { return i < 2 ? (i == 0 ? v.x : v.y) : (i == 2 ? v.z : v.w); }
-// A 32-byte sector of a row: 8 fp32 or 16 bf16 outputs from column n on, all inside it.
+// acc + bias for four columns from n on (8 or 16 aligned bytes, the same for all lanes).
 template <typename O>
-__device__ __forceinline__ void store_sector(O* dst, const uint64_t* acc, const O* bias, int n) {
+__device__ __forceinline__ void add_bias4(uint64_t* acc, const O* bias, int n) {
+  float b[4];
+  if constexpr (sizeof(O) == 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(bias + n));
+    b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(bias + n));
+    b[0] = __uint_as_float(v.x << 16); b[1] = __uint_as_float(v.x & 0xffff0000u);
+    b[2] = __uint_as_float(v.y << 16); b[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+  const float4 s = four(acc[0], acc[1]);
+  acc[0] = pair(s.x + b[0], s.y + b[1]);
+  acc[1] = pair(s.z + b[2], s.w + b[3]);
+}
+// A 32-byte sector of a row: 8 fp32 or 16 bf16 outputs.
+template <typename O>
+__device__ __forceinline__ void store_sector(O* dst, const uint64_t* acc) {
   constexpr int V = 32 / sizeof(O);
   float f[V];
 #pragma unroll
   for (int j = 0; j < V; j += 4) {
     const float4 v = four(acc[j / 2], acc[j / 2 + 1]);
     f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
-  }
-  if (bias) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {          // the sector's bias: two 16-byte loads, the same for all lanes
-      float b[V / 2];
-      unpack16<O>(__ldg(reinterpret_cast<const uint4*>(bias + n) + h), b);
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) f[h * (V / 2) + j] += b[j];
-    }
   }
   uint32_t w[8];
   if constexpr (sizeof(O) == 4) {
@@ -388,8 +402,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   using C = Cfg<BN>;
   wait_for_prior_grid();   // as a dependent launch: the rows come from the kernel before
   dependents_may_launch();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   float* scales = reinterpret_cast<float*>(smem + RING_BYTES);       // [SCALE_SLOTS][SCALE_LD]
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + SCALE_SLOTS * SCALE_LD);   // [STAGES]
   uint64_t* empty = full + C::STAGES;
@@ -438,50 +451,57 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   }
 
   // The issuing warps run converged and let one lane issue: what the TMA and MMA
-  // instructions take then sits in uniform registers. Barriers, commits and copies
-  // cost an issuer some 400 cycles of latency a round all the same, as much as
-  // the tensor core needs for an accumulator, so there are two of each kind.
+  // instructions take then sits in uniform registers. Barriers and commits cost an
+  // MMA issuer some 400 cycles of latency a round all the same, as much as the tensor
+  // core needs for an accumulator, so there are two. The scales have a warp of their
+  // own: beside the rows' copies they held narrow tiles at 345 ns a group, not 240.
   if (warp >= SUM_WARPS + MMA_WARPS) {
-    // ------------------------------ TMA producers: weights, rows ------------------------------
-    const bool leader = elect_one(), rows = warp > SUM_WARPS + MMA_WARPS;
+    // ------------------------------ producers: operands (TMA), scales ------------------------------
+    const bool leader = elect_one(), operands = warp == SUM_WARPS + MMA_WARPS;
     int stage = 0;
     int issued = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const uint32_t bytes = (uint32_t)(rows ? p.box_m * G : BN * G);
+    const uint32_t bytes = (uint32_t)((p.box_m + BN) * G);
     const uint64_t once = l2_policy_evict_first();
-    const bool stream_w = !rows && T <= BM;   // each weight is read by one tile alone
-    // The rows' producer also brings the scales: four groups of its rows at a time
-    // (16 bytes a row; one group at a time, by every summing warp, cost the L1 32
-    // lines a warp and group and took longer than the MMAs), read four groups ahead.
-    float4 cur[5], nxt[5];                  // rows lane + 32 i; weight block `lane` of the tile
+    const bool stream_w = T <= BM;          // each weight is read by one tile alone
+    // Scales come four groups at a time (16 bytes a row; one group at a time, by every
+    // summing warp, cost the L1 32 lines a warp and group and took longer than the
+    // MMAs), read four groups ahead.
+    float4 cur[5];                          // rows lane + 32 i; weight block `lane` of the tile
     for (int tile = first; ok && tile < tiles; tile += step) {
-      const int y = rows ? tile / nt * BM : tile % nt * BN;
+      const int m0 = tile / nt * BM, n0 = tile % nt * BN;
       auto fetch = [&](int kb) {            // groups kb .. kb + 3 (kb a multiple of 4)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) nxt[i] = scale4(p.xs, y + 32 * i + lane, T, kb, p.groups, p.vec_xs);
-        nxt[4] = scale4(p.ws, lane < C::PARTS ? tile % nt * C::PARTS + lane : p.wblocks, p.wblocks, kb, p.groups, p.vec_ws);
+        for (int i = 0; i < 4; ++i) cur[i] = scale4(p.xs, m0 + 32 * i + lane, T, kb, p.groups, p.vec_xs);
+        cur[4] = scale4(p.ws, lane < C::PARTS ? tile % nt * C::PARTS + lane : p.wblocks, p.wblocks, kb, p.groups, p.vec_ws);
       };
-      if (rows) fetch(kb0 & ~3);
+      if (!operands) fetch(kb0 & ~3);
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (rows && (kb == kb0 || kb % 4 == 0)) {
-#pragma unroll
-          for (int i = 0; i < 5; ++i) cur[i] = nxt[i];
-          fetch((kb & ~3) + 4);
-        }
         if (!warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.err, 21, p.wait_ns)) { ok = false; break; }
-        if (rows) {
-          float* sc = scales + issued % SCALE_SLOTS * SCALE_LD;
+        if (operands) {
+          uint8_t* dst = smem + stage * C::STAGE;
+          if (leader) {
+            mbar_arrive_expect_tx(&full[stage], bytes);
+            if (stream_w) tma_load_2d_hint(dst + A_BYTES, &wmap, &full[stage], kb * G, n0, once);
+            else tma_load_2d(dst + A_BYTES, &wmap, &full[stage], kb * G, n0);
+            tma_load_2d(dst, &xmap, &full[stage], kb * G, m0);
+          }
+        } else {
+          if (kb == kb0 || kb % 4 == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[32 * i + lane] = of4(cur[i], kb % 4);
-          if (lane < C::PARTS) sc[BM + lane] = of4(cur[4], kb % 4);
-          __syncwarp();
-        }
-        uint8_t* dst = smem + stage * C::STAGE + (rows ? 0 : A_BYTES);
-        if (leader) {
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          if (stream_w) tma_load_2d_hint(dst, &wmap, &full[stage], kb * G, y, once);
-          else tma_load_2d(dst, rows ? &xmap : &wmap, &full[stage], kb * G, y);
+            for (int j = 0; j < 4; ++j) {     // group kb - kb % 4 + j
+              const int ahead = j - kb % 4;
+              if (ahead < 0 || kb + ahead >= kb1) continue;
+              float* sc = scales + (issued + ahead) % SCALE_SLOTS * SCALE_LD;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[32 * i + lane] = of4(cur[i], j);
+              if (lane < C::PARTS) sc[BM + lane] = of4(cur[4], j);
+            }
+            __syncwarp();
+            fetch((kb & ~3) + 4);
+          }
+          if (leader) mbar_arrive(&full[stage]);
         }
         ++issued;
         if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
@@ -489,9 +509,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
     // After an abort copies may still be in flight: wait for the last one of every
     // stage (bounded) so that none lands after the CTA has exited. A stage that the
-    // other producer left unissued never completes, and when that wait has run out
+    // scales' warp has not arrived on never completes, and when that wait has run out
     // all copies have landed.
-    if (lane == 0 && *abort_flag)
+    if (operands && lane == 0 && *abort_flag)
       for (int i = max(0, issued - C::STAGES); i < issued; ++i)
         if (!mbar_wait_bounded(&full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.err, 26)) break;
     __syncwarp();
@@ -537,10 +557,8 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     int u = part / PER;                               // this thread's accumulators: every PARTS-th
     bool ok = true;
     for (int tile = first; ok && tile < tiles; tile += step) {
-      const int m0 = tile / nt * BM + quarter * 32, n0 = tile % nt * BN + part * C::COLS;
-      const int row = m0 + lane;
-      const bool live = row < T && n0 < p.N;
-      const bool warp_live = m0 < T && n0 < p.N;      // some lane's sums are wanted
+      // some lane's sums are wanted
+      const bool warp_live = tile / nt * BM + quarter * 32 < T && tile % nt * BN + part * C::COLS < p.N;
       uint64_t acc[C::COLS / 2];                      // pairs of fp32 sums
 #pragma unroll
       for (int c = 0; c < C::COLS / 2; ++c) acc[c] = 0;
@@ -577,13 +595,20 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
       // a split tile's sums go to the ring, which the other half's MMAs may still read
       if (C::PARTS > 1 && SPLIT) named_sync(1, 32 * SUM_WARPS);
       if (!ok) break;
+      int done = tile;                                // (opaque: the place of the tile is found anew,
+      asm volatile("" : "+r"(done));                  //  not held in registers through the loop)
+      const int row = done / nt * BM + quarter * 32 + lane, n0 = done % nt * BN + part * C::COLS;
       if (!SPLIT) {
-        if (live) {
+        if (row < T && n0 < p.N) {
           O* o = (O*)p.out + (size_t)row * p.N;
           constexpr int V = 32 / sizeof(O);           // a whole 32-byte sector a store
           if (p.vec32 && n0 + C::COLS <= p.N) {
+            if (p.bias) {
 #pragma unroll
-            for (int c = 0; c < C::COLS; c += V) store_sector<O>(o + n0 + c, acc + c / 2, (const O*)p.bias, n0 + c);
+              for (int c = 0; c < C::COLS; c += 4) add_bias4<O>(acc + c / 2, (const O*)p.bias, n0 + c);
+            }
+#pragma unroll
+            for (int c = 0; c < C::COLS; c += V) store_sector<O>(o + n0 + c, acc + c / 2);
           } else {
 #pragma unroll
             for (int c = 0; c < C::COLS; c += 4)
@@ -619,10 +644,8 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
     cluster_sync();                       // no CTA leaves while a peer reads its sums
   }
-  // After an abort, MMAs and copies may still be in flight: wait for the last copy
-  // of every stage and for the MMAs (bounded) so that none lands after this CTA has
-  // exited or its TMEM has been freed.
-  // every accumulator has been read; the MMAs end (bounded) before TMEM is freed
+  // every accumulator has been read, or the CTA has given up: the MMAs end (bounded)
+  // before TMEM is freed
   __syncthreads();
   if (warp == 0) {
     if (lane == 0) mbar_wait_bounded(mma_done, 0, p.err, 24);
@@ -633,19 +656,18 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 }
 
 // Tile width and split over K: the pair of least estimated time. A round of
-// clusters takes, in nanoseconds, 390 a group for a narrow tile or 600 for a wide
-// one, over the split, and for its start and end 5500 or 7500 whole, 8000 or 10500
+// clusters takes, in nanoseconds, 280 a group for a narrow tile or 470 for a wide
+// one, over the split, and for its start and end 5000 or 10500 whole, 6500 or 10000
 // with the sum over the cluster; a GB300 holds 152, 76, 36 and 15 clusters of 1, 2,
 // 4 and 8 CTAs, one an SM, at once. The constants are those of least loss over 90
 // measured products of 1 to 2048 rows, 512 to 20480 values and 512 to 32000 columns:
-// the choice is 0.1 % slower than the best of the eight in the mean and 7 % at most.
-// Measured (narrow against wide, us): 10 x 20480 x 4096 61.9 / 30.6 / 20.7 in 1 / 2
-// / 4 parts against 82.3 / 46.1 / 27.7; 10 x 4096 x 10240 15.4 / 22.2 in 1 / 2
-// against 21.5 / 16.3; 271 x 4096 x 10240 32.7 against 24.5 whole.
+// the choice is 0.3 % slower than the best of the eight in the mean and 7 % at most.
+// Measured (narrow against wide, us): 8190 x 20480 x 4096 615 against 531 whole, 400
+// x 4096 x 10240 33 against 40; 10 x 4096 x 10240 13.4 whole, 15.5 wide in two parts.
 struct Fp8Plan { int BN, S; };
 static Fp8Plan fp8_plan(int T, int N, int groups) {
   static const int kSplit[4] = {1, 2, 4, 8}, kResident[4] = {152, 76, 36, 15};
-  static const long kGroup[2] = {390, 600}, kEnds[2][2] = {{5500, 8000}, {7500, 10500}};
+  static const long kGroup[2] = {280, 470}, kEnds[2][2] = {{5000, 6500}, {10500, 10000}};
   const long mt = (T + f8::BM - 1) / f8::BM;
   Fp8Plan best{128, 1};
   long least = -1;

@@ -125,10 +125,12 @@ def test_product_llama8b_fusion_and_projection():
     _check_gemm(271, 10240, 4096, "f32", seed=2)
 
 
-@pytest.mark.parametrize("T,N,K", [(290, 4000, 8016), (300, 2500, 12048),     # wide tiles, split over K
+@pytest.mark.parametrize("T,N,K", [(290, 4000, 8016), (300, 2500, 12048),
+                                   (1500, 2600, 4112), (271, 3900, 20496),    # wide tiles, whole and split over K
                                    (20000, 100, 144)])                        # several narrow tiles a CTA
-def test_product_other_tilings(T, N, K):
-    _check_gemm(T, N, K, "bf16" if T < 300 else "f32", seed=T)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_product_other_tilings(T, N, K, dtype):
+    _check_gemm(T, N, K, dtype, seed=T, bias=dtype == "bf16")
 
 
 def test_product_of_a_prefill_on_picked_rows():
