@@ -7,7 +7,9 @@
 // the sequences itself (a few KB of lengths, from L2), which costs less than a
 // second launch or a wait between CTAs; the pages and rows are then divided
 // among the CTAs. Bound: the launch and two dependent loads for a decode
-// round, the bytes written for a prefill's slot map.
+// round, the bytes written for a prefill's slot map. Measured: resize of 64
+// sequences 3.6 us, of 1024 with a quarter admitted whole 7.9; slot map of 64 x 16
+// rows 5 us, of 512 prompts (4.2 million rows, 67 MB stored) 14.3.
 #include <algorithm>
 
 #include "common.cuh"
