@@ -220,7 +220,7 @@ slot_map_kernel(const SlotArgs a) {
     if (t0 < T) {
       while (s_cu[b + 1] <= (int)t0) ++b;    // past the sequences that end before; t0 < T ends it
       const int q = (int)((unsigned)s_off[b] + (unsigned)t0), lp = q / a.page_size, in_page = q - lp * a.page_size;
-      if (q >= 0 && (int)t0 + U <= s_cu[b + 1] && U <= a.page_size) {
+      if ((unsigned)q <= (unsigned)(INT32_MAX - U) && (int)t0 + U <= s_cu[b + 1] && U <= a.page_size) {
         // the usual case: all U rows in one sequence, so in one page or two
         const long long base = page_slot(q, lp);
         const long long next = in_page + U > a.page_size ? page_slot(q, lp + 1) : -1;

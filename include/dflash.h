@@ -675,8 +675,8 @@ int dflash_pages_resize(const dflash_pages_dims* dims, const int32_t* length, in
  *   row_seq, positions [rows_max] int32   sequence and position of each row
  *   slots [rows_max] int64   page_table[b][p / page_size] * page_size +
  *                            p % page_size, or -1 if position p has no page
- *                            (negative, past max_pages, or an entry outside
- *                            [0, num_pages))
+ *                            (negative, past max_pages or 2^31 - 1, or an
+ *                            entry outside [0, num_pages))
  * and -1 in all three for the rows T .. rows_max - 1, so that a captured graph
  * of rows_max rows writes nothing for them. rows_max in [1, 2^30]; negative
  * n_rows count as 0. No workspace.

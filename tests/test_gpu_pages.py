@@ -169,6 +169,19 @@ def test_round_of_pages_slots_and_materialisation():
     assert int(r2["n_free"]) == num - sum(r2["n_pages"].tolist())
 
 
+def test_slots_end_where_positions_end():
+    # pages that reach past the last int32 position: the rows behind it have no slot
+    page, last = 1 << 20, 2 ** 31 - 1
+    table = torch.full((2, 2050), -1, dtype=torch.int32, device=DEV)
+    table[1, 2047:2049] = torch.tensor([1, 0], dtype=torch.int32)
+    start = torch.tensor([0, last - 5], dtype=torch.int32, device=DEV)
+    n_rows = torch.tensor([0, 10], dtype=torch.int32, device=DEV)
+    sm = api.slot_map(start, n_rows, table, page, 2, 12)
+    assert sm["slots"].tolist() == [page + page - 6 + i for i in range(6)] + [-1] * 6
+    assert sm["positions"].tolist()[:6] == list(range(last - 5, last + 1))
+    assert sm["row_seq"].tolist() == [1] * 10 + [-1] * 2
+
+
 def test_graph_replay():
     g, table, have, free, n_free = _state(16, 8, 40, 5)
     length = g.integers(0, 8 * 16 + 1, 16).astype(np.int32)
