@@ -174,6 +174,22 @@ def test_product_into_an_odd_view_and_no_rows():
     assert none.shape == (0, 131) and api.last_launch_count() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(130, 256, 272), (1500, 2608, 4112)])     # narrow and wide tiles
+def test_product_alignments_of_out_and_bias(T, N, K, dtype):
+    x, xs, w, ws, b = _operands(T, N, K, 11, dtype)
+    ref = api.fp8_gemm(x, xs, w, ws, bias=b, out_dtype=DT[dtype])
+    el = ref.element_size()
+    for skip_out, skip_bias in ((0, 1), (16 // el, 0), (8 // el, 3)):    # elements past a 256-byte boundary
+        buf = torch.full((T * N + 32,), 7.0, dtype=DT[dtype], device=DEV)
+        bias = torch.zeros(N + 8, dtype=DT[dtype], device=DEV)
+        bias[skip_bias:skip_bias + N] = b
+        out = buf[skip_out:skip_out + T * N].view(T, N)
+        api.fp8_gemm(x, xs, w, ws, bias=bias[skip_bias:skip_bias + N], out=out)
+        assert torch.equal(out, ref)
+        assert bool((buf[:skip_out] == 7.0).all()) and bool((buf[skip_out + T * N:] == 7.0).all())
+
+
 def test_product_keeps_nan_and_infinity_to_their_rows():
     T, N, K = 6, 70, 256
     x, xs, w, ws, _ = _operands(T, N, K, 7)
