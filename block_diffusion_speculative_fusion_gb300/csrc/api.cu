@@ -692,7 +692,7 @@ int dflash_fp8_quant(const dflash_fp8_quant_dims* d, const void* x, void* q, flo
   a.T = d->T; a.K = d->K; a.dtype = d->dtype; a.block_rows = d->block_rows;
   a.x = x; a.q = q; a.scale = scale;
   a.stream = (cudaStream_t)stream;
-  cudaError_t e = dflash::launch_fp8_quant(a, false);
+  cudaError_t e = dflash::launch_fp8_quant(a);
   if (e != cudaSuccess) return cuda_fail(e, "fp8_quant launch");
   return ok(1);
 }
@@ -729,7 +729,7 @@ int dflash_fp8_gemm(const dflash_fp8_gemm_dims* d, const void* x, const float* x
   a.x = x; a.x_scale = x_scale; a.w = w; a.w_scale = w_scale; a.bias = bias; a.out = out;
   a.err = (int*)workspace + kMaxCounters;
   a.stream = (cudaStream_t)stream;
-  cudaError_t e = dflash::launch_fp8_gemm(a, false);
+  cudaError_t e = dflash::launch_fp8_gemm(a);
   if (e != cudaSuccess) return cuda_fail(e, "fp8_gemm launch");
   return ok(1);
 }

@@ -56,6 +56,15 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   return r;
 }
 
+// The same for a kernel whose input earlier work may still write when it is launched
+// (a dependent launch), or that writes where it reads: no read-only path.
+__device__ __forceinline__ uint4 ld_once16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void unpack16(const uint4& u, float* f);
 template <>

@@ -30,7 +30,7 @@ constexpr float kMinScale = 1.17549435e-38f;
 // Quantisation. Bound: one read and one write. A warp takes whole groups (16
 // bytes a lane: two bf16 groups or one fp32 group at once), four at a time, and
 // finds the largest magnitude by shuffles. Measured: 8190 x 20480 bf16 86 us (508
-// MB, 0.87 of the copy bandwidth), 10 x 20480 2 us.
+// MB, 0.87 of the copy bandwidth), 10 x 20480 1.6 us.
 // ---------------------------------------------------------------------------
 template <typename T> constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
 // NaN is passed over here and kept by the conversion.
@@ -64,9 +64,8 @@ template <typename T> struct QuantUnit {
 
 template <typename T>
 __global__ void __launch_bounds__(256, 6)
-f8_quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale, int T_rows,
-                     const int32_t* __restrict__ T_dev, int K) {
-  wait_for_prior_grid();   // in the materialisation's chain the rows come from the kernel before
+f8_quant_rows_kernel(const T* x, uint8_t* q, float* scale, int T_rows, const int32_t* T_dev, int K) {
+  wait_for_prior_grid();   // a dependent launch: the rows may come from the kernel before
   dependents_may_launch();
   constexpr int N = VecTraits<T>::N;
   constexpr int LPG = f8::G / N;           // lanes of a group
@@ -85,7 +84,7 @@ f8_quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * 32 * N;       // K is a multiple of 16: a vector is inside or outside
-      v[u] = k < K ? ld_stream16(src + k) : make_uint4(0, 0, 0, 0);
+      v[u] = k < K ? ld_once16(src + k) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -106,7 +105,9 @@ f8_quant_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __
 // the search for the largest magnitude and the conversion.
 template <typename T>
 __global__ void __launch_bounds__(256)
-f8_quant_blocks_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale, int T_rows, int K) {
+f8_quant_blocks_kernel(const T* x, uint8_t* q, float* scale, int T_rows, int K) {
+  wait_for_prior_grid();   // a dependent launch
+  dependents_may_launch();
   constexpr int N = VecTraits<T>::N;
   constexpr int LPG = f8::G / N, RPL = 32 / LPG;   // rows of a warp's load
   constexpr int L = 16 / RPL;
@@ -119,7 +120,7 @@ f8_quant_blocks_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* 
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int t = t0 + i * RPL;
-    v[i] = t < T_rows && k < K ? ld_stream16(x + (size_t)t * K + k) : make_uint4(0, 0, 0, 0);
+    v[i] = t < T_rows && k < K ? ld_once16(x + (size_t)t * K + k) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < L; ++i) m = fmaxf(m, vec_absmax<T>(v[i]));
@@ -139,25 +140,21 @@ f8_quant_blocks_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* 
 }
 
 template <typename T>
-static cudaError_t launch_f8_quant_t(const Fp8QuantArgs& a, bool dependent) {
-  const int groups = (a.K + f8::G - 1) / f8::G;
+static cudaError_t launch_f8_quant_t(const Fp8QuantArgs& a) {
   if (a.block_rows == f8::G) {
-    const dim3 grid(groups, (a.T + f8::G - 1) / f8::G);
-    f8_quant_blocks_kernel<T><<<grid, 256, 0, a.stream>>>((const T*)a.x, (uint8_t*)a.q, a.scale, a.T, a.K);
-    return cudaGetLastError();
+    const dim3 grid((a.K + f8::G - 1) / f8::G, (a.T + f8::G - 1) / f8::G);
+    return launch_dependent(f8_quant_blocks_kernel<T>, grid, dim3(256), 0, a.stream, (const T*)a.x, (uint8_t*)a.q,
+                            a.scale, a.T, a.K);
   }
   // a warp per unit, up to what six CTAs an SM hold
   const long units = (long)a.T * ((a.K + QuantUnit<T>::VALUES - 1) / QuantUnit<T>::VALUES);
   const int grid = (int)std::max(1L, std::min((units + 7) / 8, 6L * 152));
-  if (dependent)
-    return launch_dependent(f8_quant_rows_kernel<T>, dim3(grid), dim3(256), 0, a.stream, (const T*)a.x, (uint8_t*)a.q,
-                            a.scale, a.T, a.T_dev, a.K);
-  f8_quant_rows_kernel<T><<<grid, 256, 0, a.stream>>>((const T*)a.x, (uint8_t*)a.q, a.scale, a.T, a.T_dev, a.K);
-  return cudaGetLastError();
+  return launch_dependent(f8_quant_rows_kernel<T>, dim3(grid), dim3(256), 0, a.stream, (const T*)a.x, (uint8_t*)a.q,
+                          a.scale, a.T, a.T_dev, a.K);
 }
 
-cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent) {
-  return a.dtype == 0 ? launch_f8_quant_t<float>(a, dependent) : launch_f8_quant_t<bf16>(a, dependent);
+cudaError_t launch_fp8_quant(const Fp8QuantArgs& a) {
+  return a.dtype == 0 ? launch_f8_quant_t<float>(a) : launch_f8_quant_t<bf16>(a);
 }
 
 // ---------------------------------------------------------------------------
@@ -184,7 +181,7 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent) {
 // code), so that barriers and slots need no registers: 8 % at large sizes, where 64
 // sums and 16 values on their way leave a thread little else. A group takes 240 ns
 // (narrow) or 425 (wide); the MMAs alone, 195 and 335. Measured, bf16: 10 x 20480 x
-// 4096 20 us (84 MB at 4.2 TB/s with the launch), 271 x 4096 x 10240 (fp32) 25, 8190 x
+// 4096 19 us (84 MB at 4.4 TB/s with the launch), 271 x 4096 x 10240 (fp32) 24, 8190 x
 // 20480 x 4096 525 to 540 (2.6 PFLOP/s).
 // ---------------------------------------------------------------------------
 namespace f8 {
@@ -309,9 +306,8 @@ __device__ __forceinline__ float4 four(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float4 scale4(const float* scale, int row, int rows, int kb, int groups, int vec) {
   if (row >= rows || kb >= groups) return make_float4(0.f, 0.f, 0.f, 0.f);
   const float* s = scale + (size_t)row * groups + kb;
-  if (vec) return __ldg(reinterpret_cast<const float4*>(s));
-  return make_float4(__ldg(s), kb + 1 < groups ? __ldg(s + 1) : 0.f, kb + 2 < groups ? __ldg(s + 2) : 0.f,
-                     kb + 3 < groups ? __ldg(s + 3) : 0.f);
+  if (vec) return *reinterpret_cast<const float4*>(s);
+  return make_float4(s[0], kb + 1 < groups ? s[1] : 0.f, kb + 2 < groups ? s[2] : 0.f, kb + 3 < groups ? s[3] : 0.f);
 }
 __device__ __forceinline__ float of4(const float4& v, int i) { return i < 2 ? (i == 0 ? v.x : v.y) : (i == 2 ? v.z : v.w); }
 // acc + bias for four columns from n on (8 or 16 aligned bytes, the same for all lanes).
@@ -319,10 +315,10 @@ template <typename O>
 __device__ __forceinline__ void add_bias4(uint64_t* acc, const O* bias, int n) {
   float b[4];
   if constexpr (sizeof(O) == 4) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(bias + n));
+    const float4 v = *reinterpret_cast<const float4*>(bias + n);
     b[0] = v.x; b[1] = v.y; b[2] = v.z; b[3] = v.w;
   } else {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(bias + n));
+    const uint2 v = *reinterpret_cast<const uint2*>(bias + n);
     b[0] = __uint_as_float(v.x << 16); b[1] = __uint_as_float(v.x & 0xffff0000u);
     b[2] = __uint_as_float(v.y << 16); b[3] = __uint_as_float(v.y & 0xffff0000u);
   }
@@ -401,8 +397,6 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
                const Fp8GemmParams p) {
   using namespace f8;
   using C = Cfg<BN>;
-  wait_for_prior_grid();   // as a dependent launch: the rows come from the kernel before
-  dependents_may_launch();
   extern __shared__ __align__(1024) uint8_t smem[];
   float* scales = reinterpret_cast<float*>(smem + RING_BYTES);       // [SCALE_SLOTS][SCALE_LD]
   uint64_t* full = reinterpret_cast<uint64_t*>(scales + SCALE_SLOTS * SCALE_LD);   // [STAGES]
@@ -413,17 +407,10 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
 
-  const int T = p.T_dev ? min(*p.T_dev, p.T) : p.T;
-  const int nt = (p.N + BN - 1) / BN;
-  const int tiles = nt * ((T + BM - 1) / BM);
-  const int S = SPLIT ? p.splits : 1;
-  const int rank = SPLIT ? (int)ctarank() : 0;
-  const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
-  if (first >= tiles) return;             // (every CTA of the cluster)
-  const int kb0 = (int)((long)rank * p.groups / S), kb1 = (int)((long)(rank + 1) * p.groups / S);
-
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  // The producers need the barriers alone: their first loads go out while TMEM is allocated.
+  // A dependent launch (10 x 20480 x 4096 called in a row: 19.0 us, not 21.6): what
+  // touches no memory of the caller's goes before the wait.
+  // (TMEM does not: the kernel before may still be about to allocate its own.)
   if (warp == 1 && lane == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], TMA_WARPS);
@@ -436,10 +423,25 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     mbar_init(mma_done, MMA_WARPS);
     *abort_flag = 0;
     fence_barrier_init();
+  } else if (warp >= SUM_WARPS + MMA_WARPS && lane == 0) {
+    prefetch_tensor_map(warp == SUM_WARPS + MMA_WARPS ? &wmap : &xmap);
   }
+  __syncwarp();
+  wait_for_prior_grid();
+  dependents_may_launch();
+
+  const int T = p.T_dev ? min(*p.T_dev, p.T) : p.T;
+  const int nt = (p.N + BN - 1) / BN;
+  const int tiles = nt * ((T + BM - 1) / BM);
+  const int S = SPLIT ? p.splits : 1;
+  const int rank = SPLIT ? (int)ctarank() : 0;
+  const int first = (int)blockIdx.x / S, step = (int)gridDim.x / S;
+  if (first >= tiles) return;             // (every CTA of the cluster)
+  const int kb0 = (int)((long)rank * p.groups / S), kb1 = (int)((long)(rank + 1) * p.groups / S);
+
+  // The producers need the barriers alone: their first loads go out while TMEM is allocated.
   uint32_t tmem_base = 0;
   if (warp >= SUM_WARPS + MMA_WARPS) {
-    if (lane == 0) prefetch_tensor_map(warp > SUM_WARPS + MMA_WARPS ? &xmap : &wmap);
     named_sync(2, 32 * (TMA_WARPS + 1));
   } else {
     if (warp == 0) tmem_alloc(tmem_base_sm, 512);
@@ -687,7 +689,7 @@ static Fp8Plan fp8_plan(int T, int N, int groups) {
 }
 
 template <int BN, typename O, bool SPLIT>
-static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent) {
+static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S) {
   using namespace f8;
   Fp8GemmParams p{};
   p.xs = a.x_scale; p.ws = a.w_scale; p.bias = a.bias; p.out = a.out; p.T_dev = a.T_dev;
@@ -719,36 +721,27 @@ static cudaError_t launch_f8_gemm_t(const Fp8GemmArgs& a, int S, bool dependent)
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = a.stream;
   cudaLaunchAttribute at[2];
-  int n = 0;
-  if (S > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = S;
-    at[n].val.clusterDim.y = 1;
-    at[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  if (dependent) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = S;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = n;
+  cfg.numAttrs = S > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, O, SPLIT>, xmap, wmap, p);
 }
 
 template <typename O>
-static cudaError_t launch_f8_gemm_o(const Fp8GemmArgs& a, bool dependent) {
+static cudaError_t launch_f8_gemm_o(const Fp8GemmArgs& a) {
   const Fp8Plan plan = fp8_plan(a.T, a.N, (a.K + f8::G - 1) / f8::G);
   if (plan.BN == 256)
-    return plan.S > 1 ? launch_f8_gemm_t<256, O, true>(a, plan.S, dependent)
-                      : launch_f8_gemm_t<256, O, false>(a, 1, dependent);
-  return plan.S > 1 ? launch_f8_gemm_t<128, O, true>(a, plan.S, dependent)
-                    : launch_f8_gemm_t<128, O, false>(a, 1, dependent);
+    return plan.S > 1 ? launch_f8_gemm_t<256, O, true>(a, plan.S) : launch_f8_gemm_t<256, O, false>(a, 1);
+  return plan.S > 1 ? launch_f8_gemm_t<128, O, true>(a, plan.S) : launch_f8_gemm_t<128, O, false>(a, 1);
 }
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dependent) {
-  return a.out_dtype == 0 ? launch_f8_gemm_o<float>(a, dependent) : launch_f8_gemm_o<bf16>(a, dependent);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a) {
+  return a.out_dtype == 0 ? launch_f8_gemm_o<float>(a) : launch_f8_gemm_o<bf16>(a);
 }
 
 }  // namespace dflash

@@ -258,7 +258,7 @@ struct Fp8QuantArgs {
   float* scale;                  // [ceil(T / block_rows), ceil(K / 128)]
   cudaStream_t stream;
 };
-cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, bool dependent);
+cudaError_t launch_fp8_quant(const Fp8QuantArgs& a);
 struct Fp8GemmArgs {
   int T, N, K, out_dtype;
   const int32_t* T_dev;          // rows in use (device), or null: all T
@@ -271,7 +271,7 @@ struct Fp8GemmArgs {
   int* err;                      // the workspace's error word
   cudaStream_t stream;
 };
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, bool dependent);
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a);
 
 // ----------------------------------------------------------- materialise ---
 constexpr int kMaxLayers = 16;

@@ -628,7 +628,7 @@ cudaError_t launch_materialize_fp8(const MatArgs& a, const float* W_f_scale, con
     Fp8QuantArgs g{};
     g.T = T_max; g.K = K; g.dtype = 1; g.block_rows = 1; g.T_dev = meta;
     g.x = ws + x; g.q = ws + q; g.scale = (float*)(ws + scale); g.stream = st;
-    return launch_fp8_quant(g, true);
+    return launch_fp8_quant(g);
   };
   auto product = [&](size_t x, size_t xs, const void* w, const float* w_scale, const void* bias, void* out, int N, int K,
                      int out_dtype) {
@@ -636,7 +636,7 @@ cudaError_t launch_materialize_fp8(const MatArgs& a, const float* W_f_scale, con
     g.T = T_max; g.N = N; g.K = K; g.out_dtype = out_dtype; g.T_dev = meta;
     g.x = ws + x; g.x_scale = (const float*)(ws + xs); g.w = w; g.w_scale = w_scale; g.bias = bias; g.out = out;
     g.err = a.err; g.stream = st;
-    return launch_fp8_gemm(g, true);
+    return launch_fp8_gemm(g);
   };
   if ((e = quant(lay.X, lay.Xq, lay.xs, K1)) != cudaSuccess) return e;
   if ((e = product(lay.Xq, lay.xs, a.W_f, W_f_scale, a.b_f, ws + lay.h, a.d, K1, 1)) != cudaSuccess) return e;

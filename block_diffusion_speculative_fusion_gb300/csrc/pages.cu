@@ -6,9 +6,10 @@
 // Both operators are one launch in which every CTA forms the prefix sums over
 // the sequences itself (a few KB of lengths, from L2), which costs less than a
 // second launch or a wait between CTAs; the pages and rows are then divided
-// among the CTAs. Bound: the launch and two dependent loads for a decode
+// among the CTAs. Both are dependent launches, whose start overlaps the end of the
+// kernel before. Bound: the launch and two dependent loads for a decode
 // round, the bytes written for a prefill's slot map. Measured: resize of 64
-// sequences 3.6 us, of 1024 with a quarter admitted whole 7.9; slot map of 64 x 16
+// sequences 3.4 us, of 1024 with a quarter admitted whole 7.8; slot map of 64 x 16
 // rows 5 us, of 512 prompts (4.2 million rows, 67 MB stored) 14.3.
 #include <algorithm>
 
@@ -60,6 +61,8 @@ __device__ __forceinline__ long long block_prefix(long long x, long long* total)
 __global__ void __launch_bounds__(pages::kThreads)
 pages_resize_kernel(const PagesArgs a) {
   using namespace pages;
+  wait_for_prior_grid();
+  dependents_may_launch();
   __shared__ int s_give[kPagesMaxB + 1];    // pages given back before sequence b
   __shared__ int s_want[kPagesMaxB + 1];    // pages asked for before sequence b
   const int tid = threadIdx.x, B = a.B;
@@ -157,8 +160,7 @@ pages_resize_kernel(const PagesArgs a) {
 cudaError_t launch_pages_resize(const PagesArgs& a, int num_sms) {
   const long units = (long)a.B * ((a.max_pages + pages::kSegment - 1) / pages::kSegment);
   const int grid = (int)std::min((long)num_sms, (units + pages::kWarps - 1) / pages::kWarps);
-  pages_resize_kernel<<<grid, pages::kThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(pages_resize_kernel, dim3(grid), dim3(pages::kThreads), 0, a.stream, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -167,6 +169,8 @@ cudaError_t launch_pages_resize(const PagesArgs& a, int num_sms) {
 __global__ void __launch_bounds__(pages::kThreads, 3)
 slot_map_kernel(const SlotArgs a) {
   using namespace pages;
+  wait_for_prior_grid();
+  dependents_may_launch();
   constexpr int U = 4;                       // consecutive rows per thread: 16- and 32-byte stores
   extern __shared__ int slot_smem[];
   int* s_cu = slot_smem;                     // [B + 1] first row of each sequence
@@ -271,8 +275,8 @@ cudaError_t launch_slot_map(const SlotArgs& args, int num_sms) {
   a.vec = al(a.row_seq, 16) && al(a.positions, 16) && al(a.slots, 32);
   const long need = ((long)a.rows_max + 4 * pages::kThreads - 1) / (4 * pages::kThreads);
   const int grid = (int)std::max(1L, std::min((long)num_sms * 3, need));
-  slot_map_kernel<<<grid, pages::kThreads, (2 * (size_t)a.B + 1) * sizeof(int), a.stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(slot_map_kernel, dim3(grid), dim3(pages::kThreads), (2 * (size_t)a.B + 1) * sizeof(int),
+                          a.stream, a);
 }
 
 }  // namespace dflash

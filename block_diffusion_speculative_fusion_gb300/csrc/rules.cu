@@ -96,13 +96,6 @@ struct RulesParams {
   const uint8_t* mask_on;
 };
 
-__device__ __forceinline__ uint4 ld_rows16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
-  return r;
-}
-
 // Element j of a 16-byte vector set to -inf where bit j of `ok` is 0.
 template <typename T> __device__ __forceinline__ void forbid16(uint4& u, uint32_t ok);
 template <> __device__ __forceinline__ void forbid16<float>(uint4& u, uint32_t ok) {
@@ -151,8 +144,10 @@ struct RulesSmem {
 // that every row's vectors start at the chunk's first token.
 template <typename T, bool EVEN>
 __global__ void __launch_bounds__(rules::kVecs, rules::kCtasPerSm)
-rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParams p) {
+rules_kernel(const T* logits, T* out, const RulesParams p) {
   using namespace rules;
+  wait_for_prior_grid();                     // a dependent launch: its start overlaps the kernel before
+  dependents_may_launch();
   constexpr int N = VecTraits<T>::N;
   constexpr int U = kVecsInFlight, VPT = RulesSmem<T>::VPT, UR = RulesSmem<T>::UR;
   constexpr uint32_t kAll = (1u << N) - 1;
@@ -253,7 +248,7 @@ rules_kernel(const T* __restrict__ logits, T* __restrict__ out, const RulesParam
       for (int u = 0; u < U; ++u) {
         const int r = row_of(g, u);
         ok[u] = allowed(ok[u], r, u);
-        if (ok[u] && !(p.in_place && ok[u] == kAll)) x[u] = ld_rows16(z0 + at_vec(r, u));
+        if (ok[u] && !(p.in_place && ok[u] == kAll)) x[u] = ld_once16(z0 + at_vec(r, u));
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -447,13 +442,15 @@ static cudaError_t launch_rules_e(const RulesArgs& a, const RulesParams& p) {
   cfg.blockDim = dim3(rules::kVecs);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = cs;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, rules_kernel<T, EVEN>, (const T*)a.logits, (T*)a.out, p);
 }
 

@@ -196,3 +196,76 @@ def test_rounds_until_the_pool_is_dry():
     assert int(r2["n_pages"][3]) == 0
     live = torch.cat([s.table[b, :int(r2["n_pages"][b])] for b in range(B)] + [s.free[:int(r2["n_free"])]])
     assert sorted(live.tolist()) == list(range(12))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_launches_that_overlap_see_each_others_results(captured):
+    """Every operator's launch may begin while the kernel before it ends: calls
+    in a row that read what the one before wrote, over the same buffers, give
+    what the same calls give one at a time."""
+    B, R, V, T, K, N, page, max_pages = 4, 3, 5000, 40, 1024, 640, 16, 64
+    g = torch.Generator().manual_seed(12)
+    n = 6
+    logits = torch.randn((n, B, R, V), generator=g).to(torch.bfloat16).to(DEV)
+    hist = torch.randint(0, V, (n, B, 300), generator=g).to(DEV)
+    x = torch.randn((n, T, K), generator=g).to(torch.bfloat16).to(DEV)
+    w, ws = api.fp8_quant(torch.randn((N, K), generator=g).to(torch.bfloat16).to(DEV), block_rows=128)
+    length = torch.randint(0, page * max_pages, (n, B), generator=g).to(torch.int32).to(DEV)
+    length[-1] = 0
+    hl = torch.full((B,), 300, dtype=torch.int32, device=DEV)
+    rep = torch.full((B,), 1.5, device=DEV)
+    zero = torch.zeros(B, dtype=torch.int32, device=DEV)
+    buf = dict(z=torch.empty_like(logits[0]), hist=torch.empty_like(hist[0]), x=torch.empty_like(x[0]),
+               q=torch.empty((T, K), dtype=torch.float8_e4m3fn, device=DEV),
+               s=torch.empty((T, K // 128), dtype=torch.float32, device=DEV),
+               y=torch.empty((T, N), dtype=torch.bfloat16, device=DEV),
+               len=torch.empty(B, dtype=torch.int32, device=DEV),
+               table=torch.empty((B, max_pages), dtype=torch.int32, device=DEV),
+               free=torch.empty(B * max_pages, dtype=torch.int32, device=DEV))
+    pages = [{k: torch.zeros(m, dtype=t, device=DEV) for k, m, t in
+              (("n_pages", B, torch.int32), ("n_free", 1, torch.int32), ("short", B, torch.uint8))} for _ in range(2)]
+    y = torch.empty((n, T, N), dtype=torch.bfloat16, device=DEV)
+    z = torch.empty_like(logits)
+    slots = torch.empty((n, B * 8), dtype=torch.int64, device=DEV)
+
+    def run(one_at_a_time):
+        def call(fn, *args, **kw):
+            fn(*args, **kw)
+            if one_at_a_time:
+                torch.cuda.synchronize()
+        call(buf["table"].fill_, -1)
+        call(buf["free"].copy_, torch.arange(B * max_pages, dtype=torch.int32, device=DEV))
+        call(pages[0]["n_pages"].zero_)
+        call(pages[0]["n_free"].fill_, B * max_pages)
+        yq, ys = buf["q"].view(-1)[:T * N].view(T, N), buf["s"].view(-1)[:T * 5].view(T, 5)
+        for i in range(n):
+            call(buf["x"].copy_, x[i])
+            call(api.fp8_quant, buf["x"], q=buf["q"], scale=buf["s"])
+            call(api.fp8_gemm, buf["q"], buf["s"], w, ws, out=buf["y"])
+            call(api.fp8_gemm, buf["q"], buf["s"], w, ws, out=y[i])
+            call(api.fp8_quant, buf["y"], q=yq, scale=ys)
+            old, new = pages[i % 2], pages[1 - i % 2]
+            call(api.pages_resize, length[i], buf["table"], old["n_pages"], buf["free"], old["n_free"], page, out=new)
+            call(api.slot_map, zero, new["n_pages"], buf["table"], page, B * max_pages, B * 8, out=dict(slots=slots[i]))
+            call(buf["hist"].copy_, hist[i])
+            call(buf["z"].copy_, logits[i])
+            call(api.logits_rules, buf["z"], hist=buf["hist"], hist_len=hl, repetition=rep, out=buf["z"])
+            call(api.logits_rules, buf["z"], hist=buf["hist"], hist_len=hl, repetition=rep, out=z[i])
+
+    def result():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (y, z, slots, buf["table"], buf["free"], pages[n % 2]["n_free"])]
+
+    run(True)
+    want = result()
+    assert int(want[-1]) == B * max_pages and bool((want[2][:-1] >= 0).any())
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(False)
+    for _ in range(5):
+        for t in (y, z, slots):
+            t.zero_()
+        graph.replay() if captured else run(False)
+        for a, b in zip(result(), want):
+            assert torch.equal(a, b)
