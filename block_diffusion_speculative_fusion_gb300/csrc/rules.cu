@@ -32,7 +32,7 @@
 //
 // Measured, 64 sequences x 16 rows x 128256 bf16, histories up to 8192, 64 biases,
 // half of the sequences masked: 82 us for 359 MB (0.65 of the copy bandwidth); the
-// masks alone 66 us (0.80). 8 x 10 rows x 100003 fp32: 18 us; one row: 4.4 us.
+// masks alone 66 us (0.80). 8 x 10 rows x 100003 fp32: 14.5 us; one row: 4.3 us.
 #include <cstddef>
 
 #include "common.cuh"
@@ -115,14 +115,6 @@ template <> __device__ __forceinline__ void forbid16<bf16>(uint4& u, uint32_t ok
   }
 }
 
-// n bits (n <= 8) of a bit array at bit `at`; `words` is its length in words.
-__device__ __forceinline__ uint32_t bits_at(const uint32_t* a, int at, int n, int words) {
-  const int w = at >> 5, s = at & 31;
-  uint32_t x = a[w] >> s;
-  if (s + n > 32 && w + 1 < words) x |= a[w + 1] << (32 - s);
-  return x & ((1u << n) - 1);
-}
-
 // Shared memory of a CTA: the stages, then what is known of the tokens.
 template <typename T>
 struct RulesSmem {
@@ -195,44 +187,74 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
     const uint32_t v = sm.entry[i];
     return v ? z + __uint_as_float(v) : z;
   };
-  auto one = [&](int e, int r) {             // a token that no vector holds
-    const size_t at = (size_t)r * p.V + e;
-    const bool good = !m0 || ((m0[(size_t)r * p.W + (e >> 5)] >> (e & 31)) & 1);
+  // a token that no vector holds: its logit if the mask allows it, then what becomes of it
+  auto load_one = [&](int e, int r, bool* good) -> T {
+    *good = !m0 || ((m0[(size_t)r * p.W + (e >> 5)] >> (e & 31)) & 1);
+    return *good ? z0[(size_t)r * p.V + e] : from_f32<T>(-CUDART_INF_F);
+  };
+  auto store_one = [&](int e, int r, T z, bool good) {
     const int i = e - c0;
     const bool ruled = any && (sm.word[i] | sm.entry[i]) != 0;
     if (p.in_place && good && !ruled) return;
-    T v = from_f32<T>(-CUDART_INF_F);
-    if (good) v = ruled ? from_f32<T>(apply(to_f32(z0[at]), i, r)) : z0[at];
-    o0[at] = v;
+    o0[(size_t)r * p.V + e] = good && ruled ? from_f32<T>(apply(to_f32(z), i, r)) : z;
   };
-  // the tokens of a row before its first vector and after its last (EVEN: none),
-  // or all of them where the buffers' vectors do not meet
-  auto scalars = [&](int r) {
+  // The chunk's tokens of row r that no vector holds (EVEN: none): j < N before its
+  // first one, j < 2 N after its last; -1 if there is no such token.
+  auto edge = [&](int r, int j) -> int {
+    const int h = min(head(r), p.V);
+    if (j < N) return c0 == 0 && j < h ? j : -1;
+    const int k = (p.V - h) / N, e = h + k * N + j - N;
+    return k / (kVecs * VPT) == chunk && e < p.V ? e : -1;
+  };
+  // those of all rows from thread place `k` on, or every token where the buffers'
+  // vectors do not meet
+  auto edges = [&](int k) {
     if (EVEN) return;
-    if (!vec) {
-      for (int e = c0 + tid; e < min(p.V, c0 + C); e += kVecs) one(e, r);
-    } else if (tid < N) {
-      const int h = min(head(r), p.V);
-      if (c0 == 0 && tid < h) one(tid, r);
-      const int k = (p.V - h) / N, e = h + k * N + tid;
-      if (k / (kVecs * VPT) == chunk && e < p.V) one(e, r);
+    bool good;
+    if (vec) {
+      for (; k < 2 * N * (nd + 1); k += kVecs) {
+        const int r = k / (2 * N), e = edge(r, k % (2 * N));
+        if (e < 0) continue;
+        const T z = load_one(e, r, &good);
+        store_one(e, r, z, good);
+      }
+    } else {
+      for (int r = 0; r <= nd; ++r)
+#pragma unroll 4
+        for (int e = c0 + tid; e < min(p.V, c0 + C); e += kVecs) {
+          const T z = load_one(e, r, &good);
+          store_one(e, r, z, good);
+        }
     }
   };
   // The thread's U vectors of group g: slot u is vector u % VPT of row g * UR + u / VPT.
   auto row_of = [&](int g, int u) { return g * UR + u / VPT; };
   auto token_of = [&](int r, int u) { return head(r) + c0 + (tid + u % VPT * kVecs) * N; };   // its first
-  // whether row r has slot u's vector, the mask words (byte, if EVEN) that hold its
-  // allowed bits, and the bits: bit j is token j's
   auto has_vec = [&](int r, int u) { return r <= nd && vec && token_of(r, u) + N <= p.V; };
+  // What the thread reads of row r's mask for slot u (one register, so that it can be on
+  // its way for long), and the allowed bits of its vector, bit j for token j. EVEN: the
+  // byte that holds them. Else a lane reads one of the N + 1 words under its warp's
+  // vectors, and all lanes of the warp take part in handing them round (each lane
+  // joining its own two words waited for them a stage early: 8 x 10 rows, 3 us).
+  const int lane = tid & 31;
   auto mask_words = [&](int r, int u) -> uint32_t {
-    if (!m0 || !has_vec(r, u)) return 0xffffffffu;
-    const int e = token_of(r, u);
-    if constexpr (EVEN) return reinterpret_cast<const uint8_t*>(m0 + (size_t)r * p.W)[e / 8];
-    return bits_at(m0 + (size_t)r * p.W, e, N, p.W);
+    if constexpr (EVEN) {
+      if (!m0 || !has_vec(r, u)) return 0xffffffffu;
+      return reinterpret_cast<const uint8_t*>(m0 + (size_t)r * p.W)[token_of(r, u) / 8];
+    } else {
+      if (!m0) return 0xffffffffu;
+      const int w = ((token_of(r, u) - lane * N) >> 5) + lane;
+      return r <= nd && lane <= N && w < p.W ? m0[(size_t)r * p.W + w] : 0u;
+    }
   };
   auto allowed = [&](uint32_t words, int r, int u) -> uint32_t {
-    if (!has_vec(r, u)) return 0;
-    return (EVEN && N < 8 ? words >> (tid * N & 7) : words) & kAll;
+    if constexpr (EVEN) {
+      words = N < 8 ? words >> (tid * N & 7) : words;
+    } else {
+      const int bit = ((token_of(r, u) - lane * N) & 31) + lane * N;
+      words = __funnelshift_r(__shfl_sync(0xffffffffu, words, bit >> 5), __shfl_sync(0xffffffffu, words, (bit >> 5) + 1), bit);
+    }
+    return has_vec(r, u) ? words & kAll : 0u;
   };
   auto at_vec = [&](int r, int u) -> size_t { return (size_t)r * p.V + token_of(r, u); };
 
@@ -257,8 +279,8 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
         if (m0) forbid16<T>(x[u], ok[u]);
         *reinterpret_cast<uint4*>(o0 + at_vec(r, u)) = x[u];
       }
-      for (int r = g * UR; r < (g + 1) * UR && r <= nd; ++r) scalars(r);
     }
+    edges(tid);
     return;
   }
 
@@ -298,6 +320,11 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
     const int64_t t = (p.cand && penal && i >= 1 && i <= nd) ? p.cand[(size_t)b * p.R + i] : -1;
     sm.cand[i] = t >= 0 && t < p.V ? (int32_t)t : -1;
   }
+  // (row by row, a load at a time, the edges of 8 x 10 rows took 2 us longer)
+  const int edge_r = tid / (2 * N), edge_e = !EVEN && vec && edge_r <= nd ? edge(edge_r, tid % (2 * N)) : -1;
+  bool edge_good = false;
+  T edge_z{};
+  if (edge_e >= 0) edge_z = load_one(edge_e, edge_r, &edge_good);
   uint32_t ok_now = fetch(0, words);
   uint32_t ok_next = fetch(1, words1);
   read_mask(2, words);
@@ -339,7 +366,6 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
   {
     constexpr int TPT = C / kVecs;
     static_assert(TPT == 8, "tokens of a thread");
-    const int lane = tid & 31;
     auto ruled = [&](int i) -> bool {
       const uint32_t j = sm.entry[i];
       if (j) sm.entry[i] = __float_as_uint(p.bias_val[(size_t)b * p.nb + j - 1]);
@@ -382,6 +408,8 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
   }
   __syncthreads();
   const int n = sm.n;
+  if (edge_e >= 0) store_one(edge_e, edge_r, edge_z, edge_good);
+  edges(tid + kVecs);
 
   // pairs (row, list entry) kVecs apart
   const int dr = n ? kVecs / n : 0, di = n ? kVecs % n : 0;
@@ -417,7 +445,6 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
       if (m0) forbid16<T>(x, ok);
       *reinterpret_cast<uint4*>(o0 + at_vec(r, u)) = x;
     }
-    for (int r = g * UR; r < (g + 1) * UR && r <= nd; ++r) scalars(r);
     ok_now = ok_next;
     ok_next = fetch(g + 2, words);
     read_mask(g + 3, words);

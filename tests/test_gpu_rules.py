@@ -97,6 +97,20 @@ def test_batches_and_lists(B, R, H, nb, mask):
     _check(s, inplace=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [2051, 4099])
+def test_many_masked_rows_at_any_alignment(V, dtype):
+    # more rows than one pass over their unaligned ends takes
+    s = _case(2, 75, V, dtype, nb=30, seed=V)
+    s["n_draft"][0] = 74
+    s["mask_on"][:] = 1
+    _check(s)
+    _check(s, inplace=True)
+    only_mask = {k: s[k] for k in ("logits", "n_draft", "mask")}
+    _check(only_mask)
+    _check(only_mask, inplace=True)
+
+
 def test_one_token_repeated_everywhere():
     # the history and the candidates are one token: its count passes 4000
     s = _case(2, 6, 300, "f32", H=4096, nb=4, seed=5)
