@@ -475,10 +475,14 @@ sample_stats_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const fl
     SampleJob j;
     j.row = a;
     j.mode = rejected ? 0 : 1;
-    j.mt = rs[a].m;
-    j.st = rs[a].s;
-    j.md = rejected ? rs[R + a].m : 0.f;
-    j.sd = rejected ? rs[R + a].s : 1.f;
+    // a row of -inf alone (a mask that allows no token) has probability 0 everywhere:
+    // offset 0 and sum 1 give its terms 2^-inf, where its own would give NaN
+    const MS law_t = rs[a], law_d = rejected ? rs[R + a] : MS{-CUDART_INF_F, 0.f};
+    const bool no_t = law_t.m == -CUDART_INF_F, no_d = law_d.m == -CUDART_INF_F;
+    j.mt = no_t ? 0.f : law_t.m;
+    j.st = no_t ? 1.f : law_t.s;
+    j.md = no_d ? 0.f : law_d.m;
+    j.sd = no_d ? 1.f : law_d.s;
     j.acc = a;
     j.flags = flags;
     jobs[b] = j;

@@ -75,7 +75,7 @@ enum { DFLASH_F32 = 0, DFLASH_BF16 = 1 };
 enum {
   DFLASH_FLAG_ACCEPT_BOUNDARY = 1,  /* |u - p(x)/q(x)| < 1e-6 at an evaluated test */
   DFLASH_FLAG_CDF_BOUNDARY = 2,     /* u_final within 1e-6 of a CDF step */
-  DFLASH_FLAG_DEGENERATE = 4,       /* zero residual mass; bonus drawn from p */
+  DFLASH_FLAG_DEGENERATE = 4,       /* zero residual mass; bonus drawn from p (if that has mass) */
   DFLASH_FLAG_INVALID = 8           /* q(x) == 0: candidate was not drawn from q */
 };
 
@@ -325,6 +325,9 @@ int dflash_verify_greedy_noalloc(const dflash_verify_dims* dims,
  *   Z = sum_y max(0, p_{i-1}(y) - q_{i-1}(y)) (= 1 - beta); if all n_b are
  *   accepted: bonus ~ p_{n_b}. The draw is the inverse CDF in ascending token
  *   order: the smallest y with C(y) > u_final[b] * Z. If Z == 0 the draw uses p.
+ * A row of -inf alone (a mask that allows no token) has probability 0
+ * everywhere; where the bonus would be drawn from such a target row, it is some
+ * token of [0, V), flagged DFLASH_FLAG_DEGENERATE, and Z = 0.
  *
  * target_logits [B, n_max+1, V]; draft_logits [B, n_max, V] (row i-1 is the law
  *   cand[b, i] was drawn from); cand [B, n_max+1] int64; n_draft [B] or NULL
@@ -333,7 +336,8 @@ int dflash_verify_greedy_noalloc(const dflash_verify_dims* dims,
  * accept_len, commit_len [B] int32; bonus [B] int64; out_tokens [B, n_max+1] int64
  *   or NULL; flags [B] uint8 or NULL (DFLASH_FLAG_* bits)
  * probs [B, 2*n_max + 1] float or NULL: p(x_i) for i = 1..n_max, then q(x_i),
- *   then the mass Z of the distribution the bonus was drawn from (1 for p).
+ *   then the mass Z of the distribution the bonus was drawn from (1 for p, 0 for
+ *   a row of -inf alone).
  *   Entries of draft positions that were not evaluated are 0.
  */
 size_t dflash_verify_sample_workspace_size(const dflash_verify_dims* dims);

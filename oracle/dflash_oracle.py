@@ -220,11 +220,13 @@ def verify_greedy(target_logits, cand, n_draft=None):
 # (c) verify: sampled rule
 # ---------------------------------------------------------------------------
 def softmax(z, temperature=1.0):
-    """softmax(z / T) over the last axis, float64."""
+    """softmax(z / T) over the last axis, float64; a row of -inf alone (a mask
+    that allows no token) has probability 0 everywhere."""
     s = _f64(z) / temperature
-    s = s - s.max(axis=-1, keepdims=True)
-    e = np.exp(s)
-    return e / e.sum(axis=-1, keepdims=True)
+    top = s.max(axis=-1, keepdims=True)
+    empty = np.isneginf(top)
+    e = np.exp(s - np.where(empty, 0.0, top))
+    return e / np.where(empty, 1.0, e.sum(axis=-1, keepdims=True))
 
 
 def inverse_cdf(weights, u):
@@ -307,16 +309,21 @@ def verify_sample(target_logits, draft_logits, cand, n_draft, u_acc, u_final, te
                 dist = resid
         else:
             dist = p[n]
-        y, near = inverse_cdf(dist, float(u_final[b]))
-        if near:
-            flags[b] |= FLAG_CDF_BOUNDARY
+        if dist.sum() > 0.0:
+            y, near = inverse_cdf(dist, float(u_final[b]))
+            if near:
+                flags[b] |= FLAG_CDF_BOUNDARY
+        else:                                  # no token to draw: any of the vocabulary
+            y = V - 1
+            Z = 0.0
+            flags[b] |= FLAG_DEGENERATE
         acc[b] = a
         bonus[b] = y
         out_tokens[b, :a] = cand[b, 1:a + 1]
         out_tokens[b, a] = y
         debug.append({"p_x": np.array(p_x), "q_x": np.array(q_x), "Z": Z,
                       "one_minus_beta": one_minus_beta,
-                      "final_dist": dist / dist.sum()})
+                      "final_dist": dist / dist.sum() if dist.sum() > 0.0 else dist})
     return {"accept_len": acc, "bonus": bonus, "commit_len": acc + 1,
             "out_tokens": out_tokens, "flags": flags, "debug": debug}
 
