@@ -450,9 +450,10 @@ sample_stats_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const fl
     const double qx = zxd == -CUDART_INF_F ? 0.0 : (double)ex2_ftz(ad) * (1.0 + rd * 0.6931471805599453) / (double)pd.s;
     s_px[i - 1] = (float)px;
     s_qx[i - 1] = (float)qx;
-    // q(x) = 0: the candidate was not drawn from q (infinite ratio, flagged)
+    // q(x) = 0: the candidate was not drawn from q (infinite ratio, flagged), but one
+    // that a mask forbids is not accepted for that
     s_inv[i - 1] = qx > 0.0 ? 0 : 1;
-    s_ratio[i - 1] = qx > 0.0 ? px / qx : (double)CUDART_INF_F;
+    s_ratio[i - 1] = qx > 0.0 ? px / qx : zxt == -CUDART_INF_F ? 0.0 : (double)CUDART_INF_F;
   }
   __syncthreads();
   __shared__ int s_a, s_eval;

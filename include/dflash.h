@@ -320,7 +320,9 @@ int dflash_verify_greedy_noalloc(const dflash_verify_dims* dims,
  * Sampled rule, [SpecDec] 3 and 4, [DLoop] looped verify:
  *   p_r = softmax(target_logits[b, r] / T), q_r = softmax(draft_logits[b, r] / T)
  *   for i = 1..n_b: x = cand[b, i]; accept iff u_accept[b, i-1] < p_{i-1}(x) / q_{i-1}(x);
- *   stop at the first rejection (later drafts are discarded).
+ *   stop at the first rejection (later drafts are discarded). q(x) = 0 accepts x
+ *   (DFLASH_FLAG_INVALID), unless its target logit is -inf: a token that a mask
+ *   forbids is rejected whatever q and u.
  *   On a rejection at draft i: bonus ~ max(0, p_{i-1} - q_{i-1}) / Z with
  *   Z = sum_y max(0, p_{i-1}(y) - q_{i-1}(y)) (= 1 - beta); if all n_b are
  *   accepted: bonus ~ p_{n_b}. The draw is the inverse CDF in ascending token

@@ -286,7 +286,7 @@ def verify_sample(target_logits, draft_logits, cand, n_draft, u_acc, u_final, te
             q_x.append(qx)
             if qx == 0.0:
                 flags[b] |= FLAG_INVALID
-                ratio = np.inf
+                ratio = 0.0 if np.isneginf(zt[b, i - 1, x]) else np.inf    # forbidden, or not drawn from q
             else:
                 ratio = px / qx
             if ratio < 1.0 and abs(float(u_acc[b, i - 1]) - ratio) < BOUNDARY_EPS:

@@ -57,3 +57,36 @@ def test_target_row_without_a_token(V, dtype, lse):
     assert all(f & O.FLAG_DEGENERATE for f in ref["flags"].tolist())
     assert not any(f & api.FLAG_INVALID for f in got["flags"].tolist())
     assert all(0 <= y < V for y in got["bonus"].tolist())
+
+
+@pytest.mark.parametrize("lse", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q", ["-inf", "underflows", "row of -inf"])
+def test_forbidden_candidate_is_rejected_where_q_is_zero(q, dtype, lse):
+    """p(x) = 0 by the mask and q(x) = 0: not accepted, whatever u (0 included)."""
+    B, n, V = 4, 2, 1003
+    g = torch.Generator().manual_seed(5)
+    zt = torch.randn((B, n + 1, V), generator=g).to(DT[dtype])
+    zd = torch.randn((B, n, V), generator=g).to(DT[dtype])
+    cand = torch.randint(1, V, (B, n + 1), generator=g)
+    bad = cand[:, 1]                           # forbidden in row 0
+    zt[torch.arange(B), 0, bad] = NEG
+    if q == "row of -inf":
+        zd[:, 0] = NEG
+    else:
+        zd[torch.arange(B), 0, bad] = NEG if q == "-inf" else -1000.0
+    ua = torch.tensor([[0.0, 0.5], [0.25, 0.5], [0.5, 0.5], [1 - 2.0 ** -24, 0.5]])
+    uf = torch.tensor([0.1, 0.4, 0.7, 0.95])
+    got = _verify(zt, zd, cand, ua, uf, lse)
+    ref = O.verify_sample(_f64(zt), _f64(zd), cand.numpy(), [n] * B, ua.numpy(), uf.numpy())
+    assert got["accept_len"].tolist() == [0] * B == ref["accept_len"].tolist()
+    assert all(f & api.FLAG_INVALID for f in got["flags"].tolist())
+    assert torch.isfinite(got["probs"]).all()
+    assert got["probs"][:, 0].tolist() == [0.0] * B and got["probs"][:, n].tolist() == [0.0] * B
+    y = got["bonus"].cpu()
+    assert not torch.isneginf(zt[torch.arange(B), 0, y].float()).any()
+    # fp32 and 64 bits may differ within 1e-6 of a step, which is flagged
+    sure = (got["flags"].cpu().numpy() | ref["flags"]) & api.FLAG_CDF_BOUNDARY == 0
+    assert np.array_equal(y.numpy()[sure], ref["bonus"][sure])
+    if q == "row of -inf":                     # the draft has no law: the residual is p itself
+        assert torch.allclose(got["probs"][:, 2 * n].cpu(), torch.ones(B), atol=1e-5)
