@@ -220,7 +220,7 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
   // ---- last CTA of sequence b: chunk, then segment, then token ----
   __shared__ float2 csum[kMaxDrawChunks];
   __shared__ double s_target, s_Z, s_before;
-  __shared__ int s_chunk, s_degenerate, s_seg, s_y;
+  __shared__ int s_chunk, s_degenerate, s_seg, s_near, s_y;
   __shared__ double s_clo, s_chi;
   for (int cc = threadIdx.x; cc < nch; cc += blockDim.x) csum[cc] = __ldcg(parts + (size_t)b * nch + cc);
   __syncthreads();
@@ -252,6 +252,7 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
     s_chunk = cstar;
     s_degenerate = degenerate;
     s_seg = -1;
+    s_near = 0;
     s_y = INT32_MAX;
   }
   __syncthreads();
@@ -271,6 +272,9 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
   double base = s_before;
   for (int q = 0; q < wid; ++q) base += wsum[q];
   const double excl = base + incl - (double)ts;
+  // for a target that rounding leaves in no segment: the last one with weight before
+  // it, else the first after it
+  if (ts > 0.f) atomicMax(&s_near, excl + (double)ts <= s_target ? kThreads + (int)threadIdx.x : kThreads - 1 - (int)threadIdx.x);
   if (ts > 0.f && excl <= s_target && excl + (double)ts > s_target) {
     s_seg = threadIdx.x;        // unique: the segment ranges are disjoint
     s_clo = excl;
@@ -280,8 +284,8 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
   if (wid == 0) {
     int seg = s_seg;
     double sbase = s_clo;
-    if (seg < 0) {              // rounding: take the last segment with weight
-      seg = kThreads - 1;
+    if (seg < 0) {              // its last token with weight is taken
+      seg = s_near >= kThreads ? s_near - kThreads : kThreads - 1 - s_near;
       sbase = s_target;
     }
     const int es = s_chunk * kDrawChunk + seg * kDrawSeg;

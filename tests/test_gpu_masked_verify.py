@@ -90,3 +90,27 @@ def test_forbidden_candidate_is_rejected_where_q_is_zero(q, dtype, lse):
     assert np.array_equal(y.numpy()[sure], ref["bonus"][sure])
     if q == "row of -inf":                     # the draft has no law: the residual is p itself
         assert torch.allclose(got["probs"][:, 2 * n].cpu(), torch.ones(B), atol=1e-5)
+
+
+@pytest.mark.parametrize("reject", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,keep", [(9000, 4000), (20011, 17000), (128256, 30000)])
+def test_last_uniform_draws_an_allowed_token(V, keep, dtype, reject):
+    """u_final next to 1 puts the target at the end of the allowed tokens, past
+    the sum of the steps as it was rounded for some rows: the token drawn is the
+    last one with weight, or one of those before it, never a forbidden one."""
+    B, n = 64, 1
+    g = torch.Generator().manual_seed(V + keep)
+    zt = (2 * torch.randn((B, n + 1, V), generator=g)).to(DT[dtype])
+    zt[:, :, keep:] = NEG
+    zd = (2 * torch.randn((B, n, V), generator=g)).to(DT[dtype])
+    cand = torch.zeros((B, n + 1), dtype=torch.int64)
+    cand[:, 1] = V - 1 if reject else zt[:, 0].float().argmax(-1)
+    ua = torch.zeros((B, n))
+    uf = torch.full((B,), 1 - 2.0 ** -24)
+    got = _verify(zt, zd, cand, ua, uf, False)
+    assert got["accept_len"].tolist() == [0 if reject else 1] * B
+    y = got["bonus"].cpu()
+    assert (y < keep).all(), y[y >= keep].tolist()
+    row = zt[:, 0 if reject else 1].float()
+    assert (torch.softmax(row.double(), -1)[torch.arange(B), y] > 0).all()
