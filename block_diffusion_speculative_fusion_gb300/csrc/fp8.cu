@@ -296,6 +296,20 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+// The product f of two scales may leave fp32's normal range where a term (f times a
+// group's sum, which is 0 or 2^-18 to 2^25 in magnitude) does not. Then the sums take
+// `first` and f in turn: the larger factor first where the product is too small (the
+// sum times it is not below the term), the smaller one where it is too large (not
+// above the term). A factor of 0, NaN or infinity gives what it gives either way,
+// but for an infinite one times a sum of 0, NaN as it has to be.
+__device__ __forceinline__ bool scales_apart(float xs, float ws, float& f, float& first) {
+  const float a = fabsf(f);
+  if ((a >= kMinScale && a < CUDART_INF_F) || xs == 0.f || ws == 0.f) return false;
+  const bool x_first = (fabsf(xs) > fabsf(ws)) == (a < kMinScale);
+  first = x_first ? xs : ws;
+  f = x_first ? ws : xs;
+  return true;
+}
 __device__ __forceinline__ float4 four(uint64_t a, uint64_t b) {
   float4 v;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(a));
@@ -573,7 +587,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         }
         tc_fence_after();
         const float* sc = scales + u / C::PARTS % SCALE_SLOTS * SCALE_LD;
-        const float f = sc[quarter * 32 + lane] * sc[BM + part / PER];
+        const float xs = sc[quarter * 32 + lane], ws = sc[BM + part / PER];
+        float f = xs * ws, first = 1.f;
+        const bool far = __any_sync(0xffffffffu, scales_apart(xs, ws, f, first));
         const uint64_t s = pair(f, f);
         const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BUF_N + part % PER * C::COLS);
         auto release = [&]() {                        // the warp has read it out: the MMAs may have it
@@ -588,6 +604,10 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             else tmem_ld16(tbase + (uint32_t)c0, r);
             tmem_ld_wait();
             if (c0 + C::LD == C::COLS) release();
+            if (far) {
+#pragma unroll
+              for (int q = 0; q < C::LD; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * first);
+            }
 #pragma unroll
             for (int q = 0; q < C::LD; q += 2)
               acc[(c0 + q) / 2] = fma2(pair(__uint_as_float(r[q]), __uint_as_float(r[q + 1])), s, acc[(c0 + q) / 2]);

@@ -548,7 +548,8 @@ typedef struct {
  * out = x w^T + bias of e4m3 operands with block scales:
  *   out[t][n] = bias[n] + sum_g x_scale[t][g] * w_scale[n / 128][g] *
  *                               sum_{k = 128 g}^{128 g + 127} x[t][k] * w[n][k]
- * with fp32 sums, rounded to out_dtype once.
+ * with fp32 sums, rounded to out_dtype once. A term is as exact where the product
+ * of its two scales alone would be subnormal or infinite.
  * x [T, K], w [N, K] e4m3, 16-byte aligned; x_scale [T, ceil(K / 128)],
  * w_scale [ceil(N / 128), ceil(K / 128)] float (dflash_fp8_quant with
  * block_rows 1 and 128); bias [N] or NULL; out [T, N]. Repeated calls give
