@@ -420,6 +420,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   uint64_t* mma_done = tempty + BUFS;
   uint32_t* tmem_base_sm = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sm + 1);
+  int* groups_sent = reinterpret_cast<int*>(tmem_base_sm + 2);   // by the operands' and the scales' producer
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   // A dependent launch (10 x 20480 x 4096 called in a row: 19.0 us, not 21.6): what
@@ -524,13 +525,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    // After an abort copies may still be in flight: wait for the last one of every
-    // stage (bounded) so that none lands after the CTA has exited. A stage that the
-    // scales' warp has not arrived on never completes, and when that wait has run out
-    // all copies have landed.
-    if (operands && lane == 0 && *abort_flag)
-      for (int i = max(0, issued - C::STAGES); i < issued; ++i)
-        if (!mbar_wait_bounded(&full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.err, 26)) break;
+    if (lane == 0) groups_sent[operands ? 0 : 1] = issued;
     __syncwarp();
   } else if (warp >= SUM_WARPS) {
     // ------------------------------ MMA issuers ------------------------------
@@ -648,8 +643,21 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
     }
   }
   tc_fence_before();
+  __syncthreads();
+  // After an abort copies may still be in flight: the last one of every stage is waited
+  // for (bounded), so that none lands after the CTA has exited. No role issues any more,
+  // and whichever gave up has set the flag before the barrier, also where all copies had
+  // been issued before. A copy whose group the scales' producer has not arrived on gets
+  // that arrival here: without it its stage would never complete. (It is at most STAGES
+  // groups behind: a stage is filled again after its group has been multiplied.)
+  if (warp == SUM_WARPS + MMA_WARPS && lane == 0 && *abort_flag) {
+    const int issued = groups_sent[0], oldest = max(0, issued - C::STAGES);
+    for (int i = max(oldest, groups_sent[1]); i < issued; ++i) mbar_arrive(&full[i % C::STAGES]);
+    for (int i = oldest; i < issued; ++i)
+      if (!mbar_wait_bounded(&full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.err, 26)) break;
+  }
+  __syncwarp();
   if (SPLIT) {
-    __syncthreads();
     cluster_sync();
     const int m0 = first / nt * BM, n0 = first % nt * BN;   // a cluster has one tile
     const int rows = min(BM, T - m0), cells = rows * (BN / 4);
@@ -669,7 +677,6 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
   }
   // every accumulator has been read, or the CTA has given up: the MMAs end (bounded)
   // before TMEM is freed
-  __syncthreads();
   if (warp == 0) {
     if (lane == 0) mbar_wait_bounded(mma_done, 0, p.err, 24);
     __syncwarp();
