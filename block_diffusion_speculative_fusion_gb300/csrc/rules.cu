@@ -381,17 +381,6 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
         for (int j = 0; j < 4; ++j) ruled(tid * TPT + 4 * q + j);
     }
     if (!EVEN && tid < N && ruled(C + tid)) m |= 1u << TPT;
-    if (EVEN && p.in_place)
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        uint32_t any_rule = 0;
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-          const int i = (tid + j * kVecs) * N + q;
-          any_rule |= sm.word[i] | sm.entry[i];   // (an entry turned into a value of 0 changes nothing)
-        }
-        plain |= any_rule ? 0u : 1u << j;
-      }
     int before = __popc(m);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -406,7 +395,18 @@ rules_kernel(const T* logits, T* out, const RulesParams p) {
       sm.list[at++] = (uint16_t)(j < TPT ? tid * TPT + j : C + tid);
     }
   }
-  __syncthreads();
+  __syncthreads();                           // the list is whole, every entry its value
+  if (EVEN && p.in_place)
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      uint32_t any_rule = 0;
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const int i = (tid + j * kVecs) * N + q;
+        any_rule |= sm.word[i] | sm.entry[i];   // (a value of 0 changes nothing)
+      }
+      plain |= any_rule ? 0u : 1u << j;
+    }
   const int n = sm.n;
   if (edge_e >= 0) store_one(edge_e, edge_r, edge_z, edge_good);
   edges(tid + kVecs);
