@@ -262,7 +262,7 @@ def _launch(dev: int, fn, *args) -> None:
 
 
 _WS: Dict[Tuple[int, int], torch.Tensor] = {}
-_WS_OUTGROWN: List[torch.Tensor] = []
+_WS_OUTGROWN: List[Tuple[Tuple[int, int], torch.Tensor]] = []
 
 
 def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
@@ -277,7 +277,7 @@ def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
         if ws is not None:
-            _WS_OUTGROWN.append(ws)
+            _WS_OUTGROWN.append((key, ws))
         ws = torch.zeros(max(nbytes, WS_COUNTER_BYTES), dtype=torch.uint8, device=f"cuda:{idx}")
         _WS[key] = ws
     return ws
@@ -286,6 +286,12 @@ def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
 def reset_workspaces():
     _WS.clear()
     _WS_OUTGROWN.clear()
+
+
+def cached_workspaces() -> List[Tuple[Tuple[int, int], torch.Tensor]]:
+    """((device, slot), tensor) of every cached workspace, those that a larger
+    call has outgrown included."""
+    return _WS_OUTGROWN + list(_WS.items())
 
 
 # ---------------------------------------------------------------------------
@@ -716,9 +722,13 @@ def clear_counters(ws: torch.Tensor) -> None:
 
 
 def error_words() -> Dict[Tuple[int, int], int]:
-    """Error word of every cached workspace (see ``workspace``), keyed by
-    (device, slot)."""
-    return {k: device_error_word(v) for k, v in _WS.items()}
+    """Error word of the cached workspaces (see ``workspace``), keyed by (device,
+    slot): the first nonzero one among a slot's outgrown workspaces, with which a
+    captured graph may still replay, and its current one."""
+    words: Dict[Tuple[int, int], int] = {}
+    for key, ws in cached_workspaces():
+        words[key] = words.get(key, 0) or device_error_word(ws)
+    return words
 
 
 # ---------------------------------------------------------------------------

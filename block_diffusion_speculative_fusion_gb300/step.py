@@ -116,8 +116,9 @@ class DflashStep:
         return g
 
     def workspaces(self) -> List[torch.Tensor]:
-        """The device workspaces this step's calls use."""
-        out = [w for (dev, _), w in api._WS.items() if dev == (self.dev.index or 0)]
+        """The device workspaces this step's calls use, and those that a graph
+        captured before a larger call may still use."""
+        out = [w for (dev, _), w in api.cached_workspaces() if dev == (self.dev.index or 0)]
         if self.ws_greedy is not None:
             out.append(self.ws_greedy)
         return out
