@@ -269,7 +269,8 @@ def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
     """A zero-initialised device workspace of at least ``nbytes`` (cached per
     device and slot; calls on one stream may share a slot). One that a larger
     call outgrows is kept until ``reset_workspaces``: a captured graph may still
-    replay with it."""
+    replay with it. The one that takes its place is at least twice as large, so
+    that all those kept take no more than it does."""
     idx = torch.device(device).index
     if idx is None:
         idx = torch.cuda.current_device()
@@ -278,6 +279,7 @@ def workspace(device: torch.device, nbytes: int, slot: int = 0) -> torch.Tensor:
     if ws is None or ws.numel() < nbytes:
         if ws is not None:
             _WS_OUTGROWN.append((key, ws))
+            nbytes = max(nbytes, 2 * ws.numel())
         ws = torch.zeros(max(nbytes, WS_COUNTER_BYTES), dtype=torch.uint8, device=f"cuda:{idx}")
         _WS[key] = ws
     return ws
