@@ -685,6 +685,8 @@ int dflash_fp8_quant(const dflash_fp8_quant_dims* d, const void* x, void* q, flo
     return fail(DFLASH_ERR_INVALID_ARG, "block_rows=%d is not 1 or 128", d->block_rows);
   if (d->K % 16) return fail(DFLASH_ERR_UNSUPPORTED, "K=%d is not a multiple of 16", d->K);
   if (d->T > 1 << 23 || d->K > 1 << 23) return fail(DFLASH_ERR_UNSUPPORTED, "T=%d or K=%d > 2^23", d->T, d->K);
+  if (d->block_rows == 128 && ((long)d->T + 127) / 128 * (((long)d->K + 127) / 128) > 0x7fffffffL)
+    return fail(DFLASH_ERR_UNSUPPORTED, "T=%d x K=%d has more than 2^31 - 1 blocks", d->T, d->K);
   if (d->T == 0) return ok(0);
   if (!x || !q || !scale) return fail(DFLASH_ERR_INVALID_ARG, "fp8_quant: a required pointer is NULL");
   if (!aligned16(x) || !aligned16(q)) return fail(DFLASH_ERR_INVALID_ARG, "fp8_quant: x or q is not 16-byte aligned");

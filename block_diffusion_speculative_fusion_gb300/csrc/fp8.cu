@@ -101,8 +101,9 @@ f8_quant_rows_kernel(const T* x, uint8_t* q, float* scale, int T_rows, const int
   }
 }
 
-// One CTA per 128 x 128 block, a warp 16 of its rows, held in registers between
-// the search for the largest magnitude and the conversion.
+// One CTA per 128 x 128 block (all in the grid's x: its y ends at 65535, below the
+// row blocks and the groups that are allowed), a warp 16 of its rows, held in registers
+// between the search for the largest magnitude and the conversion.
 template <typename T>
 __global__ void __launch_bounds__(256)
 f8_quant_blocks_kernel(const T* x, uint8_t* q, float* scale, int T_rows, int K) {
@@ -113,8 +114,9 @@ f8_quant_blocks_kernel(const T* x, uint8_t* q, float* scale, int T_rows, int K) 
   constexpr int L = 16 / RPL;
   __shared__ float s_max[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int k = blockIdx.x * f8::G + (lane % LPG) * N;
-  const int t0 = blockIdx.y * f8::G + warp * 16 + lane / LPG;
+  const unsigned groups = (K + f8::G - 1) / f8::G, row_block = blockIdx.x / groups;
+  const int k = (int)(blockIdx.x - row_block * groups) * f8::G + (lane % LPG) * N;
+  const int t0 = (int)row_block * f8::G + warp * 16 + lane / LPG;
   uint4 v[L];
   float m = 0.f;
 #pragma unroll
@@ -136,13 +138,13 @@ f8_quant_blocks_kernel(const T* x, uint8_t* q, float* scale, int T_rows, int K) 
     const int t = t0 + i * RPL;
     if (t < T_rows && k < K) f8_store<T>(q + (size_t)t * K + k, v[i], r);
   }
-  if (threadIdx.x == 0) scale[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = s;
+  if (threadIdx.x == 0) scale[blockIdx.x] = s;
 }
 
 template <typename T>
 static cudaError_t launch_f8_quant_t(const Fp8QuantArgs& a) {
   if (a.block_rows == f8::G) {
-    const dim3 grid((a.K + f8::G - 1) / f8::G, (a.T + f8::G - 1) / f8::G);
+    const dim3 grid((unsigned)((a.K + f8::G - 1) / f8::G) * (unsigned)((a.T + f8::G - 1) / f8::G));
     return launch_dependent(f8_quant_blocks_kernel<T>, grid, dim3(256), 0, a.stream, (const T*)a.x, (uint8_t*)a.q,
                             a.scale, a.T, a.K);
   }

@@ -517,8 +517,8 @@ int dflash_ddtree_verify_greedy(const dflash_tree_dims* dims, const void* target
 /* 8-bit floating point with a scale per 128 values                           */
 /* ------------------------------------------------------------------------- */
 typedef struct {
-  int32_t T;           /* rows, >= 0 (0: nothing is done) */
-  int32_t K;           /* columns, a multiple of 16 */
+  int32_t T;           /* rows, 0 .. 2^23 (0: nothing is done) */
+  int32_t K;           /* columns, a multiple of 16, <= 2^23 */
   int32_t dtype;       /* type of x */
   int32_t block_rows;  /* rows that share a scale: 1 (activations) or 128 (weights) */
 } dflash_fp8_quant_dims;
@@ -538,9 +538,9 @@ int dflash_fp8_quant(const dflash_fp8_quant_dims* dims, const void* x, void* q, 
                      dflash_stream_t stream);
 
 typedef struct {
-  int32_t T;          /* rows of x, >= 0 (0: nothing is done) */
-  int32_t N;          /* rows of w: columns of out */
-  int32_t K;          /* shared dimension, a multiple of 16 */
+  int32_t T;          /* rows of x, 0 .. 2^23 (0: nothing is done) */
+  int32_t N;          /* rows of w: columns of out, <= 2^23 */
+  int32_t K;          /* shared dimension, a multiple of 16, <= 2^23 */
   int32_t out_dtype;  /* type of out and bias */
 } dflash_fp8_gemm_dims;
 
