@@ -83,6 +83,25 @@ namespace dflash {
 unsigned long long wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
 }  // namespace dflash
 
+namespace {
+// A buffer of a call, and whether the call writes it.
+struct Span {
+  const void* p;
+  size_t bytes;
+  bool written;
+};
+// Some buffer that the call writes shares bytes with another one (null ones share none).
+template <size_t N>
+bool any_overlap(const Span (&s)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      const uintptr_t a = (uintptr_t)s[i].p, b = (uintptr_t)s[j].p;
+      if (a && b && (s[i].written || s[j].written) && a < b + s[j].bytes && b < a + s[i].bytes) return true;
+    }
+  return false;
+}
+}  // namespace
+
 extern "C" {
 
 const char* dflash_last_error(void) { return g_err.c_str(); }
@@ -509,8 +528,13 @@ int dflash_pages_resize(const dflash_pages_dims* d, const int32_t* length, int32
   if (rc) return rc;
   if (!length || !page_table || !n_pages || !free_pages || !n_free || !n_pages_out || !n_free_out)
     return fail(DFLASH_ERR_INVALID_ARG, "pages_resize: a required pointer is NULL");
-  if (n_pages_out == n_pages || n_free_out == n_free || n_pages_out == length)
-    return fail(DFLASH_ERR_INVALID_ARG, "pages_resize: n_pages_out and n_free_out must not alias an input");
+  // every CTA reads the lengths and counts while others write: shared bytes would send pages past their rows
+  const size_t seq = (size_t)d->B * 4;
+  const Span spans[] = {{length, seq, false}, {n_pages, seq, false}, {n_free, 4, false},
+                        {page_table, seq * d->max_pages, true}, {free_pages, (size_t)d->num_pages * 4, true},
+                        {n_pages_out, seq, true}, {n_free_out, 4, true}, {short_seq, (size_t)d->B, true}};
+  if (any_overlap(spans))
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_resize: buffers overlap (no output may alias another buffer)");
   dflash::PagesArgs a{};
   a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
   a.length = length; a.page_table = page_table; a.n_pages = n_pages; a.free_pages = free_pages; a.n_free = n_free;
@@ -530,6 +554,10 @@ int dflash_slot_map(const dflash_pages_dims* d, int32_t rows_max, const int32_t*
   if (rows_max < 1 || rows_max > 1 << 30) return fail(DFLASH_ERR_INVALID_ARG, "rows_max=%d outside [1, 2^30]", rows_max);
   if (!start_pos || !n_rows || !page_table || !cu_rows || !row_seq || !positions || !slots)
     return fail(DFLASH_ERR_INVALID_ARG, "slot_map: a required pointer is NULL");
+  const size_t seq = (size_t)d->B * 4, rows = (size_t)rows_max * 4;
+  const Span spans[] = {{start_pos, seq, false}, {n_rows, seq, false}, {page_table, seq * d->max_pages, false},
+                        {cu_rows, seq + 4, true}, {row_seq, rows, true}, {positions, rows, true}, {slots, 2 * rows, true}};
+  if (any_overlap(spans)) return fail(DFLASH_ERR_INVALID_ARG, "slot_map: an output overlaps another buffer");
   dflash::SlotArgs a{};
   a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages; a.rows_max = rows_max;
   a.start_pos = start_pos; a.n_rows = n_rows; a.page_table = page_table;

@@ -663,9 +663,11 @@ typedef struct {
  * length [B] int32 (negative: 0); page_table [B, max_pages] int32, in and out
  * n_pages [B] int32  pages that each row holds (clamped to [0, max_pages])
  * free_pages [num_pages] int32, in and out: the first n_free[0] entries are free
- * n_pages_out [B], n_free_out [1] int32: the new counts; must not alias n_pages
- *   and n_free, so that the call can be repeated with the same result
+ * n_pages_out [B], n_free_out [1] int32: the new counts, in buffers of their own,
+ *   so that the call can be repeated with the same result
  * short_seq [B] uint8 or NULL: 1 where the pages asked for were not given
+ * No two of these buffers may overlap (length, n_pages and n_free among
+ * themselves may).
  * No page may appear twice among the free list and the rows' first n_pages
  * entries (pages are not counted by reference). No workspace.
  */
@@ -686,7 +688,7 @@ int dflash_pages_resize(const dflash_pages_dims* dims, const int32_t* length, in
  *                            entry outside [0, num_pages))
  * and -1 in all three for the rows T .. rows_max - 1, so that a captured graph
  * of rows_max rows writes nothing for them. rows_max in [1, 2^30]; negative
- * n_rows count as 0. No workspace.
+ * n_rows count as 0. No output may overlap another buffer. No workspace.
  */
 int dflash_slot_map(const dflash_pages_dims* dims, int32_t rows_max, const int32_t* start_pos,
                     const int32_t* n_rows, const int32_t* page_table, int32_t* cu_rows, int32_t* row_seq,
