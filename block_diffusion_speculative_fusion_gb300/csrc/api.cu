@@ -752,6 +752,9 @@ int dflash_fp8_gemm(const dflash_fp8_gemm_dims* d, const void* x, const float* x
   if (d->T == 0) return ok(0);
   if (!x || !x_scale || !w || !w_scale || !out) return fail(DFLASH_ERR_INVALID_ARG, "fp8_gemm: a required pointer is NULL");
   if (!aligned16(x) || !aligned16(w)) return fail(DFLASH_ERR_INVALID_ARG, "fp8_gemm: x or w is not 16-byte aligned");
+  const uintptr_t el = d->out_dtype == DFLASH_BF16 ? 2 : 4;
+  if ((uintptr_t)out % el || (uintptr_t)bias % el)
+    return fail(DFLASH_ERR_INVALID_ARG, "fp8_gemm: out or bias is not aligned to its type");
   rc = check_ws(workspace, ws_bytes, DFLASH_WS_COUNTER_BYTES);
   if (rc) return rc;
   dflash::Fp8GemmArgs a{};

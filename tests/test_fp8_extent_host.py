@@ -1,4 +1,4 @@
-"""Refusals at the ends of the 8-bit quantisation's extents, before a launch."""
+"""Refusals of the 8-bit calls at the ends of their extents and alignments, before a launch."""
 import ctypes
 
 import pytest
@@ -18,3 +18,13 @@ def test_quant_refuses_more_blocks_than_a_grid_holds(L, T, K, rows):
     d = api.Fp8QuantDims(T, K, api.BF16, rows)
     assert L.dflash_fp8_quant(ctypes.byref(d), p, p, p, None) == api.ERR_UNSUPPORTED
     assert "2^23" in api.last_error() or "blocks" in api.last_error()
+
+
+@pytest.mark.parametrize("dtype,off", [(api.BF16, 1), (api.F32, 2), (api.F32, 1)])
+def test_product_refuses_out_and_bias_between_elements(L, dtype, off):
+    d = api.Fp8GemmDims(4, 8, 128, dtype)
+    for i in (4, 5):                            # bias, out
+        p = [ctypes.c_void_p(0x10000)] * 7
+        p[i] = ctypes.c_void_p(0x10000 + off)
+        assert L.dflash_fp8_gemm(ctypes.byref(d), *p, api.WS_COUNTER_BYTES, None) == api.ERR_INVALID_ARG
+        assert "aligned to its type" in api.last_error()
