@@ -484,8 +484,8 @@ int dflash_logits_rules(const dflash_rules_dims* d, const void* logits, const in
     return fail(DFLASH_ERR_UNSUPPORTED, "n_rows=%d > %d", d->n_rows, dflash::kRulesMaxRows);
   if (d->hist_max >= 1 << dflash::kRulesCountBits)
     return fail(DFLASH_ERR_UNSUPPORTED, "hist_max=%d > %d", d->hist_max, (1 << dflash::kRulesCountBits) - 1);
-  if (d->n_bias >= 1 << dflash::kRulesBiasBits)
-    return fail(DFLASH_ERR_UNSUPPORTED, "n_bias=%d > %d", d->n_bias, (1 << dflash::kRulesBiasBits) - 1);
+  if (d->n_bias > dflash::kRulesMaxBias)
+    return fail(DFLASH_ERR_UNSUPPORTED, "n_bias=%d > %d", d->n_bias, dflash::kRulesMaxBias);
   if (d->B > 65535) return fail(DFLASH_ERR_UNSUPPORTED, "B=%d > 65535", d->B);
   if (d->V > 1 << 25) return fail(DFLASH_ERR_UNSUPPORTED, "V=%d > 2^25", d->V);
   if (!logits || !out || (d->hist_max > 0 && (!hist || !hist_len)) || (d->n_bias > 0 && (!bias_tok || !bias_val)))

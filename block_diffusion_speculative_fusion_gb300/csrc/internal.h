@@ -177,7 +177,7 @@ cudaError_t launch_ddtree_verify(const TreeArgs& a);
 // ----------------------------------------------------------- logit rules ---
 constexpr int kRulesMaxRows = 256;
 constexpr int kRulesCountBits = 18;   // of a token's word: its occurrences in the output
-constexpr int kRulesBiasBits = 11;    // its bias entry
+constexpr int kRulesMaxBias = 2047;   // entries of a sequence's bias list
 struct RulesArgs {
   int B, n_rows, V, dtype, hist_max, n_bias;
   const void* logits;          // [B, n_rows, V]
