@@ -298,19 +298,19 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-// The product f of two scales may leave fp32's normal range where a term (f times a
-// group's sum, which is 0 or 2^-18 to 2^25 in magnitude) does not. Then the sums take
-// `first` and f in turn: the larger factor first where the product is too small (the
-// sum times it is not below the term), the smaller one where it is too large (not
-// above the term). A factor of 0, NaN or infinity gives what it gives either way,
-// but for an infinite one times a sum of 0, NaN as it has to be.
-__device__ __forceinline__ bool scales_apart(float xs, float ws, float& f, float& first) {
-  const float a = fabsf(f);
-  if ((a >= kMinScale && a < CUDART_INF_F) || xs == 0.f || ws == 0.f) return false;
-  const bool x_first = (fabsf(xs) > fabsf(ws)) == (a < kMinScale);
-  first = x_first ? xs : ws;
-  f = x_first ? ws : xs;
-  return true;
+// The product of two scales may leave fp32's normal range where a term (the product
+// times a group's sum, which is 0 or 2^-18 to 2^25 in magnitude) does not. Then the sums
+// take the two scales in turn: the larger one first where the product is too small (the
+// sum times it is not below the term), the smaller one where it is too large (not above
+// it). A product with 0, NaN or infinity stays what it is either way.
+__device__ __forceinline__ bool in_range(float f) {
+  constexpr uint32_t kLow = 2u * 0x00800000u, kHigh = 2u * 0x7f800000u;   // 2^-126 and infinity, without a sign
+  return 2u * __float_as_uint(f) - kLow < kHigh - kLow;
+}
+__device__ __forceinline__ float2 scales_in_turn(float xs, float ws) {
+  const float a = fabsf(xs), b = fabsf(ws);
+  if (in_range(xs * ws)) return make_float2(1.f, xs * ws);
+  return (a > b) == (a * b < 1.f) ? make_float2(xs, ws) : make_float2(ws, xs);
 }
 __device__ __forceinline__ float4 four(uint64_t a, uint64_t b) {
   float4 v;
@@ -318,12 +318,12 @@ __device__ __forceinline__ float4 four(uint64_t a, uint64_t b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(v.z), "=f"(v.w) : "l"(b));
   return v;
 }
-// Scales kb .. kb + 3 of a row, 0 past the last group or row.
+// Scales kb .. kb + 3 of a row, 1 past the last group or row.
 __device__ __forceinline__ float4 scale4(const float* scale, int row, int rows, int kb, int groups, int vec) {
-  if (row >= rows || kb >= groups) return make_float4(0.f, 0.f, 0.f, 0.f);
+  if (row >= rows || kb >= groups) return make_float4(1.f, 1.f, 1.f, 1.f);
   const float* s = scale + (size_t)row * groups + kb;
   if (vec) return *reinterpret_cast<const float4*>(s);
-  return make_float4(s[0], kb + 1 < groups ? s[1] : 0.f, kb + 2 < groups ? s[2] : 0.f, kb + 3 < groups ? s[3] : 0.f);
+  return make_float4(s[0], kb + 1 < groups ? s[1] : 1.f, kb + 2 < groups ? s[2] : 1.f, kb + 3 < groups ? s[3] : 1.f);
 }
 __device__ __forceinline__ float of4(const float4& v, int i) { return i < 2 ? (i == 0 ? v.x : v.y) : (i == 2 ? v.z : v.w); }
 // acc + bias for four columns from n on (8 or 16 aligned bytes, the same for all lanes).
@@ -585,9 +585,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
         tc_fence_after();
         const float* sc = scales + u / C::PARTS % SCALE_SLOTS * SCALE_LD;
         const float xs = sc[quarter * 32 + lane], ws = sc[BM + part / PER];
-        float f = xs * ws, first = 1.f;
-        const bool far = __any_sync(0xffffffffu, scales_apart(xs, ws, f, first));
+        const float f = xs * ws;
         const uint64_t s = pair(f, f);
+        bool apart = false;
         const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * BUF_N + part % PER * C::COLS);
         auto release = [&]() {                        // the warp has read it out: the MMAs may have it
           tc_fence_before();
@@ -599,15 +599,23 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
             uint32_t r[C::LD];
             if constexpr (C::LD == 32) tmem_ld32(tbase + (uint32_t)c0, r);
             else tmem_ld16(tbase + (uint32_t)c0, r);
+            // Found while the first columns are on their way. Before them, each narrow tile's
+            // group took 10 % longer and a wide one's 5; marked by the scales' producer instead,
+            // 10 to 20 and none; so, 6 and none (2048 x 4096 x 10240 87 -> 93 us).
+            if (c0 == 0) apart = __any_sync(0xffffffffu, !in_range(f));
             tmem_ld_wait();
             if (c0 + C::LD == C::COLS) release();
-            if (far) {
+            if (apart) {
+              const float2 t = scales_in_turn(xs, ws);
 #pragma unroll
-              for (int q = 0; q < C::LD; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * first);
+              for (int q = 0; q < C::LD; q += 2)
+                acc[(c0 + q) / 2] = fma2(pair(__uint_as_float(r[q]) * t.x, __uint_as_float(r[q + 1]) * t.x), pair(t.y, t.y),
+                                         acc[(c0 + q) / 2]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < C::LD; q += 2)
+                acc[(c0 + q) / 2] = fma2(pair(__uint_as_float(r[q]), __uint_as_float(r[q + 1])), s, acc[(c0 + q) / 2]);
             }
-#pragma unroll
-            for (int q = 0; q < C::LD; q += 2)
-              acc[(c0 + q) / 2] = fma2(pair(__uint_as_float(r[q]), __uint_as_float(r[q + 1])), s, acc[(c0 + q) / 2]);
           }
         }
         else release();

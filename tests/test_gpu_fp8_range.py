@@ -79,3 +79,23 @@ def test_one_group_each_way():
         y = float(api.fp8_gemm(q(xv), s(a), q(wv), s(b), out_dtype=torch.float32))
         want = xv * wv * float(np.float32(a)) * float(np.float32(b))
         assert abs(y - want) <= 2 * 2.0 ** -24 * abs(want), (y, want)
+
+
+@pytest.mark.parametrize("T,N,K", [(64, 128, 256), (40, 256, 2944), (1500, 2600, 528)])
+def test_rows_whose_products_differ_in_kind(T, N, K):
+    """Beside rows whose scales' product leaves the range, rows whose product is in the
+    middle of it while one scale times the sum would overflow, and rows of scale 0."""
+    g = np.random.default_rng(T)
+    kind = np.arange(T) % 3
+    xs = g.uniform(1.5, 2, (T, -(-K // 128))) * np.exp2(np.array([-76, 115, 0])[kind][:, None])
+    xs[kind == 2] = 0.0
+    ws = g.uniform(1.5, 2, (-(-N // 128), -(-K // 128))) * 2.0 ** -75
+    x, w = np.full((T, K), 448.0), np.full((N, K), 448.0)
+    to8 = lambda a: torch.from_numpy(a).float().to(torch.float8_e4m3fn).to(DEV)
+    xs, ws = xs.astype(np.float32), ws.astype(np.float32)
+    got = _f64(api.fp8_gemm(to8(x), torch.from_numpy(xs).to(DEV), to8(w), torch.from_numpy(ws).to(DEV),
+                            out_dtype=torch.float32))
+    ref, size = O.fp8_gemm(x, xs.astype(np.float64), w, ws.astype(np.float64))
+    assert size.max() < 2.0 ** 128 and np.all((ref == 0) == (kind == 2)[:, None])
+    tol = (128 * 2.0 ** -23 + (-(-K // 128) + 12) * 2.0 ** -24) * size
+    assert np.all(np.abs(got - ref) <= tol)
