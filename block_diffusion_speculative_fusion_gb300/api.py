@@ -588,8 +588,9 @@ def logits_rules(logits: torch.Tensor, cand: Optional[torch.Tensor] = None, n_dr
     n_draft [B] int32; repetition, presence, frequency [B] float32; bias_tok
     [B, n] int64 with bias_val [B, n] float32; mask [B, R, ceil(V / 32)] int32,
     bit 1 = allowed, for the sequences with mask_on[b] != 0 (uint8; None: all).
-    Returns ``out`` (a new tensor, whose rows past n_draft[b] are then zero, if
-    not given); ``out=logits`` works in place."""
+    Returns ``out``; ``out=logits`` works in place. If not given, ``out`` is a new
+    tensor, which with ``n_draft`` is zeroed whole before the call, as its rows past
+    n_draft[b] are not written: pass one to save that."""
     _dev(logits, "logits")
     B, R, V = logits.shape
     dev = logits.get_device()
@@ -625,7 +626,7 @@ def pages_resize(length: torch.Tensor, page_table: torch.Tensor, n_pages: torch.
     tokens (``dflash_pages_resize``). length, n_pages [B], page_table [B,
     max_pages], free_pages [num_pages], n_free [1], all int32; page_table and
     free_pages are changed in place. Returns n_pages [B] and n_free [1] int32
-    (tensors other than the inputs), short [B] uint8."""
+    (tensors that overlap no other one of the call), short [B] uint8."""
     _dev(page_table, "page_table", torch.int32)
     B, max_pages = page_table.shape
     dev = page_table.get_device()
@@ -836,7 +837,9 @@ def materialize_ctx_kv_fp8(hidden: torch.Tensor, commit_len: torch.Tensor, start
                            new_len: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> None:
     """``materialize_ctx_kv`` with e4m3 weights (``dflash_materialize_ctx_kv_fp8``):
     W_f [d, m*d] and W_kv [L, 2, Hkv*D, d] float8_e4m3fn with the scales of
-    ``fp8_quant(..., block_rows=128)`` over W_f and over W_kv.view(-1, d)."""
+    ``fp8_quant(..., block_rows=128)`` over W_f and over W_kv.view(-1, d). Faster
+    than the bf16 call where most of the B x rows_max rows are committed, slower
+    where few of many are."""
     _dev(hidden, "hidden", torch.bfloat16)
     B, rows_max, md = hidden.shape
     dev = hidden.get_device()

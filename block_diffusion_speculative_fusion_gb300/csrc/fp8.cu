@@ -30,7 +30,7 @@ constexpr float kMinScale = 1.17549435e-38f;
 // Quantisation. Bound: one read and one write. A warp takes whole groups (16
 // bytes a lane: two bf16 groups or one fp32 group at once), four at a time, and
 // finds the largest magnitude by shuffles. Measured: 8190 x 20480 bf16 86 us (508
-// MB, 0.87 of the copy bandwidth), 10 x 20480 1.6 us.
+// MB, 0.87 of the copy bandwidth), 10 x 20480 2.0 us.
 // ---------------------------------------------------------------------------
 template <typename T> constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
 // NaN is passed over here and kept by the conversion.
@@ -182,9 +182,10 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a) {
 // Shared memory begins at a constant address (aligned by its declaration, not by
 // code), so that barriers and slots need no registers: 8 % at large sizes, where 64
 // sums and 16 values on their way leave a thread little else. A group takes 240 ns
-// (narrow) or 425 (wide); the MMAs alone, 195 and 335. Measured, bf16: 10 x 20480 x
-// 4096 19 us (84 MB at 4.4 TB/s with the launch), 271 x 4096 x 10240 (fp32) 24, 8190 x
-// 20480 x 4096 525 to 540 (2.6 PFLOP/s).
+// (narrow; 255 where the CTAs' tiles go many rounds) or 425 (wide); the MMAs alone, 195
+// and 335. Measured, bf16: 10 x 20480 x 4096 19.5 us (84 MB at 4.3 TB/s with the launch),
+// 271 x 4096 x 10240 (fp32) 24, 8190 x 20480 x 4096 535 to 545 for a few calls (2.5
+// PFLOP/s) and 610 to 625 in a long run, under the power cap (2.2).
 // ---------------------------------------------------------------------------
 namespace f8 {
 constexpr int BM = 128;
@@ -702,7 +703,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__
 // 4 and 8 CTAs, one an SM, at once. The constants are those of least loss over 90
 // measured products of 1 to 2048 rows, 512 to 20480 values and 512 to 32000 columns:
 // the choice is 0.3 % slower than the best of the eight in the mean and 7 % at most.
-// Measured (narrow against wide, us): 8190 x 20480 x 4096 615 against 531 whole, 400
+// Measured then (narrow against wide, us): 8190 x 20480 x 4096 615 against 531 whole, 400
 // x 4096 x 10240 33 against 40; 10 x 4096 x 10240 13.4 whole, 15.5 wide in two parts.
 struct Fp8Plan { int BN, S; };
 static Fp8Plan fp8_plan(int T, int N, int groups) {

@@ -9,8 +9,8 @@
 // among the CTAs. Both are dependent launches, whose start overlaps the end of the
 // kernel before. Bound: the launch and two dependent loads for a decode
 // round, the bytes written for a prefill's slot map. Measured: resize of 64
-// sequences 3.4 us, of 1024 with a quarter admitted whole 7.8; slot map of 64 x 16
-// rows 5 us, of 512 prompts (4.2 million rows, 67 MB stored) 14.3.
+// sequences 3.8 us, of 1024 with a quarter admitted whole 8.0; slot map of 64 x 16
+// rows 5.4 us, of 512 prompts (4.2 million rows, 67 MB stored) 14.6.
 #include <algorithm>
 
 #include "common.cuh"
