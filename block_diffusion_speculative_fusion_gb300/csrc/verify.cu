@@ -290,6 +290,7 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
     }
     const int es = s_chunk * kDrawChunk + seg * kDrawSeg;
     float w2[2];
+    int lastp = -1;             // the lane's last token with p > 0
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int e = es + 2 * l + q;
@@ -297,6 +298,7 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
       if (e < V) {
         // the same arithmetic as the segment sums of pass 1
         const float pt = ex2_ftz(fmaf(to_f32(zt_row[e]), k2, -j.mt)) * (1.f / j.st);
+        if (pt > 0.f) lastp = e;
         if (usep_r || degenerate) {
           wt = pt;
         } else {
@@ -318,7 +320,7 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
     int yl = INT32_MAX;
     double clo = 0.0, chi = 0.0;
     if (s_seg >= 0 && ex <= rel && inc > rel) {
-      const bool first = ex + w2[0] > rel;
+      const bool first = !(w2[1] > 0.f) || ex + w2[0] > rel;   // (a token without weight is not drawn by rounding)
       yl = es + 2 * l + (first ? 0 : 1);
       clo = sbase + (double)(first ? ex : ex + w2[0]);
       chi = sbase + (double)(first ? ex + w2[0] : inc);
@@ -330,7 +332,10 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
     for (int q = 0; q < 2; ++q)
       if (w2[q] > 0.f) lastw = es + 2 * l + q;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lastw = max(lastw, __shfl_xor_sync(0xffffffffu, lastw, o));
+    for (int o = 16; o > 0; o >>= 1) {
+      lastw = max(lastw, __shfl_xor_sync(0xffffffffu, lastw, o));
+      lastp = max(lastp, __shfl_xor_sync(0xffffffffu, lastp, o));
+    }
     if (hit) {
       const int src = __ffs(hit) - 1;
       if (l == src) {
@@ -339,7 +344,8 @@ sample_draw_kernel(const T* __restrict__ zt, const T* __restrict__ zd, const flo
         s_chi = chi;
       }
     } else if (l == 0) {
-      s_y = lastw >= 0 ? lastw : es;
+      // (a segment whose residual is rounding alone may have none here: its last token with p)
+      s_y = lastw >= 0 ? lastw : lastp >= 0 ? lastp : es;
       s_clo = s_target;
       s_chi = s_target;
     }

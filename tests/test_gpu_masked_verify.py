@@ -114,3 +114,35 @@ def test_last_uniform_draws_an_allowed_token(V, keep, dtype, reject):
     assert (y < keep).all(), y[y >= keep].tolist()
     row = zt[:, 0 if reject else 1].float()
     assert (torch.softmax(row.double(), -1)[torch.arange(B), y] > 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sparse_masks_at_every_step_of_the_law(dtype):
+    """Every other token forbidden, and u_final at, just below and just above the steps
+    of the law: the token drawn is one that the mask allows."""
+    B, V = 64, 300
+    g = torch.Generator().manual_seed(3)
+    row = (2 * torch.randn((1, 1, V), generator=g)).to(DT[dtype])
+    row[..., 1::2] = NEG
+    zt = row.expand(B, 1, V).contiguous()
+    zd = torch.zeros((B, 0, V), dtype=DT[dtype])
+    steps = torch.softmax(row[0, 0].double(), -1).cumsum(-1)[::2].float()
+    us = torch.cat([steps, torch.nextafter(steps, torch.zeros(())), torch.nextafter(steps, torch.ones(()))])
+    us = us.clamp(0, 1 - 2.0 ** -24)
+    us = torch.cat([us, us.new_zeros(-len(us) % B)])
+    cand = torch.zeros((B, 1), dtype=torch.int64)
+    for u in us.split(B):
+        got = _verify(zt, zd, cand, torch.zeros((B, 0)), u.contiguous(), False)
+        assert (got["bonus"] % 2 == 0).all() and got["accept_len"].tolist() == [0] * B
+
+
+@pytest.mark.parametrize("dtype,u", [("f32", float.fromhex("0x1.d1970ep-1")), ("bf16", float.fromhex("0x1.515a64p-2"))])
+def test_uniform_between_a_token_and_its_forbidden_neighbour(dtype, u):
+    """The one uniform of each row's 2^24 whose target fp32 sums put behind an allowed
+    token and before the step of the forbidden one next to it."""
+    V = 300
+    row = (2 * torch.randn((1, 1, V), generator=torch.Generator().manual_seed(0))).to(DT[dtype])
+    row[..., 1::2] = NEG
+    got = _verify(row, torch.zeros((1, 0, V), dtype=DT[dtype]), torch.zeros((1, 1), dtype=torch.int64),
+                  torch.zeros((1, 0)), torch.tensor([u]), False)
+    assert int(got["bonus"]) % 2 == 0 and int(got["flags"]) & api.FLAG_CDF_BOUNDARY
