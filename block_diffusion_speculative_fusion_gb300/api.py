@@ -73,6 +73,10 @@ class Fp8QuantDims(ctypes.Structure):
     _fields_ = [(n, c_i32) for n in ("T", "K", "dtype", "block_rows")]
 
 
+class RmsNormDims(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("T", "d", "dtype")]
+
+
 class Fp8GemmDims(ctypes.Structure):
     _fields_ = [(n, c_i32) for n in ("T", "N", "K", "out_dtype")]
 
@@ -113,6 +117,18 @@ _SIGS = {
     "dflash_logits_rules": (ctypes.c_int, [ctypes.POINTER(RulesDims)] + [c_p] * 15),
     "dflash_pages_resize": (ctypes.c_int, [ctypes.POINTER(PagesDims)] + [c_p] * 9),
     "dflash_slot_map": (ctypes.c_int, [ctypes.POINTER(PagesDims), c_i32] + [c_p] * 8),
+    # dims, parent, length, page_table, n_pages, shares, free_pages, n_free, n_pools, row_bytes, pools, n_pages_out,
+    # n_free_out, shares_out, short_seq, stream
+    "dflash_pages_fork": (ctypes.c_int, [ctypes.POINTER(PagesDims)] + [c_p] * 7 + [c_i32, ctypes.c_size_t] + [c_p] * 6),
+    "dflash_pages_release_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(PagesDims)]),
+    "dflash_pages_release": (ctypes.c_int, [ctypes.POINTER(PagesDims)] + [c_p] * 10 + [ctypes.c_size_t, c_p]),
+    "dflash_pages_compact_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(PagesDims)]),
+    # dims, page_table, n_pages, shares, n_pools, row_bytes, pools, page_table_out, shares_out, free_out, n_free_out,
+    # workspace, ws_bytes, stream
+    "dflash_pages_compact": (ctypes.c_int, [ctypes.POINTER(PagesDims)] + [c_p] * 3 + [c_i32, ctypes.c_size_t] +
+                             [c_p] * 6 + [ctypes.c_size_t, c_p]),
+    # dims, x, residual, weight, eps, sum, y, q, scale, stream
+    "dflash_rms_norm": (ctypes.c_int, [ctypes.POINTER(RmsNormDims)] + [c_p] * 3 + [ctypes.c_float] + [c_p] * 5),
     "dflash_fp8_quant": (ctypes.c_int, [ctypes.POINTER(Fp8QuantDims)] + [c_p] * 4),
     "dflash_fp8_gemm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(Fp8GemmDims)]),
     "dflash_fp8_gemm": (ctypes.c_int, [ctypes.POINTER(Fp8GemmDims)] + [c_p] * 7 + [ctypes.c_size_t, c_p]),
@@ -126,6 +142,11 @@ _SIGS = {
                                          ctypes.c_float, c_p, c_p, ctypes.c_size_t, c_p]),
     "dflash_block_attn_active": (ctypes.c_int, [ctypes.POINTER(AttnDims), c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_p,
                                                 ctypes.c_float, c_p, c_p, ctypes.c_size_t, c_p]),
+    "dflash_prefix_attn_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(AttnDims), c_i32]),
+    # dims, n_groups, q, k_blk, v_blk, k_pool, v_pool, page_table, ctx_len, group, prefix_len, scale, out, workspace,
+    # ws_bytes, stream
+    "dflash_prefix_attn": (ctypes.c_int, [ctypes.POINTER(AttnDims), c_i32] + [c_p] * 9 +
+                           [ctypes.c_float, c_p, c_p, ctypes.c_size_t, c_p]),
     "dflash_materialize_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(CtxKvDims)]),
     "dflash_materialize_ctx_kv": (ctypes.c_int, [ctypes.POINTER(CtxKvDims), c_p, c_p, c_p, c_p, c_p,
                                                  c_p, c_p, ctypes.c_float, ctypes.c_float, c_p, c_p,
@@ -660,6 +681,102 @@ def slot_map(start_pos: torch.Tensor, n_rows: torch.Tensor, page_table: torch.Te
 
 
 # ---------------------------------------------------------------------------
+# pages that rows of the block table hold together
+# ---------------------------------------------------------------------------
+def _pools(pools: Sequence[torch.Tensor], dev: int, num_pages: int, page_size: int):
+    """(count, bytes of one position, pointers) of pools [num_pages, page_size, ...] of one shape and type."""
+    if not len(pools):
+        return 0, 0, None
+    first = pools[0]
+    if not isinstance(first, torch.Tensor) or first.dim() < 2 or tuple(first.shape[:2]) != (num_pages, page_size):
+        raise ValueError(f"pools must be tensors [{num_pages}, {page_size}, ...]")
+    ptrs = (c_p * len(pools))(*[_arg(t, f"pools[{i}]", dev, first.dtype, first.shape) for i, t in enumerate(pools)])
+    return len(pools), first.stride(1) * first.element_size(), ctypes.cast(ptrs, c_p)
+
+
+def pages_fork(parent: torch.Tensor, length: torch.Tensor, page_table: torch.Tensor, n_pages: torch.Tensor,
+               shares: torch.Tensor, free_pages: torch.Tensor, n_free: torch.Tensor, page_size: int,
+               pools: Sequence[torch.Tensor] = (), out: Optional[dict] = None) -> dict:
+    """Rows that begin as copies of others (``dflash_pages_fork``): row b with
+    parent[b] = p >= 0 holds the whole pages of row p's length[p] tokens together
+    with it and gets a page of its own with the rows of the page begun, copied in
+    every pool [num_pages, page_size, ...] (K and V of every layer). parent,
+    length, n_pages [B], page_table [B, max_pages], shares, free_pages
+    [num_pages], n_free [1], all int32; page_table and the pools are changed in
+    place. Returns n_pages [B], n_free [1], shares [num_pages] int32 and short [B]
+    uint8 (1: not forked), tensors of their own."""
+    _dev(page_table, "page_table", torch.int32)
+    B, max_pages = page_table.shape
+    dev = page_table.get_device()
+    num = len(free_pages)
+    i32, seq = torch.int32, (B,)
+    n_pools, row_bytes, ptrs = _pools(pools, dev, num, page_size)
+    o = out if out is not None else {}
+    _launch(dev, lib().dflash_pages_fork, ctypes.byref(PagesDims(B, page_size, max_pages, num)),
+            _arg(parent, "parent", dev, i32, seq), _arg(length, "length", dev, i32, seq), page_table.data_ptr(),
+            _arg(n_pages, "n_pages", dev, i32, seq), _arg(shares, "shares", dev, i32, (num,)),
+            _arg(free_pages, "free_pages", dev, i32, (num,)), _arg(n_free, "n_free", dev, i32, (1,)), n_pools,
+            row_bytes, ptrs, _out(o, "n_pages", page_table, dev, i32, seq), _out(o, "n_free", page_table, dev, i32, (1,)),
+            _out(o, "shares", page_table, dev, i32, (num,)), _out(o, "short", page_table, dev, torch.uint8, seq))
+    return o
+
+
+def pages_release(length: torch.Tensor, page_table: torch.Tensor, n_pages: torch.Tensor, shares: torch.Tensor,
+                  free_pages: torch.Tensor, n_free: torch.Tensor, page_size: int, out: Optional[dict] = None,
+                  ws: Optional[torch.Tensor] = None) -> dict:
+    """Pages past length[b] tokens let go by their rows, freed where no row holds
+    them any more (``dflash_pages_release``); length 0 ends a sequence. length,
+    n_pages [B], page_table [B, max_pages], shares, free_pages [num_pages],
+    n_free [1], all int32; free_pages is changed in place. Returns n_pages [B],
+    n_free [1] and shares [num_pages] int32, tensors of their own."""
+    _dev(page_table, "page_table", torch.int32)
+    B, max_pages = page_table.shape
+    dev = page_table.get_device()
+    num = len(free_pages)
+    i32, seq = torch.int32, (B,)
+    dims = PagesDims(B, page_size, max_pages, num)
+    need = lib().dflash_pages_release_workspace_size(ctypes.byref(dims))
+    if need == 0:
+        raise DflashError(ERR_INVALID_ARG, last_error())
+    w = ws if ws is not None else workspace(page_table.device, need, slot=5)
+    o = out if out is not None else {}
+    _launch(dev, lib().dflash_pages_release, ctypes.byref(dims), _arg(length, "length", dev, i32, seq),
+            page_table.data_ptr(), _arg(n_pages, "n_pages", dev, i32, seq), _arg(shares, "shares", dev, i32, (num,)),
+            _arg(free_pages, "free_pages", dev, i32, (num,)), _arg(n_free, "n_free", dev, i32, (1,)),
+            _out(o, "n_pages", page_table, dev, i32, seq), _out(o, "n_free", page_table, dev, i32, (1,)),
+            _out(o, "shares", page_table, dev, i32, (num,)), w.data_ptr(), w.numel())
+    return o
+
+
+def pages_compact(page_table: torch.Tensor, n_pages: torch.Tensor, shares: torch.Tensor, page_size: int,
+                  pools: Sequence[torch.Tensor] = (), out: Optional[dict] = None,
+                  ws: Optional[torch.Tensor] = None) -> dict:
+    """The pages that rows hold moved to the pools' low end
+    (``dflash_pages_compact``). page_table [B, max_pages], n_pages [B], shares
+    [num_pages], all int32, are left as they are; the pools [num_pages,
+    page_size, ...] are changed in place. Returns page_table [B, max_pages],
+    shares and free_pages [num_pages], n_free [1] int32, tensors of their own."""
+    _dev(page_table, "page_table", torch.int32)
+    B, max_pages = page_table.shape
+    dev = page_table.get_device()
+    num = len(shares)
+    i32 = torch.int32
+    dims = PagesDims(B, page_size, max_pages, num)
+    need = lib().dflash_pages_compact_workspace_size(ctypes.byref(dims))
+    if need == 0:
+        raise DflashError(ERR_INVALID_ARG, last_error())
+    w = ws if ws is not None else workspace(page_table.device, need, slot=5)
+    n_pools, row_bytes, ptrs = _pools(pools, dev, num, page_size)
+    o = out if out is not None else {}
+    _launch(dev, lib().dflash_pages_compact, ctypes.byref(dims), page_table.data_ptr(),
+            _arg(n_pages, "n_pages", dev, i32, (B,)), _arg(shares, "shares", dev, i32, (num,)), n_pools, row_bytes, ptrs,
+            _out(o, "page_table", page_table, dev, i32, (B, max_pages)), _out(o, "shares", page_table, dev, i32, (num,)),
+            _out(o, "free_pages", page_table, dev, i32, (num,)), _out(o, "n_free", page_table, dev, i32, (1,)),
+            w.data_ptr(), w.numel())
+    return o
+
+
+# ---------------------------------------------------------------------------
 # (b) block attention
 # ---------------------------------------------------------------------------
 def block_attn(q: torch.Tensor, k_blk: torch.Tensor, v_blk: torch.Tensor, k_pool: torch.Tensor,
@@ -706,6 +823,44 @@ def block_attn(q: torch.Tensor, k_blk: torch.Tensor, v_blk: torch.Tensor, k_pool
         rc = lib().dflash_block_attn_active(*args, _dev(active, "active", torch.uint8, (B,)), *tail)
     _check(rc)
     return out
+
+
+def prefix_attn(q: torch.Tensor, k_blk: torch.Tensor, v_blk: torch.Tensor, k_pool: torch.Tensor,
+                v_pool: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor, group: torch.Tensor,
+                prefix_len: torch.Tensor, max_ctx: Optional[int] = None, scale: Optional[float] = None,
+                out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                causal: bool = False) -> torch.Tensor:
+    """``block_attn`` for a batch whose sequences share prefixes
+    (``dflash_prefix_attn``): sequence b's first prefix_len[group[b]] context
+    positions are those of every other sequence of its group (the same table
+    entries), and their K/V rows are read once for all of them. group [B],
+    prefix_len [n_groups] int32, n_groups <= B; a group outside [0, n_groups): no
+    shared prefix. The other arguments are those of ``block_attn``."""
+    _dev(q, "q")
+    B, n_q, Hq, D = q.shape
+    n_kv, Hkv = k_blk.shape[1], k_blk.shape[2]
+    num_pages, page = k_pool.shape[0], k_pool.shape[1]
+    max_pages = page_table.shape[1]
+    if max_ctx is None:
+        max_ctx = max_pages * page
+    dev, dt, i32 = q.get_device(), q.dtype, torch.int32
+    n_groups = len(prefix_len)
+    dims = AttnDims(B, n_q, n_kv, Hq, Hkv, D, page, max_pages, num_pages, int(max_ctx), _dtype_code(q),
+                    1 if causal else 0)
+    need = lib().dflash_prefix_attn_workspace_size(ctypes.byref(dims), n_groups)
+    if need == 0:
+        raise DflashError(ERR_INVALID_ARG, last_error())
+    w = ws if ws is not None else workspace(q.device, need, slot=6)
+    o = {"out": out}
+    blk, pool = (B, n_kv, Hkv, D), (num_pages, page, Hkv, D)
+    _launch(dev, lib().dflash_prefix_attn, ctypes.byref(dims), n_groups, q.data_ptr(),
+            _arg(k_blk, "k_blk", dev, dt, blk), _arg(v_blk, "v_blk", dev, dt, blk),
+            _arg(k_pool, "k_pool", dev, dt, pool), _arg(v_pool, "v_pool", dev, dt, pool),
+            _arg(page_table, "page_table", dev, i32, (B, max_pages)), _arg(ctx_len, "ctx_len", dev, i32, (B,)),
+            _arg(group, "group", dev, i32, (B,)), _arg(prefix_len, "prefix_len", dev, i32, (n_groups,)),
+            scale if scale is not None else D ** -0.5, _out(o, "out", q, dev, dt, tuple(q.shape)), w.data_ptr(),
+            w.numel())
+    return o["out"]
 
 
 def device_error_word(ws: torch.Tensor) -> int:
@@ -801,6 +956,29 @@ def fp8_quant(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = 
             _out(o, "q", x, dev, _E4M3, (T, K)),
             _out(o, "scale", x, dev, torch.float32, (-(-T // block_rows) if block_rows > 0 else T, -(-K // 128))))
     return o["q"], o["scale"]
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+             fp8: bool = False, want_y: Optional[bool] = None, out: Optional[dict] = None) -> dict:
+    """Root-mean-square norm of x + residual times weight, rows [T, d]
+    (``dflash_rms_norm``). Returns "sum" [T, d] if there is a residual (or ``out``
+    has it), "y" [T, d] unless ``fp8`` (or with ``want_y``), and with ``fp8`` "q"
+    [T, d] float8_e4m3fn and "scale" [T, ceil(d / 128)] float32, as ``fp8_gemm``
+    takes them (d a multiple of 16). ``out["sum"]`` may be x or residual itself,
+    and so may ``out["y"]``."""
+    _dev(x, "x")
+    T, d = x.shape
+    dev, dt = x.get_device(), x.dtype
+    rows = (T, d)
+    o = out if out is not None else {}
+    if want_y is None:
+        want_y = not fp8 or o.get("y") is not None
+    _launch(dev, lib().dflash_rms_norm, ctypes.byref(RmsNormDims(T, d, _dtype_code(x))), x.data_ptr(),
+            _arg(residual, "residual", dev, dt, rows), _arg(weight, "weight", dev, dt, (d,)), eps,
+            _out(o, "sum", x, dev, dt, rows) if residual is not None or o.get("sum") is not None else None,
+            _out(o, "y", x, dev, dt, rows) if want_y else None, _out(o, "q", x, dev, _E4M3, rows) if fp8 else None,
+            _out(o, "scale", x, dev, torch.float32, (T, -(-d // 128))) if fp8 else None)
+    return o
 
 
 def fp8_gemm(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,

@@ -91,14 +91,17 @@ struct Span {
   bool written;
 };
 // Some buffer that the call writes shares bytes with another one (null ones share none).
-template <size_t N>
-bool any_overlap(const Span (&s)[N]) {
-  for (size_t i = 0; i < N; ++i)
-    for (size_t j = i + 1; j < N; ++j) {
+bool any_overlap(const Span* s, size_t n) {
+  for (size_t i = 0; i < n; ++i)
+    for (size_t j = i + 1; j < n; ++j) {
       const uintptr_t a = (uintptr_t)s[i].p, b = (uintptr_t)s[j].p;
       if (a && b && (s[i].written || s[j].written) && a < b + s[j].bytes && b < a + s[i].bytes) return true;
     }
   return false;
+}
+template <size_t N>
+bool any_overlap(const Span (&s)[N]) {
+  return any_overlap(s, N);
 }
 }  // namespace
 
@@ -568,6 +571,139 @@ int dflash_slot_map(const dflash_pages_dims* d, int32_t rows_max, const int32_t*
   return ok(1);
 }
 
+// ------------------------------------------- pages that rows hold together ---
+static int check_share_dims(const dflash_pages_dims* d) {
+  int rc = check_pages_dims(d);
+  if (rc) return rc;
+  if (d->num_pages > 1 << 30) return fail(DFLASH_ERR_UNSUPPORTED, "num_pages=%d > 2^30", d->num_pages);
+  return DFLASH_OK;
+}
+
+// The pools of a call, checked, and appended to its buffers.
+static int take_pools(const dflash_pages_dims* d, const char* call, int32_t n, size_t row_bytes, void* const* pools,
+                      dflash::PagePools* out, Span* spans, size_t* n_spans) {
+  if (n < 0 || n > dflash::kMaxPools) return fail(DFLASH_ERR_UNSUPPORTED, "%s: n_pools=%d outside [0, %d]", call, n, dflash::kMaxPools);
+  if (n > 0 && (row_bytes == 0 || row_bytes % 2 || row_bytes > 1u << 30))
+    return fail(DFLASH_ERR_INVALID_ARG, "%s: row_bytes=%zu is not an even number in [2, 2^30]", call, row_bytes);
+  if (n > 0 && !pools) return fail(DFLASH_ERR_INVALID_ARG, "%s: a required pointer is NULL", call);
+  out->n = n;
+  out->row_bytes = row_bytes;
+  for (int i = 0; i < n; ++i) {
+    if (!pools[i]) return fail(DFLASH_ERR_INVALID_ARG, "%s: pool %d is NULL", call, i);
+    if ((uintptr_t)pools[i] % 2) return fail(DFLASH_ERR_INVALID_ARG, "%s: pool %d is not aligned to 2 bytes", call, i);
+    out->p[i] = pools[i];
+    spans[(*n_spans)++] = Span{pools[i], (size_t)d->num_pages * d->page_size * row_bytes, true};
+  }
+  return DFLASH_OK;
+}
+
+int dflash_pages_fork(const dflash_pages_dims* d, const int32_t* parent, const int32_t* length, int32_t* page_table,
+                      const int32_t* n_pages, const int32_t* shares, const int32_t* free_pages, const int32_t* n_free,
+                      int32_t n_pools, size_t row_bytes, void* const* pools, int32_t* n_pages_out, int32_t* n_free_out,
+                      int32_t* shares_out, uint8_t* short_seq, dflash_stream_t stream) {
+  CallRange range_("dflash_pages_fork");
+  int rc = check_share_dims(d);
+  if (rc) return rc;
+  if (!parent || !length || !page_table || !n_pages || !shares || !free_pages || !n_free || !n_pages_out ||
+      !n_free_out || !shares_out)
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_fork: a required pointer is NULL");
+  const size_t seq = (size_t)d->B * 4, all = (size_t)d->num_pages * 4;
+  Span spans[11 + dflash::kMaxPools] = {{parent, seq, false}, {length, seq, false}, {n_pages, seq, false},
+                                        {shares, all, false}, {free_pages, all, false}, {n_free, 4, false},
+                                        {page_table, seq * d->max_pages, true}, {n_pages_out, seq, true},
+                                        {n_free_out, 4, true}, {shares_out, all, true}, {short_seq, (size_t)d->B, true}};
+  size_t n_spans = 11;
+  dflash::ForkArgs a{};
+  rc = take_pools(d, "pages_fork", n_pools, row_bytes, pools, &a.pools, spans, &n_spans);
+  if (rc) return rc;
+  if (any_overlap(spans, n_spans))
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_fork: buffers overlap (no output may alias another buffer)");
+  a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
+  a.parent = parent; a.length = length; a.page_table = page_table; a.n_pages = n_pages; a.shares = shares;
+  a.free_pages = free_pages; a.n_free = n_free; a.n_pages_out = n_pages_out; a.n_free_out = n_free_out;
+  a.shares_out = shares_out; a.short_ = short_seq;
+  a.stream = (cudaStream_t)stream;
+  int launches = 0;
+  cudaError_t e = dflash::launch_pages_fork(a, kPlanSms, &launches);
+  if (e != cudaSuccess) return cuda_fail(e, "pages_fork launch");
+  return ok(launches);
+}
+
+size_t dflash_pages_release_workspace_size(const dflash_pages_dims* d) {
+  if (check_share_dims(d) != DFLASH_OK) return 0;
+  return DFLASH_WS_COUNTER_BYTES + dflash::pages_release_ws_bytes(d->num_pages);
+}
+
+int dflash_pages_release(const dflash_pages_dims* d, const int32_t* length, const int32_t* page_table,
+                         const int32_t* n_pages, const int32_t* shares, int32_t* free_pages, const int32_t* n_free,
+                         int32_t* n_pages_out, int32_t* n_free_out, int32_t* shares_out, void* workspace,
+                         size_t ws_bytes, dflash_stream_t stream) {
+  CallRange range_("dflash_pages_release");
+  int rc = check_share_dims(d);
+  if (rc) return rc;
+  if (!length || !page_table || !n_pages || !shares || !free_pages || !n_free || !n_pages_out || !n_free_out ||
+      !shares_out)
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_release: a required pointer is NULL");
+  const size_t need = dflash_pages_release_workspace_size(d);
+  rc = check_ws(workspace, ws_bytes, need);
+  if (rc) return rc;
+  const size_t seq = (size_t)d->B * 4, all = (size_t)d->num_pages * 4;
+  const Span spans[] = {{length, seq, false}, {page_table, seq * d->max_pages, false}, {n_pages, seq, false},
+                        {shares, all, false}, {n_free, 4, false}, {free_pages, all, true}, {n_pages_out, seq, true},
+                        {n_free_out, 4, true}, {shares_out, all, true}, {workspace, need, true}};
+  if (any_overlap(spans))
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_release: buffers overlap (no output may alias another buffer)");
+  dflash::ReleaseArgs a{};
+  a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
+  a.length = length; a.page_table = page_table; a.n_pages = n_pages; a.shares = shares; a.free_pages = free_pages;
+  a.n_free = n_free; a.n_pages_out = n_pages_out; a.n_free_out = n_free_out; a.shares_out = shares_out;
+  a.scratch = (char*)workspace + DFLASH_WS_COUNTER_BYTES;
+  a.stream = (cudaStream_t)stream;
+  int launches = 0;
+  cudaError_t e = dflash::launch_pages_release(a, kPlanSms, &launches);
+  if (e != cudaSuccess) return cuda_fail(e, "pages_release launch");
+  return ok(launches);
+}
+
+size_t dflash_pages_compact_workspace_size(const dflash_pages_dims* d) {
+  if (check_share_dims(d) != DFLASH_OK) return 0;
+  return DFLASH_WS_COUNTER_BYTES + dflash::pages_compact_ws_bytes(d->num_pages);
+}
+
+int dflash_pages_compact(const dflash_pages_dims* d, const int32_t* page_table, const int32_t* n_pages,
+                         const int32_t* shares, int32_t n_pools, size_t row_bytes, void* const* pools,
+                         int32_t* page_table_out, int32_t* shares_out, int32_t* free_out, int32_t* n_free_out,
+                         void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  CallRange range_("dflash_pages_compact");
+  int rc = check_share_dims(d);
+  if (rc) return rc;
+  if (!page_table || !n_pages || !shares || !page_table_out || !shares_out || !free_out || !n_free_out)
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_compact: a required pointer is NULL");
+  const size_t need = dflash_pages_compact_workspace_size(d);
+  rc = check_ws(workspace, ws_bytes, need);
+  if (rc) return rc;
+  const size_t seq = (size_t)d->B * 4, all = (size_t)d->num_pages * 4;
+  Span spans[8 + dflash::kMaxPools] = {{page_table, seq * d->max_pages, false}, {n_pages, seq, false},
+                                       {shares, all, false}, {page_table_out, seq * d->max_pages, true},
+                                       {shares_out, all, true}, {free_out, all, true}, {n_free_out, 4, true},
+                                       {workspace, need, true}};
+  size_t n_spans = 8;
+  dflash::CompactArgs a{};
+  rc = take_pools(d, "pages_compact", n_pools, row_bytes, pools, &a.pools, spans, &n_spans);
+  if (rc) return rc;
+  if (any_overlap(spans, n_spans))
+    return fail(DFLASH_ERR_INVALID_ARG, "pages_compact: buffers overlap (no output may alias another buffer)");
+  a.B = d->B; a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
+  a.page_table = page_table; a.n_pages = n_pages; a.shares = shares; a.page_table_out = page_table_out;
+  a.shares_out = shares_out; a.free_out = free_out; a.n_free_out = n_free_out;
+  a.scratch = (char*)workspace + DFLASH_WS_COUNTER_BYTES;
+  a.stream = (cudaStream_t)stream;
+  int launches = 0;
+  cudaError_t e = dflash::launch_pages_compact(a, kPlanSms, &launches);
+  if (e != cudaSuccess) return cuda_fail(e, "pages_compact launch");
+  return ok(launches);
+}
+
 // --------------------------------------------------------------- attention ---
 static int check_attn_dims(const dflash_attn_dims* d) {
   if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
@@ -640,6 +776,32 @@ int dflash_block_attn_active(const dflash_attn_dims* d, const void* q, const voi
                              void* workspace, size_t ws_bytes, dflash_stream_t stream) {
   CallRange range_("dflash_block_attn_active");
   return block_attn_call(d, q, k_blk, v_blk, k_pool, v_pool, page_table, ctx_len, active, scale, out, workspace,
+                         ws_bytes, stream);
+}
+
+static int check_prefix_dims(const dflash_attn_dims* d, int32_t n_groups) {
+  int rc = check_attn_dims(d);
+  if (rc) return rc;
+  if (n_groups < 0 || n_groups > d->B)
+    return fail(DFLASH_ERR_INVALID_ARG, "prefix_attn: n_groups=%d outside [0, B=%d]", n_groups, d->B);
+  return DFLASH_OK;
+}
+
+size_t dflash_prefix_attn_workspace_size(const dflash_attn_dims* d, int32_t n_groups) {
+  if (check_prefix_dims(d, n_groups) != DFLASH_OK) return 0;
+  return dflash_block_attn_workspace_size(d);
+}
+
+int dflash_prefix_attn(const dflash_attn_dims* d, int32_t n_groups, const void* q, const void* k_blk,
+                       const void* v_blk, const void* k_pool, const void* v_pool, const int32_t* page_table,
+                       const int32_t* ctx_len, const int32_t* group, const int32_t* prefix_len, float scale, void* out,
+                       void* workspace, size_t ws_bytes, dflash_stream_t stream) {
+  CallRange range_("dflash_prefix_attn");
+  int rc = check_prefix_dims(d, n_groups);
+  if (rc) return rc;
+  if (!group || (n_groups > 0 && !prefix_len))
+    return fail(DFLASH_ERR_INVALID_ARG, "prefix_attn: a required pointer is NULL");
+  return block_attn_call(d, q, k_blk, v_blk, k_pool, v_pool, page_table, ctx_len, nullptr, scale, out, workspace,
                          ws_bytes, stream);
 }
 
@@ -724,6 +886,41 @@ int dflash_fp8_quant(const dflash_fp8_quant_dims* d, const void* x, void* q, flo
   a.stream = (cudaStream_t)stream;
   cudaError_t e = dflash::launch_fp8_quant(a);
   if (e != cudaSuccess) return cuda_fail(e, "fp8_quant launch");
+  return ok(1);
+}
+
+int dflash_rms_norm(const dflash_rms_norm_dims* d, const void* x, const void* residual, const void* weight, float eps,
+                    void* sum, void* y, void* q, float* scale, dflash_stream_t stream) {
+  CallRange range_("dflash_rms_norm");
+  if (!d) return fail(DFLASH_ERR_INVALID_ARG, "dims is NULL");
+  if (d->T < 0 || d->d < 1) return fail(DFLASH_ERR_INVALID_ARG, "bad dims T=%d d=%d", d->T, d->d);
+  if (bad_dtype(d->dtype)) return fail(DFLASH_ERR_INVALID_ARG, "bad dtype %d", d->dtype);
+  if (d->T > 1 << 23 || d->d > 1 << 23) return fail(DFLASH_ERR_UNSUPPORTED, "T=%d or d=%d > 2^23", d->T, d->d);
+  if (!(eps >= 0.f) || !(eps < 3.0e38f)) return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: eps must be >= 0 and finite");
+  if ((q == nullptr) != (scale == nullptr)) return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: q and scale come together");
+  if (q && d->d % 16) return fail(DFLASH_ERR_UNSUPPORTED, "rms_norm: d=%d is not a multiple of 16", d->d);
+  if (d->T == 0) return ok(0);
+  if (!x || !weight || (!y && !q)) return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: a required pointer is NULL");
+  const uintptr_t el = d->dtype == DFLASH_BF16 ? 2 : 4;
+  for (const void* p : {x, residual, weight, (const void*)sum, (const void*)y})
+    if ((uintptr_t)p % el) return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: a tensor is not aligned to its type");
+  if (!aligned16(q) || (uintptr_t)scale % 4)
+    return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: q is not 16-byte or scale not 4-byte aligned");
+  const size_t rows = (size_t)d->T * d->d, bytes = rows * el;
+  // (an output that is an input stands for it: the thread that writes an element has read it)
+  if (y && y == sum) return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: sum and y are the same buffer");
+  const Span spans[] = {{x == sum || x == y ? nullptr : x, bytes, false},
+                        {residual == sum || residual == y ? nullptr : residual, bytes, false},
+                        {weight, d->d * el, false}, {sum, bytes, true}, {y, bytes, true}, {q, rows, true},
+                        {scale, (size_t)d->T * ((d->d + 127) / 128) * 4, true}};
+  if (any_overlap(spans))
+    return fail(DFLASH_ERR_INVALID_ARG, "rms_norm: buffers overlap without being the same");
+  dflash::NormArgs a{};
+  a.T = d->T; a.d = d->d; a.dtype = d->dtype; a.eps = eps;
+  a.x = x; a.residual = residual; a.weight = weight; a.sum = sum; a.y = y; a.q = q; a.scale = scale;
+  a.stream = (cudaStream_t)stream;
+  cudaError_t e = dflash::launch_rms_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, "rms_norm launch");
   return ok(1);
 }
 

@@ -9,22 +9,14 @@
 // more than the tensor core's fp32; the groups' sums meet in fp32 registers,
 // each multiplied by its own scales (the scales are arbitrary fp32 numbers, so
 // they cannot ride in the MMA, which takes powers of two per 32 values).
-#include <cuda_fp8.h>
-
 #include <algorithm>
 
-#include "common.cuh"
+#include "e4m3.cuh"
 #include "internal.h"
 #include "tc.cuh"
 #include "tma.cuh"
 
 namespace dflash {
-
-namespace f8 {
-constexpr int G = 128;                    // values per scale, and the k-block
-constexpr float kMax = 448.f;             // largest finite e4m3
-constexpr float kMinScale = 1.17549435e-38f;
-}  // namespace f8
 
 // ---------------------------------------------------------------------------
 // Quantisation. Bound: one read and one write. A warp takes whole groups (16
@@ -37,8 +29,6 @@ template <typename T> constexpr uint32_t kAbs = sizeof(T) == 4 ? 0x7fffffffu : 0
 template <typename T> __device__ __forceinline__ float vec_absmax(const uint4& u) {
   return vec_max<T>(make_uint4(u.x & kAbs<T>, u.y & kAbs<T>, u.z & kAbs<T>, u.w & kAbs<T>));
 }
-__device__ __forceinline__ float f8_scale(float amax) { return fmaxf(__fdiv_rn(amax, f8::kMax), f8::kMinScale); }
-
 // The vector's values times 1 / scale (a division each would bound the kernel by
 // its instructions: 138 us instead of 99 for 8190 x 20480 bf16), four e4m3 to a word.
 template <typename T> __device__ __forceinline__ void f8_store(uint8_t* dst, const uint4& u, float r) {
@@ -47,11 +37,7 @@ template <typename T> __device__ __forceinline__ void f8_store(uint8_t* dst, con
   unpack16<T>(u, f);
   uint32_t w[N / 4];
 #pragma unroll
-  for (int j = 0; j < N; j += 4) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[j] * r, f[j + 1] * r), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[j + 2] * r, f[j + 3] * r), __NV_SATFINITE, __NV_E4M3);
-    w[j / 4] = lo | (hi << 16);
-  }
+  for (int j = 0; j < N; j += 4) w[j / 4] = f8_pack4(f[j] * r, f[j + 1] * r, f[j + 2] * r, f[j + 3] * r);
   if constexpr (N == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t*>(dst) = w[0];
 }

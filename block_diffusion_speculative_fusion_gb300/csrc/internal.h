@@ -227,6 +227,62 @@ struct SlotArgs {
 };
 cudaError_t launch_slot_map(const SlotArgs& a, int num_sms);
 
+// Pages that rows hold together: shares[p] rows hold page p beyond the first.
+constexpr int kMaxPools = 32;            // K and V of every draft layer
+struct PagePools {
+  int n;
+  size_t row_bytes;            // of one position in one pool
+  void* p[kMaxPools];          // [num_pages, page_size, row_bytes]
+};
+struct ForkArgs {
+  int B, page_size, max_pages, num_pages;
+  const int32_t* parent;       // [B], -1: none
+  const int32_t* length;       // [B]
+  int32_t* page_table;         // [B, max_pages]
+  const int32_t* n_pages;      // [B]
+  const int32_t* shares;       // [num_pages]
+  const int32_t* free_pages;   // [num_pages]
+  const int32_t* n_free;       // [1]
+  int32_t* n_pages_out;        // [B]
+  int32_t* n_free_out;         // [1]
+  int32_t* shares_out;         // [num_pages]
+  uint8_t* short_;             // [B] or null
+  PagePools pools;
+  cudaStream_t stream;
+};
+cudaError_t launch_pages_fork(const ForkArgs& a, int num_sms, int* launches);
+struct ReleaseArgs {
+  int B, page_size, max_pages, num_pages;
+  const int32_t* length;       // [B]
+  const int32_t* page_table;   // [B, max_pages]
+  const int32_t* n_pages;      // [B]
+  const int32_t* shares;       // [num_pages]
+  int32_t* free_pages;         // [num_pages]
+  const int32_t* n_free;       // [1]
+  int32_t* n_pages_out;        // [B]
+  int32_t* n_free_out;         // [1]
+  int32_t* shares_out;         // [num_pages]
+  void* scratch;
+  cudaStream_t stream;
+};
+size_t pages_release_ws_bytes(int num_pages);
+cudaError_t launch_pages_release(const ReleaseArgs& a, int num_sms, int* launches);
+struct CompactArgs {
+  int B, page_size, max_pages, num_pages;
+  const int32_t* page_table;   // [B, max_pages]
+  const int32_t* n_pages;      // [B]
+  const int32_t* shares;       // [num_pages]
+  int32_t* page_table_out;     // [B, max_pages]
+  int32_t* shares_out;         // [num_pages]
+  int32_t* free_out;           // [num_pages]
+  int32_t* n_free_out;         // [1]
+  PagePools pools;
+  void* scratch;
+  cudaStream_t stream;
+};
+size_t pages_compact_ws_bytes(int num_pages);
+cudaError_t launch_pages_compact(const CompactArgs& a, int num_sms, int* launches);
+
 // ------------------------------------------------------------- attention ---
 struct AttnArgs {
   int B, n_q, n_kv, Hq, Hkv, D, page_size, max_pages, num_pages, max_ctx, dtype;
@@ -272,6 +328,21 @@ struct Fp8GemmArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a);
+
+// ------------------------------------------------ root-mean-square norm ---
+struct NormArgs {
+  int T, d, dtype;
+  float eps;
+  const void* x;                 // [T, d]
+  const void* residual;          // [T, d] or null
+  const void* weight;            // [d]
+  void* sum;                     // [T, d] x + residual, or null; may be x or residual
+  void* y;                       // [T, d] or null; may be x or residual
+  void* q;                       // [T, d] e4m3, or null
+  float* scale;                  // [T, ceil(d / 128)] with q
+  cudaStream_t stream;
+};
+cudaError_t launch_rms_norm(const NormArgs& a);
 
 // ----------------------------------------------------------- materialise ---
 constexpr int kMaxLayers = 16;

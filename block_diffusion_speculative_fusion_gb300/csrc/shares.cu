@@ -1,0 +1,425 @@
+// Pages of the paged cache that several rows of the block table hold together:
+// sequences that begin as copies of others (fork), pages let go and freed where no
+// row holds them any more (release), and the pages in use moved to the pools' low
+// end (compact). shares[p] counts the rows that hold page p beyond the first, so a
+// page held once, and every page that dflash_pages_resize hands out, has 0.
+//   [SGLang] 5.1: the block table (req_to_token) that these rewrite.
+//
+// Each is a chain of dependent launches, one per value that all CTAs must agree on
+// (a count reset, the counts, the places that follow from them); no CTA waits for
+// another. Counts are whole numbers, so the order of the atomics does not show;
+// freed pages are listed by their number, not by who came last. Outputs stand in
+// buffers of their own: a call can be repeated with the same result. Bound: the
+// launches for a small batch, the bytes copied for fork and compact.
+#include <algorithm>
+
+#include "internal.h"
+#include "pages.cuh"
+
+namespace dflash {
+
+namespace shares {
+constexpr int kSeg = 2048;               // pages of one CTA of the kernels that go by page
+constexpr int kPer = kSeg / pages::kThreads;
+constexpr int kCopyVecs = 8;             // vectors a lane that a copying warp keeps in flight
+}  // namespace shares
+
+// `bytes` from src to dst by one warp, V bytes a lane at a time.
+template <typename V>
+__device__ __forceinline__ void warp_copy(char* dst, const char* src, size_t bytes, int lane) {
+  using namespace shares;
+  const V* s = reinterpret_cast<const V*>(src);
+  V* d = reinterpret_cast<V*>(dst);
+  const size_t n = bytes / sizeof(V);
+  for (size_t i0 = lane; i0 < n; i0 += 32 * kCopyVecs) {
+    V v[kCopyVecs];
+#pragma unroll
+    for (int u = 0; u < kCopyVecs; ++u)
+      if (i0 + 32 * u < n) v[u] = s[i0 + 32 * u];
+#pragma unroll
+    for (int u = 0; u < kCopyVecs; ++u)
+      if (i0 + 32 * u < n) d[i0 + 32 * u] = v[u];
+  }
+}
+
+static bool vectors16(const PagePools& p) {
+  bool ok = p.row_bytes % 16 == 0;
+  for (int i = 0; i < p.n; ++i) ok = ok && (reinterpret_cast<uintptr_t>(p.p[i]) & 15u) == 0;
+  return ok;
+}
+
+__device__ __forceinline__ bool in_pool(int page, int num_pages) { return page >= 0 && page < num_pages; }
+
+// Pages that the length takes; a row that must not grow counts no more than it holds.
+__device__ __forceinline__ int pages_of(int length, int page_size) {
+  const int n = max(length, 0);
+  return n / page_size + (n % page_size != 0);
+}
+
+// ---------------------------------------------------------------------------
+// Counts copied to where they will change (negative ones are 0), and words zeroed.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(pages::kThreads)
+shares_copy_kernel(const int32_t* from, int32_t* to, int n, int32_t* zero, int n_zero) {
+  wait_for_prior_grid();
+  dependents_may_launch();
+  for (int i = blockIdx.x * pages::kThreads + threadIdx.x; i < max(n, n_zero); i += gridDim.x * pages::kThreads) {
+    if (i < n) to[i] = max(from[i], 0);
+    if (i < n_zero) zero[i] = 0;
+  }
+}
+
+static cudaError_t launch_shares_copy(const int32_t* from, int32_t* to, int n, int32_t* zero, int n_zero, int num_sms,
+                                      cudaStream_t st) {
+  const int grid = std::max(1, std::min(num_sms, (std::max(n, n_zero) + pages::kThreads - 1) / pages::kThreads));
+  return launch_dependent(shares_copy_kernel, dim3(grid), dim3(pages::kThreads), 0, st, from, to, n, zero, n_zero);
+}
+
+// ---------------------------------------------------------------------------
+// Fork. Every CTA forms the prefix of the pages asked for (one a child whose parent
+// has begun a page), as pages_resize does. Then warps take units: a segment of a
+// child's row, a segment of a parent's pages (one atomic for all its children), or
+// the rows of a begun page in one pool.
+// ---------------------------------------------------------------------------
+template <typename V>
+__global__ void __launch_bounds__(pages::kThreads, 2)
+pages_fork_kernel(const __grid_constant__ ForkArgs a) {
+  using namespace pages;
+  wait_for_prior_grid();
+  dependents_may_launch();
+  __shared__ int s_take[kPagesMaxB];        // a child's page, counted from the list's end; -1: no fork
+  __shared__ int s_kids[kPagesMaxB];        // children that a parent gets
+  const int tid = threadIdx.x, lane = tid & 31, B = a.B;
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  const int n_free = min(max(*a.n_free, 0), a.num_pages);
+  auto held = [&](int b) { return min(max(a.n_pages[b], 0), a.max_pages); };
+  // whether row b can be forked from its parent, its pages aside
+  auto valid = [&](int b, int p) {
+    return in_pool(p, B) && p != b && a.parent[p] < 0 && held(b) == 0 && pages_of(a.length[p], a.page_size) <= held(p);
+  };
+  for (int b = tid; b < B; b += kThreads) s_kids[b] = 0;
+  long long want = 0, total;
+  for (int b = b0; b < b1; ++b) {
+    const int p = a.parent[b];
+    const bool ok = p >= 0 && valid(b, p);
+    const int rest = ok && max(a.length[p], 0) % a.page_size != 0;
+    s_take[b] = ok ? rest : -1;
+    want += rest;
+  }
+  int at = (int)block_prefix(want, &total);   // (its barriers stand between s_kids' two writers)
+  int taken = 0;                              // pages of the granted: their prefix ends at the largest
+  for (int b = b0; b < b1; ++b) {
+    const int w = s_take[b];
+    if (w < 0) continue;
+    const bool granted = !w || at < n_free;   // not, if the list cannot meet it with those before it
+    s_take[b] = granted ? at : -1;
+    if (granted) atomicAdd(&s_kids[a.parent[b]], 1);
+    at += w;
+    if (granted && w) taken = at;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int b = tid; b < B; b += kThreads) {
+      const int p = a.parent[b];
+      a.n_pages_out[b] = s_take[b] >= 0 ? pages_of(a.length[p], a.page_size) : held(b);
+      if (a.short_) a.short_[b] = p >= 0 && s_take[b] < 0;
+    }
+    __shared__ int s_max;
+    if (tid == 0) s_max = 0;
+    __syncthreads();
+    atomicMax(&s_max, taken);
+    __syncthreads();
+    if (tid == 0) *a.n_free_out = n_free - s_max;
+  }
+  const int segs = (a.max_pages + kSegment - 1) / kSegment;
+  // (the widest units first: the copies of begun pages)
+  const long copies = (long)B * a.pools.n, rows = (long)B * segs;
+  for (long u = (long)blockIdx.x * kWarps + (tid >> 5); u < copies + 2 * rows; u += (long)gridDim.x * kWarps) {
+    if (u < copies) {
+      const int b = (int)(u / a.pools.n), i = (int)(u - (long)b * a.pools.n);
+      if (s_take[b] < 0) continue;
+      const int p = a.parent[b], n = max(a.length[p], 0), rest = n % a.page_size;
+      if (!rest) continue;
+      const int src = a.page_table[(size_t)p * a.max_pages + n / a.page_size];
+      const int dst = a.free_pages[n_free - 1 - s_take[b]];
+      if (!in_pool(src, a.num_pages) || !in_pool(dst, a.num_pages) || src == dst) continue;
+      char* pool = (char*)a.pools.p[i];
+      const size_t page_bytes = a.pools.row_bytes * a.page_size;
+      warp_copy<V>(pool + dst * page_bytes, pool + src * page_bytes, a.pools.row_bytes * rest, lane);
+    } else if (u < copies + rows) {
+      const long w = u - copies;
+      const int b = (int)(w / segs), i0 = (int)(w - (long)b * segs) * kSegment + lane;
+      if (s_take[b] < 0) continue;
+      const int p = a.parent[b], n = max(a.length[p], 0), full = n / a.page_size, rest = n % a.page_size;
+      const int32_t* from = a.page_table + (size_t)p * a.max_pages;
+      int32_t* to = a.page_table + (size_t)b * a.max_pages;
+      int page[kSegment / 32];
+#pragma unroll
+      for (int q = 0; q < kSegment / 32; ++q)
+        if (i0 + 32 * q < full) page[q] = from[i0 + 32 * q];
+#pragma unroll
+      for (int q = 0; q < kSegment / 32; ++q) {
+        const int i = i0 + 32 * q;
+        if (i < full) to[i] = page[q];
+        if (i == full && rest) to[i] = a.free_pages[n_free - 1 - s_take[b]];
+      }
+    } else {
+      const long w = u - copies - rows;
+      const int p = (int)(w / segs), i0 = (int)(w - (long)p * segs) * kSegment + lane;
+      const int kids = s_kids[p];
+      if (!kids) continue;
+      const int full = max(a.length[p], 0) / a.page_size;
+#pragma unroll
+      for (int q = 0; q < kSegment / 32; ++q) {
+        const int i = i0 + 32 * q;
+        if (i >= full) continue;
+        const int page = a.page_table[(size_t)p * a.max_pages + i];
+        if (in_pool(page, a.num_pages)) atomicAdd(a.shares_out + page, kids);
+      }
+    }
+  }
+}
+
+cudaError_t launch_pages_fork(const ForkArgs& a, int num_sms, int* launches) {
+  cudaError_t e = launch_shares_copy(a.shares, a.shares_out, a.num_pages, nullptr, 0, num_sms, a.stream);
+  if (e != cudaSuccess) return e;
+  const int segs = (a.max_pages + pages::kSegment - 1) / pages::kSegment;
+  const long units = (long)a.B * (a.pools.n + 2L * segs);
+  const dim3 grid((unsigned)std::min(2L * num_sms, (units + pages::kWarps - 1) / pages::kWarps));
+  *launches = 2;
+  if (vectors16(a.pools)) return launch_dependent(pages_fork_kernel<uint4>, grid, dim3(pages::kThreads), 0, a.stream, a);
+  return launch_dependent(pages_fork_kernel<uint16_t>, grid, dim3(pages::kThreads), 0, a.stream, a);
+}
+
+// ---------------------------------------------------------------------------
+// Release. A page's count goes down by one for every row that lets it go; who takes
+// it from 0 to -1 frees it and counts it for its segment of the pool, so that the
+// last kernel lists the freed pages by their number with one prefix sum a segment.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(pages::kThreads)
+pages_let_go_kernel(const ReleaseArgs a) {
+  using namespace pages;
+  wait_for_prior_grid();
+  dependents_may_launch();
+  int32_t* seg = (int32_t*)a.scratch;
+  const int lane = threadIdx.x & 31, segs = (a.max_pages + kSegment - 1) / kSegment;
+  const long units = (long)a.B * segs;
+  for (long u = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (long)gridDim.x * kWarps) {
+    const int b = (int)(u / segs), i0 = (int)(u - (long)b * segs) * kSegment + lane;
+    const int h = min(max(a.n_pages[b], 0), a.max_pages), k = min(pages_of(a.length[b], a.page_size), h);
+    if (i0 == 0) a.n_pages_out[b] = k;
+    int page[kSegment / 32], old[kSegment / 32];
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q) {
+      const int i = i0 + 32 * q;
+      page[q] = i >= k && i < h ? a.page_table[(size_t)b * a.max_pages + i] : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q)
+      old[q] = in_pool(page[q], a.num_pages) ? atomicSub(a.shares_out + page[q], 1) : 1;
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q)
+      if (old[q] == 0) atomicAdd(seg + page[q] / shares::kSeg, 1);
+  }
+}
+
+__global__ void __launch_bounds__(pages::kThreads)
+pages_freed_kernel(const ReleaseArgs a) {
+  using namespace pages;
+  using namespace shares;
+  wait_for_prior_grid();
+  dependents_may_launch();
+  const int32_t* seg = (const int32_t*)a.scratch;
+  const int n_free = min(max(*a.n_free, 0), a.num_pages);
+  long long before = 0, all;
+  for (int i = threadIdx.x; i < (int)blockIdx.x; i += kThreads) before += seg[i];
+  block_prefix(before, &before);            // the total: freed pages of the segments before
+  const int p0 = blockIdx.x * kSeg + threadIdx.x * kPer;
+  int s[kPer], n = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    s[j] = p0 + j < a.num_pages ? a.shares_out[p0 + j] : 0;
+    n += s[j] < 0;
+  }
+  long long at = n_free + before + block_prefix(n, &all);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j)
+    if (s[j] < 0) {
+      a.shares_out[p0 + j] = 0;
+      if (at < a.num_pages) a.free_pages[at] = p0 + j;
+      ++at;
+    }
+  if (blockIdx.x == gridDim.x - 1 && threadIdx.x == 0)
+    *a.n_free_out = (int)min(n_free + before + all, (long long)a.num_pages);
+}
+
+static int seg_count(int num_pages) { return (int)(((long)num_pages + shares::kSeg - 1) / shares::kSeg); }
+
+size_t pages_release_ws_bytes(int num_pages) { return align_up((size_t)seg_count(num_pages) * sizeof(int32_t)); }
+
+cudaError_t launch_pages_release(const ReleaseArgs& a, int num_sms, int* launches) {
+  const int segs = seg_count(a.num_pages);
+  cudaError_t e =
+      launch_shares_copy(a.shares, a.shares_out, a.num_pages, (int32_t*)a.scratch, segs, num_sms, a.stream);
+  if (e != cudaSuccess) return e;
+  const long units = (long)a.B * ((a.max_pages + pages::kSegment - 1) / pages::kSegment);
+  const dim3 grid((unsigned)std::min(4L * num_sms, (units + pages::kWarps - 1) / pages::kWarps));
+  e = launch_dependent(pages_let_go_kernel, grid, dim3(pages::kThreads), 0, a.stream, a);
+  if (e != cudaSuccess) return e;
+  *launches = 3;
+  return launch_dependent(pages_freed_kernel, dim3(segs), dim3(pages::kThreads), 0, a.stream, a);
+}
+
+// ---------------------------------------------------------------------------
+// Compact. A bit for every page that a row holds, and their number per segment; with
+// U(p) the pages in use below p and n those in use in all, page p < n not in use is
+// the (p - U(p))-th hole and page p >= n in use the (U(p) - U(n))-th to move.
+// ---------------------------------------------------------------------------
+struct CompactScratch {
+  int32_t *seg, *bits, *hole, *mover, *rank, *n_moves;
+};
+__host__ __device__ inline CompactScratch compact_scratch(void* base, int num_pages) {
+  const size_t segs = ((size_t)num_pages + shares::kSeg - 1) / shares::kSeg;
+  CompactScratch c;
+  c.seg = (int32_t*)base;                     // [segs] pages in use of each segment
+  c.bits = c.seg + segs;                      // [segs * kSeg / 32]
+  c.n_moves = c.bits + segs * (shares::kSeg / 32);
+  c.hole = c.n_moves + 1;                     // [num_pages] the holes in order
+  c.mover = c.hole + num_pages;               // [num_pages] the pages to move in order
+  c.rank = c.mover + num_pages;               // [num_pages] a moving page's place in that order
+  return c;
+}
+
+__global__ void __launch_bounds__(pages::kThreads)
+pages_mark_kernel(const CompactArgs a) {
+  using namespace pages;
+  wait_for_prior_grid();
+  dependents_may_launch();
+  const CompactScratch c = compact_scratch(a.scratch, a.num_pages);
+  const int lane = threadIdx.x & 31, segs = (a.max_pages + kSegment - 1) / kSegment;
+  const long units = (long)a.B * segs;
+  for (long u = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (long)gridDim.x * kWarps) {
+    const int b = (int)(u / segs), i0 = (int)(u - (long)b * segs) * kSegment + lane;
+    const int h = min(max(a.n_pages[b], 0), a.max_pages);
+    int page[kSegment / 32], old[kSegment / 32];
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q)
+      page[q] = i0 + 32 * q < h ? a.page_table[(size_t)b * a.max_pages + i0 + 32 * q] : -1;
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q)
+      old[q] = in_pool(page[q], a.num_pages) ? atomicOr(c.bits + (page[q] >> 5), 1 << (page[q] & 31)) : -1;
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q)
+      if (!((old[q] >> (page[q] & 31)) & 1)) atomicAdd(c.seg + page[q] / shares::kSeg, 1);
+  }
+}
+
+__global__ void __launch_bounds__(pages::kThreads)
+pages_plan_kernel(const CompactArgs a) {
+  using namespace pages;
+  using namespace shares;
+  wait_for_prior_grid();
+  dependents_may_launch();
+  const CompactScratch c = compact_scratch(a.scratch, a.num_pages);
+  const int segs = gridDim.x, s0 = blockIdx.x;
+  long long mine = 0, sum = 0, n_used, before;
+  for (int i = threadIdx.x; i < segs; i += kThreads) {
+    const int n = c.seg[i];
+    sum += n;
+    mine += i < s0 ? n : 0;
+  }
+  block_prefix(sum, &n_used);
+  block_prefix(mine, &before);                // in use in the segments before this one
+  // U(n): the segments before n's, and the bits before n in it
+  const int n = (int)n_used, sn = n / kSeg;
+  long long un = 0;
+  for (int i = threadIdx.x; i < min(sn, segs); i += kThreads) un += c.seg[i];
+  for (int w = sn * (kSeg / 32) + threadIdx.x; w * 32 < n; w += kThreads) {
+    const unsigned m = n - w * 32 >= 32 ? 0xffffffffu : (1u << (n - w * 32)) - 1;
+    un += __popc((unsigned)c.bits[w] & m);
+  }
+  block_prefix(un, &un);
+  const int p0 = s0 * kSeg + threadIdx.x * kPer;
+  const unsigned word = (unsigned)c.bits[p0 >> 5] >> (p0 & 31);   // kPer divides 32
+  long long all;
+  int U = (int)(before + block_prefix(__popc(word & ((1u << kPer) - 1)), &all));
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int p = p0 + j;
+    if (p >= a.num_pages) break;
+    const bool used = (word >> j) & 1;
+    if (p < n && !used) c.hole[p - U] = p;
+    if (p >= n && used) {
+      c.mover[U - un] = p;
+      c.rank[p] = U - (int)un;
+    }
+    if (used || p >= n) a.shares_out[p] = used && p < n ? max(a.shares[p], 0) : 0;   // a hole's comes with its page
+    a.free_out[p] = a.num_pages - 1 - p;
+    U += used;
+  }
+  if (s0 == 0 && threadIdx.x == 0) {
+    *a.n_free_out = a.num_pages - n;
+    *c.n_moves = n - (int)un;
+  }
+}
+
+template <typename V>
+__global__ void __launch_bounds__(pages::kThreads, 2)
+pages_move_kernel(const __grid_constant__ CompactArgs a) {
+  using namespace pages;
+  wait_for_prior_grid();
+  dependents_may_launch();
+  const CompactScratch c = compact_scratch(a.scratch, a.num_pages);
+  const int lane = threadIdx.x & 31, segs = (a.max_pages + kSegment - 1) / kSegment;
+  const int n = a.num_pages - *a.n_free_out, moves = *c.n_moves;
+  const long warp = (long)blockIdx.x * kWarps + (threadIdx.x >> 5), warps = (long)gridDim.x * kWarps;
+  // the table's rows, and a moving page's count
+  const long rows = (long)a.B * segs;
+  for (long u = warp; u < rows; u += warps) {
+    const int b = (int)(u / segs), i0 = (int)(u - (long)b * segs) * kSegment + lane;
+    const int h = min(max(a.n_pages[b], 0), a.max_pages);
+#pragma unroll
+    for (int q = 0; q < kSegment / 32; ++q) {
+      const int i = i0 + 32 * q;
+      if (i >= a.max_pages) break;
+      int page = a.page_table[(size_t)b * a.max_pages + i];
+      if (i < h && page >= n && page < a.num_pages) page = c.hole[c.rank[page]];
+      a.page_table_out[(size_t)b * a.max_pages + i] = page;
+    }
+  }
+  for (long r = warp * 32 + lane; r < moves; r += warps * 32) a.shares_out[c.hole[r]] = max(a.shares[c.mover[r]], 0);
+  // the pages: a warp's unit is one page of one pool
+  const size_t page_bytes = a.pools.row_bytes * a.page_size;
+  for (long u = warp; u < (long)moves * a.pools.n; u += warps) {
+    const int i = (int)(u / moves), r = (int)(u - (long)i * moves);
+    char* pool = (char*)a.pools.p[i];
+    warp_copy<V>(pool + c.hole[r] * page_bytes, pool + c.mover[r] * page_bytes, page_bytes, lane);
+  }
+}
+
+size_t pages_compact_ws_bytes(int num_pages) {
+  const size_t segs = seg_count(num_pages);
+  return align_up((segs * (1 + shares::kSeg / 32) + 1 + 3 * (size_t)num_pages) * sizeof(int32_t));
+}
+
+cudaError_t launch_pages_compact(const CompactArgs& a, int num_sms, int* launches) {
+  const int segs = seg_count(a.num_pages);
+  const CompactScratch c = compact_scratch(a.scratch, a.num_pages);
+  cudaError_t e = launch_shares_copy(nullptr, nullptr, 0, c.seg, segs * (1 + shares::kSeg / 32), num_sms, a.stream);
+  if (e != cudaSuccess) return e;
+  const long units = (long)a.B * ((a.max_pages + pages::kSegment - 1) / pages::kSegment);
+  const dim3 rows((unsigned)std::min(4L * num_sms, (units + pages::kWarps - 1) / pages::kWarps));
+  e = launch_dependent(pages_mark_kernel, rows, dim3(pages::kThreads), 0, a.stream, a);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(pages_plan_kernel, dim3(segs), dim3(pages::kThreads), 0, a.stream, a);
+  if (e != cudaSuccess) return e;
+  *launches = 4;
+  // how many pages move is known on the device: a full wave, or what all of them could take
+  const long most = units + (long)a.num_pages / 2 * a.pools.n;
+  const dim3 grid((unsigned)std::max(1L, std::min(2L * num_sms, (most + pages::kWarps - 1) / pages::kWarps)));
+  if (vectors16(a.pools)) return launch_dependent(pages_move_kernel<uint4>, grid, dim3(pages::kThreads), 0, a.stream, a);
+  return launch_dependent(pages_move_kernel<uint16_t>, grid, dim3(pages::kThreads), 0, a.stream, a);
+}
+
+}  // namespace dflash

@@ -11,8 +11,10 @@
  *   dflash_verify_sample       the min(1, p/q) accept rule with residual resample
  *   dflash_gate                the DLoop block gate c_s >= g
  * and the operators that a serving program runs around them: rules on the
- * verify rows' logits, block tables and slot maps of the paged cache, and the
- * 8-bit quantisation, product and materialisation.
+ * verify rows' logits, block tables and slot maps of the paged cache, pages that
+ * sequences hold together (fork, release, compact) and attention that reads a
+ * shared prefix once, the residual norm, and the 8-bit quantisation, product and
+ * materialisation.
  *
  * Conventions shared by every call:
  *   - Tensor arguments are DEVICE pointers owned by the caller; the library
@@ -32,7 +34,8 @@
  *     stream; such a call's later kernels (the attention split merge, the
  *     materialisation's GEMMs, bias and epilogue, the sampled draw), and the
  *     one kernel of dflash_logits_rules, dflash_pages_resize, dflash_slot_map,
- *     dflash_fp8_quant and dflash_fp8_gemm, are programmatic dependent launches
+ *     dflash_fp8_quant, dflash_fp8_gemm and dflash_rms_norm, and every kernel of
+ *     dflash_pages_fork, _release and _compact, are programmatic dependent launches
  *     that may become resident while the kernel before them runs but read and
  *     write none of the caller's memory until it completes.
  *   - Return value: DFLASH_OK, or an error code with a message available from
@@ -255,6 +258,31 @@ int dflash_block_attn_active(const dflash_attn_dims* dims,
                              const int32_t* page_table, const int32_t* ctx_len, const uint8_t* active,
                              float scale, void* out, void* workspace, size_t ws_bytes,
                              dflash_stream_t stream);
+
+/*
+ * dflash_block_attn for a batch whose sequences share prefixes: the result is
+ * that of dflash_block_attn (up to the rounding of its sums), but the K/V rows of
+ * a shared prefix are read once for the queries of all its sequences, which then
+ * fill the matrix instructions' rows, and not once a sequence. The tables that
+ * dflash_pages_fork makes are such.
+ * group [B] int32: the sequence's prefix, in [0, n_groups); any other value: none
+ * prefix_len [n_groups] int32: the context positions that the group's sequences
+ *   have in common. Their table entries must be the same in all of the group's
+ *   rows; those of the first one (by its number) are read. At most the smallest
+ *   ctx_len of the group counts (negative: 0).
+ * Every other argument as dflash_block_attn, whose checks and error words apply.
+ * n_groups in [0, B]. The shared kernel takes bf16, D = 128, pages of 8, 16, 32, 64
+ * or 128 positions, B <= 1024, n_kv_blk <= 128 and pointers aligned to 16 bytes;
+ * for other calls the prefix is read once a sequence, as by dflash_block_attn.
+ * Repeated calls on the same inputs return identical bits.
+ */
+size_t dflash_prefix_attn_workspace_size(const dflash_attn_dims* dims, int32_t n_groups);
+int dflash_prefix_attn(const dflash_attn_dims* dims, int32_t n_groups,
+                       const void* q, const void* k_blk, const void* v_blk,
+                       const void* k_pool, const void* v_pool,
+                       const int32_t* page_table, const int32_t* ctx_len,
+                       const int32_t* group, const int32_t* prefix_len, float scale,
+                       void* out, void* workspace, size_t ws_bytes, dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
 /* (c) Verify                                                                 */
@@ -542,6 +570,34 @@ int dflash_fp8_quant(const dflash_fp8_quant_dims* dims, const void* x, void* q, 
                      dflash_stream_t stream);
 
 typedef struct {
+  int32_t T;      /* rows, 0 .. 2^23 (0: nothing is done) */
+  int32_t d;      /* columns, <= 2^23 */
+  int32_t dtype;  /* type of x, residual, weight, sum and y */
+} dflash_rms_norm_dims;
+
+/*
+ * Root-mean-square norm of a sum with the residual, for the rows that a product
+ * takes next: in their own type, in the e4m3 of dflash_fp8_quant (block_rows 1),
+ * or both.
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight   (mean over a row)
+ *   scale = max(amax / 448, 2^-126) per 128 values of y,  q = e4m3(y * (1 / scale))
+ * in fp32, y rounded to dtype once and q rounded from the unrounded y. A row whose
+ * squares leave fp32's range is normed as exactly as any other.
+ * x [T, d]; residual [T, d] or NULL (s = x); weight [d]; eps >= 0
+ * sum [T, d] or NULL: s rounded to dtype (what the next layer adds to)
+ * y [T, d] or NULL; q [T, d] e4m3 with scale [T, ceil(d / 128)] float, both or
+ *   neither; one of y and q at least
+ * sum may be x or residual, and so may y (in place; sum and y are then not the
+ * same one); no other overlap. With q: d is a multiple of 16 and q 16-byte
+ * aligned. Every other tensor is aligned to its type; rows are taken by vectors
+ * where all of them start at multiples of 16 bytes, d is a multiple of 16 bytes'
+ * elements and a row is at most 65536 bytes (an element at a time otherwise).
+ * No workspace; repeated calls give identical bits.
+ */
+int dflash_rms_norm(const dflash_rms_norm_dims* dims, const void* x, const void* residual, const void* weight,
+                    float eps, void* sum, void* y, void* q, float* scale, dflash_stream_t stream);
+
+typedef struct {
   int32_t T;          /* rows of x, 0 .. 2^23 (0: nothing is done) */
   int32_t N;          /* rows of w: columns of out, <= 2^23 */
   int32_t K;          /* shared dimension, a multiple of 16, <= 2^23 */
@@ -709,6 +765,88 @@ int dflash_pages_resize(const dflash_pages_dims* dims, const int32_t* length, in
 int dflash_slot_map(const dflash_pages_dims* dims, int32_t rows_max, const int32_t* start_pos,
                     const int32_t* n_rows, const int32_t* page_table, int32_t* cu_rows, int32_t* row_seq,
                     int32_t* positions, int64_t* slots, dflash_stream_t stream);
+
+/*
+ * Pages that several rows of the table hold together: shares[p] rows hold page p
+ * beyond the first. It is 0 for a free page, for a page held once, and so for
+ * every page that dflash_pages_resize gives a row: that call knows no shares, so
+ * it may take back the pages of a row's headroom but none with shares[p] > 0; rows
+ * that hold such pages end by dflash_pages_release. Rows of the table that are held
+ * together are read only up to the pages begun: what a sequence writes goes to
+ * pages of its own.
+ *
+ * In the three calls below shares [num_pages] int32 is read (negative: 0) and
+ * shares_out [num_pages] int32 written; the outputs stand in buffers of their own,
+ * so that a call can be repeated with the same result. No two buffers may overlap
+ * unless both are only read. num_pages <= 2^30. Table entries outside
+ * [0, num_pages) inside a row's n_pages[b] are carried along and otherwise passed
+ * over.
+ */
+
+/*
+ * Rows that begin as copies of others: n samples of one prompt, or a search that
+ * branches. Row b with parent[b] = p >= 0 gets the floor(length[p] / page_size)
+ * whole pages of row p, which both then hold (shares_out counts it), and, where
+ * length[p] is no multiple of page_size, a page of its own, taken from the end of
+ * the free list, with the begun page's first length[p] % page_size rows copied to
+ * it in every pool (its other rows stay as they are). Children take pages in the
+ * order of their rows.
+ * Row b must hold no page (n_pages[b] = 0), and p must be another row of the table,
+ * not a child itself in this call, that holds ceil(length[p] / page_size) pages; a
+ * child for which this fails, or whose page the list cannot meet together with
+ * those asked for before it, is left as it is and flagged.
+ *
+ * parent [B] int32 (-1: no child); length [B] int32, the tokens of a row, read for
+ *   parents only (negative: 0)
+ * page_table [B, max_pages] int32, in and out: children's rows are written
+ * n_pages [B]; free_pages [num_pages], n_free [1] int32: read; pages taken are
+ *   those behind n_free_out
+ * n_pools (0 .. 32), row_bytes (an even number of bytes of one position), pools: a
+ *   HOST array of n_pools device pointers, each [num_pages, page_size, row_bytes]
+ *   (K and V of every layer)
+ * n_pages_out [B], n_free_out [1] int32; short_seq [B] uint8 or NULL: the flags
+ */
+int dflash_pages_fork(const dflash_pages_dims* dims, const int32_t* parent, const int32_t* length,
+                      int32_t* page_table, const int32_t* n_pages, const int32_t* shares,
+                      const int32_t* free_pages, const int32_t* n_free, int32_t n_pools, size_t row_bytes,
+                      void* const* pools, int32_t* n_pages_out, int32_t* n_free_out, int32_t* shares_out,
+                      uint8_t* short_seq, dflash_stream_t stream);
+
+/*
+ * Pages past ceil(length[b] / page_size) are let go by row b (0 ends a sequence; a
+ * row that holds no more than that is left as it is). A page that no row holds any
+ * more is freed: the freed pages are appended to the free list in ascending order.
+ * A page that others still hold loses one of shares[p]. Table entries stay as they
+ * are. A length that ends inside a page held by others leaves the row reading it:
+ * such a row must be forked, not written.
+ *
+ * length, n_pages [B], page_table [B, max_pages] int32; free_pages [num_pages]
+ * int32, in and out; n_free [1]; n_pages_out [B], n_free_out [1] int32
+ */
+size_t dflash_pages_release_workspace_size(const dflash_pages_dims* dims);
+int dflash_pages_release(const dflash_pages_dims* dims, const int32_t* length, const int32_t* page_table,
+                         const int32_t* n_pages, const int32_t* shares, int32_t* free_pages, const int32_t* n_free,
+                         int32_t* n_pages_out, int32_t* n_free_out, int32_t* shares_out, void* workspace,
+                         size_t ws_bytes, dflash_stream_t stream);
+
+/*
+ * The pages in use, n of them, moved to the low end [0, n) of the pools, which can
+ * then be cut or handed to others there: of the pages that rows hold in their first
+ * n_pages[b] entries, those numbered n or more move, in ascending order, to the
+ * pages below n that no row holds, in ascending order; whole pages of every pool
+ * are copied, and the contents of no page in use are lost. Every other page counts as
+ * free, whether the old list had it or not (page_table holds all rows of the pool).
+ *
+ * page_table_out [B, max_pages] int32: the rows with the moved pages' new numbers
+ *   (entries past n_pages[b] as they were); free_out [num_pages] int32:
+ *   num_pages - 1, num_pages - 2, .., 0, of which the first n_free_out[0] =
+ *   num_pages - n are free; pools as in dflash_pages_fork
+ */
+size_t dflash_pages_compact_workspace_size(const dflash_pages_dims* dims);
+int dflash_pages_compact(const dflash_pages_dims* dims, const int32_t* page_table, const int32_t* n_pages,
+                         const int32_t* shares, int32_t n_pools, size_t row_bytes, void* const* pools,
+                         int32_t* page_table_out, int32_t* shares_out, int32_t* free_out, int32_t* n_free_out,
+                         void* workspace, size_t ws_bytes, dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
 /* Diagnostics                                                                */

@@ -715,3 +715,112 @@ def fp8_gemm(x, x_scale, w, w_scale, bias=None):
     wd = _f64(w) * fp8_spread(w_scale, 128, *w.shape)
     b = 0.0 if bias is None else _f64(bias)
     return xd @ wd.T + b, np.abs(xd) @ np.abs(wd).T + np.abs(b)
+
+
+# ---------------------------------------------------------------------------
+# pages that rows hold together
+# ---------------------------------------------------------------------------
+def _held(n_pages, max_pages):
+    return [min(max(int(n), 0), max_pages) for n in n_pages]
+
+
+def pages_fork(parent, length, page_table, n_pages, shares, free_pages, n_free, page_size, pools=()):
+    """Rows that begin as copies of others, one after the other: returns page_table,
+    n_pages, shares, n_free, short and the pools [num_pages, page_size, ...]."""
+    table = [list(map(int, r)) for r in page_table]
+    pools = [p.copy() for p in pools]
+    count = [max(int(s), 0) for s in shares]
+    num, B, max_pages = len(count), len(table), len(table[0])
+    held = _held(n_pages, max_pages)
+    now, short = list(held), [0] * B
+    n_free = min(max(int(n_free), 0), num)
+    asked = taken = 0
+    for b in range(B):
+        p = int(parent[b])
+        if p < 0:
+            continue
+        short[b] = 1
+        if p >= B or p == b or int(parent[p]) >= 0 or held[b]:
+            continue
+        full, rest = divmod(max(int(length[p]), 0), page_size)
+        if full + (rest > 0) > held[p]:
+            continue
+        if rest:
+            asked += 1
+            if asked > n_free:
+                continue
+            taken = asked
+        short[b] = 0
+        for j in range(full):
+            table[b][j] = table[p][j]
+            if 0 <= table[p][j] < num:
+                count[table[p][j]] += 1
+        now[b] = full
+        if rest:
+            src, dst = table[p][full], int(free_pages[n_free - asked])
+            table[b][full] = dst
+            now[b] += 1
+            if 0 <= src < num and 0 <= dst < num:
+                for pool in pools:
+                    pool[dst, :rest] = pool[src, :rest]
+    return (np.array(table, dtype=np.int32), np.array(now, dtype=np.int32), np.array(count, dtype=np.int32),
+            n_free - taken, np.array(short, dtype=np.uint8), pools)
+
+
+def pages_release(length, page_table, n_pages, shares, free_pages, n_free, page_size):
+    """Pages past the lengths let go by their rows: returns n_pages, shares,
+    free_pages, n_free; a page is freed when the last row lets it go."""
+    count = [max(int(s), 0) for s in shares]
+    free = list(map(int, free_pages))
+    num, max_pages = len(count), len(page_table[0])
+    now = _held(n_pages, max_pages)
+    at, freed = min(max(int(n_free), 0), num), set()
+    for b, n in enumerate(length):
+        keep = min(now[b], -(-max(int(n), 0) // page_size))
+        for page in map(int, page_table[b][keep:now[b]]):
+            if not 0 <= page < num or page in freed:
+                continue
+            if count[page]:
+                count[page] -= 1
+            else:
+                freed.add(page)
+        now[b] = keep
+    back = sorted(freed)[:num - at]
+    free[at:at + len(back)] = back
+    return np.array(now, dtype=np.int32), np.array(count, dtype=np.int32), np.array(free, dtype=np.int32), at + len(back)
+
+
+def pages_compact(page_table, n_pages, shares, pools=()):
+    """The pages that rows hold at the pools' low end: returns page_table, shares,
+    free_pages, n_free and the pools."""
+    table = [list(map(int, r)) for r in page_table]
+    pools = [p.copy() for p in pools]
+    num = len(shares)
+    held = _held(n_pages, len(table[0]))
+    used = sorted({p for row, n in zip(table, held) for p in row[:n] if 0 <= p < num})
+    n, inside = len(used), set(used)
+    to = dict(zip([p for p in used if p >= n], [p for p in range(n) if p not in inside]))
+    count = np.zeros(num, dtype=np.int32)
+    for p in used:
+        count[to.get(p, p)] = max(int(shares[p]), 0)
+    for row, k in zip(table, held):
+        row[:k] = [to.get(p, p) for p in row[:k]]
+    for src, dst in to.items():
+        for pool in pools:
+            pool[dst] = pool[src]
+    return np.array(table, dtype=np.int32), count, np.arange(num - 1, -1, -1, dtype=np.int32), num - n, pools
+
+
+# ---------------------------------------------------------------------------
+# root-mean-square norm
+# ---------------------------------------------------------------------------
+def rms_norm(x, weight, eps, residual=None):
+    """(s, y, scale): s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight and the
+    e4m3 scale of every 128 values of y."""
+    s = np.asarray(x, dtype=np.float64)
+    if residual is not None:
+        s = s + np.asarray(residual, dtype=np.float64)
+    d = s.shape[1]
+    y = s / np.sqrt((s * s).mean(1, keepdims=True) + eps) * np.asarray(weight, dtype=np.float64)
+    scale = np.stack([np.abs(y[:, j:j + 128]).max(1) for j in range(0, d, 128)], 1) / 448.0
+    return s, y, np.maximum(scale, 2.0 ** -126)
