@@ -732,6 +732,22 @@ size_t dflash_block_attn_workspace_size(const dflash_attn_dims* d) {
 
 namespace {
 
+// The arguments of an attention call whose dims have been checked.
+dflash::AttnArgs attn_args(const dflash_attn_dims* d, const void* q, const void* k_blk, const void* v_blk,
+                           const void* k_pool, const void* v_pool, const int32_t* page_table, const int32_t* ctx_len,
+                           const uint8_t* active, float scale, void* out, void* workspace, dflash_stream_t stream) {
+  dflash::AttnArgs a{};
+  a.B = d->B; a.n_q = d->n_q; a.n_kv = d->n_kv_blk; a.Hq = d->Hq; a.Hkv = d->Hkv; a.D = d->D;
+  a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
+  a.max_ctx = d->max_ctx; a.dtype = d->dtype; a.causal = d->causal;
+  a.q = q; a.k_blk = k_blk; a.v_blk = v_blk; a.k_pool = k_pool; a.v_pool = v_pool;
+  a.page_table = page_table; a.ctx_len = ctx_len; a.active = active; a.scale = scale; a.out = out;
+  a.err = (int*)workspace + kMaxCounters;
+  a.scratch = (char*)workspace + DFLASH_WS_COUNTER_BYTES;
+  a.stream = (cudaStream_t)stream;
+  return a;
+}
+
 int block_attn_call(const dflash_attn_dims* d, const void* q, const void* k_blk, const void* v_blk,
                     const void* k_pool, const void* v_pool, const int32_t* page_table, const int32_t* ctx_len,
                     const uint8_t* active, float scale, void* out, void* workspace, size_t ws_bytes,
@@ -742,15 +758,8 @@ int block_attn_call(const dflash_attn_dims* d, const void* q, const void* k_blk,
     return fail(DFLASH_ERR_INVALID_ARG, "block_attn: a required pointer is NULL");
   rc = check_ws(workspace, ws_bytes, dflash_block_attn_workspace_size(d));
   if (rc) return rc;
-  dflash::AttnArgs a{};
-  a.B = d->B; a.n_q = d->n_q; a.n_kv = d->n_kv_blk; a.Hq = d->Hq; a.Hkv = d->Hkv; a.D = d->D;
-  a.page_size = d->page_size; a.max_pages = d->max_pages; a.num_pages = d->num_pages;
-  a.max_ctx = d->max_ctx; a.dtype = d->dtype; a.causal = d->causal;
-  a.q = q; a.k_blk = k_blk; a.v_blk = v_blk; a.k_pool = k_pool; a.v_pool = v_pool;
-  a.page_table = page_table; a.ctx_len = ctx_len; a.active = active; a.scale = scale; a.out = out;
-  a.err = (int*)workspace + kMaxCounters;
-  a.scratch = (char*)workspace + DFLASH_WS_COUNTER_BYTES;
-  a.stream = (cudaStream_t)stream;
+  const dflash::AttnArgs a = attn_args(d, q, k_blk, v_blk, k_pool, v_pool, page_table, ctx_len, active, scale, out,
+                                       workspace, stream);
   int launches = 0;
   cudaError_t e = dflash::launch_block_attn(a, &launches);
   if (e != cudaSuccess) return cuda_fail(e, "block_attn launch");
@@ -789,7 +798,8 @@ static int check_prefix_dims(const dflash_attn_dims* d, int32_t n_groups) {
 
 size_t dflash_prefix_attn_workspace_size(const dflash_attn_dims* d, int32_t n_groups) {
   if (check_prefix_dims(d, n_groups) != DFLASH_OK) return 0;
-  return dflash_block_attn_workspace_size(d);
+  return DFLASH_WS_COUNTER_BYTES + dflash::prefix_attn_ws_bytes(d->B, n_groups, d->n_q, d->n_kv_blk, d->Hq, d->Hkv, d->D,
+                                                                d->max_ctx, d->page_size, d->dtype);
 }
 
 int dflash_prefix_attn(const dflash_attn_dims* d, int32_t n_groups, const void* q, const void* k_blk,
@@ -799,10 +809,18 @@ int dflash_prefix_attn(const dflash_attn_dims* d, int32_t n_groups, const void* 
   CallRange range_("dflash_prefix_attn");
   int rc = check_prefix_dims(d, n_groups);
   if (rc) return rc;
-  if (!group || (n_groups > 0 && !prefix_len))
+  if (!q || !k_pool || !v_pool || !page_table || !ctx_len || !out || (d->n_kv_blk > 0 && (!k_blk || !v_blk)) || !group ||
+      (n_groups > 0 && !prefix_len))
     return fail(DFLASH_ERR_INVALID_ARG, "prefix_attn: a required pointer is NULL");
-  return block_attn_call(d, q, k_blk, v_blk, k_pool, v_pool, page_table, ctx_len, nullptr, scale, out, workspace,
-                         ws_bytes, stream);
+  rc = check_ws(workspace, ws_bytes, dflash_prefix_attn_workspace_size(d, n_groups));
+  if (rc) return rc;
+  dflash::PrefixArgs a{};
+  a.attn = attn_args(d, q, k_blk, v_blk, k_pool, v_pool, page_table, ctx_len, nullptr, scale, out, workspace, stream);
+  a.n_groups = n_groups; a.group = group; a.prefix_len = prefix_len;
+  int launches = 0;
+  cudaError_t e = dflash::launch_prefix_attn(a, &launches);
+  if (e != cudaSuccess) return cuda_fail(e, "prefix_attn launch");
+  return ok(launches);
 }
 
 // ------------------------------------------------------------- materialise ---

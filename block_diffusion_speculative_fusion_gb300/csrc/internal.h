@@ -305,6 +305,17 @@ struct AttnArgs {
 size_t attn_ws_bytes(int B, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size, int dtype);
 cudaError_t launch_block_attn(const AttnArgs& a, int* launches);
 
+// The same with prefixes shared by groups of sequences.
+struct PrefixArgs {
+  AttnArgs attn;
+  int n_groups;
+  const int32_t* group;        // [B]
+  const int32_t* prefix_len;   // [n_groups]
+};
+size_t prefix_attn_ws_bytes(int B, int n_groups, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size,
+                            int dtype);
+cudaError_t launch_prefix_attn(const PrefixArgs& a, int* launches);
+
 // -------------------------------------- 8-bit product with block scales ---
 struct Fp8QuantArgs {
   int T, K, dtype, block_rows;   // block_rows 1 or 128

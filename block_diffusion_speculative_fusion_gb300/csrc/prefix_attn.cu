@@ -1,0 +1,933 @@
+// Draft block attention for a batch whose sequences share prefixes in groups:
+// softmax(scale * Q K^T) V as dflash_block_attn, with the K/V rows of a shared prefix
+// read once for the packed query rows of all its sequences.
+//   [DFlash] 块扩散, KV 注入 step 3: the attention; [SGLang] 5.1: the block table whose
+//   rows hold the prefix's pages together.
+//
+// A softmax over a set of keys splits over parts of it: with (m_i, l_i, O_i) the
+// maximum, sum and unnormalised output of part i,
+//   out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
+// The parts here are the group's prefix (whole tiles of 128 positions), worked on with
+// the queries of all its sequences, and what each sequence has of its own: the rest
+// of its context and the block's rows. Both are pieces of one work list (below); every
+// piece leaves fp32 partials, which a second kernel joins in a fixed order.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+#include "tma.cuh"
+
+namespace dflash {
+
+namespace pfx {
+constexpr int kD = 128;
+constexpr int kTK = 128;                    // keys of a tile
+constexpr int kM = 128;                     // packed query rows of a Q tile (TMEM lanes)
+constexpr int kGrid = 152;                  // persistent CTAs: one per SM
+constexpr int kMaxSeqs = 1024;
+constexpr int kSlots = 5;                   // ring of K and V tiles, 32 KB each
+constexpr int kTileBytes = kTK * kD * 2;    // a Q, K or V tile: two d-halves of 128 rows x 128 bytes
+constexpr int kHalf = kTileBytes / 2;
+constexpr int kThreads = 352;               // warps 0-3, 4-7 softmax; 8 K/V loads; 9 MMA; 10 Q loads
+constexpr int kWarps = kThreads / 32;
+constexpr int kKept = 8;                    // piece descriptors kept in shared memory
+constexpr int kItemCost = 2;                // an own part's start and end, in tiles
+constexpr int kMinShare = 2;                // least work of a CTA
+constexpr float kRescaleLog2 = 8.f;         // O is rescaled when the row maximum grows by more than 2^8
+// TMEM: S of the two softmax groups (P over its first half), then their O
+constexpr uint32_t kSCol = 0, kOCol = 256;
+constexpr int kTmemCols = 512;
+}  // namespace pfx
+
+// A run of tiles of one item: one kv head, up to 256 packed rows, the keys of one part.
+struct PfxPiece {
+  int first;     // sequence whose table row is read
+  int member0;   // prefix: where the group's sequences begin in the order; own part: -1
+  int key0;      // position of the part's first key
+  int C;         // and past its last context key
+  int nct;       // context tiles of the part; the tile after them is the block's own rows
+  int t0, nt;    // this piece's tiles
+  int head;
+  int row0, nrows;   // packed rows of the part's sequences
+  int slot;      // partials
+  int pad;
+};
+
+// What the merge kernel needs to find a row's partials.
+struct PfxSeq {
+  int group, pos;     // shared prefix (-1: none) and the sequence's place among its sequences
+  int base, nt;       // own part: cost before its first item, tiles
+};
+struct PfxGroup {
+  int base, item, tiles, rows;   // cost before and number of its first item, tiles, packed rows
+};
+
+struct PfxParams {
+  const bf16* q;
+  const int32_t* page_table;
+  const int32_t* ctx_len;
+  const int32_t* group;
+  const int32_t* prefix_len;
+  bf16* out;
+  float* po_p;  float2* ml_p;    // partials of prefixes [slot][2][128][128], [slot][2][128]
+  float* po_s;  float2* ml_s;    // of own parts [slot][2][Rs2][128], [slot][2][Rs2]
+  PfxPiece* pieces;
+  PfxSeq* seqs;
+  PfxGroup* groups;
+  int32_t* header;               // [share]
+  int* err;
+  int B, n_groups, n_q, n_kv, Hq, Hkv, G, R;   // R = n_q * G packed rows of a sequence and kv head
+  int sblk, Rs2;                 // blocks of 256 rows of a sequence; rows of a half's partials
+  int page_shift, max_pages, num_pages, max_ctx, causal, br;   // br: rows of a page's box
+  float scale_log2;
+  unsigned long long wait_ns;
+};
+
+// ---------------------------------------------------------------------------
+// The work list. Items, in order: for each group with a prefix worth sharing, block of
+// 256 packed rows, kv head: the prefix's tiles; then for each sequence, block, head: its
+// own tiles. A tile costs 1, or 2 with more than 128 rows (two Q tiles), an own part
+// kItemCost more. The costs in a row are cut into equal ranges, one a CTA; a tile
+// belongs to the range in which its cost begins. So the partition, and with it the
+// rounding, depends on the dims, lengths and groups alone.
+// ---------------------------------------------------------------------------
+__host__ __device__ __forceinline__ int pfx_blocks(int rows) { return (rows + 2 * pfx::kM - 1) / (2 * pfx::kM); }
+// weight of block k of `rows` packed rows
+__device__ __forceinline__ int pfx_weight(int rows, int k) { return rows - k * 2 * pfx::kM > pfx::kM ? 2 : 1; }
+
+// First tile of an item (from position `base`, `ov` before its tiles, `nt` tiles of
+// weight w) that begins at or after position `at`.
+__device__ __forceinline__ int pfx_first_tile(int base, int ov, int w, int nt, int at) {
+  const int x = at - base - ov;
+  return x <= 0 ? 0 : min(nt, (x + w - 1) / w);
+}
+// Cost before item (block k, head) among the items of a part of `rows` rows whose tiles
+// cost nt * weight + ov each; all of them together for k = number of blocks.
+__device__ __forceinline__ int pfx_cost_before(int rows, int nt, int ov, int Hkv, int k, int head) {
+  const int n = pfx_blocks(rows);
+  const int full = min(k, n - 1);                  // blocks before the last one have 256 rows
+  int c = full * Hkv * (2 * nt + ov);
+  if (k == n) c += Hkv * (pfx_weight(rows, n - 1) * nt + ov);
+  else c += head * (pfx_weight(rows, k) * nt + ov);
+  return c;
+}
+
+__device__ __forceinline__ int pfx_scan(int x, int* s_w, int* total) {
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  int in = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, in, o);
+    if (l >= o) in += y;
+  }
+  __syncthreads();
+  if (l == 31) s_w[w] = in;
+  __syncthreads();
+  int base = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < pfx::kWarps; ++i) {
+    const int v = s_w[i];
+    base += i < w ? v : 0;
+    all += v;
+  }
+  *total = all;
+  return base + in - x;
+}
+
+// Last i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+__device__ __forceinline__ int pfx_find(const int* a, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Shared memory: Q tiles, ring, then the small things.
+struct PfxShared {
+  uint64_t kv_full[pfx::kSlots], kv_empty[pfx::kSlots];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full[2], q_empty[2], mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int n_pieces, piece0;            // this CTA's pieces, in the list from piece0 on
+  int scan[pfx::kWarps + 1];
+  PfxPiece kept[pfx::kKept];
+  uint16_t order[pfx::kMaxSeqs];   // the groups' sequences, group after group
+};
+constexpr size_t kPfxSmem = (2 + pfx::kSlots) * (size_t)pfx::kTileBytes + sizeof(PfxShared);
+static_assert(kPfxSmem <= 232448, "shared memory");
+
+// The plan, in scratch that the ring takes over afterwards.
+struct PfxPlan {
+  int ctx[pfx::kMaxSeqs], grp[pfx::kMaxSeqs], pos[pfx::kMaxSeqs];
+  int sbase[pfx::kMaxSeqs + 1];                            // cost before a sequence's own part
+  int cnt[pfx::kMaxSeqs], minc[pfx::kMaxSeqs], first[pfx::kMaxSeqs], tiles[pfx::kMaxSeqs], fill[pfx::kMaxSeqs];
+  int gstart[pfx::kMaxSeqs + 1], gbase[pfx::kMaxSeqs + 1], gitem[pfx::kMaxSeqs + 1];
+};
+static_assert(sizeof(PfxPlan) <= (2 + pfx::kSlots) * (size_t)pfx::kTileBytes, "plan scratch");
+
+__device__ __forceinline__ int pfx_own_tiles(const PfxParams& p, int ctx, int prefix_tiles) {
+  return (ctx - prefix_tiles * pfx::kTK + pfx::kTK - 1) / pfx::kTK + (p.n_kv > 0 ? 1 : 0);
+}
+
+__device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShared& sh) {
+  using namespace pfx;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int per_g = (p.n_groups + kThreads - 1) / kThreads, per_b = (p.B + kThreads - 1) / kThreads;
+  const int g0 = min(p.n_groups, tid * per_g), g1 = min(p.n_groups, g0 + per_g);
+  const int b0 = min(p.B, tid * per_b), b1 = min(p.B, b0 + per_b);
+  for (int g = tid; g < p.n_groups; g += kThreads) {
+    s.cnt[g] = 0;
+    s.minc[g] = s.first[g] = INT_MAX;
+    s.fill[g] = 0;
+  }
+  __syncthreads();
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int raw = p.ctx_len[b], C = max(0, min(raw, p.max_ctx)), g = p.group[b];
+    const bool in = g >= 0 && g < p.n_groups;
+    s.ctx[b] = C;
+    s.grp[b] = in ? g : -1;
+    if (in) {
+      atomicAdd(&s.cnt[g], 1);
+      atomicMin(&s.minc[g], C);
+      atomicMin(&s.first[g], b);
+    }
+#ifdef DFLASH_DEBUG
+    // context lengths outside [0, max_ctx] are clamped; debug builds record them
+    if (blockIdx.x == 0 && raw != C) record_dev_error(p.err, kDevErrBadCtxLen);
+#endif
+  }
+  __syncthreads();
+  // groups: the tiles shared (none for a lone sequence), where their sequences, items and costs begin
+  int n_m = 0, n_i = 0, n_c = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int P = max(0, min(p.prefix_len[g], s.minc[g]));
+    const int t = s.cnt[g] >= 2 ? P / kTK : 0;
+    s.tiles[g] = t;
+    if (t) {
+      n_m += s.cnt[g];
+      n_i += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
+      n_c += pfx_cost_before(s.cnt[g] * p.R, t, 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
+    }
+  }
+  int all_m, all_i, all_c, all_s;
+  int m = pfx_scan(n_m, sh.scan, &all_m), i = pfx_scan(n_i, sh.scan, &all_i), c = pfx_scan(n_c, sh.scan, &all_c);
+  for (int g = g0; g < g1; ++g) {
+    s.gstart[g] = m;
+    s.gitem[g] = i;
+    s.gbase[g] = c;
+    if (s.tiles[g]) {
+      m += s.cnt[g];
+      i += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
+      c += pfx_cost_before(s.cnt[g] * p.R, s.tiles[g], 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
+    }
+  }
+  __syncthreads();
+  // own parts
+  int n_s = 0;
+  auto own_cost = [&](int b) {
+    const int nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
+    return nt ? pfx_cost_before(p.R, nt, kItemCost, p.Hkv, p.sblk, 0) : 0;
+  };
+  for (int b = b0; b < b1; ++b) n_s += own_cost(b);
+  int at = all_c + pfx_scan(n_s, sh.scan, &all_s);
+  for (int b = b0; b < b1; ++b) {
+    s.sbase[b] = at;
+    at += own_cost(b);
+  }
+  // a group's sequences in ascending order
+  if (tid < 32) {
+    for (int k = 0; k < p.B; k += 32) {
+      const int b = k + lane;
+      const int g = b < p.B ? s.grp[b] : -1;
+      const bool in = g >= 0 && s.tiles[g] > 0;
+      const unsigned same = __match_any_sync(0xffffffffu, in ? g : -1 - lane);
+      if (in) {
+        const int pos = s.fill[g] + __popc(same & ((1u << lane) - 1));
+        s.pos[b] = pos;
+        sh.order[s.gstart[g] + pos] = (uint16_t)b;
+      }
+      __syncwarp();
+      if (in && (same >> lane) == 1u) s.fill[g] += __popc(same);   // the last lane of each
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  const int N = all_c + all_s, n_items = all_i + p.B * p.Hkv * p.sblk;
+  const int share = max(kMinShare, (N + kGrid - 1) / kGrid);
+  const int lo = min((long)N, (long)blockIdx.x * share), hi = min((long)N, (long)lo + share);
+  // the item that position x lies in
+  auto item_at = [&](int x) {
+    if (x < all_c) {
+      const int g = pfx_find(s.gbase, p.n_groups, x), rows = s.cnt[g] * p.R;
+      const int rel = x - s.gbase[g], full = p.Hkv * 2 * s.tiles[g];
+      const int k = min(rel / full, pfx_blocks(rows) - 1), in = rel - k * full;
+      return s.gitem[g] + k * p.Hkv + in / (pfx_weight(rows, k) * s.tiles[g]);
+    }
+    const int b = pfx_find(s.sbase, p.B, x), nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
+    const int rel = x - s.sbase[b], full = p.Hkv * (2 * nt + kItemCost);
+    const int k = min(rel / full, p.sblk - 1), in = rel - k * full;
+    return all_i + (b * p.sblk + k) * p.Hkv + in / (pfx_weight(p.R, k) * nt + kItemCost);
+  };
+  const int i0 = lo < hi ? item_at(lo) : 0, i1 = lo < hi ? item_at(hi - 1) : -1;
+  for (int k = tid; k <= i1 - i0; k += kThreads) {
+    const int it = i0 + k;
+    PfxPiece d;
+    int base, ov, w, nt;
+    if (it < all_i) {
+      const int g = pfx_find(s.gitem, p.n_groups, it), rows = s.cnt[g] * p.R;
+      const int rel = it - s.gitem[g], blk = rel / p.Hkv;
+      d.head = rel - blk * p.Hkv;
+      nt = s.tiles[g];
+      w = pfx_weight(rows, blk);
+      ov = 0;
+      base = s.gbase[g] + pfx_cost_before(rows, nt, 0, p.Hkv, blk, d.head);
+      d.first = s.first[g];
+      d.member0 = s.gstart[g];
+      d.key0 = 0;
+      d.C = nt * kTK;
+      d.nct = nt;
+      d.row0 = blk * 2 * kM;
+      d.nrows = min(2 * kM, rows - d.row0);
+      d.slot = it + (int)blockIdx.x;
+    } else {
+      const int j = it - all_i, b = j / (p.sblk * p.Hkv), rel = j - b * p.sblk * p.Hkv, blk = rel / p.Hkv;
+      d.head = rel - blk * p.Hkv;
+      const int t = s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0;
+      nt = pfx_own_tiles(p, s.ctx[b], t);
+      w = pfx_weight(p.R, blk);
+      ov = kItemCost;
+      base = s.sbase[b] + pfx_cost_before(p.R, nt, ov, p.Hkv, blk, d.head);
+      d.first = b;
+      d.member0 = -1;
+      d.key0 = t * kTK;
+      d.C = s.ctx[b];
+      d.nct = nt - (p.n_kv > 0 ? 1 : 0);
+      d.row0 = blk * 2 * kM;
+      d.nrows = min(2 * kM, p.R - d.row0);
+      d.slot = j + (int)blockIdx.x;
+    }
+    d.t0 = pfx_first_tile(base, ov, w, nt, lo);
+    d.nt = pfx_first_tile(base, ov, w, nt, hi) - d.t0;
+    d.pad = 0;
+    p.pieces[it + (int)blockIdx.x] = d;
+    if (k < kKept) sh.kept[k] = d;
+  }
+  if (tid == 0) {
+    sh.n_pieces = i1 - i0 + 1;
+    sh.piece0 = i0 + (int)blockIdx.x;
+  }
+  (void)n_items;
+  if (blockIdx.x == 0) {
+    for (int b = tid; b < p.B; b += kThreads) {
+      const int g = s.grp[b], t = g >= 0 ? s.tiles[g] : 0;
+      p.seqs[b] = PfxSeq{t ? g : -1, t ? s.pos[b] : 0, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t)};
+    }
+    for (int g = tid; g < p.n_groups; g += kThreads)
+      p.groups[g] = PfxGroup{s.gbase[g], s.gitem[g], s.tiles[g], s.cnt[g] * p.R};
+    if (tid == 0) p.header[0] = share;
+  }
+}
+
+__device__ __forceinline__ float pfx_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pfx_pack(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// A walk over the units of this CTA's pieces. A unit is one Q tile on one K/V tile: with
+// more than 128 rows the two Q tiles take each K/V tile in turn, with fewer the one Q
+// tile takes the K/V tiles one after the other. Units go to the two softmax groups
+// alternately, over all pieces.
+struct PfxWalk {
+  PfxPiece p;
+  int k;          // piece
+  int w, n;       // unit of the piece, and how many it has
+  int u;          // units before, over all pieces: u & 1 is the softmax group
+  int tile0, q0;  // K/V tiles and Q tiles of the pieces before
+  bool two, live;
+  __device__ __forceinline__ void open(const PfxParams& P, const PfxShared& sh) {
+    live = false;
+    for (; k < sh.n_pieces; ++k) {
+      p = k < pfx::kKept ? sh.kept[k] : P.pieces[sh.piece0 + k];
+      if (p.nt > 0) {
+        two = p.nrows > pfx::kM;
+        n = two ? 2 * p.nt : p.nt;
+        w = 0;
+        live = true;
+        return;
+      }
+    }
+  }
+  __device__ __forceinline__ void begin(const PfxParams& P, const PfxShared& sh) {
+    k = u = tile0 = q0 = 0;
+    open(P, sh);
+  }
+  __device__ __forceinline__ void next_piece(const PfxParams& P, const PfxShared& sh) {
+    tile0 += p.nt;
+    q0 += two ? 2 : 1;
+    ++k;
+    open(P, sh);
+  }
+  __device__ __forceinline__ void next_unit(const PfxParams& P, const PfxShared& sh) {
+    ++u;
+    if (++w == n) next_piece(P, sh);
+  }
+  __device__ __forceinline__ int tile() const { return two ? w >> 1 : w; }   // in the piece
+};
+
+__global__ void __launch_bounds__(pfx::kThreads, 1)
+prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap kbmap, const __grid_constant__ CUtensorMap vbmap,
+                   const __grid_constant__ PfxParams p) {
+  using namespace pfx;
+  extern __shared__ __align__(1024) uint8_t pfx_smem[];
+  uint8_t* q_s = pfx_smem;                           // two Q tiles
+  uint8_t* kv_s = pfx_smem + 2 * kTileBytes;
+  PfxShared& sh = *reinterpret_cast<PfxShared*>(pfx_smem + (2 + kSlots) * kTileBytes);
+  volatile int* abort_flag = &sh.abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh.kv_full[i], 1);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.o_empty[i], 4);
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&sh.tmem_base, kTmemCols);
+  dependents_may_launch();
+  pfx_plan(p, *reinterpret_cast<PfxPlan*>(pfx_smem), sh);
+  fence_proxy_async_smem();        // the scratch becomes the ring: its writes come before the copies
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  PfxWalk wk;
+  int issued = 0;                  // tiles (K and V counted apart) that the producer has asked for
+
+  if (warp == 8) {
+    // ------------------------------ K/V loads ------------------------------
+    const uint64_t pol_once = l2_policy_evict_first();
+    const int bpt = kTK / p.br;                       // boxes of a context tile
+    const int per = 32 / bpt;                         // tiles whose page numbers the warp holds at once
+    // page number of box `lane` of the tiles from t on; the lanes' entries fit the context
+    auto fetch = [&](const PfxPiece& d, int t) -> int {
+      const int key = d.key0 + t * kTK + lane * p.br;
+      const int lp = key >> p.page_shift;
+      if (t + lane / bpt >= min(d.nct, d.t0 + d.nt) || key >= d.C || lp >= p.max_pages) return 0;
+      const int page = __ldg(p.page_table + (size_t)d.first * p.max_pages + lp);
+      if (page >= 0 && page < p.num_pages) return page;
+      record_dev_error(p.err, kDevErrBadPage);        // page 0 is read instead, never out of bounds
+      return 0;
+    };
+    bool ok = true;
+    wk.begin(p, sh);
+    int ids = wk.live ? fetch(wk.p, wk.p.t0) : 0;
+    while (ok && wk.live) {
+      const PfxPiece d = wk.p;
+      // the next piece's first page numbers are asked for while this one's tiles go out
+      PfxWalk nx = wk;
+      nx.next_piece(p, sh);
+      int ids_nx = nx.live ? fetch(nx.p, nx.p.t0) : 0;
+      int ids_on = fetch(d, d.t0 + per);
+      for (int j = 0; j < d.nt && ok; ++j) {
+        const int t = d.t0 + j, jj = j % per;
+        if (j > 0 && jj == 0) {
+          ids = ids_on;
+          ids_on = fetch(d, t + per);
+        }
+        const bool ctx = t < d.nct;
+        const int left = d.C - (d.key0 + t * kTK);
+        const int nb = ctx ? min(bpt, (left + p.br - 1) / p.br) : 1;      // boxes with a key in use
+        const uint32_t bytes = ctx ? (uint32_t)(nb * p.br * 256) : (uint32_t)(p.n_kv * 256);
+        const int box = lane >> 1, h = lane & 1;
+        const int page = __shfl_sync(0xffffffffu, ids, (jj * bpt + box) & 31);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int seq = 2 * (wk.tile0 + j) + v, st = seq % kSlots;
+          if (!__all_sync(0xffffffffu, wait_or_abort(&sh.kv_empty[st], (uint32_t)(((seq / kSlots) & 1) ^ 1),
+                                                     abort_flag, p.err, 41, p.wait_ns))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], bytes);
+          __syncwarp();
+          ++issued;
+          uint8_t* dst = kv_s + st * kTileBytes + h * kHalf;
+          if (ctx) {
+            if (box < nb) {
+              const int row = (page << p.page_shift) + ((d.key0 + t * kTK + box * p.br) & ((1 << p.page_shift) - 1));
+              dst += box * p.br * 128;
+              if (d.member0 < 0)
+                tma_load_3d_hint(dst, v ? &vmap : &kmap, &sh.kv_full[st], h * 64, d.head, row, pol_once);
+              else
+                tma_load_3d(dst, v ? &vmap : &kmap, &sh.kv_full[st], h * 64, d.head, row);
+            }
+          } else if (box == 0) {
+            tma_load_3d(dst, v ? &vbmap : &kbmap, &sh.kv_full[st], h * 64, d.head, d.first * p.n_kv);
+          }
+        }
+      }
+      wk = nx;
+      ids = ids_nx;
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------ Q loads ------------------------------
+    // Packed row r of a part: sequence r / R of its sequences, query row (r % R) / G,
+    // head r % G of the kv head's. 16 lanes bring a row, in the swizzle of its tile.
+    wk.begin(p, sh);
+    bool ok = true;
+    while (ok && wk.live) {
+      const PfxPiece d = wk.p;
+      for (int i = 0; i < (wk.two ? 2 : 1) && ok; ++i) {
+        const int qc = wk.q0 + i, buf = qc & 1;
+        int off[4];                                   // of rows lane, lane + 32, .. of the tile, in rows of q; -1: none
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int in = i * kM + j * 32 + lane, r = d.row0 + in;
+          const int mem = r / p.R, rem = r - mem * p.R, qi = rem / p.G;
+          off[j] = -1;
+          if (in < d.nrows) {
+            const int b = d.member0 < 0 ? d.first : sh.order[d.member0 + mem];
+            off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
+          }
+        }
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag,
+                                                   p.err, 42, p.wait_ns))) {
+          ok = false;
+          break;
+        }
+        const int c = lane & 15;
+        const uint32_t dst0 = smem_u32(q_s + buf * kTileBytes + (c >> 3) * kHalf);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int s = 0; s < 16; ++s) {
+            const int in = 2 * s + (lane >> 4), row = j * 32 + in;
+            const int o = __shfl_sync(0xffffffffu, off[j], in);
+            const bf16* src = p.q + (size_t)max(o, 0) * kD + c * 8;
+            const uint32_t dst = dst0 + (uint32_t)(row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            const int bytes = o < 0 ? 0 : 16;          // rows past the last are zero
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+          }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+      }
+      wk.next_piece(p, sh);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------ MMA ------------------------------
+    // S of unit u + 2 follows P V of unit u: while one softmax group works on its S, the
+    // tensor cores have the other's. S(u + 2) overwrites P(u) (same TMEM columns), which
+    // the P V before it in the pipe has read.
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
+      PfxWalk pv;
+      wk.begin(p, sh);
+      pv.begin(p, sh);
+      uint32_t o_phase[2] = {0, 0};
+      auto wait = [&](uint64_t* bar, uint32_t par, int code) {
+        return wait_or_abort(bar, par, abort_flag, p.err, code, p.wait_ns);
+      };
+      auto issue_s = [&]() -> bool {
+        if (!wk.live) return true;
+        const int x = wk.u & 1, seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots;
+        const int qi = wk.two ? wk.w & 1 : 0, qc = wk.q0 + qi, buf = qc & 1;
+        if (wk.w == qi && !wait(&sh.q_full[buf], (uint32_t)((qc >> 1) & 1), 43)) return false;
+        if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 44)) return false;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(q_s + buf * kTileBytes), ka = smem_u32(kv_s + st * kTileBytes);
+#pragma unroll
+        for (int i = 0; i < kD / 16; ++i) {
+          const uint32_t off = (uint32_t)((i >> 2) * kHalf + (i & 3) * 32);
+          tc_mma_bf16(tmem + kSCol + (uint32_t)(x * kTK), sdesc_sw128(qa + off), sdesc_sw128(ka + off), id_s,
+                      i > 0 ? 1u : 0u);
+        }
+        tc_commit(&sh.s_full[x]);
+        if (!wk.two || (wk.w & 1)) tc_commit(&sh.kv_empty[st]);
+        if (wk.w + (wk.two ? 2 : 1) >= wk.n) tc_commit(&sh.q_empty[buf]);
+        wk.next_unit(p, sh);
+        return true;
+      };
+      auto issue_pv = [&]() -> bool {
+        const int x = pv.u & 1, seq = 2 * (pv.tile0 + pv.tile()) + 1, st = seq % kSlots;
+        if (pv.w < 2) {     // the group's first unit of the piece: its O has been read out
+          if (!wait(&sh.o_empty[x], o_phase[x] ^ 1u, 45)) return false;
+          o_phase[x] ^= 1u;
+        }
+        if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 46)) return false;
+        if (!wait(&sh.p_full[x], (uint32_t)((pv.u >> 1) & 1), 47)) return false;
+        tc_fence_after();
+        const uint32_t pa = tmem + kSCol + (uint32_t)(x * kTK), va = smem_u32(kv_s + st * kTileBytes);
+#pragma unroll
+        for (int i = 0; i < kTK / 16; ++i)
+          tc_mma_bf16_ta(tmem + kOCol + (uint32_t)(x * kD), pa + (uint32_t)(i * 8), sdesc_sw128_mn(va + i * 2048, kHalf),
+                         id_pv, (pv.w >= 2 || i > 0) ? 1u : 0u);
+        if (!pv.two || (pv.w & 1)) tc_commit(&sh.kv_empty[st]);
+        if (pv.w >= pv.n - 2) tc_commit(&sh.o_full[x]);
+        pv.next_unit(p, sh);
+        return true;
+      };
+      bool ok = issue_s() && issue_s();
+      while (ok && pv.live) ok = issue_pv() && issue_s();
+      tc_commit(&sh.mma_done);
+      mbar_wait_bounded(&sh.mma_done, 0, p.err, 48);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------ softmax ------------------------------
+    const int x = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;   // a thread: one row, TMEM lane r
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_t = tmem + lane_off + kSCol + (uint32_t)(x * kTK), o_t = tmem + lane_off + kOCol + (uint32_t)(x * kD);
+    auto wait = [&](uint64_t* bar, uint32_t par, int code) {
+      return __all_sync(0xffffffffu, wait_or_abort(bar, par, abort_flag, p.err, code, p.wait_ns));
+    };
+    uint32_t units = 0, outs = 0;
+    bool ok = true;
+    for (wk.begin(p, sh); ok && wk.live; wk.u += wk.n, wk.next_piece(p, sh)) {
+      const PfxPiece d = wk.p;
+      const int w0 = (wk.u + x) & 1;                  // this group's first unit of the piece
+      const int row = (wk.two ? w0 * kM : 0) + r;     // in the item's block of 256
+      const int half = wk.two ? w0 : x;
+      float m_run = -CUDART_INF_F, l_run = 0.f;
+      for (int w = w0; w < wk.n; w += 2, ++units) {
+        const int j = wk.two ? w >> 1 : w, t = d.t0 + j;
+        const bool ctx = t < d.nct;
+        const int valid = ctx ? min(kTK, d.C - (d.key0 + t * kTK)) : p.n_kv;
+        if (!wait(&sh.s_full[x], units & 1, 49)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sv[kTK];
+#pragma unroll
+        for (int c = 0; c < kTK; c += 32) tmem_ld32(s_t + (uint32_t)c, sv + c);
+        tmem_ld_wait();
+        if (valid < kTK || (p.causal && !ctx)) {
+          // causal: the row of query i sees the block's rows up to its own
+          const int seen = p.causal && !ctx ? min(valid, ((d.row0 + row) % p.R) / p.G + 1 + p.n_kv - p.n_q) : valid;
+#pragma unroll
+          for (int c = 0; c < kTK; ++c)
+            if (c >= seen) sv[c] = 0xff800000u;       // -inf, whatever stood there
+          // V rows past the last key may hold anything, and 0 * NaN is NaN: zero them
+          const int seq = 2 * (wk.tile0 + j) + 1, st = seq % kSlots;
+          if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 50)) {
+            ok = false;
+            break;
+          }
+          if (r >= valid) {
+            uint8_t* v = kv_s + st * kTileBytes + r * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int c = 0; c < kTK; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const bool raise = mt > m_run + kRescaleLog2 || (m_run == -CUDART_INF_F && mt != -CUDART_INF_F);
+        if (w > w0 + 1 && __any_sync(0xffffffffu, raise)) {
+          // (S of this unit was issued after P V of the group's last one, which is complete with it)
+          const float alpha = !raise ? 1.f : m_run == -CUDART_INF_F ? 0.f : exp2f(m_run - mt);
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_t + (uint32_t)c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(o_t + (uint32_t)c, o);
+          }
+          tmem_st_wait();
+          l_run *= alpha;
+        }
+        if (raise) m_run = mt;
+        const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
+        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kTK; c += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = pfx_ex2(fmaf(__uint_as_float(sv[c + 2 * i]), p.scale_log2, -base));
+            const float b = pfx_ex2(fmaf(__uint_as_float(sv[c + 2 * i + 1]), p.scale_log2, -base));
+            rs[(2 * i) & 3] += a;
+            rs[(2 * i + 1) & 3] += b;
+            pk[i] = pfx_pack(a, b);
+          }
+          tmem_st32(s_t + (uint32_t)(c / 2), pk);
+        }
+        l_run += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[x]);
+      }
+      if (!ok) break;
+      // the piece's partials of this group
+      const int rows = d.member0 < 0 ? p.Rs2 : kM;
+      const size_t at = ((size_t)d.slot * 2 + half) * rows + r;
+      float2* ml = (d.member0 < 0 ? p.ml_s : p.ml_p) + at;
+      float* po = (d.member0 < 0 ? p.po_s : p.po_p) + at * kD;
+      const bool mine = row < d.nrows;
+      if (mine) *ml = make_float2(m_run, l_run);
+      if (w0 < wk.n) {
+        if (!wait(&sh.o_full[x], outs & 1, 51)) break;
+        ++outs;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_t + (uint32_t)c, o);
+          tmem_ld_wait();
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(po + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_empty[x]);
+      }
+    }
+  }
+
+  // ------------------------------ end ------------------------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8 && lane == 0 && *abort_flag)     // copies in flight land before the CTA leaves
+    for (int i = max(0, issued - kSlots); i < issued; ++i)
+      mbar_wait_bounded(&sh.kv_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 52);
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The parts of every row joined, in the order own part, prefix, each by range and group.
+// ---------------------------------------------------------------------------
+namespace pfx {
+constexpr int kJoinRows = 32, kJoinCols = 8, kJoinThreads = kJoinRows * (kD / kJoinCols);
+}
+
+__global__ void __launch_bounds__(pfx::kJoinThreads)
+prefix_join_kernel(const __grid_constant__ PfxParams p) {
+  using namespace pfx;
+  wait_for_prior_grid();
+  const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
+  const int r = blockIdx.y * kJoinRows + threadIdx.x / (kD / kJoinCols), c0 = threadIdx.x % (kD / kJoinCols) * kJoinCols;
+  if (r >= p.R) return;
+  const int share = p.header[0];
+  const PfxSeq s = p.seqs[b];
+  // ranges that hold tiles of an item: [v0, v1]
+  auto ranges = [&](int base, int ov, int w, int nt, int& v0, int& v1) {
+    v0 = 0;
+    v1 = -1;
+    if (nt <= 0) return;
+    v0 = (base + ov) / share;                        // where the first and the last tile begin
+    v1 = (base + ov + (nt - 1) * w) / share;
+  };
+  // source 0: the own part; source 1: the prefix
+  int v0[2], n[2], halves[2];
+  const float2* ml[2];
+  const float* po[2];
+  size_t step[2];                                    // rows of a slot
+  {
+    const int blk = r / (2 * kM), in = r - blk * 2 * kM, w = pfx_weight(p.R, blk);
+    int v1;
+    ranges(s.base + pfx_cost_before(p.R, s.nt, kItemCost, p.Hkv, blk, head), kItemCost, w, s.nt, v0[0], v1);
+    n[0] = v1 - v0[0] + 1;
+    halves[0] = w == 2 ? 1 : 2;
+    step[0] = (size_t)2 * p.Rs2;
+    const size_t at = ((size_t)((b * p.sblk + blk) * p.Hkv + head) + v0[0]) * step[0] + (w == 2 ? in / kM * p.Rs2 + in % kM : in);
+    ml[0] = p.ml_s + at;
+    po[0] = p.po_s + at * kD + c0;
+  }
+  n[1] = 0;
+  if (s.group >= 0) {
+    const PfxGroup g = p.groups[s.group];
+    const int pr = s.pos * p.R + r, blk = pr / (2 * kM), in = pr - blk * 2 * kM, w = pfx_weight(g.rows, blk);
+    int v1;
+    ranges(g.base + pfx_cost_before(g.rows, g.tiles, 0, p.Hkv, blk, head), 0, w, g.tiles, v0[1], v1);
+    n[1] = v1 - v0[1] + 1;
+    halves[1] = w == 2 ? 1 : 2;
+    step[1] = 2 * kM;
+    const size_t at = ((size_t)(g.item + blk * p.Hkv + head) + v0[1]) * step[1] + in;   // (two Q tiles: in / 128 is the half)
+    ml[1] = p.ml_p + at;
+    po[1] = p.po_p + at * kD + c0;
+  }
+  const size_t hs[2] = {(size_t)p.Rs2, (size_t)kM};  // rows of a half
+  float m = -CUDART_INF_F;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll 4
+    for (int i = 0; i < n[e] * halves[e]; ++i)
+      m = fmaxf(m, ml[e][(halves[e] == 2 ? i >> 1 : i) * step[e] + (halves[e] == 2 ? (i & 1) * hs[e] : 0)].x);
+  float l = 0.f, acc[kJoinCols];
+#pragma unroll
+  for (int q = 0; q < kJoinCols; ++q) acc[q] = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll 4
+    for (int i = 0; i < n[e] * halves[e]; ++i) {
+      const size_t at = (halves[e] == 2 ? i >> 1 : i) * step[e] + (halves[e] == 2 ? (i & 1) * hs[e] : 0);
+      const float2 x = ml[e][at];
+      if (x.x == -CUDART_INF_F) continue;            // a part without a key for this row: its O may never have been written
+      const float w = exp2f(x.x - m);
+      l = fmaf(x.y, w, l);
+      const float4* o = reinterpret_cast<const float4*>(po[e] + at * kD);
+#pragma unroll
+      for (int q = 0; q < kJoinCols / 4; ++q) {
+        const float4 y = o[q];
+        acc[4 * q] = fmaf(y.x, w, acc[4 * q]);
+        acc[4 * q + 1] = fmaf(y.y, w, acc[4 * q + 1]);
+        acc[4 * q + 2] = fmaf(y.z, w, acc[4 * q + 2]);
+        acc[4 * q + 3] = fmaf(y.w, w, acc[4 * q + 3]);
+      }
+    }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key at all: 0 (and NaN stays NaN)
+  const int i = r / p.G, hh = r - i * p.G;
+  bf16* dst = p.out + ((size_t)(b * p.n_q + i) * p.Hq + head * p.G + hh) * kD + c0;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(pfx_pack(acc[0] * inv, acc[1] * inv), pfx_pack(acc[2] * inv, acc[3] * inv),
+                                              pfx_pack(acc[4] * inv, acc[5] * inv), pfx_pack(acc[6] * inv, acc[7] * inv));
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+// Sizes that the shared kernel takes (pointers aside).
+static bool pfx_dims_ok(int B, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size, int dtype) {
+  using namespace pfx;
+  if (dtype != 1 || D != kD || B > kMaxSeqs || n_kv > kTK) return false;
+  if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return false;
+  // costs are 32-bit: twice every tile of every sequence, head and block
+  const double tiles = (double)max_ctx / kTK + 2 + kItemCost;
+  return 2.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
+}
+
+struct PfxLayout {
+  size_t pieces, seqs, groups, header, po_p, ml_p, po_s, ml_s, end;
+  int sblk, Rs2;
+};
+static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
+  using namespace pfx;
+  PfxLayout l;
+  const int R = n_q * (Hq / Hkv);
+  l.sblk = pfx_blocks(R);
+  l.Rs2 = std::min(R, kM);
+  // items of prefixes: blocks of 256 rows, one more begun per group of two sequences at least
+  const size_t ip = (size_t)Hkv * ((size_t)B * R / (2 * kM) + std::min(n_groups, B / 2));
+  const size_t is = (size_t)Hkv * B * l.sblk, sp = n_groups ? ip + kGrid : 0, ss = is + kGrid;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align_up(bytes);
+    return o;
+  };
+  l.pieces = take((ip + is + kGrid) * sizeof(PfxPiece));
+  l.seqs = take(B * sizeof(PfxSeq));
+  l.groups = take(std::max(n_groups, 1) * sizeof(PfxGroup));
+  l.header = take(sizeof(int32_t));
+  l.po_p = take(sp * 2 * kM * kD * sizeof(float));
+  l.ml_p = take(sp * 2 * kM * sizeof(float2));
+  l.po_s = take(ss * 2 * l.Rs2 * kD * sizeof(float));
+  l.ml_s = take(ss * 2 * l.Rs2 * sizeof(float2));
+  l.end = at;
+  return l;
+}
+
+size_t prefix_attn_ws_bytes(int B, int n_groups, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size,
+                            int dtype) {
+  const size_t plain = attn_ws_bytes(B, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype);   // pointers off a vector
+  if (!pfx_dims_ok(B, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype)) return plain;
+  return std::max(plain, pfx_layout(B, n_groups, n_q, Hq, Hkv).end);
+}
+
+cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
+  using namespace pfx;
+  const AttnArgs& a = pa.attn;
+  auto al = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
+  if (!pfx_dims_ok(a.B, a.n_q, a.n_kv, a.Hq, a.Hkv, a.D, a.max_ctx, a.page_size, a.dtype) || !al(a.q) || !al(a.k_blk) ||
+      !al(a.v_blk) || !al(a.k_pool) || !al(a.v_pool) || !al(a.out) || !(a.scale > 0.f && a.scale < 3.0e38f) ||
+      (long)a.num_pages * a.page_size >= 1L << 31)
+    return launch_block_attn(a, launches);
+  PfxParams p{};
+  const PfxLayout l = pfx_layout(a.B, pa.n_groups, a.n_q, a.Hq, a.Hkv);
+  char* ws = (char*)a.scratch;
+  p.q = (const bf16*)a.q;
+  p.page_table = a.page_table;
+  p.ctx_len = a.ctx_len;
+  p.group = pa.group;
+  p.prefix_len = pa.prefix_len;
+  p.out = (bf16*)a.out;
+  p.pieces = (PfxPiece*)(ws + l.pieces);
+  p.seqs = (PfxSeq*)(ws + l.seqs);
+  p.groups = (PfxGroup*)(ws + l.groups);
+  p.header = (int32_t*)(ws + l.header);
+  p.po_p = (float*)(ws + l.po_p);
+  p.ml_p = (float2*)(ws + l.ml_p);
+  p.po_s = (float*)(ws + l.po_s);
+  p.ml_s = (float2*)(ws + l.ml_s);
+  p.err = a.err;
+  p.B = a.B; p.n_groups = pa.n_groups; p.n_q = a.n_q; p.n_kv = a.n_kv; p.Hq = a.Hq; p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
+  p.R = a.n_q * p.G;
+  p.sblk = l.sblk; p.Rs2 = l.Rs2;
+  p.page_shift = 0;
+  while (1 << p.page_shift < a.page_size) ++p.page_shift;
+  p.max_pages = a.max_pages; p.num_pages = a.num_pages; p.max_ctx = a.max_ctx; p.causal = a.causal;
+  p.br = a.page_size;
+  p.scale_log2 = a.scale * kLog2e;
+  p.wait_ns = wait_limit_ns();
+  // pools and block rows as [row][head][d]: a box of 64 d x 1 head x rows lands as [row][64 d]
+  CUtensorMap maps[4];
+  const void* base[4] = {a.k_pool, a.v_pool, a.n_kv ? a.k_blk : a.k_pool, a.n_kv ? a.v_blk : a.v_pool};
+  for (int i = 0; i < 4; ++i) {
+    const bool blk = i >= 2 && a.n_kv > 0;
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hkv,
+                              blk ? (uint64_t)a.B * a.n_kv : (uint64_t)a.num_pages * a.page_size};
+    const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)a.Hkv * kD * 2};
+    const uint32_t box[3] = {64, 1, blk ? (uint32_t)a.n_kv : (uint32_t)p.br};
+    if (!encode_tensor_map(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base[i]), dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorNotSupported;   // tensor-map encoding refused a layout
+  }
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.ensure(prefix_attn_kernel, kPfxSmem);
+  if (e != cudaSuccess) return e;
+  prefix_attn_kernel<<<kGrid, kThreads, kPfxSmem, a.stream>>>(maps[0], maps[1], maps[2], maps[3], p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  *launches = 2;
+  const dim3 grid(a.B * a.Hkv, (p.R + kJoinRows - 1) / kJoinRows);
+  return launch_dependent(prefix_join_kernel, grid, dim3(kJoinThreads), 0, a.stream, p);
+}
+
+}  // namespace dflash
