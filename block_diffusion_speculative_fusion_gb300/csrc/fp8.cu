@@ -209,47 +209,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-// One lane of the (converged) warp, the same at every use of the returned flag.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-// Bounded wait of a whole (converged) warp, which also gives up when another
-// warp of the CTA has. The usual short wait is spun through (a suspended attempt
-// wakes late), a longer one suspends. One that took longer than the limit counts
-// as run out even if its phase came at last. The limit is counted in SM cycles,
-// two to a nanosecond (1.9 to 2.1 at full clock): the global timer ticks too
-// seldom for a limit below a few microseconds.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code,
-                                          unsigned long long limit_ns) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  const long long t0 = clock64();
-  for (int i = 0;; ++i) {
-    const bool done = __all_sync(0xffffffffu, i < 32 ? mbar_test(bar, parity) : mbar_try_wait(bar, parity));
-    if (!done && (i & 3) != 3) continue;
-    if (__any_sync(0xffffffffu, (unsigned long long)(clock64() - t0) / 2 > limit_ns)) {
-      *abort_flag = 1;
-      if (err && (threadIdx.x & 31) == 0) atomicCAS(err, 0, code);
-      return false;
-    }
-    if (done) return true;
-    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-  }
-}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }

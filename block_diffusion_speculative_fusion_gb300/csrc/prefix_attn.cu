@@ -29,7 +29,7 @@ constexpr int kMaxSeqs = 1024;
 constexpr int kSlots = 5;                   // ring of K and V tiles, 32 KB each
 constexpr int kTileBytes = kTK * kD * 2;    // a Q, K or V tile: two d-halves of 128 rows x 128 bytes
 constexpr int kHalf = kTileBytes / 2;
-constexpr int kThreads = 352;               // warps 0-3, 4-7 softmax; 8 K/V loads; 9 MMA; 10 Q loads
+constexpr int kThreads = 384;               // warps 0-3, 4-7 softmax; 8 K, 11 Q and V loads; 9, 10 MMA
 constexpr int kWarps = kThreads / 32;
 constexpr int kKept = 8;                    // piece descriptors kept in shared memory
 constexpr int kItemCost = 2;                // an own part's start and end, in tiles
@@ -336,6 +336,23 @@ __device__ __forceinline__ float pfx_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 pfx_fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 pfx_add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 __device__ __forceinline__ uint32_t pfx_pack(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
@@ -344,23 +361,25 @@ __device__ __forceinline__ uint32_t pfx_pack(float lo, float hi) {
 // A walk over the units of this CTA's pieces. A unit is one Q tile on one K/V tile: with
 // more than 128 rows the two Q tiles take each K/V tile in turn, with fewer the one Q
 // tile takes the K/V tiles one after the other. Units go to the two softmax groups
-// alternately, over all pieces.
+// alternately, over all pieces. (The descriptor stays where it is: the roles read the
+// fields they need, and a walk fits the registers of the one thread that issues MMAs.)
 struct PfxWalk {
-  PfxPiece p;
-  int k;          // piece
-  int w, n;       // unit of the piece, and how many it has
-  int u;          // units before, over all pieces: u & 1 is the softmax group
-  int tile0, q0;  // K/V tiles and Q tiles of the pieces before
-  bool two, live;
+  const PfxPiece* p;   // null: no more
+  int k;               // piece
+  int w, n;            // unit of the piece, and how many it has
+  int u;               // units before, over all pieces: u & 1 is the softmax group
+  int tile0, q0;       // K/V tiles and Q tiles of the pieces before
+  int two;             // two Q tiles
   __device__ __forceinline__ void open(const PfxParams& P, const PfxShared& sh) {
-    live = false;
+    p = nullptr;
     for (; k < sh.n_pieces; ++k) {
-      p = k < pfx::kKept ? sh.kept[k] : P.pieces[sh.piece0 + k];
-      if (p.nt > 0) {
-        two = p.nrows > pfx::kM;
-        n = two ? 2 * p.nt : p.nt;
+      const PfxPiece* d = k < pfx::kKept ? &sh.kept[k] : P.pieces + sh.piece0 + k;
+      const int nt = d->nt;
+      if (nt > 0) {
+        two = d->nrows > pfx::kM ? 1 : 0;
+        n = nt << two;
         w = 0;
-        live = true;
+        p = d;
         return;
       }
     }
@@ -370,8 +389,8 @@ struct PfxWalk {
     open(P, sh);
   }
   __device__ __forceinline__ void next_piece(const PfxParams& P, const PfxShared& sh) {
-    tile0 += p.nt;
-    q0 += two ? 2 : 1;
+    tile0 += n >> two;
+    q0 += 1 + two;
     ++k;
     open(P, sh);
   }
@@ -379,7 +398,7 @@ struct PfxWalk {
     ++u;
     if (++w == n) next_piece(P, sh);
   }
-  __device__ __forceinline__ int tile() const { return two ? w >> 1 : w; }   // in the piece
+  __device__ __forceinline__ int tile() const { return w >> two; }   // in the piece
 };
 
 __global__ void __launch_bounds__(pfx::kThreads, 1)
@@ -396,7 +415,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 1);
+      mbar_init(&sh.kv_empty[i], 2);       // both MMA warps, or one for both
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -404,9 +423,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.o_empty[i], 4);
       mbar_init(&sh.q_full[i], 1);
-      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.q_empty[i], 2);
     }
-    mbar_init(&sh.mma_done, 1);
+    mbar_init(&sh.mma_done, 2);
     sh.abort_flag = 0;
     fence_barrier_init();
   }
@@ -419,85 +438,34 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   PfxWalk wk;
-  int issued = 0;                  // tiles (K and V counted apart) that the producer has asked for
+  int issued = 0;                  // one past the last tile (K and V counted apart) that this warp has asked for
 
-  if (warp == 8) {
-    // ------------------------------ K/V loads ------------------------------
+  if (warp == 8 || warp == 11) {
+    // ------------------------------ K loads, Q and V loads ------------------------------
+    // A warp each: a box takes some hundred cycles to issue, and a tile of 16-position
+    // pages is 16 of them for K and as many for V.
+    const int v = warp == 11;
+    const CUtensorMap *map = v ? &vmap : &kmap, *bmap = v ? &vbmap : &kbmap;
+    const bool leader = elect_one();
     const uint64_t pol_once = l2_policy_evict_first();
-    const int bpt = kTK / p.br;                       // boxes of a context tile
+    const int bpt = kTK / p.br;                       // boxes of a context tile and d-half
     const int per = 32 / bpt;                         // tiles whose page numbers the warp holds at once
-    // page number of box `lane` of the tiles from t on; the lanes' entries fit the context
+    // first pool row of box `lane` of the tiles from t on; the lanes' entries fit the context
     auto fetch = [&](const PfxPiece& d, int t) -> int {
       const int key = d.key0 + t * kTK + lane * p.br;
       const int lp = key >> p.page_shift;
       if (t + lane / bpt >= min(d.nct, d.t0 + d.nt) || key >= d.C || lp >= p.max_pages) return 0;
       const int page = __ldg(p.page_table + (size_t)d.first * p.max_pages + lp);
-      if (page >= 0 && page < p.num_pages) return page;
+      if (page >= 0 && page < p.num_pages) return page << p.page_shift;
       record_dev_error(p.err, kDevErrBadPage);        // page 0 is read instead, never out of bounds
       return 0;
     };
-    bool ok = true;
-    wk.begin(p, sh);
-    int ids = wk.live ? fetch(wk.p, wk.p.t0) : 0;
-    while (ok && wk.live) {
-      const PfxPiece d = wk.p;
-      // the next piece's first page numbers are asked for while this one's tiles go out
-      PfxWalk nx = wk;
-      nx.next_piece(p, sh);
-      int ids_nx = nx.live ? fetch(nx.p, nx.p.t0) : 0;
-      int ids_on = fetch(d, d.t0 + per);
-      for (int j = 0; j < d.nt && ok; ++j) {
-        const int t = d.t0 + j, jj = j % per;
-        if (j > 0 && jj == 0) {
-          ids = ids_on;
-          ids_on = fetch(d, t + per);
-        }
-        const bool ctx = t < d.nct;
-        const int left = d.C - (d.key0 + t * kTK);
-        const int nb = ctx ? min(bpt, (left + p.br - 1) / p.br) : 1;      // boxes with a key in use
-        const uint32_t bytes = ctx ? (uint32_t)(nb * p.br * 256) : (uint32_t)(p.n_kv * 256);
-        const int box = lane >> 1, h = lane & 1;
-        const int page = __shfl_sync(0xffffffffu, ids, (jj * bpt + box) & 31);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int seq = 2 * (wk.tile0 + j) + v, st = seq % kSlots;
-          if (!__all_sync(0xffffffffu, wait_or_abort(&sh.kv_empty[st], (uint32_t)(((seq / kSlots) & 1) ^ 1),
-                                                     abort_flag, p.err, 41, p.wait_ns))) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[st], bytes);
-          __syncwarp();
-          ++issued;
-          uint8_t* dst = kv_s + st * kTileBytes + h * kHalf;
-          if (ctx) {
-            if (box < nb) {
-              const int row = (page << p.page_shift) + ((d.key0 + t * kTK + box * p.br) & ((1 << p.page_shift) - 1));
-              dst += box * p.br * 128;
-              if (d.member0 < 0)
-                tma_load_3d_hint(dst, v ? &vmap : &kmap, &sh.kv_full[st], h * 64, d.head, row, pol_once);
-              else
-                tma_load_3d(dst, v ? &vmap : &kmap, &sh.kv_full[st], h * 64, d.head, row);
-            }
-          } else if (box == 0) {
-            tma_load_3d(dst, v ? &vbmap : &kbmap, &sh.kv_full[st], h * 64, d.head, d.first * p.n_kv);
-          }
-        }
-      }
-      wk = nx;
-      ids = ids_nx;
-    }
-    __syncwarp();
-  } else if (warp == 10) {
-    // ------------------------------ Q loads ------------------------------
-    // Packed row r of a part: sequence r / R of its sequences, query row (r % R) / G,
-    // head r % G of the kv head's. 16 lanes bring a row, in the swizzle of its tile.
-    wk.begin(p, sh);
-    bool ok = true;
-    while (ok && wk.live) {
-      const PfxPiece d = wk.p;
-      for (int i = 0; i < (wk.two ? 2 : 1) && ok; ++i) {
-        const int qc = wk.q0 + i, buf = qc & 1;
+    // The piece's Q tiles. Packed row r of a part: sequence r / R of its sequences, query
+    // row (r % R) / G, head r % G of the kv head's. 16 lanes bring a row, in the swizzle
+    // of its tile.
+    auto load_q = [&](const PfxPiece& d, const PfxWalk& w) -> bool {
+      for (int i = 0; i <= w.two; ++i) {
+        const int qc = w.q0 + i, buf = qc & 1;
         int off[4];                                   // of rows lane, lane + 32, .. of the tile, in rows of q; -1: none
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -509,11 +477,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
           }
         }
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag,
-                                                   p.err, 42, p.wait_ns))) {
-          ok = false;
-          break;
-        }
+        if (!warp_wait(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag, p.err, 42, p.wait_ns)) return false;
         const int c = lane & 15;
         const uint32_t dst0 = smem_u32(q_s + buf * kTileBytes + (c >> 3) * kHalf);
 #pragma unroll
@@ -532,64 +496,137 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full[buf]);
       }
-      wk.next_piece(p, sh);
+      return true;
+    };
+    bool ok = true;
+    wk.begin(p, sh);
+    int ids = wk.p ? fetch(*wk.p, wk.p->t0) : 0;
+    while (ok && wk.p) {
+      const PfxPiece d = *wk.p;
+      if (v && !load_q(d, wk)) break;
+      // the next piece's first page numbers are asked for while this one's tiles go out
+      PfxWalk nx = wk;
+      nx.next_piece(p, sh);
+      int ids_nx = nx.p ? fetch(*nx.p, nx.p->t0) : 0;
+      int ids_on = fetch(d, d.t0 + per);
+      for (int j = 0; j < d.nt; ++j) {
+        const int t = d.t0 + j, jj = j % per;
+        if (j > 0 && jj == 0) {
+          ids = ids_on;
+          ids_on = fetch(d, t + per);
+        }
+        const bool ctx = t < d.nct;
+        const int nb = ctx ? min(bpt, (d.C - (d.key0 + t * kTK) + p.br - 1) / p.br) : 1;   // boxes with a key in use
+        const uint32_t bytes = (uint32_t)((ctx ? nb * p.br : p.n_kv) * 256);
+        const int seq = 2 * (wk.tile0 + j) + v, st = seq % kSlots;
+        if (!warp_wait(&sh.kv_empty[st], (uint32_t)(((seq / kSlots) & 1) ^ 1), abort_flag, p.err, 41 + 12 * v, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        uint64_t* full = &sh.kv_full[st];
+        uint8_t* dst = kv_s + st * kTileBytes;
+        if (leader) mbar_arrive_expect_tx(full, bytes);
+        issued = seq + 1;
+        if (!ctx) {
+          if (leader)
+            for (int h = 0; h < 2; ++h) tma_load_3d(dst + h * kHalf, bmap, full, h * 64, d.head, d.first * p.n_kv);
+        } else {
+          for (int box = 0; box < nb; ++box, dst += p.br * 128) {
+            const int row = __shfl_sync(0xffffffffu, ids, jj * bpt + box);
+            if (leader) {
+              if (d.member0 < 0) {
+                tma_load_3d_hint(dst, map, full, 0, d.head, row, pol_once);
+                tma_load_3d_hint(dst + kHalf, map, full, 64, d.head, row, pol_once);
+              } else {
+                tma_load_3d(dst, map, full, 0, d.head, row);
+                tma_load_3d(dst + kHalf, map, full, 64, d.head, row);
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+      wk = nx;
+      ids = ids_nx;
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 9 || warp == 10) {
     // ------------------------------ MMA ------------------------------
-    // S of unit u + 2 follows P V of unit u: while one softmax group works on its S, the
-    // tensor cores have the other's. S(u + 2) overwrites P(u) (same TMEM columns), which
-    // the P V before it in the pipe has read.
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
-      PfxWalk pv;
-      wk.begin(p, sh);
-      pv.begin(p, sh);
-      uint32_t o_phase[2] = {0, 0};
-      auto wait = [&](uint64_t* bar, uint32_t par, int code) {
-        return wait_or_abort(bar, par, abort_flag, p.err, code, p.wait_ns);
-      };
-      auto issue_s = [&]() -> bool {
-        if (!wk.live) return true;
-        const int x = wk.u & 1, seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots;
-        const int qi = wk.two ? wk.w & 1 : 0, qc = wk.q0 + qi, buf = qc & 1;
-        if (wk.w == qi && !wait(&sh.q_full[buf], (uint32_t)((qc >> 1) & 1), 43)) return false;
-        if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 44)) return false;
-        tc_fence_after();
-        const uint32_t qa = smem_u32(q_s + buf * kTileBytes), ka = smem_u32(kv_s + st * kTileBytes);
+    // A warp for each softmax group x. S of the group's next unit follows P V of the one
+    // before; it overwrites that unit's P (same TMEM columns), which the P V before it in
+    // the pipe has read. While the group works on its S, the tensor cores have the other
+    // group's. Each warp stays converged and one elected lane issues (a lane on its own
+    // took 600 to 850 cycles for eight MMAs, more than they do), and there are two of
+    // them because what lies between two batches of MMAs, the waits and commits, keeps
+    // one warp from filling the pipe.
+    const int x = warp - 9;
+    const bool leader = elect_one();
+    const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
+    const uint32_t s_t = tmem + kSCol + (uint32_t)(x * kTK), o_t = tmem + kOCol + (uint32_t)(x * kD);
+    // (a descriptor's address counts 16 bytes, and shared memory stays below its 2^14 of them)
+    const uint64_t q_desc = sdesc_sw128(smem_u32(q_s)), k_desc = sdesc_sw128(smem_u32(kv_s));
+    const uint64_t v_desc = sdesc_sw128_mn(smem_u32(kv_s), kHalf);
+    auto wait = [&](uint64_t* bar, uint32_t par, int code) {
+      return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
+    };
+    // S of the unit that `wk` stands at
+    auto issue_s = [&]() -> bool {
+      const int seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots;
+      const int qc = wk.q0 + (wk.w & wk.two), buf = qc & 1;
+      if (wk.w < 2 && !wait(&sh.q_full[buf], (uint32_t)((qc >> 1) & 1), 43)) return false;
+      if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 44)) return false;
+      tc_fence_after();
+      const uint64_t qd = q_desc + (uint64_t)(buf * (kTileBytes / 16)), kd = k_desc + (uint64_t)(st * (kTileBytes / 16));
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i) {
-          const uint32_t off = (uint32_t)((i >> 2) * kHalf + (i & 3) * 32);
-          tc_mma_bf16(tmem + kSCol + (uint32_t)(x * kTK), sdesc_sw128(qa + off), sdesc_sw128(ka + off), id_s,
-                      i > 0 ? 1u : 0u);
+          const uint64_t off = (uint64_t)(((i >> 2) * kHalf + (i & 3) * 32) / 16);
+          tc_mma_bf16(s_t, qd + off, kd + off, id_s, i > 0 ? 1u : 0u);
         }
         tc_commit(&sh.s_full[x]);
-        if (!wk.two || (wk.w & 1)) tc_commit(&sh.kv_empty[st]);
-        if (wk.w + (wk.two ? 2 : 1) >= wk.n) tc_commit(&sh.q_empty[buf]);
-        wk.next_unit(p, sh);
-        return true;
-      };
-      auto issue_pv = [&]() -> bool {
-        const int x = pv.u & 1, seq = 2 * (pv.tile0 + pv.tile()) + 1, st = seq % kSlots;
-        if (pv.w < 2) {     // the group's first unit of the piece: its O has been read out
-          if (!wait(&sh.o_empty[x], o_phase[x] ^ 1u, 45)) return false;
-          o_phase[x] ^= 1u;
+        tc_commit(&sh.kv_empty[st]);
+        if (!wk.two) mbar_arrive(&sh.kv_empty[st]);          // no unit of the other group reads this K tile
+        if (wk.w + 2 >= wk.n) {                              // the group's last S of the piece: its Q is free
+          tc_commit(&sh.q_empty[buf]);
+          if (wk.two || wk.n == 1) mbar_arrive(&sh.q_empty[buf]);
         }
-        if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 46)) return false;
-        if (!wait(&sh.p_full[x], (uint32_t)((pv.u >> 1) & 1), 47)) return false;
-        tc_fence_after();
-        const uint32_t pa = tmem + kSCol + (uint32_t)(x * kTK), va = smem_u32(kv_s + st * kTileBytes);
+      }
+      __syncwarp();
+      return true;
+    };
+    // units of a piece go to the groups in turn: from `wk` on to this group's next unit
+    auto seek = [&]() {
+      while (wk.p && ((wk.u ^ x) & 1)) wk.next_unit(p, sh);
+    };
+    wk.begin(p, sh);
+    seek();
+    bool ok = !wk.p || issue_s();
+    uint32_t o_phase = 0;
+    while (ok && wk.p) {
+      const int w = wk.w, n = wk.n, seq = 2 * (wk.tile0 + wk.tile()) + 1, st = seq % kSlots, two = wk.two;
+      const uint32_t par = (uint32_t)((wk.u >> 1) & 1);
+      if (w < 2) {     // the group's first unit of the piece: its O has been read out
+        if (!wait(&sh.o_empty[x], o_phase ^ 1u, 45)) break;
+        o_phase ^= 1u;
+      }
+      if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 46)) break;
+      wk.next_unit(p, sh);
+      seek();
+      if (!wait(&sh.p_full[x], par, 47)) break;
+      tc_fence_after();
+      const uint64_t vd = v_desc + (uint64_t)(st * (kTileBytes / 16));
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < kTK / 16; ++i)
-          tc_mma_bf16_ta(tmem + kOCol + (uint32_t)(x * kD), pa + (uint32_t)(i * 8), sdesc_sw128_mn(va + i * 2048, kHalf),
-                         id_pv, (pv.w >= 2 || i > 0) ? 1u : 0u);
-        if (!pv.two || (pv.w & 1)) tc_commit(&sh.kv_empty[st]);
-        if (pv.w >= pv.n - 2) tc_commit(&sh.o_full[x]);
-        pv.next_unit(p, sh);
-        return true;
-      };
-      bool ok = issue_s() && issue_s();
-      while (ok && pv.live) ok = issue_pv() && issue_s();
+          tc_mma_bf16_ta(o_t, s_t + (uint32_t)(i * 8), vd + (uint64_t)(i * 2048 / 16), id_pv, (w >= 2 || i > 0) ? 1u : 0u);
+        tc_commit(&sh.kv_empty[st]);
+        if (!two) mbar_arrive(&sh.kv_empty[st]);
+        if (w + 2 >= n) tc_commit(&sh.o_full[x]);
+      }
+      __syncwarp();
+      if (wk.p) ok = issue_s();
+    }
+    if (leader) {
       tc_commit(&sh.mma_done);
       mbar_wait_bounded(&sh.mma_done, 0, p.err, 48);
     }
@@ -600,20 +637,21 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_t = tmem + lane_off + kSCol + (uint32_t)(x * kTK), o_t = tmem + lane_off + kOCol + (uint32_t)(x * kD);
     auto wait = [&](uint64_t* bar, uint32_t par, int code) {
-      return __all_sync(0xffffffffu, wait_or_abort(bar, par, abort_flag, p.err, code, p.wait_ns));
+      return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
     };
     uint32_t units = 0, outs = 0;
     bool ok = true;
-    for (wk.begin(p, sh); ok && wk.live; wk.u += wk.n, wk.next_piece(p, sh)) {
-      const PfxPiece d = wk.p;
+    for (wk.begin(p, sh); ok && wk.p; wk.u += wk.n, wk.next_piece(p, sh)) {
+      const PfxPiece& d = *wk.p;
+      const int t0 = d.t0, nct = d.nct, left0 = d.C - d.key0;   // (of the own part from its first key on)
       const int w0 = (wk.u + x) & 1;                  // this group's first unit of the piece
       const int row = (wk.two ? w0 * kM : 0) + r;     // in the item's block of 256
       const int half = wk.two ? w0 : x;
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int w = w0; w < wk.n; w += 2, ++units) {
-        const int j = wk.two ? w >> 1 : w, t = d.t0 + j;
-        const bool ctx = t < d.nct;
-        const int valid = ctx ? min(kTK, d.C - (d.key0 + t * kTK)) : p.n_kv;
+        const int j = w >> wk.two, t = t0 + j;
+        const bool ctx = t < nct;
+        const int valid = ctx ? min(kTK, left0 - t * kTK) : p.n_kv;
         if (!wait(&sh.s_full[x], units & 1, 49)) {
           ok = false;
           break;
@@ -647,41 +685,43 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int c = 0; c < kTK; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
+        for (int c = 0; c < kTK; c += 2)
+          mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(sv[c])), __uint_as_float(sv[c + 1]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const bool raise = mt > m_run + kRescaleLog2 || (m_run == -CUDART_INF_F && mt != -CUDART_INF_F);
         if (w > w0 + 1 && __any_sync(0xffffffffu, raise)) {
           // (S of this unit was issued after P V of the group's last one, which is complete with it)
           const float alpha = !raise ? 1.f : m_run == -CUDART_INF_F ? 0.f : exp2f(m_run - mt);
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_t + (uint32_t)c, o);
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_t + (uint32_t)c, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_t + (uint32_t)c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(o_t + (uint32_t)c, o);
           }
           tmem_st_wait();
           l_run *= alpha;
         }
         if (raise) m_run = mt;
         const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        const float2 sc2 = {p.scale_log2, p.scale_log2}, nb2 = {-base, -base};
 #pragma unroll
-        for (int c = 0; c < kTK; c += 64) {
-          uint32_t pk[32];
+        for (int c = 0; c < kTK; c += 32) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = pfx_ex2(fmaf(__uint_as_float(sv[c + 2 * i]), p.scale_log2, -base));
-            const float b = pfx_ex2(fmaf(__uint_as_float(sv[c + 2 * i + 1]), p.scale_log2, -base));
-            rs[(2 * i) & 3] += a;
-            rs[(2 * i + 1) & 3] += b;
-            pk[i] = pfx_pack(a, b);
+          for (int i = 0; i < 16; ++i) {
+            float2 e = pfx_fma2(make_float2(__uint_as_float(sv[c + 2 * i]), __uint_as_float(sv[c + 2 * i + 1])), sc2, nb2);
+            e.x = pfx_ex2(e.x);
+            e.y = pfx_ex2(e.y);
+            rs[i & 1] = pfx_add2(rs[i & 1], e);
+            pk[i] = pfx_pack(e.x, e.y);
           }
-          tmem_st32(s_t + (uint32_t)(c / 2), pk);
+          tmem_st16(s_t + (uint32_t)(c / 2), pk);
         }
-        l_run += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        l_run += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -720,8 +760,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   // ------------------------------ end ------------------------------
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 && lane == 0 && *abort_flag)     // copies in flight land before the CTA leaves
-    for (int i = max(0, issued - kSlots); i < issued; ++i)
+  if ((warp == 8 || warp == 11) && lane == 0 && *abort_flag)   // copies in flight land before the CTA leaves
+    for (int i = issued - 1; i >= max(0, issued - kSlots); i -= 2)
       mbar_wait_bounded(&sh.kv_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 52);
   __syncthreads();
   if (warp == 9) {
