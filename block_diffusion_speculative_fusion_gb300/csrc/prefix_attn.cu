@@ -31,9 +31,11 @@ constexpr int kTileBytes = kTK * kD * 2;    // a Q, K or V tile: two d-halves of
 constexpr int kHalf = kTileBytes / 2;
 constexpr int kThreads = 384;               // warps 0-3, 4-7 softmax; 8 K, 11 Q and V loads; 9, 10 MMA
 constexpr int kWarps = kThreads / 32;
-constexpr int kKept = 8;                    // piece descriptors kept in shared memory
-constexpr int kItemCost = 2;                // an own part's start and end, in tiles
-constexpr int kMinShare = 2;                // least work of a CTA
+constexpr int kKept = 48;                   // piece descriptors kept in shared memory
+// Costs of the work list, in halves of a microsecond: a K/V tile for two Q tiles, for one,
+// and an own part's start and end.
+constexpr int kCostTwo = 4, kCostOne = 3, kItemCost = 6;
+constexpr int kMinShare = 4;                // least work of a CTA (no less than a tile)
 constexpr float kRescaleLog2 = 8.f;         // O is rescaled when the row maximum grows by more than 2^8
 // TMEM: S of the two softmax groups (P over its first half), then their O
 constexpr uint32_t kSCol = 0, kOCol = 256;
@@ -44,13 +46,12 @@ constexpr int kTmemCols = 512;
 struct PfxPiece {
   int first;     // sequence whose table row is read
   int member0;   // prefix: where the group's sequences begin in the order; own part: -1
-  int key0;      // position of the part's first key
-  int C;         // and past its last context key
-  int nct;       // context tiles of the part; the tile after them is the block's own rows
-  int t0, nt;    // this piece's tiles
+  int key0, len;     // position of the part's first context key, and their number
+  int blk;           // the tile that the block's own rows stand in (its last one); -1: none
+  int t0, nt;        // this piece's tiles
   int head;
   int row0, nrows;   // packed rows of the part's sequences
-  int slot;      // partials
+  int slot;          // partials
   int pad;
 };
 
@@ -73,6 +74,7 @@ struct PfxParams {
   float* po_p;  float2* ml_p;    // partials of prefixes [slot][2][128][128], [slot][2][128]
   float* po_s;  float2* ml_s;    // of own parts [slot][2][Rs2][128], [slot][2][Rs2]
   PfxPiece* pieces;
+  uint16_t* order;               // the groups' sequences, group after group
   PfxSeq* seqs;
   PfxGroup* groups;
   int32_t* header;               // [share]
@@ -87,14 +89,16 @@ struct PfxParams {
 // ---------------------------------------------------------------------------
 // The work list. Items, in order: for each group with a prefix worth sharing, block of
 // 256 packed rows, kv head: the prefix's tiles; then for each sequence, block, head: its
-// own tiles. A tile costs 1, or 2 with more than 128 rows (two Q tiles), an own part
-// kItemCost more. The costs in a row are cut into equal ranges, one a CTA; a tile
+// own tiles. A tile costs kCostOne, or kCostTwo with more than 128 rows (two Q tiles), an
+// own part kItemCost more. The costs in a row are cut into equal ranges, one a CTA; a tile
 // belongs to the range in which its cost begins. So the partition, and with it the
 // rounding, depends on the dims, lengths and groups alone.
 // ---------------------------------------------------------------------------
 __host__ __device__ __forceinline__ int pfx_blocks(int rows) { return (rows + 2 * pfx::kM - 1) / (2 * pfx::kM); }
 // weight of block k of `rows` packed rows
-__device__ __forceinline__ int pfx_weight(int rows, int k) { return rows - k * 2 * pfx::kM > pfx::kM ? 2 : 1; }
+__device__ __forceinline__ int pfx_weight(int rows, int k) {
+  return rows - k * 2 * pfx::kM > pfx::kM ? pfx::kCostTwo : pfx::kCostOne;
+}
 
 // First tile of an item (from position `base`, `ov` before its tiles, `nt` tiles of
 // weight w) that begins at or after position `at`.
@@ -107,32 +111,43 @@ __device__ __forceinline__ int pfx_first_tile(int base, int ov, int w, int nt, i
 __device__ __forceinline__ int pfx_cost_before(int rows, int nt, int ov, int Hkv, int k, int head) {
   const int n = pfx_blocks(rows);
   const int full = min(k, n - 1);                  // blocks before the last one have 256 rows
-  int c = full * Hkv * (2 * nt + ov);
+  int c = full * Hkv * (pfx::kCostTwo * nt + ov);
   if (k == n) c += Hkv * (pfx_weight(rows, n - 1) * nt + ov);
   else c += head * (pfx_weight(rows, k) * nt + ov);
   return c;
 }
 
-__device__ __forceinline__ int pfx_scan(int x, int* s_w, int* total) {
+// Exclusive prefixes of K values per thread over the CTA, and their totals.
+template <int K>
+__device__ __forceinline__ void pfx_scan(int (&x)[K], int* s_w, int (&total)[K]) {
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  int in = x;
+  int in[K];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, in, o);
-    if (l >= o) in += y;
-  }
-  __syncthreads();
-  if (l == 31) s_w[w] = in;
-  __syncthreads();
-  int base = 0, all = 0;
+  for (int k = 0; k < K; ++k) in[k] = x[k];
 #pragma unroll
-  for (int i = 0; i < pfx::kWarps; ++i) {
-    const int v = s_w[i];
-    base += i < w ? v : 0;
-    all += v;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, in[k], o);
+      if (l >= o) in[k] += y;
+    }
+  __syncthreads();
+  if (l == 31)
+#pragma unroll
+    for (int k = 0; k < K; ++k) s_w[k * pfx::kWarps + w] = in[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    int base = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < pfx::kWarps; ++i) {
+      const int v = s_w[k * pfx::kWarps + i];
+      base += i < w ? v : 0;
+      all += v;
+    }
+    total[k] = all;
+    x[k] = base + in[k] - x[k];
   }
-  *total = all;
-  return base + in - x;
 }
 
 // Last i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
@@ -152,9 +167,8 @@ struct PfxShared {
   uint32_t tmem_base;
   int abort_flag;
   int n_pieces, piece0;            // this CTA's pieces, in the list from piece0 on
-  int scan[pfx::kWarps + 1];
+  int scan[3 * pfx::kWarps];
   PfxPiece kept[pfx::kKept];
-  uint16_t order[pfx::kMaxSeqs];   // the groups' sequences, group after group
 };
 constexpr size_t kPfxSmem = (2 + pfx::kSlots) * (size_t)pfx::kTileBytes + sizeof(PfxShared);
 static_assert(kPfxSmem <= 232448, "shared memory");
@@ -168,8 +182,13 @@ struct PfxPlan {
 };
 static_assert(sizeof(PfxPlan) <= (2 + pfx::kSlots) * (size_t)pfx::kTileBytes, "plan scratch");
 
+// Tiles of a sequence's own part: its context keys behind the prefix, then the block's
+// rows, behind the last box of the last context tile where they fit there.
 __device__ __forceinline__ int pfx_own_tiles(const PfxParams& p, int ctx, int prefix_tiles) {
-  return (ctx - prefix_tiles * pfx::kTK + pfx::kTK - 1) / pfx::kTK + (p.n_kv > 0 ? 1 : 0);
+  const int len = ctx - prefix_tiles * pfx::kTK, nct = (len + pfx::kTK - 1) / pfx::kTK;
+  if (p.n_kv == 0 || nct == 0) return nct + (p.n_kv > 0);
+  const int boxes = (len - (nct - 1) * pfx::kTK + p.br - 1) >> p.page_shift;
+  return nct + (boxes * p.br + p.n_kv > pfx::kTK);
 }
 
 __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShared& sh) {
@@ -201,41 +220,41 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
   }
   __syncthreads();
   // groups: the tiles shared (none for a lone sequence), where their sequences, items and costs begin
-  int n_m = 0, n_i = 0, n_c = 0;
+  int at_g[3] = {0, 0, 0}, all_g[3];
   for (int g = g0; g < g1; ++g) {
     const int P = max(0, min(p.prefix_len[g], s.minc[g]));
     const int t = s.cnt[g] >= 2 ? P / kTK : 0;
     s.tiles[g] = t;
     if (t) {
-      n_m += s.cnt[g];
-      n_i += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
-      n_c += pfx_cost_before(s.cnt[g] * p.R, t, 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
+      at_g[0] += s.cnt[g];
+      at_g[1] += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
+      at_g[2] += pfx_cost_before(s.cnt[g] * p.R, t, 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
-  int all_m, all_i, all_c, all_s;
-  int m = pfx_scan(n_m, sh.scan, &all_m), i = pfx_scan(n_i, sh.scan, &all_i), c = pfx_scan(n_c, sh.scan, &all_c);
+  pfx_scan(at_g, sh.scan, all_g);
   for (int g = g0; g < g1; ++g) {
-    s.gstart[g] = m;
-    s.gitem[g] = i;
-    s.gbase[g] = c;
+    s.gstart[g] = at_g[0];
+    s.gitem[g] = at_g[1];
+    s.gbase[g] = at_g[2];
     if (s.tiles[g]) {
-      m += s.cnt[g];
-      i += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
-      c += pfx_cost_before(s.cnt[g] * p.R, s.tiles[g], 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
+      at_g[0] += s.cnt[g];
+      at_g[1] += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
+      at_g[2] += pfx_cost_before(s.cnt[g] * p.R, s.tiles[g], 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
+  const int all_i = all_g[1], all_c = all_g[2];
   __syncthreads();
   // own parts
-  int n_s = 0;
+  int at_s[1] = {0}, all_s[1];
   auto own_cost = [&](int b) {
     const int nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
     return nt ? pfx_cost_before(p.R, nt, kItemCost, p.Hkv, p.sblk, 0) : 0;
   };
-  for (int b = b0; b < b1; ++b) n_s += own_cost(b);
-  int at = all_c + pfx_scan(n_s, sh.scan, &all_s);
+  for (int b = b0; b < b1; ++b) at_s[0] += own_cost(b);
+  pfx_scan(at_s, sh.scan, all_s);
   for (int b = b0; b < b1; ++b) {
-    s.sbase[b] = at;
-    at += own_cost(b);
+    s.sbase[b] = all_c + at_s[0];
+    at_s[0] += own_cost(b);
   }
   // a group's sequences in ascending order
   if (tid < 32) {
@@ -247,7 +266,7 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       if (in) {
         const int pos = s.fill[g] + __popc(same & ((1u << lane) - 1));
         s.pos[b] = pos;
-        sh.order[s.gstart[g] + pos] = (uint16_t)b;
+        p.order[s.gstart[g] + pos] = (uint16_t)b;   // every CTA writes the same
       }
       __syncwarp();
       if (in && (same >> lane) == 1u) s.fill[g] += __popc(same);   // the last lane of each
@@ -255,19 +274,19 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     }
   }
   __syncthreads();
-  const int N = all_c + all_s, n_items = all_i + p.B * p.Hkv * p.sblk;
+  const int N = all_c + all_s[0];
   const int share = max(kMinShare, (N + kGrid - 1) / kGrid);
   const int lo = min((long)N, (long)blockIdx.x * share), hi = min((long)N, (long)lo + share);
   // the item that position x lies in
   auto item_at = [&](int x) {
     if (x < all_c) {
       const int g = pfx_find(s.gbase, p.n_groups, x), rows = s.cnt[g] * p.R;
-      const int rel = x - s.gbase[g], full = p.Hkv * 2 * s.tiles[g];
+      const int rel = x - s.gbase[g], full = p.Hkv * kCostTwo * s.tiles[g];
       const int k = min(rel / full, pfx_blocks(rows) - 1), in = rel - k * full;
       return s.gitem[g] + k * p.Hkv + in / (pfx_weight(rows, k) * s.tiles[g]);
     }
     const int b = pfx_find(s.sbase, p.B, x), nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
-    const int rel = x - s.sbase[b], full = p.Hkv * (2 * nt + kItemCost);
+    const int rel = x - s.sbase[b], full = p.Hkv * (kCostTwo * nt + kItemCost);
     const int k = min(rel / full, p.sblk - 1), in = rel - k * full;
     return all_i + (b * p.sblk + k) * p.Hkv + in / (pfx_weight(p.R, k) * nt + kItemCost);
   };
@@ -287,8 +306,8 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       d.first = s.first[g];
       d.member0 = s.gstart[g];
       d.key0 = 0;
-      d.C = nt * kTK;
-      d.nct = nt;
+      d.len = nt * kTK;
+      d.blk = -1;
       d.row0 = blk * 2 * kM;
       d.nrows = min(2 * kM, rows - d.row0);
       d.slot = it + (int)blockIdx.x;
@@ -303,8 +322,8 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       d.first = b;
       d.member0 = -1;
       d.key0 = t * kTK;
-      d.C = s.ctx[b];
-      d.nct = nt - (p.n_kv > 0 ? 1 : 0);
+      d.len = s.ctx[b] - d.key0;
+      d.blk = p.n_kv > 0 ? nt - 1 : -1;
       d.row0 = blk * 2 * kM;
       d.nrows = min(2 * kM, p.R - d.row0);
       d.slot = j + (int)blockIdx.x;
@@ -319,7 +338,6 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     sh.n_pieces = i1 - i0 + 1;
     sh.piece0 = i0 + (int)blockIdx.x;
   }
-  (void)n_items;
   if (blockIdx.x == 0) {
     for (int b = tid; b < p.B; b += kThreads) {
       const int g = s.grp[b], t = g >= 0 ? s.tiles[g] : 0;
@@ -404,6 +422,7 @@ struct PfxWalk {
 __global__ void __launch_bounds__(pfx::kThreads, 1)
 prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap kbmap, const __grid_constant__ CUtensorMap vbmap,
+                   const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ PfxParams p) {
   using namespace pfx;
   extern __shared__ __align__(1024) uint8_t pfx_smem[];
@@ -438,6 +457,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
   PfxWalk wk;
+  int q_boxes = 0;                 // one past the last Q tile that came as boxes
   int issued = 0;                  // one past the last tile (K and V counted apart) that this warp has asked for
 
   if (warp == 8 || warp == 11) {
@@ -452,20 +472,39 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int per = 32 / bpt;                         // tiles whose page numbers the warp holds at once
     // first pool row of box `lane` of the tiles from t on; the lanes' entries fit the context
     auto fetch = [&](const PfxPiece& d, int t) -> int {
-      const int key = d.key0 + t * kTK + lane * p.br;
-      const int lp = key >> p.page_shift;
-      if (t + lane / bpt >= min(d.nct, d.t0 + d.nt) || key >= d.C || lp >= p.max_pages) return 0;
+      const int key = t * kTK + lane * p.br, lp = (d.key0 + key) >> p.page_shift;
+      if (t + lane / bpt >= d.t0 + d.nt || key >= d.len || lp >= p.max_pages) return 0;
       const int page = __ldg(p.page_table + (size_t)d.first * p.max_pages + lp);
       if (page >= 0 && page < p.num_pages) return page << p.page_shift;
       record_dev_error(p.err, kDevErrBadPage);        // page 0 is read instead, never out of bounds
       return 0;
     };
-    // The piece's Q tiles. Packed row r of a part: sequence r / R of its sequences, query
-    // row (r % R) / G, head r % G of the kv head's. 16 lanes bring a row, in the swizzle
-    // of its tile.
-    auto load_q = [&](const PfxPiece& d, const PfxWalk& w) -> bool {
+    // The Q tiles of the piece that `w` stands at. Packed row r of a part: sequence r / R
+    // of its sequences, query row (r % R) / G, head r % G of the kv head's. A sequence's R
+    // rows are one box a d-half where they start at a multiple of eight tile rows and do
+    // not run over the tile's end; else 16 lanes bring a row, in the swizzle of its tile.
+    auto load_q = [&](const PfxWalk& w) -> bool {
+      const PfxPiece d = *w.p;
+      const bool boxes = p.R <= kM && (d.member0 < 0 || (p.R % 8 == 0 && kM % p.R == 0));
       for (int i = 0; i <= w.two; ++i) {
         const int qc = w.q0 + i, buf = qc & 1;
+        uint8_t* tile = q_s + buf * kTileBytes;
+        if (boxes) {
+          const int n = (min(d.nrows - i * kM, kM) + p.R - 1) / p.R, m0 = (d.row0 + i * kM) / p.R;
+          const int seq = d.member0 < 0 ? d.first : lane < n ? p.order[d.member0 + m0 + lane] : 0;
+          if (!warp_wait(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag, p.err, 42, p.wait_ns)) return false;
+          if (leader) mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(n * p.R * 256));
+          q_boxes = qc + 1;
+          for (int m = 0; m < n; ++m, tile += p.R * 128) {
+            const int b = __shfl_sync(0xffffffffu, seq, m);
+            if (leader) {
+              tma_load_3d(tile, &qmap, &sh.q_full[buf], 0, d.head * p.G, b * p.n_q);
+              tma_load_3d(tile + kHalf, &qmap, &sh.q_full[buf], 64, d.head * p.G, b * p.n_q);
+            }
+          }
+          __syncwarp();
+          continue;
+        }
         int off[4];                                   // of rows lane, lane + 32, .. of the tile, in rows of q; -1: none
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -473,13 +512,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const int mem = r / p.R, rem = r - mem * p.R, qi = rem / p.G;
           off[j] = -1;
           if (in < d.nrows) {
-            const int b = d.member0 < 0 ? d.first : sh.order[d.member0 + mem];
+            const int b = d.member0 < 0 ? d.first : p.order[d.member0 + mem];
             off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
           }
         }
         if (!warp_wait(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag, p.err, 42, p.wait_ns)) return false;
         const int c = lane & 15;
-        const uint32_t dst0 = smem_u32(q_s + buf * kTileBytes + (c >> 3) * kHalf);
+        const uint32_t dst0 = smem_u32(tile + (c >> 3) * kHalf);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -501,23 +540,26 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     bool ok = true;
     wk.begin(p, sh);
     int ids = wk.p ? fetch(*wk.p, wk.p->t0) : 0;
+    if (v && wk.p) ok = load_q(wk);
     while (ok && wk.p) {
       const PfxPiece d = *wk.p;
-      if (v && !load_q(d, wk)) break;
       // the next piece's first page numbers are asked for while this one's tiles go out
       PfxWalk nx = wk;
       nx.next_piece(p, sh);
       int ids_nx = nx.p ? fetch(*nx.p, nx.p->t0) : 0;
       int ids_on = fetch(d, d.t0 + per);
+      // and its Q, where that does not wait for this piece's tiles (two Q tiles in turn)
+      const bool q_first = nx.p && !wk.two && !nx.two;
+      if (v && q_first && !load_q(nx)) break;
       for (int j = 0; j < d.nt; ++j) {
         const int t = d.t0 + j, jj = j % per;
         if (j > 0 && jj == 0) {
           ids = ids_on;
           ids_on = fetch(d, t + per);
         }
-        const bool ctx = t < d.nct;
-        const int nb = ctx ? min(bpt, (d.C - (d.key0 + t * kTK) + p.br - 1) / p.br) : 1;   // boxes with a key in use
-        const uint32_t bytes = (uint32_t)((ctx ? nb * p.br : p.n_kv) * 256);
+        // boxes with a context key in use, then the block's rows
+        const int nb = min(bpt, max(0, (d.len - t * kTK + p.br - 1) >> p.page_shift));
+        const uint32_t bytes = (uint32_t)((nb * p.br + (t == d.blk ? p.n_kv : 0)) * 256);
         const int seq = 2 * (wk.tile0 + j) + v, st = seq % kSlots;
         if (!warp_wait(&sh.kv_empty[st], (uint32_t)(((seq / kSlots) & 1) ^ 1), abort_flag, p.err, 41 + 12 * v, p.wait_ns)) {
           ok = false;
@@ -527,25 +569,25 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         uint8_t* dst = kv_s + st * kTileBytes;
         if (leader) mbar_arrive_expect_tx(full, bytes);
         issued = seq + 1;
-        if (!ctx) {
-          if (leader)
-            for (int h = 0; h < 2; ++h) tma_load_3d(dst + h * kHalf, bmap, full, h * 64, d.head, d.first * p.n_kv);
-        } else {
-          for (int box = 0; box < nb; ++box, dst += p.br * 128) {
-            const int row = __shfl_sync(0xffffffffu, ids, jj * bpt + box);
-            if (leader) {
-              if (d.member0 < 0) {
-                tma_load_3d_hint(dst, map, full, 0, d.head, row, pol_once);
-                tma_load_3d_hint(dst + kHalf, map, full, 64, d.head, row, pol_once);
-              } else {
-                tma_load_3d(dst, map, full, 0, d.head, row);
-                tma_load_3d(dst + kHalf, map, full, 64, d.head, row);
-              }
+        for (int box = 0; box < nb; ++box, dst += p.br * 128) {
+          const int row = __shfl_sync(0xffffffffu, ids, jj * bpt + box);
+          if (leader) {
+            if (d.member0 < 0) {
+              tma_load_3d_hint(dst, map, full, 0, d.head, row, pol_once);
+              tma_load_3d_hint(dst + kHalf, map, full, 64, d.head, row, pol_once);
+            } else {
+              tma_load_3d(dst, map, full, 0, d.head, row);
+              tma_load_3d(dst + kHalf, map, full, 64, d.head, row);
             }
           }
         }
+        if (t == d.blk && leader) {
+          tma_load_3d(dst, bmap, full, 0, d.head, d.first * p.n_kv);
+          tma_load_3d(dst + kHalf, bmap, full, 64, d.head, d.first * p.n_kv);
+        }
         __syncwarp();
       }
+      if (ok && v && nx.p && !q_first) ok = load_q(nx);
       wk = nx;
       ids = ids_nx;
     }
@@ -640,19 +682,22 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
     };
     uint32_t units = 0, outs = 0;
-    bool ok = true;
+    // The first pass is made on nothing, while the first copies are on their way: it brings
+    // the instructions (some 20 KB, 3 us of misses if the first unit had them).
+    bool ok = true, dry = true;
     for (wk.begin(p, sh); ok && wk.p; wk.u += wk.n, wk.next_piece(p, sh)) {
       const PfxPiece& d = *wk.p;
-      const int t0 = d.t0, nct = d.nct, left0 = d.C - d.key0;   // (of the own part from its first key on)
+      const int t0 = d.t0, len = d.len, blk = d.blk;
       const int w0 = (wk.u + x) & 1;                  // this group's first unit of the piece
       const int row = (wk.two ? w0 * kM : 0) + r;     // in the item's block of 256
       const int half = wk.two ? w0 : x;
       float m_run = -CUDART_INF_F, l_run = 0.f;
-      for (int w = w0; w < wk.n; w += 2, ++units) {
+      for (int w = w0; w < wk.n;) {
         const int j = w >> wk.two, t = t0 + j;
-        const bool ctx = t < nct;
-        const int valid = ctx ? min(kTK, left0 - t * kTK) : p.n_kv;
-        if (!wait(&sh.s_full[x], units & 1, 49)) {
+        // the tile's keys: context rows [0, keys), and in its last tile the block's from row blk0 on
+        const int keys = min(kTK, max(0, len - t * kTK));
+        const int blk0 = t == blk ? (keys + p.br - 1) >> p.page_shift << p.page_shift : kTK;
+        if (!dry && !wait(&sh.s_full[x], units & 1, 49)) {
           ok = false;
           break;
         }
@@ -661,19 +706,19 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
         for (int c = 0; c < kTK; c += 32) tmem_ld32(s_t + (uint32_t)c, sv + c);
         tmem_ld_wait();
-        if (valid < kTK || (p.causal && !ctx)) {
+        if (keys < kTK && !dry) {
           // causal: the row of query i sees the block's rows up to its own
-          const int seen = p.causal && !ctx ? min(valid, ((d.row0 + row) % p.R) / p.G + 1 + p.n_kv - p.n_q) : valid;
+          const int seen = p.causal ? min(p.n_kv, ((d.row0 + row) % p.R) / p.G + 1 + p.n_kv - p.n_q) : p.n_kv;
 #pragma unroll
           for (int c = 0; c < kTK; ++c)
-            if (c >= seen) sv[c] = 0xff800000u;       // -inf, whatever stood there
-          // V rows past the last key may hold anything, and 0 * NaN is NaN: zero them
+            if (c >= keys && (unsigned)(c - blk0) >= (unsigned)seen) sv[c] = 0xff800000u;   // -inf, whatever stood there
+          // V rows of no key may hold anything, and 0 * NaN is NaN: zero them
           const int seq = 2 * (wk.tile0 + j) + 1, st = seq % kSlots;
           if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 50)) {
             ok = false;
             break;
           }
-          if (r >= valid) {
+          if (r >= keys && (unsigned)(r - blk0) >= (unsigned)p.n_kv) {
             uint8_t* v = kv_s + st * kTileBytes + r * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -706,6 +751,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         if (raise) m_run = mt;
         const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
+        const uint32_t p_t = dry ? o_t : s_t;     // (nothing has been written to O yet)
         float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
         const float2 sc2 = {p.scale_log2, p.scale_log2}, nb2 = {-base, -base};
 #pragma unroll
@@ -719,13 +765,21 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             rs[i & 1] = pfx_add2(rs[i & 1], e);
             pk[i] = pfx_pack(e.x, e.y);
           }
-          tmem_st16(s_t + (uint32_t)(c / 2), pk);
+          tmem_st16(p_t + (uint32_t)(c / 2), pk);
         }
         l_run += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[x]);
+        if (!dry) {
+          if (lane == 0) mbar_arrive(&sh.p_full[x]);
+          w += 2;
+          ++units;
+        } else {
+          dry = false;
+          m_run = -CUDART_INF_F;
+          l_run = 0.f;
+        }
       }
       if (!ok) break;
       // the piece's partials of this group
@@ -746,8 +800,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           tmem_ld_wait();
           if (mine) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(po + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 8)     // whole sectors
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + c + i), "r"(o[i]),
+                           "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
+                           "r"(o[i + 7])
+                           : "memory");
           }
         }
         tc_fence_before();
@@ -763,6 +820,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   if ((warp == 8 || warp == 11) && lane == 0 && *abort_flag)   // copies in flight land before the CTA leaves
     for (int i = issued - 1; i >= max(0, issued - kSlots); i -= 2)
       mbar_wait_bounded(&sh.kv_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 52);
+  if (warp == 11 && lane == 0 && *abort_flag)
+    for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i)
+      mbar_wait_bounded(&sh.q_full[i & 1], (uint32_t)((i >> 1) & 1), p.err, 54);
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
@@ -804,9 +864,9 @@ prefix_join_kernel(const __grid_constant__ PfxParams p) {
     int v1;
     ranges(s.base + pfx_cost_before(p.R, s.nt, kItemCost, p.Hkv, blk, head), kItemCost, w, s.nt, v0[0], v1);
     n[0] = v1 - v0[0] + 1;
-    halves[0] = w == 2 ? 1 : 2;
+    halves[0] = w == kCostTwo ? 1 : 2;
     step[0] = (size_t)2 * p.Rs2;
-    const size_t at = ((size_t)((b * p.sblk + blk) * p.Hkv + head) + v0[0]) * step[0] + (w == 2 ? in / kM * p.Rs2 + in % kM : in);
+    const size_t at = ((size_t)((b * p.sblk + blk) * p.Hkv + head) + v0[0]) * step[0] + (w == kCostTwo ? in / kM * p.Rs2 + in % kM : in);
     ml[0] = p.ml_s + at;
     po[0] = p.po_s + at * kD + c0;
   }
@@ -817,7 +877,7 @@ prefix_join_kernel(const __grid_constant__ PfxParams p) {
     int v1;
     ranges(g.base + pfx_cost_before(g.rows, g.tiles, 0, p.Hkv, blk, head), 0, w, g.tiles, v0[1], v1);
     n[1] = v1 - v0[1] + 1;
-    halves[1] = w == 2 ? 1 : 2;
+    halves[1] = w == kCostTwo ? 1 : 2;
     step[1] = 2 * kM;
     const size_t at = ((size_t)(g.item + blk * p.Hkv + head) + v0[1]) * step[1] + in;   // (two Q tiles: in / 128 is the half)
     ml[1] = p.ml_p + at;
@@ -867,13 +927,13 @@ static bool pfx_dims_ok(int B, int n_q, int n_kv, int Hq, int Hkv, int D, int ma
   using namespace pfx;
   if (dtype != 1 || D != kD || B > kMaxSeqs || n_kv > kTK) return false;
   if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return false;
-  // costs are 32-bit: twice every tile of every sequence, head and block
+  // costs are 32-bit
   const double tiles = (double)max_ctx / kTK + 2 + kItemCost;
-  return 2.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
+  return 4.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
 }
 
 struct PfxLayout {
-  size_t pieces, seqs, groups, header, po_p, ml_p, po_s, ml_s, end;
+  size_t pieces, order, seqs, groups, header, po_p, ml_p, po_s, ml_s, end;
   int sblk, Rs2;
 };
 static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
@@ -892,6 +952,7 @@ static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
     return o;
   };
   l.pieces = take((ip + is + kGrid) * sizeof(PfxPiece));
+  l.order = take(B * sizeof(uint16_t));
   l.seqs = take(B * sizeof(PfxSeq));
   l.groups = take(std::max(n_groups, 1) * sizeof(PfxGroup));
   l.header = take(sizeof(int32_t));
@@ -928,6 +989,7 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   p.prefix_len = pa.prefix_len;
   p.out = (bf16*)a.out;
   p.pieces = (PfxPiece*)(ws + l.pieces);
+  p.order = (uint16_t*)(ws + l.order);
   p.seqs = (PfxSeq*)(ws + l.seqs);
   p.groups = (PfxGroup*)(ws + l.groups);
   p.header = (int32_t*)(ws + l.header);
@@ -947,7 +1009,7 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   p.scale_log2 = a.scale * kLog2e;
   p.wait_ns = wait_limit_ns();
   // pools and block rows as [row][head][d]: a box of 64 d x 1 head x rows lands as [row][64 d]
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   const void* base[4] = {a.k_pool, a.v_pool, a.n_kv ? a.k_blk : a.k_pool, a.n_kv ? a.v_blk : a.v_pool};
   for (int i = 0; i < 4; ++i) {
     const bool blk = i >= 2 && a.n_kv > 0;
@@ -959,10 +1021,20 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
                            CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorNotSupported;   // tensor-map encoding refused a layout
   }
+  {
+    // a sequence's packed rows of one kv head, [query][head][64 d]; not used for more than a tile's
+    const bool fits = p.R <= kM;
+    const uint64_t dims[3] = {(uint64_t)kD, (uint64_t)a.Hq, (uint64_t)a.B * a.n_q};
+    const uint64_t strides[2] = {(uint64_t)kD * 2, (uint64_t)a.Hq * kD * 2};
+    const uint32_t box[3] = {64, fits ? (uint32_t)p.G : 1, fits ? (uint32_t)a.n_q : 1};
+    if (!encode_tensor_map(&maps[4], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorNotSupported;
+  }
   static SmemOptIn opt_in;
   cudaError_t e = opt_in.ensure(prefix_attn_kernel, kPfxSmem);
   if (e != cudaSuccess) return e;
-  prefix_attn_kernel<<<kGrid, kThreads, kPfxSmem, a.stream>>>(maps[0], maps[1], maps[2], maps[3], p);
+  prefix_attn_kernel<<<kGrid, kThreads, kPfxSmem, a.stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches = 2;
