@@ -7,7 +7,7 @@
 // A softmax over a set of keys splits over parts of it: with (m_i, l_i, O_i) the
 // maximum, sum and unnormalised output of part i,
 //   out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
-// The parts here are the group's prefix (whole tiles of 128 positions), worked on with
+// The parts here are the group's prefix (whole tiles of 64 positions), worked on with
 // the queries of all its sequences, and what each sequence has of its own: the rest
 // of its context and the block's rows. Both are pieces of one work list (below); every
 // piece leaves fp32 partials, which a second kernel joins in a fixed order.
@@ -22,23 +22,25 @@ namespace dflash {
 
 namespace pfx {
 constexpr int kD = 128;
-constexpr int kTK = 128;                    // keys of a tile
+constexpr int kTK = 64;                     // keys of a tile
 constexpr int kM = 128;                     // packed query rows of a Q tile (TMEM lanes)
 constexpr int kGrid = 152;                  // persistent CTAs: one per SM
 constexpr int kMaxSeqs = 1024;
-constexpr int kSlots = 5;                   // ring of K and V tiles, 32 KB each
-constexpr int kTileBytes = kTK * kD * 2;    // a Q, K or V tile: two d-halves of 128 rows x 128 bytes
+constexpr int kSlots = 10;                  // ring of K and V tiles
+constexpr int kTileBytes = kTK * kD * 2;    // a K or V tile: two d-halves of 64 rows x 128 bytes
 constexpr int kHalf = kTileBytes / 2;
-constexpr int kThreads = 384;               // warps 0-3, 4-7 softmax; 8 K, 11 Q and V loads; 9, 10 MMA
+constexpr int kQBytes = kM * kD * 2;        // a Q tile: two d-halves of 128 rows
+constexpr int kQHalf = kQBytes / 2;
+constexpr int kThreads = 416;               // warps 0-3, 4-7 softmax; 8 K, 9 V, 10 Q loads; 11, 12 MMA
 constexpr int kWarps = kThreads / 32;
 constexpr int kKept = 48;                   // piece descriptors kept in shared memory
 // Costs of the work list, in halves of a microsecond: a K/V tile for two Q tiles, for one,
 // and an own part's start and end.
-constexpr int kCostTwo = 4, kCostOne = 3, kItemCost = 6;
+constexpr int kCostTwo = 4, kCostOne = 3, kItemCost = 9;
 constexpr int kMinShare = 4;                // least work of a CTA (no less than a tile)
 constexpr float kRescaleLog2 = 8.f;         // O is rescaled when the row maximum grows by more than 2^8
-// TMEM: S of the two softmax groups (P over its first half), then their O
-constexpr uint32_t kSCol = 0, kOCol = 256;
+// TMEM columns: S of the two softmax groups, their P (bf16 pairs), their O
+constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 256;
 constexpr int kTmemCols = 512;
 }  // namespace pfx
 
@@ -81,7 +83,8 @@ struct PfxParams {
   int* err;
   int B, n_groups, n_q, n_kv, Hq, Hkv, G, R;   // R = n_q * G packed rows of a sequence and kv head
   int sblk, Rs2;                 // blocks of 256 rows of a sequence; rows of a half's partials
-  int page_shift, max_pages, num_pages, max_ctx, causal, br;   // br: rows of a page's box
+  int page_shift, max_pages, num_pages, max_ctx, causal;
+  int br, br_shift;              // rows of a box: a page's, at most a tile's
   float scale_log2;
   unsigned long long wait_ns;
 };
@@ -163,14 +166,14 @@ __device__ __forceinline__ int pfx_find(const int* a, int n, int x) {
 // Shared memory: Q tiles, ring, then the small things.
 struct PfxShared {
   uint64_t kv_full[pfx::kSlots], kv_empty[pfx::kSlots];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], q_full[2], q_empty[2], mma_done;
+  uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], q_full[2], q_empty[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int n_pieces, piece0;            // this CTA's pieces, in the list from piece0 on
   int scan[3 * pfx::kWarps];
   PfxPiece kept[pfx::kKept];
 };
-constexpr size_t kPfxSmem = (2 + pfx::kSlots) * (size_t)pfx::kTileBytes + sizeof(PfxShared);
+constexpr size_t kPfxSmem = 2 * (size_t)pfx::kQBytes + pfx::kSlots * (size_t)pfx::kTileBytes + sizeof(PfxShared);
 static_assert(kPfxSmem <= 232448, "shared memory");
 
 // The plan, in scratch that the ring takes over afterwards.
@@ -180,14 +183,14 @@ struct PfxPlan {
   int cnt[pfx::kMaxSeqs], minc[pfx::kMaxSeqs], first[pfx::kMaxSeqs], tiles[pfx::kMaxSeqs], fill[pfx::kMaxSeqs];
   int gstart[pfx::kMaxSeqs + 1], gbase[pfx::kMaxSeqs + 1], gitem[pfx::kMaxSeqs + 1];
 };
-static_assert(sizeof(PfxPlan) <= (2 + pfx::kSlots) * (size_t)pfx::kTileBytes, "plan scratch");
+static_assert(sizeof(PfxPlan) <= 2 * (size_t)pfx::kQBytes + pfx::kSlots * (size_t)pfx::kTileBytes, "plan scratch");
 
 // Tiles of a sequence's own part: its context keys behind the prefix, then the block's
 // rows, behind the last box of the last context tile where they fit there.
 __device__ __forceinline__ int pfx_own_tiles(const PfxParams& p, int ctx, int prefix_tiles) {
   const int len = ctx - prefix_tiles * pfx::kTK, nct = (len + pfx::kTK - 1) / pfx::kTK;
   if (p.n_kv == 0 || nct == 0) return nct + (p.n_kv > 0);
-  const int boxes = (len - (nct - 1) * pfx::kTK + p.br - 1) >> p.page_shift;
+  const int boxes = (len - (nct - 1) * pfx::kTK + p.br - 1) >> p.br_shift;
   return nct + (boxes * p.br + p.n_kv > pfx::kTK);
 }
 
@@ -427,8 +430,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   using namespace pfx;
   extern __shared__ __align__(1024) uint8_t pfx_smem[];
   uint8_t* q_s = pfx_smem;                           // two Q tiles
-  uint8_t* kv_s = pfx_smem + 2 * kTileBytes;
-  PfxShared& sh = *reinterpret_cast<PfxShared*>(pfx_smem + (2 + kSlots) * kTileBytes);
+  uint8_t* kv_s = pfx_smem + 2 * kQBytes;            // ring: K of tile 0, V of tile 0, K of tile 1, ..
+  PfxShared& sh = *reinterpret_cast<PfxShared*>(kv_s + kSlots * kTileBytes);
   volatile int* abort_flag = &sh.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -438,8 +441,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_read[i], 4);
       mbar_init(&sh.p_full[i], 4);
-      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.o_empty[i], 4);
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 2);
@@ -448,7 +452,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     sh.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(&sh.tmem_base, kTmemCols);
+  if (warp == 11) tmem_alloc(&sh.tmem_base, kTmemCols);
   dependents_may_launch();
   pfx_plan(p, *reinterpret_cast<PfxPlan*>(pfx_smem), sh);
   fence_proxy_async_smem();        // the scratch becomes the ring: its writes come before the copies
@@ -460,87 +464,29 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   int q_boxes = 0;                 // one past the last Q tile that came as boxes
   int issued = 0;                  // one past the last tile (K and V counted apart) that this warp has asked for
 
-  if (warp == 8 || warp == 11) {
-    // ------------------------------ K loads, Q and V loads ------------------------------
+  if (warp == 8 || warp == 9) {
+    // ------------------------------ K loads, V loads ------------------------------
     // A warp each: a box takes some hundred cycles to issue, and a tile of 16-position
-    // pages is 16 of them for K and as many for V.
-    const int v = warp == 11;
+    // pages is 8 of them for K and as many for V.
+    const int v = warp == 9;
     const CUtensorMap *map = v ? &vmap : &kmap, *bmap = v ? &vbmap : &kbmap;
     const bool leader = elect_one();
     const uint64_t pol_once = l2_policy_evict_first();
-    const int bpt = kTK / p.br;                       // boxes of a context tile and d-half
+    const int bpt = kTK >> p.br_shift;                // boxes of a context tile and d-half
     const int per = 32 / bpt;                         // tiles whose page numbers the warp holds at once
     // first pool row of box `lane` of the tiles from t on; the lanes' entries fit the context
     auto fetch = [&](const PfxPiece& d, int t) -> int {
-      const int key = t * kTK + lane * p.br, lp = (d.key0 + key) >> p.page_shift;
+      const int key = t * kTK + lane * p.br, pos = d.key0 + key, lp = pos >> p.page_shift;
       if (t + lane / bpt >= d.t0 + d.nt || key >= d.len || lp >= p.max_pages) return 0;
       const int page = __ldg(p.page_table + (size_t)d.first * p.max_pages + lp);
-      if (page >= 0 && page < p.num_pages) return page << p.page_shift;
+      const int in = pos & ((1 << p.page_shift) - 1);
+      if (page >= 0 && page < p.num_pages) return (page << p.page_shift) + in;
       record_dev_error(p.err, kDevErrBadPage);        // page 0 is read instead, never out of bounds
-      return 0;
-    };
-    // The Q tiles of the piece that `w` stands at. Packed row r of a part: sequence r / R
-    // of its sequences, query row (r % R) / G, head r % G of the kv head's. A sequence's R
-    // rows are one box a d-half where they start at a multiple of eight tile rows and do
-    // not run over the tile's end; else 16 lanes bring a row, in the swizzle of its tile.
-    auto load_q = [&](const PfxWalk& w) -> bool {
-      const PfxPiece d = *w.p;
-      const bool boxes = p.R <= kM && (d.member0 < 0 || (p.R % 8 == 0 && kM % p.R == 0));
-      for (int i = 0; i <= w.two; ++i) {
-        const int qc = w.q0 + i, buf = qc & 1;
-        uint8_t* tile = q_s + buf * kTileBytes;
-        if (boxes) {
-          const int n = (min(d.nrows - i * kM, kM) + p.R - 1) / p.R, m0 = (d.row0 + i * kM) / p.R;
-          const int seq = d.member0 < 0 ? d.first : lane < n ? p.order[d.member0 + m0 + lane] : 0;
-          if (!warp_wait(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag, p.err, 42, p.wait_ns)) return false;
-          if (leader) mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(n * p.R * 256));
-          q_boxes = qc + 1;
-          for (int m = 0; m < n; ++m, tile += p.R * 128) {
-            const int b = __shfl_sync(0xffffffffu, seq, m);
-            if (leader) {
-              tma_load_3d(tile, &qmap, &sh.q_full[buf], 0, d.head * p.G, b * p.n_q);
-              tma_load_3d(tile + kHalf, &qmap, &sh.q_full[buf], 64, d.head * p.G, b * p.n_q);
-            }
-          }
-          __syncwarp();
-          continue;
-        }
-        int off[4];                                   // of rows lane, lane + 32, .. of the tile, in rows of q; -1: none
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int in = i * kM + j * 32 + lane, r = d.row0 + in;
-          const int mem = r / p.R, rem = r - mem * p.R, qi = rem / p.G;
-          off[j] = -1;
-          if (in < d.nrows) {
-            const int b = d.member0 < 0 ? d.first : p.order[d.member0 + mem];
-            off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
-          }
-        }
-        if (!warp_wait(&sh.q_empty[buf], (uint32_t)(((qc >> 1) & 1) ^ 1), abort_flag, p.err, 42, p.wait_ns)) return false;
-        const int c = lane & 15;
-        const uint32_t dst0 = smem_u32(tile + (c >> 3) * kHalf);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int s = 0; s < 16; ++s) {
-            const int in = 2 * s + (lane >> 4), row = j * 32 + in;
-            const int o = __shfl_sync(0xffffffffu, off[j], in);
-            const bf16* src = p.q + (size_t)max(o, 0) * kD + c * 8;
-            const uint32_t dst = dst0 + (uint32_t)(row * 128 + (((c & 7) ^ (row & 7)) << 4));
-            const int bytes = o < 0 ? 0 : 16;          // rows past the last are zero
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-          }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full[buf]);
-      }
-      return true;
+      return in;
     };
     bool ok = true;
     wk.begin(p, sh);
     int ids = wk.p ? fetch(*wk.p, wk.p->t0) : 0;
-    if (v && wk.p) ok = load_q(wk);
     while (ok && wk.p) {
       const PfxPiece d = *wk.p;
       // the next piece's first page numbers are asked for while this one's tiles go out
@@ -548,9 +494,6 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       nx.next_piece(p, sh);
       int ids_nx = nx.p ? fetch(*nx.p, nx.p->t0) : 0;
       int ids_on = fetch(d, d.t0 + per);
-      // and its Q, where that does not wait for this piece's tiles (two Q tiles in turn)
-      const bool q_first = nx.p && !wk.two && !nx.two;
-      if (v && q_first && !load_q(nx)) break;
       for (int j = 0; j < d.nt; ++j) {
         const int t = d.t0 + j, jj = j % per;
         if (j > 0 && jj == 0) {
@@ -558,7 +501,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           ids_on = fetch(d, t + per);
         }
         // boxes with a context key in use, then the block's rows
-        const int nb = min(bpt, max(0, (d.len - t * kTK + p.br - 1) >> p.page_shift));
+        const int nb = min(bpt, max(0, (d.len - t * kTK + p.br - 1) >> p.br_shift));
         const uint32_t bytes = (uint32_t)((nb * p.br + (t == d.blk ? p.n_kv : 0)) * 256);
         const int seq = 2 * (wk.tile0 + j) + v, st = seq % kSlots;
         if (!warp_wait(&sh.kv_empty[st], (uint32_t)(((seq / kSlots) & 1) ^ 1), abort_flag, p.err, 41 + 12 * v, p.wait_ns)) {
@@ -587,44 +530,112 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         __syncwarp();
       }
-      if (ok && v && nx.p && !q_first) ok = load_q(nx);
       wk = nx;
       ids = ids_nx;
     }
     __syncwarp();
-  } else if (warp == 9 || warp == 10) {
+  } else if (warp == 10) {
+    // ------------------------------ Q loads ------------------------------
+    // Packed row r of a part: sequence r / R of its sequences, query row (r % R) / G,
+    // head r % G of the kv head's. A sequence's R rows are one box a d-half where they
+    // start at a multiple of eight tile rows and do not run over the tile's end; else 16
+    // lanes bring a row, in the swizzle of its tile.
+    const bool leader = elect_one();
+    bool ok = true;
+    for (wk.begin(p, sh); ok && wk.p; wk.next_piece(p, sh)) {
+      const PfxPiece d = *wk.p;
+      const bool boxes = p.R <= kM && (d.member0 < 0 || (p.R % 8 == 0 && kM % p.R == 0));
+      for (int i = 0; i <= wk.two && ok; ++i) {
+        const int qc = wk.q0 + i, buf = qc & 1;
+        uint8_t* tile = q_s + buf * kQBytes;
+        const uint32_t par = (uint32_t)(((qc >> 1) & 1) ^ 1);
+        if (boxes) {
+          const int n = (min(d.nrows - i * kM, kM) + p.R - 1) / p.R, m0 = (d.row0 + i * kM) / p.R;
+          const int seq = d.member0 < 0 ? d.first : lane < n ? p.order[d.member0 + m0 + lane] : 0;
+          ok = warp_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
+          if (!ok) break;
+          if (leader) mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(n * p.R * 256));
+          q_boxes = qc + 1;
+          for (int m = 0; m < n; ++m, tile += p.R * 128) {
+            const int b = __shfl_sync(0xffffffffu, seq, m);
+            if (leader) {
+              tma_load_3d(tile, &qmap, &sh.q_full[buf], 0, d.head * p.G, b * p.n_q);
+              tma_load_3d(tile + kQHalf, &qmap, &sh.q_full[buf], 64, d.head * p.G, b * p.n_q);
+            }
+          }
+          __syncwarp();
+          continue;
+        }
+        int off[4];                                   // of rows lane, lane + 32, .. of the tile, in rows of q; -1: none
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int in = i * kM + j * 32 + lane, r = d.row0 + in;
+          const int mem = r / p.R, rem = r - mem * p.R, qi = rem / p.G;
+          off[j] = -1;
+          if (in < d.nrows) {
+            const int b = d.member0 < 0 ? d.first : p.order[d.member0 + mem];
+            off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
+          }
+        }
+        ok = warp_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
+        if (!ok) break;
+        const int c = lane & 15;
+        const uint32_t dst0 = smem_u32(tile + (c >> 3) * kQHalf);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int s = 0; s < 16; ++s) {
+            const int in = 2 * s + (lane >> 4), row = j * 32 + in;
+            const int o = __shfl_sync(0xffffffffu, off[j], in);
+            const bf16* src = p.q + (size_t)max(o, 0) * kD + c * 8;
+            const uint32_t dst = dst0 + (uint32_t)(row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            const int bytes = o < 0 ? 0 : 16;          // rows past the last are zero
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+          }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 11) {
     // ------------------------------ MMA ------------------------------
-    // A warp for each softmax group x. S of the group's next unit follows P V of the one
-    // before; it overwrites that unit's P (same TMEM columns), which the P V before it in
-    // the pipe has read. While the group works on its S, the tensor cores have the other
-    // group's. Each warp stays converged and one elected lane issues (a lane on its own
-    // took 600 to 850 cycles for eight MMAs, more than they do), and there are two of
-    // them because what lies between two batches of MMAs, the waits and commits, keeps
-    // one warp from filling the pipe.
-    const int x = warp - 9;
+    // A warp for each softmax group x, since what lies between two batches of MMAs, the
+    // waits and commits, keeps one warp from filling the pipe. S of the group's next unit
+    // goes out as soon as the group holds this unit's S in registers, so that it is there
+    // when the group is done. The warp stays converged and one elected lane issues (a
+    // lane on its own took 600 to 850 cycles for eight MMAs, more than they do).
+    const int x = warp - 11;
     const bool leader = elect_one();
     const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
-    const uint32_t s_t = tmem + kSCol + (uint32_t)(x * kTK), o_t = tmem + kOCol + (uint32_t)(x * kD);
+    const uint32_t s_t = tmem + kSCol + (uint32_t)(x * kTK), p_t = tmem + kPCol + (uint32_t)(x * kTK / 2);
+    const uint32_t o_t = tmem + kOCol + (uint32_t)(x * kD);
     // (a descriptor's address counts 16 bytes, and shared memory stays below its 2^14 of them)
     const uint64_t q_desc = sdesc_sw128(smem_u32(q_s)), k_desc = sdesc_sw128(smem_u32(kv_s));
     const uint64_t v_desc = sdesc_sw128_mn(smem_u32(kv_s), kHalf);
     auto wait = [&](uint64_t* bar, uint32_t par, int code) {
       return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
     };
-    // S of the unit that `wk` stands at
-    auto issue_s = [&]() -> bool {
+    // S of the unit that `wk` stands at; `now`: only if its operands have landed. 1: issued, 0: not yet, -1: gave up
+    auto issue_s = [&](bool now) -> int {
       const int seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots;
       const int qc = wk.q0 + (wk.w & wk.two), buf = qc & 1;
-      if (wk.w < 2 && !wait(&sh.q_full[buf], (uint32_t)((qc >> 1) & 1), 43)) return false;
-      if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 44)) return false;
+      const uint32_t q_par = (uint32_t)((qc >> 1) & 1), k_par = (uint32_t)((seq / kSlots) & 1);
+      if (now) {
+        if (!__all_sync(0xffffffffu, mbar_test(&sh.kv_full[st], k_par) && (wk.w >= 2 || mbar_test(&sh.q_full[buf], q_par))))
+          return 0;
+      } else {
+        if (wk.w < 2 && !wait(&sh.q_full[buf], q_par, 43)) return -1;
+        if (!wait(&sh.kv_full[st], k_par, 44)) return -1;
+      }
       tc_fence_after();
-      const uint64_t qd = q_desc + (uint64_t)(buf * (kTileBytes / 16)), kd = k_desc + (uint64_t)(st * (kTileBytes / 16));
+      const uint64_t qd = q_desc + (uint64_t)(buf * (kQBytes / 16)), kd = k_desc + (uint64_t)(st * (kTileBytes / 16));
       if (leader) {
 #pragma unroll
-        for (int i = 0; i < kD / 16; ++i) {
-          const uint64_t off = (uint64_t)(((i >> 2) * kHalf + (i & 3) * 32) / 16);
-          tc_mma_bf16(s_t, qd + off, kd + off, id_s, i > 0 ? 1u : 0u);
-        }
+        for (int i = 0; i < kD / 16; ++i)
+          tc_mma_bf16(s_t, qd + (uint64_t)(((i >> 2) * kQHalf + (i & 3) * 32) / 16),
+                      kd + (uint64_t)(((i >> 2) * kHalf + (i & 3) * 32) / 16), id_s, i > 0 ? 1u : 0u);
         tc_commit(&sh.s_full[x]);
         tc_commit(&sh.kv_empty[st]);
         if (!wk.two) mbar_arrive(&sh.kv_empty[st]);          // no unit of the other group reads this K tile
@@ -634,7 +645,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
       }
       __syncwarp();
-      return true;
+      return 1;
     };
     // units of a piece go to the groups in turn: from `wk` on to this group's next unit
     auto seek = [&]() {
@@ -642,35 +653,37 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     };
     wk.begin(p, sh);
     seek();
-    bool ok = !wk.p || issue_s();
+    int s_out = wk.p ? issue_s(false) : 0;
     uint32_t o_phase = 0;
-    while (ok && wk.p) {
-      const int w = wk.w, n = wk.n, seq = 2 * (wk.tile0 + wk.tile()) + 1, st = seq % kSlots, two = wk.two;
+    while (wk.p && s_out > 0) {
+      const int w = wk.w, seq = 2 * (wk.tile0 + wk.tile()) + 1, st = seq % kSlots, two = wk.two;
       const uint32_t par = (uint32_t)((wk.u >> 1) & 1);
-      if (w < 2) {     // the group's first unit of the piece: its O has been read out
-        if (!wait(&sh.o_empty[x], o_phase ^ 1u, 45)) break;
-        o_phase ^= 1u;
-      }
-      if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 46)) break;
       wk.next_unit(p, sh);
       seek();
-      if (!wait(&sh.p_full[x], par, 47)) break;
+      if (!wait(&sh.s_read[x], par, 45)) break;
+      s_out = wk.p ? issue_s(true) : 1;
+      if (w < 2) {     // the group's first unit of the piece: its O has been read out
+        if (!wait(&sh.o_empty[x], o_phase ^ 1u, 46)) break;
+        o_phase ^= 1u;
+      }
+      if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 47)) break;
+      if (!wait(&sh.p_full[x], par, 48)) break;
       tc_fence_after();
       const uint64_t vd = v_desc + (uint64_t)(st * (kTileBytes / 16));
       if (leader) {
 #pragma unroll
         for (int i = 0; i < kTK / 16; ++i)
-          tc_mma_bf16_ta(o_t, s_t + (uint32_t)(i * 8), vd + (uint64_t)(i * 2048 / 16), id_pv, (w >= 2 || i > 0) ? 1u : 0u);
+          tc_mma_bf16_ta(o_t, p_t + (uint32_t)(i * 8), vd + (uint64_t)(i * 2048 / 16), id_pv, (w >= 2 || i > 0) ? 1u : 0u);
+        tc_commit(&sh.pv_done[x]);
         tc_commit(&sh.kv_empty[st]);
         if (!two) mbar_arrive(&sh.kv_empty[st]);
-        if (w + 2 >= n) tc_commit(&sh.o_full[x]);
       }
       __syncwarp();
-      if (wk.p) ok = issue_s();
+      if (s_out == 0) s_out = issue_s(false);
     }
     if (leader) {
       tc_commit(&sh.mma_done);
-      mbar_wait_bounded(&sh.mma_done, 0, p.err, 48);
+      mbar_wait_bounded(&sh.mma_done, 0, p.err, 49);
     }
     __syncwarp();
   } else {
@@ -678,12 +691,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int x = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;   // a thread: one row, TMEM lane r
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_t = tmem + lane_off + kSCol + (uint32_t)(x * kTK), o_t = tmem + lane_off + kOCol + (uint32_t)(x * kD);
+    const uint32_t p_t = tmem + lane_off + kPCol + (uint32_t)(x * kTK / 2);
     auto wait = [&](uint64_t* bar, uint32_t par, int code) {
       return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
     };
-    uint32_t units = 0, outs = 0;
+    uint32_t units = 0;
     // The first pass is made on nothing, while the first copies are on their way: it brings
-    // the instructions (some 20 KB, 3 us of misses if the first unit had them).
+    // the instructions, whose misses would else come between the first unit's steps.
     bool ok = true, dry = true;
     for (wk.begin(p, sh); ok && wk.p; wk.u += wk.n, wk.next_piece(p, sh)) {
       const PfxPiece& d = *wk.p;
@@ -696,8 +710,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const int j = w >> wk.two, t = t0 + j;
         // the tile's keys: context rows [0, keys), and in its last tile the block's from row blk0 on
         const int keys = min(kTK, max(0, len - t * kTK));
-        const int blk0 = t == blk ? (keys + p.br - 1) >> p.page_shift << p.page_shift : kTK;
-        if (!dry && !wait(&sh.s_full[x], units & 1, 49)) {
+        const int blk0 = t == blk ? (keys + p.br - 1) >> p.br_shift << p.br_shift : kTK;
+        if (!dry && !wait(&sh.s_full[x], units & 1, 50)) {
           ok = false;
           break;
         }
@@ -706,6 +720,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
         for (int c = 0; c < kTK; c += 32) tmem_ld32(s_t + (uint32_t)c, sv + c);
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && !dry) mbar_arrive(&sh.s_read[x]);
         if (keys < kTK && !dry) {
           // causal: the row of query i sees the block's rows up to its own
           const int seen = p.causal ? min(p.n_kv, ((d.row0 + row) % p.R) / p.G + 1 + p.n_kv - p.n_q) : p.n_kv;
@@ -714,17 +731,15 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             if (c >= keys && (unsigned)(c - blk0) >= (unsigned)seen) sv[c] = 0xff800000u;   // -inf, whatever stood there
           // V rows of no key may hold anything, and 0 * NaN is NaN: zero them
           const int seq = 2 * (wk.tile0 + j) + 1, st = seq % kSlots;
-          if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 50)) {
+          if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 51)) {
             ok = false;
             break;
           }
-          if (r >= keys && (unsigned)(r - blk0) >= (unsigned)p.n_kv) {
-            uint8_t* v = kv_s + st * kTileBytes + r * 128;
+          const int vr = r & (kTK - 1);               // a row's half for each of two threads
+          if (vr >= keys && (unsigned)(vr - blk0) >= (unsigned)p.n_kv) {
+            uint8_t* v = kv_s + st * kTileBytes + (r >= kTK ? kHalf : 0) + vr * 128;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(v + kHalf + c * 16) = make_uint4(0, 0, 0, 0);
-            }
+            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -734,9 +749,14 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(sv[c])), __uint_as_float(sv[c + 1]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const bool raise = mt > m_run + kRescaleLog2 || (m_run == -CUDART_INF_F && mt != -CUDART_INF_F);
-        if (w > w0 + 1 && __any_sync(0xffffffffu, raise)) {
-          // (S of this unit was issued after P V of the group's last one, which is complete with it)
+        // P V of the group's last unit has read P, and O holds it
+        if (w > w0 && !wait(&sh.pv_done[x], (units - 1) & 1, 52)) {
+          ok = false;
+          break;
+        }
+        if (w > w0 && __any_sync(0xffffffffu, raise)) {
           const float alpha = !raise ? 1.f : m_run == -CUDART_INF_F ? 0.f : exp2f(m_run - mt);
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < kD; c += 16) {
             uint32_t o[16];
@@ -746,12 +766,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
             tmem_st16(o_t + (uint32_t)c, o);
           }
-          tmem_st_wait();
           l_run *= alpha;
         }
         if (raise) m_run = mt;
         const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
-        const uint32_t p_t = dry ? o_t : s_t;     // (nothing has been written to O yet)
         float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
         const float2 sc2 = {p.scale_log2, p.scale_log2}, nb2 = {-base, -base};
 #pragma unroll
@@ -765,7 +783,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             rs[i & 1] = pfx_add2(rs[i & 1], e);
             pk[i] = pfx_pack(e.x, e.y);
           }
-          tmem_st16(p_t + (uint32_t)(c / 2), pk);
+          tmem_st16(p_t + (uint32_t)(c / 2), pk);     // (the dry pass too: no P V reads it)
         }
         l_run += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
         tmem_st_wait();
@@ -790,8 +808,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       const bool mine = row < d.nrows;
       if (mine) *ml = make_float2(m_run, l_run);
       if (w0 < wk.n) {
-        if (!wait(&sh.o_full[x], outs & 1, 51)) break;
-        ++outs;
+        if (!wait(&sh.pv_done[x], (units - 1) & 1, 55)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < kD; c += 32) {
@@ -817,14 +834,16 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   // ------------------------------ end ------------------------------
   tc_fence_before();
   __syncthreads();
-  if ((warp == 8 || warp == 11) && lane == 0 && *abort_flag)   // copies in flight land before the CTA leaves
-    for (int i = issued - 1; i >= max(0, issued - kSlots); i -= 2)
-      mbar_wait_bounded(&sh.kv_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 52);
-  if (warp == 11 && lane == 0 && *abort_flag)
-    for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i)
-      mbar_wait_bounded(&sh.q_full[i & 1], (uint32_t)((i >> 1) & 1), p.err, 54);
+  if (lane == 0 && *abort_flag) {     // copies in flight land before the CTA leaves
+    if (warp == 8 || warp == 9)
+      for (int i = issued - 1; i >= max(0, issued - kSlots); i -= 2)
+        mbar_wait_bounded(&sh.kv_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 56);
+    if (warp == 10)
+      for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i)
+        mbar_wait_bounded(&sh.q_full[i & 1], (uint32_t)((i >> 1) & 1), p.err, 57);
+  }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 11) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -1005,7 +1024,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   p.page_shift = 0;
   while (1 << p.page_shift < a.page_size) ++p.page_shift;
   p.max_pages = a.max_pages; p.num_pages = a.num_pages; p.max_ctx = a.max_ctx; p.causal = a.causal;
-  p.br = a.page_size;
+  p.br_shift = std::min(p.page_shift, 6);
+  p.br = 1 << p.br_shift;
   p.scale_log2 = a.scale * kLog2e;
   p.wait_ns = wait_limit_ns();
   // pools and block rows as [row][head][d]: a box of 64 d x 1 head x rows lands as [row][64 d]

@@ -272,7 +272,7 @@ int dflash_block_attn_active(const dflash_attn_dims* dims,
  *   ctx_len of the group counts (negative: 0).
  * Every other argument as dflash_block_attn, whose checks and error words apply.
  * n_groups in [0, B]. The shared kernel takes bf16, D = 128, pages of 8, 16, 32, 64
- * or 128 positions, B <= 1024, n_kv_blk <= 128 and pointers aligned to 16 bytes;
+ * or 128 positions, B <= 1024, n_kv_blk <= 64 and pointers aligned to 16 bytes;
  * for other calls the prefix is read once a sequence, as by dflash_block_attn.
  * Repeated calls on the same inputs return identical bits.
  */
