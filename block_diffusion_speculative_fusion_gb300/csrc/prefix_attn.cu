@@ -357,6 +357,11 @@ __device__ __forceinline__ float pfx_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A value that all lanes have, said so: addresses and descriptors of what one lane issues
+// then stay in uniform registers. (Moved there for each MMA, they made it 93 cycles; it
+// takes 48 for 64 columns with A in shared memory, 64 for 128.)
+__device__ __forceinline__ uint32_t pfx_uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 pfx_fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -459,7 +464,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem_base;
+  const uint32_t tmem = pfx_uniform(sh.tmem_base);
   PfxWalk wk;
   int q_boxes = 0;                 // one past the last Q tile that came as boxes
   int issued = 0;                  // one past the last tile (K and V counted apart) that this warp has asked for
@@ -468,7 +473,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // ------------------------------ K loads, V loads ------------------------------
     // A warp each: a box takes some hundred cycles to issue, and a tile of 16-position
     // pages is 8 of them for K and as many for V.
-    const int v = warp == 9;
+    const int v = (int)pfx_uniform((uint32_t)warp) - 8;
     const CUtensorMap *map = v ? &vmap : &kmap, *bmap = v ? &vbmap : &kbmap;
     const bool leader = elect_one();
     const uint64_t pol_once = l2_policy_evict_first();
@@ -508,25 +513,27 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           ok = false;
           break;
         }
-        uint64_t* full = &sh.kv_full[st];
-        uint8_t* dst = kv_s + st * kTileBytes;
+        const int su = (int)pfx_uniform((uint32_t)st), head = (int)pfx_uniform((uint32_t)d.head);
+        const bool once = pfx_uniform(d.member0 < 0) != 0;
+        uint64_t* full = &sh.kv_full[su];
+        uint8_t* dst = kv_s + su * kTileBytes;
         if (leader) mbar_arrive_expect_tx(full, bytes);
         issued = seq + 1;
         for (int box = 0; box < nb; ++box, dst += p.br * 128) {
           const int row = __shfl_sync(0xffffffffu, ids, jj * bpt + box);
           if (leader) {
-            if (d.member0 < 0) {
-              tma_load_3d_hint(dst, map, full, 0, d.head, row, pol_once);
-              tma_load_3d_hint(dst + kHalf, map, full, 64, d.head, row, pol_once);
+            if (once) {
+              tma_load_3d_hint(dst, map, full, 0, head, row, pol_once);
+              tma_load_3d_hint(dst + kHalf, map, full, 64, head, row, pol_once);
             } else {
-              tma_load_3d(dst, map, full, 0, d.head, row);
-              tma_load_3d(dst + kHalf, map, full, 64, d.head, row);
+              tma_load_3d(dst, map, full, 0, head, row);
+              tma_load_3d(dst + kHalf, map, full, 64, head, row);
             }
           }
         }
         if (t == d.blk && leader) {
-          tma_load_3d(dst, bmap, full, 0, d.head, d.first * p.n_kv);
-          tma_load_3d(dst + kHalf, bmap, full, 64, d.head, d.first * p.n_kv);
+          tma_load_3d(dst, bmap, full, 0, head, d.first * p.n_kv);
+          tma_load_3d(dst + kHalf, bmap, full, 64, head, d.first * p.n_kv);
         }
         __syncwarp();
       }
@@ -602,36 +609,47 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   } else if (warp >= 11) {
     // ------------------------------ MMA ------------------------------
     // A warp for each softmax group x, since what lies between two batches of MMAs, the
-    // waits and commits, keeps one warp from filling the pipe. S of the group's next unit
-    // goes out as soon as the group holds this unit's S in registers, so that it is there
-    // when the group is done. The warp stays converged and one elected lane issues (a
-    // lane on its own took 600 to 850 cycles for eight MMAs, more than they do).
-    const int x = warp - 11;
-    const bool leader = elect_one();
+    // waits and commits, keeps one from filling the pipe; one thread of it, which polls
+    // what a batch needs together (a vote of the warp on each barrier cost more than the
+    // MMAs). S of the group's next unit goes out as soon as the group holds this unit's S
+    // in registers, so that it is there when the group is done.
+    const int x = (int)pfx_uniform((uint32_t)warp) - 11;
     const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
     const uint32_t s_t = tmem + kSCol + (uint32_t)(x * kTK), p_t = tmem + kPCol + (uint32_t)(x * kTK / 2);
     const uint32_t o_t = tmem + kOCol + (uint32_t)(x * kD);
     // (a descriptor's address counts 16 bytes, and shared memory stays below its 2^14 of them)
     const uint64_t q_desc = sdesc_sw128(smem_u32(q_s)), k_desc = sdesc_sw128(smem_u32(kv_s));
     const uint64_t v_desc = sdesc_sw128_mn(smem_u32(kv_s), kHalf);
-    auto wait = [&](uint64_t* bar, uint32_t par, int code) {
-      return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
-    };
-    // S of the unit that `wk` stands at; `now`: only if its operands have landed. 1: issued, 0: not yet, -1: gave up
-    auto issue_s = [&](bool now) -> int {
-      const int seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots;
-      const int qc = wk.q0 + (wk.w & wk.two), buf = qc & 1;
-      const uint32_t q_par = (uint32_t)((qc >> 1) & 1), k_par = (uint32_t)((seq / kSlots) & 1);
-      if (now) {
-        if (!__all_sync(0xffffffffu, mbar_test(&sh.kv_full[st], k_par) && (wk.w >= 2 || mbar_test(&sh.q_full[buf], q_par))))
-          return 0;
-      } else {
-        if (wk.w < 2 && !wait(&sh.q_full[buf], q_par, 43)) return -1;
-        if (!wait(&sh.kv_full[st], k_par, 44)) return -1;
-      }
-      tc_fence_after();
-      const uint64_t qd = q_desc + (uint64_t)(buf * (kQBytes / 16)), kd = k_desc + (uint64_t)(st * (kTileBytes / 16));
-      if (leader) {
+    if (elect_one()) {
+      // all three phases complete (null: none), or the wait has run out (`once`: one look)
+      auto poll = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc, bool once, int code) {
+        auto look = [&]() {
+          const bool ra = mbar_test(a, pa), rb = mbar_test(b, pb), rc = c == nullptr || mbar_test(c, pc);
+          return ra && rb && rc;
+        };
+        if (look()) return true;
+        if (once) return false;
+        const long long t0 = clock64();
+        while (true) {
+          for (int i = 0; i < 32; ++i)
+            if (look()) return true;
+          if (*abort_flag) return false;
+          if ((unsigned long long)(clock64() - t0) / 2 > p.wait_ns) {    // (two cycles to a nanosecond)
+            *abort_flag = 1;
+            record_dev_error(p.err, code);
+            return false;
+          }
+        }
+      };
+      // S of the unit that `wk` stands at, once `rd` has completed phase `rp`. `once`: only if
+      // that and the operands are there. 1: issued, 0: not yet, -1: gave up
+      auto issue_s = [&](uint64_t* rd, uint32_t rp, bool once) -> int {
+        const int seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots, qc = wk.q0 + (wk.w & wk.two), buf = qc & 1;
+        if (!poll(rd, rp, &sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), wk.w < 2 ? &sh.q_full[buf] : nullptr,
+                  (uint32_t)((qc >> 1) & 1), once, 44))
+          return once ? 0 : -1;
+        tc_fence_after();
+        const uint64_t qd = q_desc + (uint64_t)(buf * (kQBytes / 16)), kd = k_desc + (uint64_t)(st * (kTileBytes / 16));
 #pragma unroll
         for (int i = 0; i < kD / 16; ++i)
           tc_mma_bf16(s_t, qd + (uint64_t)(((i >> 2) * kQHalf + (i & 3) * 32) / 16),
@@ -643,45 +661,56 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           tc_commit(&sh.q_empty[buf]);
           if (wk.two || wk.n == 1) mbar_arrive(&sh.q_empty[buf]);
         }
-      }
-      __syncwarp();
-      return 1;
-    };
-    // units of a piece go to the groups in turn: from `wk` on to this group's next unit
-    auto seek = [&]() {
-      while (wk.p && ((wk.u ^ x) & 1)) wk.next_unit(p, sh);
-    };
-    wk.begin(p, sh);
-    seek();
-    int s_out = wk.p ? issue_s(false) : 0;
-    uint32_t o_phase = 0;
-    while (wk.p && s_out > 0) {
-      const int w = wk.w, seq = 2 * (wk.tile0 + wk.tile()) + 1, st = seq % kSlots, two = wk.two;
-      const uint32_t par = (uint32_t)((wk.u >> 1) & 1);
-      wk.next_unit(p, sh);
-      seek();
-      if (!wait(&sh.s_read[x], par, 45)) break;
-      s_out = wk.p ? issue_s(true) : 1;
-      if (w < 2) {     // the group's first unit of the piece: its O has been read out
-        if (!wait(&sh.o_empty[x], o_phase ^ 1u, 46)) break;
-        o_phase ^= 1u;
-      }
-      if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 47)) break;
-      if (!wait(&sh.p_full[x], par, 48)) break;
-      tc_fence_after();
-      const uint64_t vd = v_desc + (uint64_t)(st * (kTileBytes / 16));
-      if (leader) {
+        return 1;
+      };
+      // units of a piece go to the groups in turn: to this group's next unit (from one that
+      // need not be its own)
+      auto own_unit = [&]() {
+        while (wk.p) {
+          const int w = wk.w + ((wk.u ^ x) & 1);
+          if (w < wk.n) {
+            wk.u += w - wk.w;
+            wk.w = w;
+            return;
+          }
+          wk.u += wk.n - wk.w;
+          wk.next_piece(p, sh);
+        }
+      };
+      wk.begin(p, sh);
+      own_unit();
+      int s_out = 0;
+      if (wk.p) s_out = issue_s(&sh.p_full[x], 1, false);    // (a fresh barrier's phase 1 counts as complete)
+      uint32_t o_phase = 0;
+      while (wk.p && s_out > 0) {
+        const int w = wk.w, seq = 2 * (wk.tile0 + wk.tile()) + 1, st = seq % kSlots, two = wk.two;
+        const uint32_t par = (uint32_t)((wk.u >> 1) & 1), v_par = (uint32_t)((seq / kSlots) & 1);
+        const uint64_t vd = v_desc + (uint64_t)(st * (kTileBytes / 16));
+        ++wk.u;
+        if (++wk.w == wk.n) wk.next_piece(p, sh);
+        own_unit();
+        // S of the next unit first, if the group has read this one's by the time its P is made
+        s_out = 1;
+        bool p_ready = false;
+        if (wk.p) {
+          s_out = 0;
+          for (int i = 0; i < 1 << 20 && s_out == 0 && !p_ready; ++i) {
+            s_out = issue_s(&sh.s_read[x], par, true);
+            p_ready = s_out == 0 && mbar_test(&sh.p_full[x], par);
+          }
+        }
+        // (the group's first unit of a piece: its O has been read out)
+        if (!poll(&sh.p_full[x], par, &sh.kv_full[st], v_par, w < 2 ? &sh.o_empty[x] : nullptr, o_phase ^ 1u, false, 46)) break;
+        if (w < 2) o_phase ^= 1u;
+        tc_fence_after();
 #pragma unroll
         for (int i = 0; i < kTK / 16; ++i)
-          tc_mma_bf16_ta(o_t, p_t + (uint32_t)(i * 8), vd + (uint64_t)(i * 2048 / 16), id_pv, (w >= 2 || i > 0) ? 1u : 0u);
+          tc_mma_bf16_ta(o_t, p_t + (uint32_t)(i * 8), vd + (uint64_t)(i * 2048 / 16), id_pv, i > 0 || w >= 2 ? 1u : 0u);
         tc_commit(&sh.pv_done[x]);
         tc_commit(&sh.kv_empty[st]);
         if (!two) mbar_arrive(&sh.kv_empty[st]);
+        if (s_out == 0) s_out = issue_s(&sh.s_read[x], par, false);
       }
-      __syncwarp();
-      if (s_out == 0) s_out = issue_s(false);
-    }
-    if (leader) {
       tc_commit(&sh.mma_done);
       mbar_wait_bounded(&sh.mma_done, 0, p.err, 49);
     }
