@@ -26,12 +26,12 @@ constexpr int kTK = 64;                     // keys of a tile
 constexpr int kM = 128;                     // packed query rows of a Q tile (TMEM lanes)
 constexpr int kGrid = 152;                  // persistent CTAs: one per SM
 constexpr int kMaxSeqs = 1024;
-constexpr int kSlots = 10;                  // ring of K and V tiles
+constexpr int kSlots = 5;                   // ring of tiles, K and V
 constexpr int kTileBytes = kTK * kD * 2;    // a K or V tile: two d-halves of 64 rows x 128 bytes
 constexpr int kHalf = kTileBytes / 2;
 constexpr int kQBytes = kM * kD * 2;        // a Q tile: two d-halves of 128 rows
 constexpr int kQHalf = kQBytes / 2;
-constexpr int kThreads = 416;               // warps 0-3, 4-7 softmax; 8 K, 9 V, 10 Q loads; 11, 12 MMA
+constexpr int kThreads = 480;               // warps 0-3, 4-7 softmax; 8 K, 9 V, 10 Q loads; 11, 12 S, 13, 14 P V
 constexpr int kWarps = kThreads / 32;
 constexpr int kKept = 48;                   // piece descriptors kept in shared memory
 // Costs of the work list, in halves of a microsecond: a K/V tile for two Q tiles, for one,
@@ -165,7 +165,7 @@ __device__ __forceinline__ int pfx_find(const int* a, int n, int x) {
 
 // Shared memory: Q tiles, ring, then the small things.
 struct PfxShared {
-  uint64_t kv_full[pfx::kSlots], kv_empty[pfx::kSlots];
+  uint64_t k_full[pfx::kSlots], v_full[pfx::kSlots], k_empty[pfx::kSlots], v_empty[pfx::kSlots];
   uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], q_full[2], q_empty[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -173,7 +173,7 @@ struct PfxShared {
   int scan[3 * pfx::kWarps];
   PfxPiece kept[pfx::kKept];
 };
-constexpr size_t kPfxSmem = 2 * (size_t)pfx::kQBytes + pfx::kSlots * (size_t)pfx::kTileBytes + sizeof(PfxShared);
+constexpr size_t kPfxSmem = 2 * (size_t)pfx::kQBytes + pfx::kSlots * 2 * (size_t)pfx::kTileBytes + sizeof(PfxShared);
 static_assert(kPfxSmem <= 232448, "shared memory");
 
 // The plan, in scratch that the ring takes over afterwards.
@@ -183,7 +183,7 @@ struct PfxPlan {
   int cnt[pfx::kMaxSeqs], minc[pfx::kMaxSeqs], first[pfx::kMaxSeqs], tiles[pfx::kMaxSeqs], fill[pfx::kMaxSeqs];
   int gstart[pfx::kMaxSeqs + 1], gbase[pfx::kMaxSeqs + 1], gitem[pfx::kMaxSeqs + 1];
 };
-static_assert(sizeof(PfxPlan) <= 2 * (size_t)pfx::kQBytes + pfx::kSlots * (size_t)pfx::kTileBytes, "plan scratch");
+static_assert(sizeof(PfxPlan) <= 2 * (size_t)pfx::kQBytes + pfx::kSlots * 2 * (size_t)pfx::kTileBytes, "plan scratch");
 
 // Tiles of a sequence's own part: its context keys behind the prefix, then the block's
 // rows, behind the last box of the last context tile where they fit there.
@@ -362,6 +362,24 @@ __device__ __forceinline__ float pfx_ex2(float x) {
 // takes 48 for 64 columns with A in shared memory, 64 for 128.)
 __device__ __forceinline__ uint32_t pfx_uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
+// Bounded wait of a whole warp that suspends at once: a dozen warps that spin make every
+// barrier operation of the CTA slow (50 -> 160 cycles).
+__device__ __forceinline__ bool pfx_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code,
+                                         unsigned long long limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+    for (int i = 0; i < 4; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+    if (__any_sync(0xffffffffu, (unsigned long long)(clock64() - t0) / 2 > limit_ns)) {   // (two cycles to a nanosecond)
+      *abort_flag = 1;
+      if ((threadIdx.x & 31) == 0) record_dev_error(err, code);
+      return false;
+    }
+  }
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 pfx_fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -435,14 +453,16 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   using namespace pfx;
   extern __shared__ __align__(1024) uint8_t pfx_smem[];
   uint8_t* q_s = pfx_smem;                           // two Q tiles
-  uint8_t* kv_s = pfx_smem + 2 * kQBytes;            // ring: K of tile 0, V of tile 0, K of tile 1, ..
-  PfxShared& sh = *reinterpret_cast<PfxShared*>(kv_s + kSlots * kTileBytes);
+  uint8_t *k_s = pfx_smem + 2 * kQBytes, *v_s = k_s + kSlots * kTileBytes;   // rings of K and V tiles
+  PfxShared& sh = *reinterpret_cast<PfxShared*>(v_s + kSlots * kTileBytes);
   volatile int* abort_flag = &sh.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_empty[i], 2);       // both MMA warps, or one for both
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.k_empty[i], 2);        // both MMA warps, or one for both
+      mbar_init(&sh.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -453,7 +473,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 2);
     }
-    mbar_init(&sh.mma_done, 2);
+    mbar_init(&sh.mma_done, 4);
     sh.abort_flag = 0;
     fence_barrier_init();
   }
@@ -467,7 +487,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   const uint32_t tmem = pfx_uniform(sh.tmem_base);
   PfxWalk wk;
   int q_boxes = 0;                 // one past the last Q tile that came as boxes
-  int issued = 0;                  // one past the last tile (K and V counted apart) that this warp has asked for
+  int issued = 0;                  // tiles that this warp has asked for
 
   if (warp == 8 || warp == 9) {
     // ------------------------------ K loads, V loads ------------------------------
@@ -508,17 +528,18 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         // boxes with a context key in use, then the block's rows
         const int nb = min(bpt, max(0, (d.len - t * kTK + p.br - 1) >> p.br_shift));
         const uint32_t bytes = (uint32_t)((nb * p.br + (t == d.blk ? p.n_kv : 0)) * 256);
-        const int seq = 2 * (wk.tile0 + j) + v, st = seq % kSlots;
-        if (!warp_wait(&sh.kv_empty[st], (uint32_t)(((seq / kSlots) & 1) ^ 1), abort_flag, p.err, 41 + 12 * v, p.wait_ns)) {
+        const int st = issued % kSlots;
+        const uint32_t par = (uint32_t)((issued / kSlots) & 1);
+        if (!pfx_wait(v ? &sh.v_empty[st] : &sh.k_empty[st], par ^ 1u, abort_flag, p.err, 41 + 12 * v, p.wait_ns)) {
           ok = false;
           break;
         }
         const int su = (int)pfx_uniform((uint32_t)st), head = (int)pfx_uniform((uint32_t)d.head);
         const bool once = pfx_uniform(d.member0 < 0) != 0;
-        uint64_t* full = &sh.kv_full[su];
-        uint8_t* dst = kv_s + su * kTileBytes;
+        uint64_t* full = v ? &sh.v_full[su] : &sh.k_full[su];
+        uint8_t* dst = (v ? v_s : k_s) + su * kTileBytes;
         if (leader) mbar_arrive_expect_tx(full, bytes);
-        issued = seq + 1;
+        ++issued;
         for (int box = 0; box < nb; ++box, dst += p.br * 128) {
           const int row = __shfl_sync(0xffffffffu, ids, jj * bpt + box);
           if (leader) {
@@ -559,7 +580,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (boxes) {
           const int n = (min(d.nrows - i * kM, kM) + p.R - 1) / p.R, m0 = (d.row0 + i * kM) / p.R;
           const int seq = d.member0 < 0 ? d.first : lane < n ? p.order[d.member0 + m0 + lane] : 0;
-          ok = warp_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
+          ok = pfx_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
           if (!ok) break;
           if (leader) mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(n * p.R * 256));
           q_boxes = qc + 1;
@@ -584,7 +605,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
           }
         }
-        ok = warp_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
+        ok = pfx_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
         if (!ok) break;
         const int c = lane & 15;
         const uint32_t dst0 = smem_u32(tile + (c >> 3) * kQHalf);
@@ -608,108 +629,76 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     __syncwarp();
   } else if (warp >= 11) {
     // ------------------------------ MMA ------------------------------
-    // A warp for each softmax group x, since what lies between two batches of MMAs, the
-    // waits and commits, keeps one from filling the pipe; one thread of it, which polls
-    // what a batch needs together (a vote of the warp on each barrier cost more than the
-    // MMAs). S of the group's next unit goes out as soon as the group holds this unit's S
-    // in registers, so that it is there when the group is done.
-    const int x = (int)pfx_uniform((uint32_t)warp) - 11;
+    // S and P V of each softmax group x by a thread of its own: one that issues is held for
+    // about as long as its MMAs run, and what lies between two batches (waits of 50 cycles
+    // and more, commits) is as long again, so that it takes four to fill the pipe. S of the
+    // group's next unit goes out as soon as the group holds this unit's S in registers.
+    const int role = (int)pfx_uniform((uint32_t)warp) - 11, x = role & 1;
     const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
     const uint32_t s_t = tmem + kSCol + (uint32_t)(x * kTK), p_t = tmem + kPCol + (uint32_t)(x * kTK / 2);
     const uint32_t o_t = tmem + kOCol + (uint32_t)(x * kD);
     // (a descriptor's address counts 16 bytes, and shared memory stays below its 2^14 of them)
-    const uint64_t q_desc = sdesc_sw128(smem_u32(q_s)), k_desc = sdesc_sw128(smem_u32(kv_s));
-    const uint64_t v_desc = sdesc_sw128_mn(smem_u32(kv_s), kHalf);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(q_s)), k_desc = sdesc_sw128(smem_u32(k_s));
+    const uint64_t v_desc = sdesc_sw128_mn(smem_u32(v_s), kHalf);
     if (elect_one()) {
-      // all three phases complete (null: none), or the wait has run out (`once`: one look)
-      auto poll = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc, bool once, int code) {
-        auto look = [&]() {
-          const bool ra = mbar_test(a, pa), rb = mbar_test(b, pb), rc = c == nullptr || mbar_test(c, pc);
-          return ra && rb && rc;
-        };
-        if (look()) return true;
-        if (once) return false;
-        const long long t0 = clock64();
-        while (true) {
-          for (int i = 0; i < 32; ++i)
-            if (look()) return true;
-          if (*abort_flag) return false;
-          if ((unsigned long long)(clock64() - t0) / 2 > p.wait_ns) {    // (two cycles to a nanosecond)
-            *abort_flag = 1;
-            record_dev_error(p.err, code);
-            return false;
-          }
-        }
+      auto wait = [&](uint64_t* bar, uint32_t par, int code) {
+        return mbar_try_wait(bar, par) || wait_or_abort(bar, par, abort_flag, p.err, code, p.wait_ns);
       };
-      // S of the unit that `wk` stands at, once `rd` has completed phase `rp`. `once`: only if
-      // that and the operands are there. 1: issued, 0: not yet, -1: gave up
-      auto issue_s = [&](uint64_t* rd, uint32_t rp, bool once) -> int {
-        const int seq = 2 * (wk.tile0 + wk.tile()), st = seq % kSlots, qc = wk.q0 + (wk.w & wk.two), buf = qc & 1;
-        if (!poll(rd, rp, &sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), wk.w < 2 ? &sh.q_full[buf] : nullptr,
-                  (uint32_t)((qc >> 1) & 1), once, 44))
-          return once ? 0 : -1;
-        tc_fence_after();
-        const uint64_t qd = q_desc + (uint64_t)(buf * (kQBytes / 16)), kd = k_desc + (uint64_t)(st * (kTileBytes / 16));
+      bool ok = true;
+      uint32_t units = 0, pieces = 0;      // of the group so far
+      int u0 = 0, tile0 = 0, q0 = 0;       // units, tiles and Q tiles of the pieces before
+      for (int k = 0; ok && k < sh.n_pieces; ++k) {
+        const PfxPiece* d = k < kKept ? &sh.kept[k] : p.pieces + sh.piece0 + k;
+        const int nt = d->nt;
+        if (nt == 0) continue;
+        const bool one = d->nrows <= kM;
+        const int n = one ? nt : 2 * nt, w0 = (u0 ^ x) & 1, mine = (n - w0 + 1) >> 1;
+        const int t = tile0 + (one ? w0 : 0), q = q0 + (one ? 0 : w0), step = one ? 2 : 1;
+        int slot = t % kSlots;
+        uint32_t ph = (uint32_t)(t / kSlots & 1);
+        if (role < 2) {
+          const uint64_t qd = q_desc + (uint64_t)((q & 1) * (kQBytes / 16));
+          for (int i = 0; i < mine; ++i, ++units) {
+            if (units > 0 && !wait(&sh.s_read[x], (units - 1) & 1, 43)) { ok = false; break; }
+            if (i == 0 && !wait(&sh.q_full[q & 1], (uint32_t)(q >> 1 & 1), 44)) { ok = false; break; }
+            if (!wait(&sh.k_full[slot], ph, 45)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t kd = k_desc + (uint64_t)(slot * (kTileBytes / 16));
 #pragma unroll
-        for (int i = 0; i < kD / 16; ++i)
-          tc_mma_bf16(s_t, qd + (uint64_t)(((i >> 2) * kQHalf + (i & 3) * 32) / 16),
-                      kd + (uint64_t)(((i >> 2) * kHalf + (i & 3) * 32) / 16), id_s, i > 0 ? 1u : 0u);
-        tc_commit(&sh.s_full[x]);
-        tc_commit(&sh.kv_empty[st]);
-        if (!wk.two) mbar_arrive(&sh.kv_empty[st]);          // no unit of the other group reads this K tile
-        if (wk.w + 2 >= wk.n) {                              // the group's last S of the piece: its Q is free
-          tc_commit(&sh.q_empty[buf]);
-          if (wk.two || wk.n == 1) mbar_arrive(&sh.q_empty[buf]);
-        }
-        return 1;
-      };
-      // units of a piece go to the groups in turn: to this group's next unit (from one that
-      // need not be its own)
-      auto own_unit = [&]() {
-        while (wk.p) {
-          const int w = wk.w + ((wk.u ^ x) & 1);
-          if (w < wk.n) {
-            wk.u += w - wk.w;
-            wk.w = w;
-            return;
+            for (int j = 0; j < kD / 16; ++j)
+              tc_mma_bf16(s_t, qd + (uint64_t)(((j >> 2) * kQHalf + (j & 3) * 32) / 16),
+                          kd + (uint64_t)(((j >> 2) * kHalf + (j & 3) * 32) / 16), id_s, j > 0 ? 1u : 0u);
+            tc_commit(&sh.s_full[x]);
+            tc_commit(&sh.k_empty[slot]);
+            if (one) mbar_arrive(&sh.k_empty[slot]);         // no unit of the other group reads this K tile
+            slot += step;
+            if (slot >= kSlots) slot -= kSlots, ph ^= 1u;
           }
-          wk.u += wk.n - wk.w;
-          wk.next_piece(p, sh);
-        }
-      };
-      wk.begin(p, sh);
-      own_unit();
-      int s_out = 0;
-      if (wk.p) s_out = issue_s(&sh.p_full[x], 1, false);    // (a fresh barrier's phase 1 counts as complete)
-      uint32_t o_phase = 0;
-      while (wk.p && s_out > 0) {
-        const int w = wk.w, seq = 2 * (wk.tile0 + wk.tile()) + 1, st = seq % kSlots, two = wk.two;
-        const uint32_t par = (uint32_t)((wk.u >> 1) & 1), v_par = (uint32_t)((seq / kSlots) & 1);
-        const uint64_t vd = v_desc + (uint64_t)(st * (kTileBytes / 16));
-        ++wk.u;
-        if (++wk.w == wk.n) wk.next_piece(p, sh);
-        own_unit();
-        // S of the next unit first, if the group has read this one's by the time its P is made
-        s_out = 1;
-        bool p_ready = false;
-        if (wk.p) {
-          s_out = 0;
-          for (int i = 0; i < 1 << 20 && s_out == 0 && !p_ready; ++i) {
-            s_out = issue_s(&sh.s_read[x], par, true);
-            p_ready = s_out == 0 && mbar_test(&sh.p_full[x], par);
+          if (ok && mine) {                                  // nor this Q tile, which is free now
+            tc_commit(&sh.q_empty[q & 1]);
+            if (!one || n == 1) mbar_arrive(&sh.q_empty[q & 1]);
           }
-        }
-        // (the group's first unit of a piece: its O has been read out)
-        if (!poll(&sh.p_full[x], par, &sh.kv_full[st], v_par, w < 2 ? &sh.o_empty[x] : nullptr, o_phase ^ 1u, false, 46)) break;
-        if (w < 2) o_phase ^= 1u;
-        tc_fence_after();
+        } else {
+          for (int i = 0; i < mine; ++i, ++units) {
+            // (the group's first unit of a piece: its O has been read out)
+            if (i == 0 && !wait(&sh.o_empty[x], (pieces++ & 1) ^ 1, 46)) { ok = false; break; }
+            if (!wait(&sh.v_full[slot], ph, 47) || !wait(&sh.p_full[x], units & 1, 48)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t vd = v_desc + (uint64_t)(slot * (kTileBytes / 16));
+            tc_mma_bf16_ta(o_t, p_t, vd, id_pv, i > 0 ? 1u : 0u);
 #pragma unroll
-        for (int i = 0; i < kTK / 16; ++i)
-          tc_mma_bf16_ta(o_t, p_t + (uint32_t)(i * 8), vd + (uint64_t)(i * 2048 / 16), id_pv, i > 0 || w >= 2 ? 1u : 0u);
-        tc_commit(&sh.pv_done[x]);
-        tc_commit(&sh.kv_empty[st]);
-        if (!two) mbar_arrive(&sh.kv_empty[st]);
-        if (s_out == 0) s_out = issue_s(&sh.s_read[x], par, false);
+            for (int j = 1; j < kTK / 16; ++j)
+              tc_mma_bf16_ta(o_t, p_t + (uint32_t)(j * 8), vd + (uint64_t)(j * 2048 / 16), id_pv, 1u);
+            tc_commit(&sh.pv_done[x]);
+            tc_commit(&sh.v_empty[slot]);
+            if (one) mbar_arrive(&sh.v_empty[slot]);
+            slot += step;
+            if (slot >= kSlots) slot -= kSlots, ph ^= 1u;
+          }
+        }
+        u0 += n;
+        tile0 += nt;
+        q0 += one ? 1 : 2;
       }
       tc_commit(&sh.mma_done);
       mbar_wait_bounded(&sh.mma_done, 0, p.err, 49);
@@ -722,7 +711,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const uint32_t s_t = tmem + lane_off + kSCol + (uint32_t)(x * kTK), o_t = tmem + lane_off + kOCol + (uint32_t)(x * kD);
     const uint32_t p_t = tmem + lane_off + kPCol + (uint32_t)(x * kTK / 2);
     auto wait = [&](uint64_t* bar, uint32_t par, int code) {
-      return warp_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
+      return pfx_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
     };
     uint32_t units = 0;
     // The first pass is made on nothing, while the first copies are on their way: it brings
@@ -759,14 +748,14 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           for (int c = 0; c < kTK; ++c)
             if (c >= keys && (unsigned)(c - blk0) >= (unsigned)seen) sv[c] = 0xff800000u;   // -inf, whatever stood there
           // V rows of no key may hold anything, and 0 * NaN is NaN: zero them
-          const int seq = 2 * (wk.tile0 + j) + 1, st = seq % kSlots;
-          if (!wait(&sh.kv_full[st], (uint32_t)((seq / kSlots) & 1), 51)) {
+          const int seq = wk.tile0 + j, st = seq % kSlots;
+          if (!wait(&sh.v_full[st], (uint32_t)((seq / kSlots) & 1), 51)) {
             ok = false;
             break;
           }
           const int vr = r & (kTK - 1);               // a row's half for each of two threads
           if (vr >= keys && (unsigned)(vr - blk0) >= (unsigned)p.n_kv) {
-            uint8_t* v = kv_s + st * kTileBytes + (r >= kTK ? kHalf : 0) + vr * 128;
+            uint8_t* v = v_s + st * kTileBytes + (r >= kTK ? kHalf : 0) + vr * 128;
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -865,8 +854,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   __syncthreads();
   if (lane == 0 && *abort_flag) {     // copies in flight land before the CTA leaves
     if (warp == 8 || warp == 9)
-      for (int i = issued - 1; i >= max(0, issued - kSlots); i -= 2)
-        mbar_wait_bounded(&sh.kv_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 56);
+      for (int i = issued - 1; i >= max(0, issued - kSlots); --i)
+        mbar_wait_bounded(warp == 9 ? &sh.v_full[i % kSlots] : &sh.k_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 56);
     if (warp == 10)
       for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i)
         mbar_wait_bounded(&sh.q_full[i & 1], (uint32_t)((i >> 1) & 1), p.err, 57);
