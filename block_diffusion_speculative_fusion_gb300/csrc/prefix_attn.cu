@@ -31,9 +31,11 @@ constexpr int kTileBytes = kTK * kD * 2;    // a K or V tile: two d-halves of 64
 constexpr int kHalf = kTileBytes / 2;
 constexpr int kQBytes = kM * kD * 2;        // a Q tile: two d-halves of 128 rows
 constexpr int kQHalf = kQBytes / 2;
-constexpr int kThreads = 480;               // warps 0-3, 4-7 softmax; 8 K, 9 V, 10 Q loads; 11, 12 S, 13, 14 P V
+// Warps: two softmax groups of four; loads of K, V and Q; the cleaner; two for S, two for P V.
+constexpr int kWarpK = 8, kWarpV = 9, kWarpQ = 10, kWarpClean = 11, kWarpMma = 12;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKept = 48;                   // piece descriptors kept in shared memory
+constexpr int kKept = 44;                   // piece descriptors kept in shared memory
 // Costs of the work list, in halves of a microsecond: a K/V tile for two Q tiles, for one,
 // and an own part's start and end.
 constexpr int kCostTwo = 4, kCostOne = 3, kItemCost = 9;
@@ -166,6 +168,7 @@ __device__ __forceinline__ int pfx_find(const int* a, int n, int x) {
 // Shared memory: Q tiles, ring, then the small things.
 struct PfxShared {
   uint64_t k_full[pfx::kSlots], v_full[pfx::kSlots], k_empty[pfx::kSlots], v_empty[pfx::kSlots];
+  uint64_t v_land[pfx::kSlots];    // V tiles with rows to clean have landed
   uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], q_full[2], q_empty[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
@@ -463,6 +466,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.k_empty[i], 2);        // both MMA warps, or one for both
       mbar_init(&sh.v_empty[i], 2);
+      mbar_init(&sh.v_land[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -477,7 +481,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     sh.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 11) tmem_alloc(&sh.tmem_base, kTmemCols);
+  if (warp == kWarpMma) tmem_alloc(&sh.tmem_base, kTmemCols);
   dependents_may_launch();
   pfx_plan(p, *reinterpret_cast<PfxPlan*>(pfx_smem), sh);
   fence_proxy_async_smem();        // the scratch becomes the ring: its writes come before the copies
@@ -488,12 +492,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   PfxWalk wk;
   int q_boxes = 0;                 // one past the last Q tile that came as boxes
   int issued = 0;                  // tiles that this warp has asked for
+  uint32_t landed = 0, land_ph = 0;   // V: a bit for each slot whose last tile goes by v_land, and how many have (odd)
 
-  if (warp == 8 || warp == 9) {
+  if (warp == kWarpK || warp == kWarpV) {
     // ------------------------------ K loads, V loads ------------------------------
     // A warp each: a box takes some hundred cycles to issue, and a tile of 16-position
     // pages is 8 of them for K and as many for V.
-    const int v = (int)pfx_uniform((uint32_t)warp) - 8;
+    const int v = (int)pfx_uniform((uint32_t)warp) - kWarpK;
     const CUtensorMap *map = v ? &vmap : &kmap, *bmap = v ? &vbmap : &kbmap;
     const bool leader = elect_one();
     const uint64_t pol_once = l2_policy_evict_first();
@@ -536,7 +541,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         const int su = (int)pfx_uniform((uint32_t)st), head = (int)pfx_uniform((uint32_t)d.head);
         const bool once = pfx_uniform(d.member0 < 0) != 0;
-        uint64_t* full = v ? &sh.v_full[su] : &sh.k_full[su];
+        const bool junk = v && d.len - t * kTK < kTK;      // V rows of no key: the cleaner sees them first
+        uint64_t* full = junk ? &sh.v_land[su] : v ? &sh.v_full[su] : &sh.k_full[su];
+        landed = junk ? landed | 1u << su : landed & ~(1u << su);
+        land_ph ^= (junk ? 1u : 0u) << su;
         uint8_t* dst = (v ? v_s : k_s) + su * kTileBytes;
         if (leader) mbar_arrive_expect_tx(full, bytes);
         ++issued;
@@ -562,7 +570,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       ids = ids_nx;
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kWarpQ) {
     // ------------------------------ Q loads ------------------------------
     // Packed row r of a part: sequence r / R of its sequences, query row (r % R) / G,
     // head r % G of the kv head's. A sequence's R rows are one box a d-half where they
@@ -627,13 +635,42 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       }
     }
     __syncwarp();
-  } else if (warp >= 11) {
+  } else if (warp == kWarpClean) {
+    // ------------------------------ cleaner ------------------------------
+    // V rows of no key may hold anything, and 0 * NaN is NaN: zero them, then hand the tile on.
+    uint32_t ph = 0;
+    bool ok = true;
+    for (wk.begin(p, sh); ok && wk.p; wk.next_piece(p, sh)) {
+      const PfxPiece d = *wk.p;
+      for (int j = max(0, d.len / kTK - d.t0); j < d.nt; ++j) {   // from the first tile that context keys do not fill
+        const int t = d.t0 + j, keys = max(0, d.len - t * kTK), slot = (wk.tile0 + j) % kSlots;
+        const int blk0 = t == d.blk ? (keys + p.br - 1) >> p.br_shift << p.br_shift : kTK;
+        if (!pfx_wait(&sh.v_land[slot], ph >> slot & 1u, abort_flag, p.err, 54, p.wait_ns)) {
+          ok = false;
+          break;
+        }
+        ph ^= 1u << slot;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * (i & 1);
+          if (r < keys || (unsigned)(r - blk0) < (unsigned)p.n_kv) continue;
+          uint4* v = reinterpret_cast<uint4*>(v_s + slot * kTileBytes + (i >> 1) * kHalf + r * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full[slot]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kWarpMma) {
     // ------------------------------ MMA ------------------------------
     // S and P V of each softmax group x by a thread of its own: one that issues is held for
     // about as long as its MMAs run, and what lies between two batches (waits of 50 cycles
     // and more, commits) is as long again, so that it takes four to fill the pipe. S of the
     // group's next unit goes out as soon as the group holds this unit's S in registers.
-    const int role = (int)pfx_uniform((uint32_t)warp) - 11, x = role & 1;
+    const int role = (int)pfx_uniform((uint32_t)warp) - kWarpMma, x = role & 1;
     const uint32_t id_s = idesc_bf16_ab(kM, kTK, 0), id_pv = idesc_bf16_ab(kM, kD, 1);
     const uint32_t s_t = tmem + kSCol + (uint32_t)(x * kTK), p_t = tmem + kPCol + (uint32_t)(x * kTK / 2);
     const uint32_t o_t = tmem + kOCol + (uint32_t)(x * kD);
@@ -721,17 +758,25 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       const PfxPiece& d = *wk.p;
       const int t0 = d.t0, len = d.len, blk = d.blk;
       const int w0 = (wk.u + x) & 1;                  // this group's first unit of the piece
-      const int row = (wk.two ? w0 * kM : 0) + r;     // in the item's block of 256
+      const int row0 = (wk.two ? w0 * kM : 0) + quarter * 32, row = row0 + lane;   // in the item's block of 256
       const int half = wk.two ? w0 : x;
+      const bool live = row0 < d.nrows;               // the warp has rows
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int w = w0; w < wk.n;) {
-        const int j = w >> wk.two, t = t0 + j;
-        // the tile's keys: context rows [0, keys), and in its last tile the block's from row blk0 on
-        const int keys = min(kTK, max(0, len - t * kTK));
-        const int blk0 = t == blk ? (keys + p.br - 1) >> p.br_shift << p.br_shift : kTK;
         if (!dry && !wait(&sh.s_full[x], units & 1, 50)) {
           ok = false;
           break;
+        }
+        if (!live && !dry) {                          // no row: the barriers alone, one phase of p_full at a time
+          if (lane == 0) mbar_arrive(&sh.s_read[x]);
+          if (w > w0 && !wait(&sh.pv_done[x], (units - 1) & 1, 53)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive(&sh.p_full[x]);
+          w += 2;
+          ++units;
+          continue;
         }
         tc_fence_after();
         uint32_t sv[kTK];
@@ -741,25 +786,15 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && !dry) mbar_arrive(&sh.s_read[x]);
-        if (keys < kTK && !dry) {
-          // causal: the row of query i sees the block's rows up to its own
+        const int t = t0 + (w >> wk.two), left = len - t * kTK;
+        if (left < kTK) {
+          // the tile's keys: context rows [0, keys), and in the part's last tile the block's from
+          // row blk0 on; causal: the row of query i sees them up to its own
+          const int keys = max(0, left), blk0 = t == blk ? (keys + p.br - 1) >> p.br_shift << p.br_shift : kTK;
           const int seen = p.causal ? min(p.n_kv, ((d.row0 + row) % p.R) / p.G + 1 + p.n_kv - p.n_q) : p.n_kv;
 #pragma unroll
           for (int c = 0; c < kTK; ++c)
             if (c >= keys && (unsigned)(c - blk0) >= (unsigned)seen) sv[c] = 0xff800000u;   // -inf, whatever stood there
-          // V rows of no key may hold anything, and 0 * NaN is NaN: zero them
-          const int seq = wk.tile0 + j, st = seq % kSlots;
-          if (!wait(&sh.v_full[st], (uint32_t)((seq / kSlots) & 1), 51)) {
-            ok = false;
-            break;
-          }
-          const int vr = r & (kTK - 1);               // a row's half for each of two threads
-          if (vr >= keys && (unsigned)(vr - blk0) >= (unsigned)p.n_kv) {
-            uint8_t* v = v_s + st * kTileBytes + (r >= kTK ? kHalf : 0) + vr * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + c * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
         }
         float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
@@ -767,12 +802,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           mx[c / 2 & 3] = fmaxf(fmaxf(mx[c / 2 & 3], __uint_as_float(sv[c])), __uint_as_float(sv[c + 1]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const bool raise = mt > m_run + kRescaleLog2 || (m_run == -CUDART_INF_F && mt != -CUDART_INF_F);
-        // P V of the group's last unit has read P, and O holds it
-        if (w > w0 && !wait(&sh.pv_done[x], (units - 1) & 1, 52)) {
-          ok = false;
-          break;
-        }
         if (w > w0 && __any_sync(0xffffffffu, raise)) {
+          // (P V of the group's last unit is in O)
+          if (!wait(&sh.pv_done[x], (units - 1) & 1, 52)) {
+            ok = false;
+            break;
+          }
           const float alpha = !raise ? 1.f : m_run == -CUDART_INF_F ? 0.f : exp2f(m_run - mt);
           tc_fence_after();
 #pragma unroll 1
@@ -790,20 +825,22 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
         float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
         const float2 sc2 = {p.scale_log2, p.scale_log2}, nb2 = {-base, -base};
+        // P over S, whose registers it takes
 #pragma unroll
-        for (int c = 0; c < kTK; c += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 e = pfx_fma2(make_float2(__uint_as_float(sv[c + 2 * i]), __uint_as_float(sv[c + 2 * i + 1])), sc2, nb2);
-            e.x = pfx_ex2(e.x);
-            e.y = pfx_ex2(e.y);
-            rs[i & 1] = pfx_add2(rs[i & 1], e);
-            pk[i] = pfx_pack(e.x, e.y);
-          }
-          tmem_st16(p_t + (uint32_t)(c / 2), pk);     // (the dry pass too: no P V reads it)
+        for (int i = 0; i < kTK / 2; ++i) {
+          float2 e = pfx_fma2(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), sc2, nb2);
+          e.x = pfx_ex2(e.x);
+          e.y = pfx_ex2(e.y);
+          rs[i & 1] = pfx_add2(rs[i & 1], e);
+          sv[i] = pfx_pack(e.x, e.y);
         }
         l_run += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
+        // P V of the group's last unit has read P
+        if (w > w0 && !wait(&sh.pv_done[x], (units - 1) & 1, 53)) {
+          ok = false;
+          break;
+        }
+        tmem_st32(p_t, sv);                           // (the dry pass too: no P V reads it)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -827,22 +864,24 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       if (mine) *ml = make_float2(m_run, l_run);
       if (w0 < wk.n) {
         if (!wait(&sh.pv_done[x], (units - 1) & 1, 55)) break;
-        tc_fence_after();
+        if (live) {
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_t + (uint32_t)c, o);
-          tmem_ld_wait();
-          if (mine) {
+          for (int c = 0; c < kD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_t + (uint32_t)c, o);
+            tmem_ld_wait();
+            if (mine) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)     // whole sectors
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + c + i), "r"(o[i]),
-                           "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
-                           "r"(o[i + 7])
-                           : "memory");
+              for (int i = 0; i < 32; i += 8)     // whole sectors
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + c + i), "r"(o[i]),
+                             "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
+                             "r"(o[i + 7])
+                             : "memory");
+            }
           }
+          tc_fence_before();
         }
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.o_empty[x]);
       }
@@ -853,15 +892,20 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   tc_fence_before();
   __syncthreads();
   if (lane == 0 && *abort_flag) {     // copies in flight land before the CTA leaves
-    if (warp == 8 || warp == 9)
-      for (int i = issued - 1; i >= max(0, issued - kSlots); --i)
-        mbar_wait_bounded(warp == 9 ? &sh.v_full[i % kSlots] : &sh.k_full[i % kSlots], (uint32_t)((i / kSlots) & 1), p.err, 56);
-    if (warp == 10)
+    if (warp == kWarpK || warp == kWarpV)
+      for (int i = issued - 1; i >= max(0, issued - kSlots); --i) {
+        const int st = i % kSlots;
+        if (landed >> st & 1u)
+          mbar_wait_bounded(&sh.v_land[st], (land_ph >> st & 1u) ^ 1u, p.err, 56);
+        else
+          mbar_wait_bounded(warp == kWarpV ? &sh.v_full[st] : &sh.k_full[st], (uint32_t)((i / kSlots) & 1), p.err, 56);
+      }
+    if (warp == kWarpQ)
       for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i)
         mbar_wait_bounded(&sh.q_full[i & 1], (uint32_t)((i >> 1) & 1), p.err, 57);
   }
   __syncthreads();
-  if (warp == 11) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
