@@ -36,10 +36,11 @@ constexpr int kWarpK = 8, kWarpV = 9, kWarpQ = 10, kWarpClean = 11, kWarpMma = 1
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKept = 44;                   // piece descriptors kept in shared memory
-// Costs of the work list, in halves of a microsecond: a K/V tile for two Q tiles, for one,
-// and an own part's start and end.
-constexpr int kCostTwo = 4, kCostOne = 3, kItemCost = 9;
-constexpr int kMinShare = 4;                // least work of a CTA (no less than a tile)
+// Costs of the work list, in quarters of a microsecond: a K/V tile for two Q tiles and for
+// one, of a prefix and of an own part (whose K/V come from HBM), and an own part's start and end.
+constexpr int cost(bool own, bool two) { return 3 + own + two; }
+constexpr int kItemCost = 9;
+constexpr int kMinShare = 5;                // least work of a CTA (no less than a tile)
 constexpr float kRescaleLog2 = 8.f;         // O is rescaled when the row maximum grows by more than 2^8
 // TMEM columns: S of the two softmax groups, their P (bf16 pairs), their O
 constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 256;
@@ -94,15 +95,17 @@ struct PfxParams {
 // ---------------------------------------------------------------------------
 // The work list. Items, in order: for each group with a prefix worth sharing, block of
 // 256 packed rows, kv head: the prefix's tiles; then for each sequence, block, head: its
-// own tiles. A tile costs kCostOne, or kCostTwo with more than 128 rows (two Q tiles), an
-// own part kItemCost more. The costs in a row are cut into equal ranges, one a CTA; a tile
+// own tiles. The costs of its tiles (cost) and, of an own part, kItemCost before them: the costs in a row are cut into equal ranges, one a CTA; a tile
 // belongs to the range in which its cost begins. So the partition, and with it the
 // rounding, depends on the dims, lengths and groups alone.
 // ---------------------------------------------------------------------------
 __host__ __device__ __forceinline__ int pfx_blocks(int rows) { return (rows + 2 * pfx::kM - 1) / (2 * pfx::kM); }
-// weight of block k of `rows` packed rows
+// Whether block k of `rows` packed rows has two Q tiles, and what one of its tiles costs.
+__device__ __forceinline__ bool pfx_two(int rows, int k) { return rows - k * 2 * pfx::kM > pfx::kM; }
+template <bool OWN>
 __device__ __forceinline__ int pfx_weight(int rows, int k) {
-  return rows - k * 2 * pfx::kM > pfx::kM ? pfx::kCostTwo : pfx::kCostOne;
+  constexpr int one = pfx::cost(OWN, false), two = pfx::cost(OWN, true);
+  return pfx_two(rows, k) ? two : one;
 }
 
 // First tile of an item (from position `base`, `ov` before its tiles, `nt` tiles of
@@ -111,14 +114,16 @@ __device__ __forceinline__ int pfx_first_tile(int base, int ov, int w, int nt, i
   const int x = at - base - ov;
   return x <= 0 ? 0 : min(nt, (x + w - 1) / w);
 }
-// Cost before item (block k, head) among the items of a part of `rows` rows whose tiles
-// cost nt * weight + ov each; all of them together for k = number of blocks.
-__device__ __forceinline__ int pfx_cost_before(int rows, int nt, int ov, int Hkv, int k, int head) {
+// Cost before item (block k, head) among the items of a part of `rows` rows and nt tiles;
+// all of them together for k = number of blocks.
+template <bool OWN>
+__device__ __forceinline__ int pfx_cost_before(int rows, int nt, int Hkv, int k, int head) {
+  constexpr int ov = OWN ? pfx::kItemCost : 0, two = pfx::cost(OWN, true);
   const int n = pfx_blocks(rows);
   const int full = min(k, n - 1);                  // blocks before the last one have 256 rows
-  int c = full * Hkv * (pfx::kCostTwo * nt + ov);
-  if (k == n) c += Hkv * (pfx_weight(rows, n - 1) * nt + ov);
-  else c += head * (pfx_weight(rows, k) * nt + ov);
+  int c = full * Hkv * (two * nt + ov);
+  if (k == n) c += Hkv * (pfx_weight<OWN>(rows, n - 1) * nt + ov);
+  else c += head * (pfx_weight<OWN>(rows, k) * nt + ov);
   return c;
 }
 
@@ -234,7 +239,7 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     if (t) {
       at_g[0] += s.cnt[g];
       at_g[1] += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
-      at_g[2] += pfx_cost_before(s.cnt[g] * p.R, t, 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
+      at_g[2] += pfx_cost_before<false>(s.cnt[g] * p.R, t, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
   pfx_scan(at_g, sh.scan, all_g);
@@ -245,7 +250,7 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     if (s.tiles[g]) {
       at_g[0] += s.cnt[g];
       at_g[1] += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
-      at_g[2] += pfx_cost_before(s.cnt[g] * p.R, s.tiles[g], 0, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
+      at_g[2] += pfx_cost_before<false>(s.cnt[g] * p.R, s.tiles[g], p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
   const int all_i = all_g[1], all_c = all_g[2];
@@ -254,7 +259,7 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
   int at_s[1] = {0}, all_s[1];
   auto own_cost = [&](int b) {
     const int nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
-    return nt ? pfx_cost_before(p.R, nt, kItemCost, p.Hkv, p.sblk, 0) : 0;
+    return nt ? pfx_cost_before<true>(p.R, nt, p.Hkv, p.sblk, 0) : 0;
   };
   for (int b = b0; b < b1; ++b) at_s[0] += own_cost(b);
   pfx_scan(at_s, sh.scan, all_s);
@@ -287,14 +292,14 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
   auto item_at = [&](int x) {
     if (x < all_c) {
       const int g = pfx_find(s.gbase, p.n_groups, x), rows = s.cnt[g] * p.R;
-      const int rel = x - s.gbase[g], full = p.Hkv * kCostTwo * s.tiles[g];
+      const int rel = x - s.gbase[g], full = p.Hkv * cost(false, true) * s.tiles[g];
       const int k = min(rel / full, pfx_blocks(rows) - 1), in = rel - k * full;
-      return s.gitem[g] + k * p.Hkv + in / (pfx_weight(rows, k) * s.tiles[g]);
+      return s.gitem[g] + k * p.Hkv + in / (pfx_weight<false>(rows, k) * s.tiles[g]);
     }
     const int b = pfx_find(s.sbase, p.B, x), nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
-    const int rel = x - s.sbase[b], full = p.Hkv * (kCostTwo * nt + kItemCost);
+    const int rel = x - s.sbase[b], full = p.Hkv * (cost(true, true) * nt + kItemCost);
     const int k = min(rel / full, p.sblk - 1), in = rel - k * full;
-    return all_i + (b * p.sblk + k) * p.Hkv + in / (pfx_weight(p.R, k) * nt + kItemCost);
+    return all_i + (b * p.sblk + k) * p.Hkv + in / (pfx_weight<true>(p.R, k) * nt + kItemCost);
   };
   const int i0 = lo < hi ? item_at(lo) : 0, i1 = lo < hi ? item_at(hi - 1) : -1;
   for (int k = tid; k <= i1 - i0; k += kThreads) {
@@ -306,9 +311,9 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       const int rel = it - s.gitem[g], blk = rel / p.Hkv;
       d.head = rel - blk * p.Hkv;
       nt = s.tiles[g];
-      w = pfx_weight(rows, blk);
+      w = pfx_weight<false>(rows, blk);
       ov = 0;
-      base = s.gbase[g] + pfx_cost_before(rows, nt, 0, p.Hkv, blk, d.head);
+      base = s.gbase[g] + pfx_cost_before<false>(rows, nt, p.Hkv, blk, d.head);
       d.first = s.first[g];
       d.member0 = s.gstart[g];
       d.key0 = 0;
@@ -322,9 +327,9 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       d.head = rel - blk * p.Hkv;
       const int t = s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0;
       nt = pfx_own_tiles(p, s.ctx[b], t);
-      w = pfx_weight(p.R, blk);
+      w = pfx_weight<true>(p.R, blk);
       ov = kItemCost;
-      base = s.sbase[b] + pfx_cost_before(p.R, nt, ov, p.Hkv, blk, d.head);
+      base = s.sbase[b] + pfx_cost_before<true>(p.R, nt, p.Hkv, blk, d.head);
       d.first = b;
       d.member0 = -1;
       d.key0 = t * kTK;
@@ -941,24 +946,25 @@ prefix_join_kernel(const __grid_constant__ PfxParams p) {
   const float* po[2];
   size_t step[2];                                    // rows of a slot
   {
-    const int blk = r / (2 * kM), in = r - blk * 2 * kM, w = pfx_weight(p.R, blk);
+    const int blk = r / (2 * kM), in = r - blk * 2 * kM, w = pfx_weight<true>(p.R, blk);
+    const bool two = pfx_two(p.R, blk);
     int v1;
-    ranges(s.base + pfx_cost_before(p.R, s.nt, kItemCost, p.Hkv, blk, head), kItemCost, w, s.nt, v0[0], v1);
+    ranges(s.base + pfx_cost_before<true>(p.R, s.nt, p.Hkv, blk, head), kItemCost, w, s.nt, v0[0], v1);
     n[0] = v1 - v0[0] + 1;
-    halves[0] = w == kCostTwo ? 1 : 2;
+    halves[0] = two ? 1 : 2;
     step[0] = (size_t)2 * p.Rs2;
-    const size_t at = ((size_t)((b * p.sblk + blk) * p.Hkv + head) + v0[0]) * step[0] + (w == kCostTwo ? in / kM * p.Rs2 + in % kM : in);
+    const size_t at = ((size_t)((b * p.sblk + blk) * p.Hkv + head) + v0[0]) * step[0] + (two ? in / kM * p.Rs2 + in % kM : in);
     ml[0] = p.ml_s + at;
     po[0] = p.po_s + at * kD + c0;
   }
   n[1] = 0;
   if (s.group >= 0) {
     const PfxGroup g = p.groups[s.group];
-    const int pr = s.pos * p.R + r, blk = pr / (2 * kM), in = pr - blk * 2 * kM, w = pfx_weight(g.rows, blk);
+    const int pr = s.pos * p.R + r, blk = pr / (2 * kM), in = pr - blk * 2 * kM, w = pfx_weight<false>(g.rows, blk);
     int v1;
-    ranges(g.base + pfx_cost_before(g.rows, g.tiles, 0, p.Hkv, blk, head), 0, w, g.tiles, v0[1], v1);
+    ranges(g.base + pfx_cost_before<false>(g.rows, g.tiles, p.Hkv, blk, head), 0, w, g.tiles, v0[1], v1);
     n[1] = v1 - v0[1] + 1;
-    halves[1] = w == kCostTwo ? 1 : 2;
+    halves[1] = pfx_two(g.rows, blk) ? 1 : 2;
     step[1] = 2 * kM;
     const size_t at = ((size_t)(g.item + blk * p.Hkv + head) + v0[1]) * step[1] + in;   // (two Q tiles: in / 128 is the half)
     ml[1] = p.ml_p + at;
@@ -1010,7 +1016,7 @@ static bool pfx_dims_ok(int B, int n_q, int n_kv, int Hq, int Hkv, int D, int ma
   if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return false;
   // costs are 32-bit
   const double tiles = (double)max_ctx / kTK + 2 + kItemCost;
-  return 4.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
+  return 5.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
 }
 
 struct PfxLayout {
