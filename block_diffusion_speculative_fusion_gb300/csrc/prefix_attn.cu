@@ -35,38 +35,40 @@ constexpr int kQHalf = kQBytes / 2;
 constexpr int kWarpK = 8, kWarpV = 9, kWarpQ = 10, kWarpClean = 11, kWarpMma = 12;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKept = 44;                   // piece descriptors kept in shared memory
-// Costs of the work list, in quarters of a microsecond: a K/V tile for two Q tiles and for
-// one, of a prefix and of an own part (whose K/V come from HBM), and an own part's start and end.
-constexpr int cost(bool own, bool two) { return 3 + own + two; }
+constexpr int kKept = 42;                   // piece descriptors kept in shared memory
+// What an item is: one Q tile and kv head, two Q tiles (more than 128 rows) that share the
+// K/V tiles, or the Q tiles of two kv heads with K/V tiles of their own.
+enum Kind { kOne = 0, kTwo = 1, kPair = 2 };
+// Costs of the work list, in quarters of a microsecond: 64 keys of an item, of a prefix or of
+// an own part (whose K/V come from HBM), and an own part's start and end.
+constexpr int cost(bool own, int kind) { return kind == kOne ? 3 + own : kind == kTwo ? 4 + own : own ? 9 : 6; }
 constexpr int kItemCost = 9;
-constexpr int kMinShare = 5;                // least work of a CTA (no less than a tile)
+constexpr int kMinShare = 9;                // least work of a CTA (no less than a tile)
 constexpr float kRescaleLog2 = 8.f;         // O is rescaled when the row maximum grows by more than 2^8
 // TMEM columns: S of the two softmax groups, their P (bf16 pairs), their O
 constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 256;
 constexpr int kTmemCols = 512;
 }  // namespace pfx
 
-// A run of tiles of one item: one kv head, up to 256 packed rows, the keys of one part.
+// A run of tiles (64 keys) of one item: one kv head, or two, up to 256 packed rows, the
+// keys of one part.
 struct PfxPiece {
   int first;     // sequence whose table row is read
   int member0;   // prefix: where the group's sequences begin in the order; own part: -1
   int key0, len;     // position of the part's first context key, and their number
   int blk;           // the tile that the block's own rows stand in (its last one); -1: none
   int t0, nt;        // this piece's tiles
-  int head;
+  int kind, head;    // Kind; kv head, the first of two
   int row0, nrows;   // packed rows of the part's sequences
   int slot;          // partials
-  int pad;
 };
 
-// What the merge kernel needs to find a row's partials.
+// What the second kernel needs to find the partials of a sequence's rows.
 struct PfxSeq {
-  int group, pos;     // shared prefix (-1: none) and the sequence's place among its sequences
-  int base, nt;       // own part: cost before its first item, tiles
-};
-struct PfxGroup {
-  int base, item, tiles, rows;   // cost before and number of its first item, tiles, packed rows
+  int share;                          // cost of a range
+  int base, nt;                       // own part: cost before its first item, tiles
+  int pos;                            // its place among the sequences of its prefix
+  int g_base, g_item, g_tiles, g_rows;   // the prefix: cost before and number of its first item, tiles (0: none), rows
 };
 
 struct PfxParams {
@@ -81,11 +83,9 @@ struct PfxParams {
   PfxPiece* pieces;
   uint16_t* order;               // the groups' sequences, group after group
   PfxSeq* seqs;
-  PfxGroup* groups;
-  int32_t* header;               // [share]
   int* err;
   int B, n_groups, n_q, n_kv, Hq, Hkv, G, R;   // R = n_q * G packed rows of a sequence and kv head
-  int sblk, Rs2;                 // blocks of 256 rows of a sequence; rows of a half's partials
+  int sblk, sitems, Rs2;         // blocks of 256 rows and items of a sequence; rows of a half's partials
   int page_shift, max_pages, num_pages, max_ctx, causal;
   int br, br_shift;              // rows of a box: a page's, at most a tile's
   float scale_log2;
@@ -94,18 +94,25 @@ struct PfxParams {
 
 // ---------------------------------------------------------------------------
 // The work list. Items, in order: for each group with a prefix worth sharing, block of
-// 256 packed rows, kv head: the prefix's tiles; then for each sequence, block, head: its
-// own tiles. The costs of its tiles (cost) and, of an own part, kItemCost before them: the costs in a row are cut into equal ranges, one a CTA; a tile
-// belongs to the range in which its cost begins. So the partition, and with it the
-// rounding, depends on the dims, lengths and groups alone.
+// 256 packed rows, kv head (or two): the prefix's tiles; then for each sequence, block,
+// head: its own tiles. Each tile has a cost, and an own part kItemCost before its tiles.
+// The costs in a row are cut into equal ranges, one a CTA; a tile belongs to the range in
+// which its cost begins. So the partition, and with it the rounding, depends on the dims,
+// lengths and groups alone.
 // ---------------------------------------------------------------------------
 __host__ __device__ __forceinline__ int pfx_blocks(int rows) { return (rows + 2 * pfx::kM - 1) / (2 * pfx::kM); }
-// Whether block k of `rows` packed rows has two Q tiles, and what one of its tiles costs.
-__device__ __forceinline__ bool pfx_two(int rows, int k) { return rows - k * 2 * pfx::kM > pfx::kM; }
+// Kind of the items of block k of `rows` packed rows. All blocks but the last have 256.
+__host__ __device__ __forceinline__ int pfx_kind(int rows, int k, int Hkv) {
+  return rows - k * 2 * pfx::kM > pfx::kM ? pfx::kTwo : Hkv % 2 == 0 ? pfx::kPair : pfx::kOne;
+}
+__host__ __device__ __forceinline__ int pfx_items(int rows, int Hkv) {
+  const int n = pfx_blocks(rows);
+  return (n - 1) * Hkv + (pfx_kind(rows, n - 1, Hkv) == pfx::kPair ? Hkv / 2 : Hkv);
+}
 template <bool OWN>
-__device__ __forceinline__ int pfx_weight(int rows, int k) {
-  constexpr int one = pfx::cost(OWN, false), two = pfx::cost(OWN, true);
-  return pfx_two(rows, k) ? two : one;
+__device__ __forceinline__ int pfx_weight(int kind) {
+  constexpr int one = pfx::cost(OWN, pfx::kOne), two = pfx::cost(OWN, pfx::kTwo), pair = pfx::cost(OWN, pfx::kPair);
+  return kind == pfx::kTwo ? two : kind == pfx::kPair ? pair : one;
 }
 
 // First tile of an item (from position `base`, `ov` before its tiles, `nt` tiles of
@@ -114,50 +121,48 @@ __device__ __forceinline__ int pfx_first_tile(int base, int ov, int w, int nt, i
   const int x = at - base - ov;
   return x <= 0 ? 0 : min(nt, (x + w - 1) / w);
 }
-// Cost before item (block k, head) among the items of a part of `rows` rows and nt tiles;
-// all of them together for k = number of blocks.
+// Cost before item i of block k among the items of a part of `rows` rows and nt tiles; all
+// of them together for k = number of blocks.
 template <bool OWN>
-__device__ __forceinline__ int pfx_cost_before(int rows, int nt, int Hkv, int k, int head) {
-  constexpr int ov = OWN ? pfx::kItemCost : 0, two = pfx::cost(OWN, true);
-  const int n = pfx_blocks(rows);
-  const int full = min(k, n - 1);                  // blocks before the last one have 256 rows
-  int c = full * Hkv * (two * nt + ov);
-  if (k == n) c += Hkv * (pfx_weight<OWN>(rows, n - 1) * nt + ov);
-  else c += head * (pfx_weight<OWN>(rows, k) * nt + ov);
-  return c;
+__device__ __forceinline__ int pfx_cost_before(int rows, int nt, int Hkv, int k, int i) {
+  constexpr int ov = OWN ? pfx::kItemCost : 0, two = pfx::cost(OWN, pfx::kTwo);
+  const int n = pfx_blocks(rows), full = min(k, n - 1);
+  if (k == n) i = pfx_items(rows, Hkv) - (n - 1) * Hkv;
+  return full * Hkv * (two * nt + ov) + i * (pfx_weight<OWN>(pfx_kind(rows, min(k, n - 1), Hkv)) * nt + ov);
 }
 
-// Exclusive prefixes of K values per thread over the CTA, and their totals.
+// Exclusive prefixes of K values per thread over the CTA's first nw warps (the others have
+// none), and their totals.
 template <int K>
-__device__ __forceinline__ void pfx_scan(int (&x)[K], int* s_w, int (&total)[K]) {
+__device__ __forceinline__ void pfx_scan(int (&x)[K], int nw, int* s_w, int (&total)[K]) {
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   int in[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) in[k] = x[k];
+  if (w < nw) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1)
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int y = __shfl_up_sync(0xffffffffu, in[k], o);
+        if (l >= o) in[k] += y;
+      }
+    if (l == 31)
+#pragma unroll
+      for (int k = 0; k < K; ++k) s_w[k * pfx::kWarps + w] = in[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) total[k] = 0;
+  for (int i = 0; i < nw; ++i)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int y = __shfl_up_sync(0xffffffffu, in[k], o);
-      if (l >= o) in[k] += y;
-    }
-  __syncthreads();
-  if (l == 31)
-#pragma unroll
-    for (int k = 0; k < K; ++k) s_w[k * pfx::kWarps + w] = in[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    int base = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < pfx::kWarps; ++i) {
       const int v = s_w[k * pfx::kWarps + i];
-      base += i < w ? v : 0;
-      all += v;
+      in[k] += i < w ? v : 0;
+      total[k] += v;
     }
-    total[k] = all;
-    x[k] = base + in[k] - x[k];
-  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = in[k] - x[k];
 }
 
 // Last i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
@@ -178,7 +183,7 @@ struct PfxShared {
   uint32_t tmem_base;
   int abort_flag;
   int n_pieces, piece0;            // this CTA's pieces, in the list from piece0 on
-  int scan[3 * pfx::kWarps];
+  int scan[4 * pfx::kWarps];       // of the plan: three sums over the groups, one over the sequences
   PfxPiece kept[pfx::kKept];
 };
 constexpr size_t kPfxSmem = 2 * (size_t)pfx::kQBytes + pfx::kSlots * 2 * (size_t)pfx::kTileBytes + sizeof(PfxShared);
@@ -238,18 +243,19 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     s.tiles[g] = t;
     if (t) {
       at_g[0] += s.cnt[g];
-      at_g[1] += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
+      at_g[1] += pfx_items(s.cnt[g] * p.R, p.Hkv);
       at_g[2] += pfx_cost_before<false>(s.cnt[g] * p.R, t, p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
-  pfx_scan(at_g, sh.scan, all_g);
+  const int nw_g = (p.n_groups + per_g * 32 - 1) / max(1, per_g * 32), nw_b = (p.B + per_b * 32 - 1) / (per_b * 32);
+  pfx_scan(at_g, nw_g, sh.scan, all_g);
   for (int g = g0; g < g1; ++g) {
     s.gstart[g] = at_g[0];
     s.gitem[g] = at_g[1];
     s.gbase[g] = at_g[2];
     if (s.tiles[g]) {
       at_g[0] += s.cnt[g];
-      at_g[1] += p.Hkv * pfx_blocks(s.cnt[g] * p.R);
+      at_g[1] += pfx_items(s.cnt[g] * p.R, p.Hkv);
       at_g[2] += pfx_cost_before<false>(s.cnt[g] * p.R, s.tiles[g], p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
@@ -262,14 +268,17 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     return nt ? pfx_cost_before<true>(p.R, nt, p.Hkv, p.sblk, 0) : 0;
   };
   for (int b = b0; b < b1; ++b) at_s[0] += own_cost(b);
-  pfx_scan(at_s, sh.scan, all_s);
+  pfx_scan(at_s, nw_b, sh.scan + 3 * kWarps, all_s);
   for (int b = b0; b < b1; ++b) {
     s.sbase[b] = all_c + at_s[0];
     at_s[0] += own_cost(b);
   }
-  // a group's sequences in ascending order
-  if (tid < 32) {
-    for (int k = 0; k < p.B; k += 32) {
+  __syncthreads();
+  const int N = all_c + all_s[0];
+  const int share = max(kMinShare, (N + kGrid - 1) / kGrid);
+  if (tid >= kThreads - 32) {
+    // (the last warp, while the others find their pieces) a group's sequences in ascending order
+    for (int k = 0; k < p.B && all_i > 0; k += 32) {
       const int b = k + lane;
       const int g = b < p.B ? s.grp[b] : -1;
       const bool in = g >= 0 && s.tiles[g] > 0;
@@ -283,37 +292,45 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       if (in && (same >> lane) == 1u) s.fill[g] += __popc(same);   // the last lane of each
       __syncwarp();
     }
+    if (blockIdx.x == 0) {
+      for (int b = lane; b < p.B; b += 32) {
+        const int g = s.grp[b], t = g >= 0 ? s.tiles[g] : 0;
+        p.seqs[b] = PfxSeq{share, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t), t ? s.pos[b] : 0, t ? s.gbase[g] : 0,
+                           t ? s.gitem[g] : 0, t, t ? s.cnt[g] * p.R : 0};
+      }
+    }
+    return;
   }
-  __syncthreads();
-  const int N = all_c + all_s[0];
-  const int share = max(kMinShare, (N + kGrid - 1) / kGrid);
   const int lo = min((long)N, (long)blockIdx.x * share), hi = min((long)N, (long)lo + share);
   // the item that position x lies in
   auto item_at = [&](int x) {
     if (x < all_c) {
       const int g = pfx_find(s.gbase, p.n_groups, x), rows = s.cnt[g] * p.R;
-      const int rel = x - s.gbase[g], full = p.Hkv * cost(false, true) * s.tiles[g];
+      const int rel = x - s.gbase[g], full = p.Hkv * cost(false, kTwo) * s.tiles[g];
       const int k = min(rel / full, pfx_blocks(rows) - 1), in = rel - k * full;
-      return s.gitem[g] + k * p.Hkv + in / (pfx_weight<false>(rows, k) * s.tiles[g]);
+      return s.gitem[g] + k * p.Hkv + in / (pfx_weight<false>(pfx_kind(rows, k, p.Hkv)) * s.tiles[g]);
     }
     const int b = pfx_find(s.sbase, p.B, x), nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
-    const int rel = x - s.sbase[b], full = p.Hkv * (cost(true, true) * nt + kItemCost);
+    const int rel = x - s.sbase[b], full = p.Hkv * (cost(true, kTwo) * nt + kItemCost);
     const int k = min(rel / full, p.sblk - 1), in = rel - k * full;
-    return all_i + (b * p.sblk + k) * p.Hkv + in / (pfx_weight<true>(p.R, k) * nt + kItemCost);
+    return all_i + b * p.sitems + k * p.Hkv + in / (pfx_weight<true>(pfx_kind(p.R, k, p.Hkv)) * nt + kItemCost);
   };
-  const int i0 = lo < hi ? item_at(lo) : 0, i1 = lo < hi ? item_at(hi - 1) : -1;
-  for (int k = tid; k <= i1 - i0; k += kThreads) {
+  // (two lanes find the two ends at once)
+  const int end = lo < hi ? item_at(lane == 1 ? hi - 1 : lo) : lane == 1 ? -1 : 0;
+  const int i0 = __shfl_sync(0xffffffffu, end, 0), i1 = __shfl_sync(0xffffffffu, end, 1);
+  for (int k = tid; k <= i1 - i0; k += kThreads - 32) {
     const int it = i0 + k;
     PfxPiece d;
     int base, ov, w, nt;
     if (it < all_i) {
       const int g = pfx_find(s.gitem, p.n_groups, it), rows = s.cnt[g] * p.R;
-      const int rel = it - s.gitem[g], blk = rel / p.Hkv;
-      d.head = rel - blk * p.Hkv;
+      const int rel = it - s.gitem[g], blk = min(rel / p.Hkv, pfx_blocks(rows) - 1), i = rel - blk * p.Hkv;
+      d.kind = pfx_kind(rows, blk, p.Hkv);
+      d.head = d.kind == kPair ? 2 * i : i;
       nt = s.tiles[g];
-      w = pfx_weight<false>(rows, blk);
+      w = pfx_weight<false>(d.kind);
       ov = 0;
-      base = s.gbase[g] + pfx_cost_before<false>(rows, nt, p.Hkv, blk, d.head);
+      base = s.gbase[g] + pfx_cost_before<false>(rows, nt, p.Hkv, blk, i);
       d.first = s.first[g];
       d.member0 = s.gstart[g];
       d.key0 = 0;
@@ -323,13 +340,15 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       d.nrows = min(2 * kM, rows - d.row0);
       d.slot = it + (int)blockIdx.x;
     } else {
-      const int j = it - all_i, b = j / (p.sblk * p.Hkv), rel = j - b * p.sblk * p.Hkv, blk = rel / p.Hkv;
-      d.head = rel - blk * p.Hkv;
+      const int j = it - all_i, b = j / p.sitems, rel = j - b * p.sitems;
+      const int blk = min(rel / p.Hkv, p.sblk - 1), i = rel - blk * p.Hkv;
+      d.kind = pfx_kind(p.R, blk, p.Hkv);
+      d.head = d.kind == kPair ? 2 * i : i;
       const int t = s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0;
       nt = pfx_own_tiles(p, s.ctx[b], t);
-      w = pfx_weight<true>(p.R, blk);
+      w = pfx_weight<true>(d.kind);
       ov = kItemCost;
-      base = s.sbase[b] + pfx_cost_before<true>(p.R, nt, p.Hkv, blk, d.head);
+      base = s.sbase[b] + pfx_cost_before<true>(p.R, nt, p.Hkv, blk, i);
       d.first = b;
       d.member0 = -1;
       d.key0 = t * kTK;
@@ -341,22 +360,12 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     }
     d.t0 = pfx_first_tile(base, ov, w, nt, lo);
     d.nt = pfx_first_tile(base, ov, w, nt, hi) - d.t0;
-    d.pad = 0;
     p.pieces[it + (int)blockIdx.x] = d;
     if (k < kKept) sh.kept[k] = d;
   }
   if (tid == 0) {
     sh.n_pieces = i1 - i0 + 1;
     sh.piece0 = i0 + (int)blockIdx.x;
-  }
-  if (blockIdx.x == 0) {
-    for (int b = tid; b < p.B; b += kThreads) {
-      const int g = s.grp[b], t = g >= 0 ? s.tiles[g] : 0;
-      p.seqs[b] = PfxSeq{t ? g : -1, t ? s.pos[b] : 0, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t)};
-    }
-    for (int g = tid; g < p.n_groups; g += kThreads)
-      p.groups[g] = PfxGroup{s.gbase[g], s.gitem[g], s.tiles[g], s.cnt[g] * p.R};
-    if (tid == 0) p.header[0] = share;
   }
 }
 
@@ -410,47 +419,43 @@ __device__ __forceinline__ uint32_t pfx_pack(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// A walk over the units of this CTA's pieces. A unit is one Q tile on one K/V tile: with
-// more than 128 rows the two Q tiles take each K/V tile in turn, with fewer the one Q
-// tile takes the K/V tiles one after the other. Units go to the two softmax groups
-// alternately, over all pieces. (The descriptor stays where it is: the roles read the
-// fields they need, and a walk fits the registers of the one thread that issues MMAs.)
+// A walk over this CTA's pieces. Their work goes to the two softmax groups in units, one Q
+// tile on one K/V tile each, alternately over all pieces: with two Q tiles these take each
+// K/V tile in turn, with one it takes the K/V tiles one after the other, and of two heads
+// each takes its own.
 struct PfxWalk {
   const PfxPiece* p;   // null: no more
   int k;               // piece
-  int w, n;            // unit of the piece, and how many it has
-  int u;               // units before, over all pieces: u & 1 is the softmax group
+  int n;               // its units
+  int u;               // units of the pieces before
   int tile0, q0;       // K/V tiles and Q tiles of the pieces before
-  int two;             // two Q tiles
-  __device__ __forceinline__ void open(const PfxParams& P, const PfxShared& sh) {
+  int kind, sh;        // Kind, and 1 where each 64 keys are two units
+  __device__ __forceinline__ void open(const PfxParams& P, const PfxShared& S) {
     p = nullptr;
-    for (; k < sh.n_pieces; ++k) {
-      const PfxPiece* d = k < pfx::kKept ? &sh.kept[k] : P.pieces + sh.piece0 + k;
+    for (; k < S.n_pieces; ++k) {
+      const PfxPiece* d = k < pfx::kKept ? &S.kept[k] : P.pieces + S.piece0 + k;
       const int nt = d->nt;
       if (nt > 0) {
-        two = d->nrows > pfx::kM ? 1 : 0;
-        n = nt << two;
-        w = 0;
+        kind = d->kind;
+        sh = kind == pfx::kOne ? 0 : 1;
+        n = nt << sh;
         p = d;
         return;
       }
     }
   }
-  __device__ __forceinline__ void begin(const PfxParams& P, const PfxShared& sh) {
+  __device__ __forceinline__ void begin(const PfxParams& P, const PfxShared& S) {
     k = u = tile0 = q0 = 0;
-    open(P, sh);
+    open(P, S);
   }
-  __device__ __forceinline__ void next_piece(const PfxParams& P, const PfxShared& sh) {
-    tile0 += n >> two;
-    q0 += 1 + two;
+  __device__ __forceinline__ int tiles() const { return kind == pfx::kTwo ? n >> 1 : n; }   // K/V tiles
+  __device__ __forceinline__ void next_piece(const PfxParams& P, const PfxShared& S) {
+    tile0 += tiles();
+    u += n;
+    q0 += 1 + sh;
     ++k;
-    open(P, sh);
+    open(P, S);
   }
-  __device__ __forceinline__ void next_unit(const PfxParams& P, const PfxShared& sh) {
-    ++u;
-    if (++w == n) next_piece(P, sh);
-  }
-  __device__ __forceinline__ int tile() const { return w >> two; }   // in the piece
 };
 
 __global__ void __launch_bounds__(pfx::kThreads, 1)
@@ -529,9 +534,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       nx.next_piece(p, sh);
       int ids_nx = nx.p ? fetch(*nx.p, nx.p->t0) : 0;
       int ids_on = fetch(d, d.t0 + per);
-      for (int j = 0; j < d.nt; ++j) {
-        const int t = d.t0 + j, jj = j % per;
-        if (j > 0 && jj == 0) {
+      const int two_heads = wk.kind == kPair ? 1 : 0, n_tiles = wk.tiles();
+      for (int j = 0; j < n_tiles; ++j) {
+        const int jt = j >> two_heads, t = d.t0 + jt, jj = jt % per;
+        if (jt > 0 && jj == 0 && (j & two_heads) == 0) {
           ids = ids_on;
           ids_on = fetch(d, t + per);
         }
@@ -544,7 +550,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           ok = false;
           break;
         }
-        const int su = (int)pfx_uniform((uint32_t)st), head = (int)pfx_uniform((uint32_t)d.head);
+        const int su = (int)pfx_uniform((uint32_t)st), head = (int)pfx_uniform((uint32_t)(d.head + (j & two_heads)));
         const bool once = pfx_uniform(d.member0 < 0) != 0;
         const bool junk = v && d.len - t * kTK < kTK;      // V rows of no key: the cleaner sees them first
         uint64_t* full = junk ? &sh.v_land[su] : v ? &sh.v_full[su] : &sh.k_full[su];
@@ -586,12 +592,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     for (wk.begin(p, sh); ok && wk.p; wk.next_piece(p, sh)) {
       const PfxPiece d = *wk.p;
       const bool boxes = p.R <= kM && (d.member0 < 0 || (p.R % 8 == 0 && kM % p.R == 0));
-      for (int i = 0; i <= wk.two && ok; ++i) {
+      for (int i = 0; i <= wk.sh && ok; ++i) {
         const int qc = wk.q0 + i, buf = qc & 1;
+        const int r0 = wk.kind == kTwo ? i * kM : 0, head = d.head + (wk.kind == kPair ? i : 0);
         uint8_t* tile = q_s + buf * kQBytes;
         const uint32_t par = (uint32_t)(((qc >> 1) & 1) ^ 1);
         if (boxes) {
-          const int n = (min(d.nrows - i * kM, kM) + p.R - 1) / p.R, m0 = (d.row0 + i * kM) / p.R;
+          const int n = (min(d.nrows - r0, kM) + p.R - 1) / p.R, m0 = (d.row0 + r0) / p.R;
           const int seq = d.member0 < 0 ? d.first : lane < n ? p.order[d.member0 + m0 + lane] : 0;
           ok = pfx_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
           if (!ok) break;
@@ -600,8 +607,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           for (int m = 0; m < n; ++m, tile += p.R * 128) {
             const int b = __shfl_sync(0xffffffffu, seq, m);
             if (leader) {
-              tma_load_3d(tile, &qmap, &sh.q_full[buf], 0, d.head * p.G, b * p.n_q);
-              tma_load_3d(tile + kQHalf, &qmap, &sh.q_full[buf], 64, d.head * p.G, b * p.n_q);
+              tma_load_3d(tile, &qmap, &sh.q_full[buf], 0, head * p.G, b * p.n_q);
+              tma_load_3d(tile + kQHalf, &qmap, &sh.q_full[buf], 64, head * p.G, b * p.n_q);
             }
           }
           __syncwarp();
@@ -610,12 +617,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         int off[4];                                   // of rows lane, lane + 32, .. of the tile, in rows of q; -1: none
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int in = i * kM + j * 32 + lane, r = d.row0 + in;
+          const int in = r0 + j * 32 + lane, r = d.row0 + in;
           const int mem = r / p.R, rem = r - mem * p.R, qi = rem / p.G;
           off[j] = -1;
           if (in < d.nrows) {
             const int b = d.member0 < 0 ? d.first : p.order[d.member0 + mem];
-            off[j] = (b * p.n_q + qi) * p.Hq + d.head * p.G + (rem - qi * p.G);
+            off[j] = (b * p.n_q + qi) * p.Hq + head * p.G + (rem - qi * p.G);
           }
         }
         ok = pfx_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
@@ -647,8 +654,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     bool ok = true;
     for (wk.begin(p, sh); ok && wk.p; wk.next_piece(p, sh)) {
       const PfxPiece d = *wk.p;
-      for (int j = max(0, d.len / kTK - d.t0); j < d.nt; ++j) {   // from the first tile that context keys do not fill
-        const int t = d.t0 + j, keys = max(0, d.len - t * kTK), slot = (wk.tile0 + j) % kSlots;
+      const int two_heads = wk.kind == kPair ? 1 : 0, n_tiles = wk.tiles();
+      // from the first tile that context keys do not fill
+      for (int j = max(0, d.len / kTK - d.t0) << two_heads; j < n_tiles; ++j) {
+        const int t = d.t0 + (j >> two_heads), keys = max(0, d.len - t * kTK), slot = (wk.tile0 + j) % kSlots;
         const int blk0 = t == d.blk ? (keys + p.br - 1) >> p.br_shift << p.br_shift : kTK;
         if (!pfx_wait(&sh.v_land[slot], ph >> slot & 1u, abort_flag, p.err, 54, p.wait_ns)) {
           ok = false;
@@ -693,9 +702,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const PfxPiece* d = k < kKept ? &sh.kept[k] : p.pieces + sh.piece0 + k;
         const int nt = d->nt;
         if (nt == 0) continue;
-        const bool one = d->nrows <= kM;
-        const int n = one ? nt : 2 * nt, w0 = (u0 ^ x) & 1, mine = (n - w0 + 1) >> 1;
-        const int t = tile0 + (one ? w0 : 0), q = q0 + (one ? 0 : w0), step = one ? 2 : 1;
+        const int kind = d->kind;
+        const bool alone = kind != kTwo;     // a K/V tile is read by one group
+        const int n = kind == kOne ? nt : 2 * nt, w0 = (u0 ^ x) & 1, mine = (n - w0 + 1) >> 1;
+        const int t = tile0 + (alone ? w0 : 0), q = q0 + (kind == kOne ? 0 : w0), step = alone ? 2 : 1;
         int slot = t % kSlots;
         uint32_t ph = (uint32_t)(t / kSlots & 1);
         if (role < 2) {
@@ -712,13 +722,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                           kd + (uint64_t)(((j >> 2) * kHalf + (j & 3) * 32) / 16), id_s, j > 0 ? 1u : 0u);
             tc_commit(&sh.s_full[x]);
             tc_commit(&sh.k_empty[slot]);
-            if (one) mbar_arrive(&sh.k_empty[slot]);         // no unit of the other group reads this K tile
+            if (alone) mbar_arrive(&sh.k_empty[slot]);
             slot += step;
             if (slot >= kSlots) slot -= kSlots, ph ^= 1u;
           }
-          if (ok && mine) {                                  // nor this Q tile, which is free now
+          if (ok && mine) {                                  // this Q tile is free now
             tc_commit(&sh.q_empty[q & 1]);
-            if (!one || n == 1) mbar_arrive(&sh.q_empty[q & 1]);
+            if (kind != kOne || n == 1) mbar_arrive(&sh.q_empty[q & 1]);
           }
         } else {
           for (int i = 0; i < mine; ++i, ++units) {
@@ -733,14 +743,14 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
               tc_mma_bf16_ta(o_t, p_t + (uint32_t)(j * 8), vd + (uint64_t)(j * 2048 / 16), id_pv, 1u);
             tc_commit(&sh.pv_done[x]);
             tc_commit(&sh.v_empty[slot]);
-            if (one) mbar_arrive(&sh.v_empty[slot]);
+            if (alone) mbar_arrive(&sh.v_empty[slot]);
             slot += step;
             if (slot >= kSlots) slot -= kSlots, ph ^= 1u;
           }
         }
         u0 += n;
-        tile0 += nt;
-        q0 += one ? 1 : 2;
+        tile0 += alone ? n : nt;
+        q0 += kind == kOne ? 1 : 2;
       }
       tc_commit(&sh.mma_done);
       mbar_wait_bounded(&sh.mma_done, 0, p.err, 49);
@@ -759,12 +769,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // The first pass is made on nothing, while the first copies are on their way: it brings
     // the instructions, whose misses would else come between the first unit's steps.
     bool ok = true, dry = true;
-    for (wk.begin(p, sh); ok && wk.p; wk.u += wk.n, wk.next_piece(p, sh)) {
+    for (wk.begin(p, sh); ok && wk.p; wk.next_piece(p, sh)) {
       const PfxPiece& d = *wk.p;
       const int t0 = d.t0, len = d.len, blk = d.blk;
       const int w0 = (wk.u + x) & 1;                  // this group's first unit of the piece
-      const int row0 = (wk.two ? w0 * kM : 0) + quarter * 32, row = row0 + lane;   // in the item's block of 256
-      const int half = wk.two ? w0 : x;
+      const int row0 = (wk.kind == kTwo ? w0 * kM : 0) + quarter * 32, row = row0 + lane;   // in the item's block of 256
+      const int half = wk.kind == kOne ? x : w0;     // of the slot's partials: Q tile, head, or group
       const bool live = row0 < d.nrows;               // the warp has rows
       float m_run = -CUDART_INF_F, l_run = 0.f;
       for (int w = w0; w < wk.n;) {
@@ -791,7 +801,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && !dry) mbar_arrive(&sh.s_read[x]);
-        const int t = t0 + (w >> wk.two), left = len - t * kTK;
+        const int t = t0 + (w >> wk.sh), left = len - t * kTK;
         if (left < kTK) {
           // the tile's keys: context rows [0, keys), and in the part's last tile the block's from
           // row blk0 on; causal: the row of query i sees them up to its own
@@ -921,6 +931,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 // ---------------------------------------------------------------------------
 namespace pfx {
 constexpr int kJoinRows = 32, kJoinCols = 8, kJoinThreads = kJoinRows * (kD / kJoinCols);
+constexpr int kJoinLoads = 4;
 }
 
 __global__ void __launch_bounds__(pfx::kJoinThreads)
@@ -930,75 +941,79 @@ prefix_join_kernel(const __grid_constant__ PfxParams p) {
   const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
   const int r = blockIdx.y * kJoinRows + threadIdx.x / (kD / kJoinCols), c0 = threadIdx.x % (kD / kJoinCols) * kJoinCols;
   if (r >= p.R) return;
-  const int share = p.header[0];
   const PfxSeq s = p.seqs[b];
-  // ranges that hold tiles of an item: [v0, v1]
-  auto ranges = [&](int base, int ov, int w, int nt, int& v0, int& v1) {
-    v0 = 0;
-    v1 = -1;
-    if (nt <= 0) return;
-    v0 = (base + ov) / share;                        // where the first and the last tile begin
-    v1 = (base + ov + (nt - 1) * w) / share;
-  };
-  // source 0: the own part; source 1: the prefix
-  int v0[2], n[2], halves[2];
+  // source 0: the own part, source 1: the prefix: partials, one a range that holds tiles of
+  // the item, or two (of each group)
+  int n[2] = {0, 0};
+  bool two[2];
   const float2* ml[2];
   const float* po[2];
-  size_t step[2];                                    // rows of a slot
-  {
-    const int blk = r / (2 * kM), in = r - blk * 2 * kM, w = pfx_weight<true>(p.R, blk);
-    const bool two = pfx_two(p.R, blk);
-    int v1;
-    ranges(s.base + pfx_cost_before<true>(p.R, s.nt, p.Hkv, blk, head), kItemCost, w, s.nt, v0[0], v1);
-    n[0] = v1 - v0[0] + 1;
-    halves[0] = two ? 1 : 2;
-    step[0] = (size_t)2 * p.Rs2;
-    const size_t at = ((size_t)((b * p.sblk + blk) * p.Hkv + head) + v0[0]) * step[0] + (two ? in / kM * p.Rs2 + in % kM : in);
-    ml[0] = p.ml_s + at;
-    po[0] = p.po_s + at * kD + c0;
+  const int hs[2] = {p.Rs2, kM};                     // rows of a half of a slot
+  auto source = [&](int e, int rows, int row, int item0, int base, int ov, int nt, int w, int before) {
+    const int blk = row / (2 * kM), in = row - blk * 2 * kM, kind = pfx_kind(rows, blk, p.Hkv);
+    base += before + ov;                             // where the first tile's cost begins
+    const int v0 = base / s.share, v1 = (base + (nt - 1) * w) / s.share;
+    n[e] = v1 - v0 + 1;
+    two[e] = kind == kOne;
+    const int half = kind == kTwo ? in / kM : kind == kPair ? head & 1 : 0;
+    const size_t slot = item0 + blk * p.Hkv + (kind == kPair ? head >> 1 : head) + v0;
+    const size_t at = (slot * 2 + half) * hs[e] + (kind == kTwo ? in % kM : in);
+    ml[e] = (e ? p.ml_p : p.ml_s) + at;
+    po[e] = (e ? p.po_p : p.po_s) + at * kD + c0;
+  };
+  if (s.nt > 0) {
+    const int blk = r / (2 * kM), kind = pfx_kind(p.R, blk, p.Hkv);
+    source(0, p.R, r, b * p.sitems, s.base, kItemCost, s.nt, pfx_weight<true>(kind),
+           pfx_cost_before<true>(p.R, s.nt, p.Hkv, blk, kind == kPair ? head >> 1 : head));
   }
-  n[1] = 0;
-  if (s.group >= 0) {
-    const PfxGroup g = p.groups[s.group];
-    const int pr = s.pos * p.R + r, blk = pr / (2 * kM), in = pr - blk * 2 * kM, w = pfx_weight<false>(g.rows, blk);
-    int v1;
-    ranges(g.base + pfx_cost_before<false>(g.rows, g.tiles, p.Hkv, blk, head), 0, w, g.tiles, v0[1], v1);
-    n[1] = v1 - v0[1] + 1;
-    halves[1] = pfx_two(g.rows, blk) ? 1 : 2;
-    step[1] = 2 * kM;
-    const size_t at = ((size_t)(g.item + blk * p.Hkv + head) + v0[1]) * step[1] + in;   // (two Q tiles: in / 128 is the half)
-    ml[1] = p.ml_p + at;
-    po[1] = p.po_p + at * kD + c0;
+  if (s.g_tiles > 0) {
+    const int row = s.pos * p.R + r, blk = row / (2 * kM), kind = pfx_kind(s.g_rows, blk, p.Hkv);
+    source(1, s.g_rows, row, s.g_item, s.g_base, 0, s.g_tiles, pfx_weight<false>(kind),
+           pfx_cost_before<false>(s.g_rows, s.g_tiles, p.Hkv, blk, kind == kPair ? head >> 1 : head));
   }
-  const size_t hs[2] = {(size_t)p.Rs2, (size_t)kM};  // rows of a half
-  float m = -CUDART_INF_F;
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll 4
-    for (int i = 0; i < n[e] * halves[e]; ++i)
-      m = fmaxf(m, ml[e][(halves[e] == 2 ? i >> 1 : i) * step[e] + (halves[e] == 2 ? (i & 1) * hs[e] : 0)].x);
-  float l = 0.f, acc[kJoinCols];
+  float m = -CUDART_INF_F, l = 0.f, acc[kJoinCols];
 #pragma unroll
   for (int q = 0; q < kJoinCols; ++q) acc[q] = 0.f;
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll 4
-    for (int i = 0; i < n[e] * halves[e]; ++i) {
-      const size_t at = (halves[e] == 2 ? i >> 1 : i) * step[e] + (halves[e] == 2 ? (i & 1) * hs[e] : 0);
-      const float2 x = ml[e][at];
-      if (x.x == -CUDART_INF_F) continue;            // a part without a key for this row: its O may never have been written
-      const float w = exp2f(x.x - m);
-      l = fmaf(x.y, w, l);
-      const float4* o = reinterpret_cast<const float4*>(po[e] + at * kD);
+  for (int e = 0; e < 2; ++e) {
+    const int cnt = two[e] ? 2 * n[e] : n[e];
+    for (int i0 = 0; n[e] > 0 && i0 < cnt; i0 += kJoinLoads) {   // several partials' loads at once
+      float2 x[kJoinLoads];
+      float4 y[kJoinLoads][kJoinCols / 4];
 #pragma unroll
-      for (int q = 0; q < kJoinCols / 4; ++q) {
-        const float4 y = o[q];
-        acc[4 * q] = fmaf(y.x, w, acc[4 * q]);
-        acc[4 * q + 1] = fmaf(y.y, w, acc[4 * q + 1]);
-        acc[4 * q + 2] = fmaf(y.z, w, acc[4 * q + 2]);
-        acc[4 * q + 3] = fmaf(y.w, w, acc[4 * q + 3]);
+      for (int j = 0; j < kJoinLoads; ++j) {
+        const int i = i0 + j;
+        x[j] = make_float2(-CUDART_INF_F, 0.f);
+        if (i >= cnt) continue;
+        const size_t at = two[e] ? (size_t)i * hs[e] : (size_t)i * 2 * hs[e];
+        x[j] = ml[e][at];
+#pragma unroll
+        for (int q = 0; q < kJoinCols / 4; ++q) y[j][q] = reinterpret_cast<const float4*>(po[e] + at * kD)[q];
+      }
+      float mn = m;
+#pragma unroll
+      for (int j = 0; j < kJoinLoads; ++j) mn = fmaxf(mn, x[j].x);
+      if (mn == -CUDART_INF_F) continue;
+      const float f = exp2f(m - mn);                 // (0 before the first)
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int q = 0; q < kJoinCols; ++q) acc[q] *= f;
+#pragma unroll
+      for (int j = 0; j < kJoinLoads; ++j) {
+        if (x[j].x == -CUDART_INF_F) continue;       // no key for this row: its O may never have been written
+        const float w = exp2f(x[j].x - m);
+        l = fmaf(x[j].y, w, l);
+#pragma unroll
+        for (int q = 0; q < kJoinCols / 4; ++q) {
+          acc[4 * q] = fmaf(y[j][q].x, w, acc[4 * q]);
+          acc[4 * q + 1] = fmaf(y[j][q].y, w, acc[4 * q + 1]);
+          acc[4 * q + 2] = fmaf(y[j][q].z, w, acc[4 * q + 2]);
+          acc[4 * q + 3] = fmaf(y[j][q].w, w, acc[4 * q + 3]);
+        }
       }
     }
+  }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key at all: 0 (and NaN stays NaN)
   const int i = r / p.G, hh = r - i * p.G;
   bf16* dst = p.out + ((size_t)(b * p.n_q + i) * p.Hq + head * p.G + hh) * kD + c0;
@@ -1016,22 +1031,23 @@ static bool pfx_dims_ok(int B, int n_q, int n_kv, int Hq, int Hkv, int D, int ma
   if (page_size != 8 && page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return false;
   // costs are 32-bit
   const double tiles = (double)max_ctx / kTK + 2 + kItemCost;
-  return 5.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
+  return 9.0 * B * Hkv * (pfx_blocks(n_q * (Hq / Hkv)) + 1) * tiles < 1.0e9 && (double)n_q * Hq * B < 1.0e9;
 }
 
 struct PfxLayout {
-  size_t pieces, order, seqs, groups, header, po_p, ml_p, po_s, ml_s, end;
-  int sblk, Rs2;
+  size_t pieces, order, seqs, po_p, ml_p, po_s, ml_s, end;
+  int sblk, sitems, Rs2;
 };
 static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
   using namespace pfx;
   PfxLayout l;
   const int R = n_q * (Hq / Hkv);
   l.sblk = pfx_blocks(R);
+  l.sitems = pfx_items(R, Hkv);
   l.Rs2 = std::min(R, kM);
   // items of prefixes: blocks of 256 rows, one more begun per group of two sequences at least
   const size_t ip = (size_t)Hkv * ((size_t)B * R / (2 * kM) + std::min(n_groups, B / 2));
-  const size_t is = (size_t)Hkv * B * l.sblk, sp = n_groups ? ip + kGrid : 0, ss = is + kGrid;
+  const size_t is = (size_t)B * l.sitems, sp = n_groups ? ip + kGrid : 0, ss = is + kGrid;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -1041,8 +1057,6 @@ static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
   l.pieces = take((ip + is + kGrid) * sizeof(PfxPiece));
   l.order = take(B * sizeof(uint16_t));
   l.seqs = take(B * sizeof(PfxSeq));
-  l.groups = take(std::max(n_groups, 1) * sizeof(PfxGroup));
-  l.header = take(sizeof(int32_t));
   l.po_p = take(sp * 2 * kM * kD * sizeof(float));
   l.ml_p = take(sp * 2 * kM * sizeof(float2));
   l.po_s = take(ss * 2 * l.Rs2 * kD * sizeof(float));
@@ -1078,8 +1092,6 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   p.pieces = (PfxPiece*)(ws + l.pieces);
   p.order = (uint16_t*)(ws + l.order);
   p.seqs = (PfxSeq*)(ws + l.seqs);
-  p.groups = (PfxGroup*)(ws + l.groups);
-  p.header = (int32_t*)(ws + l.header);
   p.po_p = (float*)(ws + l.po_p);
   p.ml_p = (float2*)(ws + l.ml_p);
   p.po_s = (float*)(ws + l.po_s);
@@ -1088,7 +1100,7 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   p.B = a.B; p.n_groups = pa.n_groups; p.n_q = a.n_q; p.n_kv = a.n_kv; p.Hq = a.Hq; p.Hkv = a.Hkv;
   p.G = a.Hq / a.Hkv;
   p.R = a.n_q * p.G;
-  p.sblk = l.sblk; p.Rs2 = l.Rs2;
+  p.sblk = l.sblk; p.sitems = l.sitems; p.Rs2 = l.Rs2;
   p.page_shift = 0;
   while (1 << p.page_shift < a.page_size) ++p.page_shift;
   p.max_pages = a.max_pages; p.num_pages = a.num_pages; p.max_ctx = a.max_ctx; p.causal = a.causal;
