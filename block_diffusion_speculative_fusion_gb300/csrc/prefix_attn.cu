@@ -35,7 +35,7 @@ constexpr int kQHalf = kQBytes / 2;
 constexpr int kWarpK = 8, kWarpV = 9, kWarpQ = 10, kWarpClean = 11, kWarpMma = 12;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKept = 42;                   // piece descriptors kept in shared memory
+constexpr int kKept = 36;                   // piece descriptors kept in shared memory
 // What an item is: one Q tile and kv head, two Q tiles (more than 128 rows) that share the
 // K/V tiles, or the Q tiles of two kv heads with K/V tiles of their own.
 enum Kind { kOne = 0, kTwo = 1, kPair = 2 };
@@ -177,9 +177,14 @@ __device__ __forceinline__ int pfx_find(const int* a, int n, int x) {
 
 // Shared memory: Q tiles, ring, then the small things.
 struct PfxShared {
-  uint64_t k_full[pfx::kSlots], v_full[pfx::kSlots], k_empty[pfx::kSlots], v_empty[pfx::kSlots];
+  // [0]: what both groups read, [1 + x]: what group x reads alone. A wait knows a phase from
+  // the one before by its parity only, so who waits for a barrier waits for all its phases:
+  // on one barrier for both, a group could take its tile for landed while the other group's,
+  // before it in the same slot, was still on its way.
+  uint64_t k_full[3][pfx::kSlots], v_full[3][pfx::kSlots], q_full[3][2];
+  uint64_t k_empty[pfx::kSlots], v_empty[pfx::kSlots], q_empty[2];
   uint64_t v_land[pfx::kSlots];    // V tiles with rows to clean have landed
-  uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], q_full[2], q_empty[2], mma_done;
+  uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
   int n_pieces, piece0;            // this CTA's pieces, in the list from piece0 on
@@ -448,6 +453,9 @@ struct PfxWalk {
     k = u = tile0 = q0 = 0;
     open(P, S);
   }
+  // the barrier by which unit j's group alone, or all that read K/V tile j, learn of it (PfxShared)
+  __device__ __forceinline__ int reader_alone(int j) const { return 1 + ((j ^ u) & 1); }
+  __device__ __forceinline__ int reader(int j) const { return kind == pfx::kTwo ? 0 : reader_alone(j); }
   __device__ __forceinline__ int tiles() const { return kind == pfx::kTwo ? n >> 1 : n; }   // K/V tiles
   __device__ __forceinline__ void next_piece(const PfxParams& P, const PfxShared& S) {
     tile0 += tiles();
@@ -472,9 +480,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&sh.k_full[i], 1);
-      mbar_init(&sh.v_full[i], 1);
-      mbar_init(&sh.k_empty[i], 2);        // both MMA warps, or one for both
+      for (int by = 0; by < 3; ++by) {
+        mbar_init(&sh.k_full[by][i], 1);
+        mbar_init(&sh.v_full[by][i], 1);
+      }
+      mbar_init(&sh.k_empty[i], 2);        // both groups, or one for both
       mbar_init(&sh.v_empty[i], 2);
       mbar_init(&sh.v_land[i], 1);
     }
@@ -484,7 +494,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.o_empty[i], 4);
-      mbar_init(&sh.q_full[i], 1);
+      for (int by = 0; by < 3; ++by) mbar_init(&sh.q_full[by][i], 1);
       mbar_init(&sh.q_empty[i], 2);
     }
     mbar_init(&sh.mma_done, 4);
@@ -502,7 +512,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   PfxWalk wk;
   int q_boxes = 0;                 // one past the last Q tile that came as boxes
   int issued = 0;                  // tiles that this warp has asked for
-  uint32_t landed = 0, land_ph = 0;   // V: a bit for each slot whose last tile goes by v_land, and how many have (odd)
+  uint32_t last = 0, phases = 0;   // by which of a slot's barriers its last tile goes, and which of them have had an odd number
 
   if (warp == kWarpK || warp == kWarpV) {
     // ------------------------------ K loads, V loads ------------------------------
@@ -552,10 +562,11 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         const int su = (int)pfx_uniform((uint32_t)st), head = (int)pfx_uniform((uint32_t)(d.head + (j & two_heads)));
         const bool once = pfx_uniform(d.member0 < 0) != 0;
-        const bool junk = v && d.len - t * kTK < kTK;      // V rows of no key: the cleaner sees them first
-        uint64_t* full = junk ? &sh.v_land[su] : v ? &sh.v_full[su] : &sh.k_full[su];
-        landed = junk ? landed | 1u << su : landed & ~(1u << su);
-        land_ph ^= (junk ? 1u : 0u) << su;
+        // V rows of no key: the cleaner sees them first
+        const int by = v && d.len - t * kTK < kTK ? 3 : wk.reader(j);
+        uint64_t* full = by == 3 ? &sh.v_land[su] : v ? &sh.v_full[by][su] : &sh.k_full[by][su];
+        last = (last & ~(3u << 2 * su)) | (uint32_t)by << 2 * su;
+        phases ^= 1u << (by * 8 + su);
         uint8_t* dst = (v ? v_s : k_s) + su * kTileBytes;
         if (leader) mbar_arrive_expect_tx(full, bytes);
         ++issued;
@@ -594,6 +605,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       const bool boxes = p.R <= kM && (d.member0 < 0 || (p.R % 8 == 0 && kM % p.R == 0));
       for (int i = 0; i <= wk.sh && ok; ++i) {
         const int qc = wk.q0 + i, buf = qc & 1;
+        const int by = wk.kind == kOne && wk.n > 1 ? 0 : wk.reader_alone(i);
         const int r0 = wk.kind == kTwo ? i * kM : 0, head = d.head + (wk.kind == kPair ? i : 0);
         uint8_t* tile = q_s + buf * kQBytes;
         const uint32_t par = (uint32_t)(((qc >> 1) & 1) ^ 1);
@@ -602,13 +614,15 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           const int seq = d.member0 < 0 ? d.first : lane < n ? p.order[d.member0 + m0 + lane] : 0;
           ok = pfx_wait(&sh.q_empty[buf], par, abort_flag, p.err, 42, p.wait_ns);
           if (!ok) break;
-          if (leader) mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(n * p.R * 256));
+          if (leader) mbar_arrive_expect_tx(&sh.q_full[by][buf], (uint32_t)(n * p.R * 256));
+          last = (last & ~(3u << 2 * buf)) | (uint32_t)by << 2 * buf;
+          phases ^= 1u << (by * 8 + buf);
           q_boxes = qc + 1;
           for (int m = 0; m < n; ++m, tile += p.R * 128) {
             const int b = __shfl_sync(0xffffffffu, seq, m);
             if (leader) {
-              tma_load_3d(tile, &qmap, &sh.q_full[buf], 0, head * p.G, b * p.n_q);
-              tma_load_3d(tile + kQHalf, &qmap, &sh.q_full[buf], 64, head * p.G, b * p.n_q);
+              tma_load_3d(tile, &qmap, &sh.q_full[by][buf], 0, head * p.G, b * p.n_q);
+              tma_load_3d(tile + kQHalf, &qmap, &sh.q_full[by][buf], 64, head * p.G, b * p.n_q);
             }
           }
           __syncwarp();
@@ -643,7 +657,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full[buf]);
+        if (lane == 0) mbar_arrive(&sh.q_full[by][buf]);
+        last = (last & ~(3u << 2 * buf)) | (uint32_t)by << 2 * buf;
+        phases ^= 1u << (by * 8 + buf);
       }
     }
     __syncwarp();
@@ -674,7 +690,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[slot]);
+        if (lane == 0) mbar_arrive(&sh.v_full[wk.reader(j)][slot]);
       }
     }
     __syncwarp();
@@ -697,6 +713,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       };
       bool ok = true;
       uint32_t units = 0, pieces = 0;      // of the group so far
+      uint32_t ph_both = 0, ph_alone = 0, q_ph = 0;   // parities to wait for, a bit for each slot
       int u0 = 0, tile0 = 0, q0 = 0;       // units, tiles and Q tiles of the pieces before
       for (int k = 0; ok && k < sh.n_pieces; ++k) {
         const PfxPiece* d = k < kKept ? &sh.kept[k] : p.pieces + sh.piece0 + k;
@@ -707,13 +724,16 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const int n = kind == kOne ? nt : 2 * nt, w0 = (u0 ^ x) & 1, mine = (n - w0 + 1) >> 1;
         const int t = tile0 + (alone ? w0 : 0), q = q0 + (kind == kOne ? 0 : w0), step = alone ? 2 : 1;
         int slot = t % kSlots;
-        uint32_t ph = (uint32_t)(t / kSlots & 1);
+        const int by = alone ? 1 + x : 0;
+        uint32_t ph = by ? ph_alone : ph_both;
         if (role < 2) {
           const uint64_t qd = q_desc + (uint64_t)((q & 1) * (kQBytes / 16));
+          const int q_by = kind == kOne && n > 1 ? 0 : 1 + x, q_bit = (q_by ? 2 : 0) + (q & 1);
           for (int i = 0; i < mine; ++i, ++units) {
             if (units > 0 && !wait(&sh.s_read[x], (units - 1) & 1, 43)) { ok = false; break; }
-            if (i == 0 && !wait(&sh.q_full[q & 1], (uint32_t)(q >> 1 & 1), 44)) { ok = false; break; }
-            if (!wait(&sh.k_full[slot], ph, 45)) { ok = false; break; }
+            if (i == 0 && !wait(&sh.q_full[q_by][q & 1], q_ph >> q_bit & 1u, 44)) { ok = false; break; }
+            if (!wait(&sh.k_full[by][slot], ph >> slot & 1u, 45)) { ok = false; break; }
+            ph ^= 1u << slot;
             tc_fence_after();
             const uint64_t kd = k_desc + (uint64_t)(slot * (kTileBytes / 16));
 #pragma unroll
@@ -724,9 +744,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             tc_commit(&sh.k_empty[slot]);
             if (alone) mbar_arrive(&sh.k_empty[slot]);
             slot += step;
-            if (slot >= kSlots) slot -= kSlots, ph ^= 1u;
+            if (slot >= kSlots) slot -= kSlots;
           }
           if (ok && mine) {                                  // this Q tile is free now
+            q_ph ^= 1u << q_bit;
             tc_commit(&sh.q_empty[q & 1]);
             if (kind != kOne || n == 1) mbar_arrive(&sh.q_empty[q & 1]);
           }
@@ -734,7 +755,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           for (int i = 0; i < mine; ++i, ++units) {
             // (the group's first unit of a piece: its O has been read out)
             if (i == 0 && !wait(&sh.o_empty[x], (pieces++ & 1) ^ 1, 46)) { ok = false; break; }
-            if (!wait(&sh.v_full[slot], ph, 47) || !wait(&sh.p_full[x], units & 1, 48)) { ok = false; break; }
+            if (!wait(&sh.v_full[by][slot], ph >> slot & 1u, 47) || !wait(&sh.p_full[x], units & 1, 48)) { ok = false; break; }
+            ph ^= 1u << slot;
             tc_fence_after();
             const uint64_t vd = v_desc + (uint64_t)(slot * (kTileBytes / 16));
             tc_mma_bf16_ta(o_t, p_t, vd, id_pv, i > 0 ? 1u : 0u);
@@ -745,9 +767,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             tc_commit(&sh.v_empty[slot]);
             if (alone) mbar_arrive(&sh.v_empty[slot]);
             slot += step;
-            if (slot >= kSlots) slot -= kSlots, ph ^= 1u;
+            if (slot >= kSlots) slot -= kSlots;
           }
         }
+        (by ? ph_alone : ph_both) = ph;
         u0 += n;
         tile0 += alone ? n : nt;
         q0 += kind == kOne ? 1 : 2;
@@ -909,15 +932,15 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   if (lane == 0 && *abort_flag) {     // copies in flight land before the CTA leaves
     if (warp == kWarpK || warp == kWarpV)
       for (int i = issued - 1; i >= max(0, issued - kSlots); --i) {
-        const int st = i % kSlots;
-        if (landed >> st & 1u)
-          mbar_wait_bounded(&sh.v_land[st], (land_ph >> st & 1u) ^ 1u, p.err, 56);
-        else
-          mbar_wait_bounded(warp == kWarpV ? &sh.v_full[st] : &sh.k_full[st], (uint32_t)((i / kSlots) & 1), p.err, 56);
+        const int st = i % kSlots, by = (int)(last >> 2 * st & 3u);
+        uint64_t* full = by == 3 ? &sh.v_land[st] : warp == kWarpV ? &sh.v_full[by][st] : &sh.k_full[by][st];
+        mbar_wait_bounded(full, (phases >> (by * 8 + st) & 1u) ^ 1u, p.err, 56);
       }
     if (warp == kWarpQ)
-      for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i)
-        mbar_wait_bounded(&sh.q_full[i & 1], (uint32_t)((i >> 1) & 1), p.err, 57);
+      for (int i = q_boxes - 1; i >= max(0, q_boxes - 2); --i) {
+        const int buf = i & 1, by = (int)(last >> 2 * buf & 3u);
+        mbar_wait_bounded(&sh.q_full[by][buf], (phases >> (by * 8 + buf) & 1u) ^ 1u, p.err, 57);
+      }
   }
   __syncthreads();
   if (warp == kWarpMma) {
