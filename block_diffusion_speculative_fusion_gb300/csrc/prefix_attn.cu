@@ -41,9 +41,10 @@ constexpr int kKept = 36;                   // piece descriptors kept in shared 
 enum Kind { kOne = 0, kTwo = 1, kPair = 2 };
 // Costs of the work list, in quarters of a microsecond: 64 keys of an item, of a prefix or of
 // an own part (whose K/V come from HBM), and an own part's start and end.
-constexpr int cost(bool own, int kind) { return kind == kOne ? 3 + own : kind == kTwo ? 4 + own : own ? 9 : 6; }
+constexpr int cost(bool own, int kind) { return kind == kOne ? 3 + own : kind == kTwo ? 4 + own : 6; }
 constexpr int kItemCost = 9;
 constexpr int kMinShare = 9;                // least work of a CTA (no less than a tile)
+constexpr int kApart = 128;                 // ranges of at most this cost hold tiles of one list only
 constexpr float kRescaleLog2 = 8.f;         // O is rescaled when the row maximum grows by more than 2^8
 // TMEM columns: S of the two softmax groups, their P (bf16 pairs), their O
 constexpr uint32_t kSCol = 0, kPCol = 128, kOCol = 256;
@@ -65,7 +66,7 @@ struct PfxPiece {
 
 // What the second kernel needs to find the partials of a sequence's rows.
 struct PfxSeq {
-  int share;                          // cost of a range
+  int share_p, share_s;               // cost of a range, of prefixes and of own parts
   int base, nt;                       // own part: cost before its first item, tiles
   int pos;                            // its place among the sequences of its prefix
   int g_base, g_item, g_tiles, g_rows;   // the prefix: cost before and number of its first item, tiles (0: none), rows
@@ -78,8 +79,9 @@ struct PfxParams {
   const int32_t* group;
   const int32_t* prefix_len;
   bf16* out;
-  float* po_p;  float2* ml_p;    // partials of prefixes [slot][2][128][128], [slot][2][128]
-  float* po_s;  float2* ml_s;    // of own parts [slot][2][Rs2][128], [slot][2][Rs2]
+  // Partials: O in columns of eight (a warp's rows in a row of sectors), and maximum and sum
+  float* po_p;  float2* ml_p;    // of prefixes [slot][2][16][128][8], [slot][2][128]
+  float* po_s;  float2* ml_s;    // of own parts [slot][2][16][Rs2][8], [slot][2][Rs2]
   PfxPiece* pieces;
   uint16_t* order;               // the groups' sequences, group after group
   PfxSeq* seqs;
@@ -93,12 +95,13 @@ struct PfxParams {
 };
 
 // ---------------------------------------------------------------------------
-// The work list. Items, in order: for each group with a prefix worth sharing, block of
-// 256 packed rows, kv head (or two): the prefix's tiles; then for each sequence, block,
-// head: its own tiles. Each tile has a cost, and an own part kItemCost before its tiles.
-// The costs in a row are cut into equal ranges, one a CTA; a tile belongs to the range in
-// which its cost begins. So the partition, and with it the rounding, depends on the dims,
-// lengths and groups alone.
+// The work lists. Items of the prefixes, in order: for each group with a prefix worth
+// sharing, block of 256 packed rows, kv head (or two): the prefix's tiles. Items of the own
+// parts: for each sequence, block, head: its own tiles. Each tile has a cost, and an own
+// part kItemCost before its tiles. The costs in a row of each list are cut into equal
+// ranges, and a tile belongs to the range in which its cost begins; a CTA takes a range of
+// each list, for both together of small ones a range of either (pfx_plan). So the
+// partition, and with it the rounding, depends on the dims, lengths and groups alone.
 // ---------------------------------------------------------------------------
 __host__ __device__ __forceinline__ int pfx_blocks(int rows) { return (rows + 2 * pfx::kM - 1) / (2 * pfx::kM); }
 // Kind of the items of block k of `rows` packed rows. All blocks but the last have 256.
@@ -187,9 +190,13 @@ struct PfxShared {
   uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  int n_pieces, piece0;            // this CTA's pieces, in the list from piece0 on
+  int n_pieces, n_shared;          // this CTA's pieces: so many, those of prefixes first
+  int piece0, piece1;              // where those and those of own parts begin in the list
   int scan[4 * pfx::kWarps];       // of the plan: three sums over the groups, one over the sequences
   PfxPiece kept[pfx::kKept];
+  __device__ __forceinline__ const PfxPiece* piece(const PfxPiece* list, int k) const {
+    return k < pfx::kKept ? &kept[k] : list + (k < n_shared ? piece0 + k : piece1 + (k - n_shared));
+  }
 };
 constexpr size_t kPfxSmem = 2 * (size_t)pfx::kQBytes + pfx::kSlots * 2 * (size_t)pfx::kTileBytes + sizeof(PfxShared);
 static_assert(kPfxSmem <= 232448, "shared memory");
@@ -275,12 +282,17 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
   for (int b = b0; b < b1; ++b) at_s[0] += own_cost(b);
   pfx_scan(at_s, nw_b, sh.scan + 3 * kWarps, all_s);
   for (int b = b0; b < b1; ++b) {
-    s.sbase[b] = all_c + at_s[0];
+    s.sbase[b] = at_s[0];
     at_s[0] += own_cost(b);
   }
   __syncthreads();
-  const int N = all_c + all_s[0];
-  const int share = max(kMinShare, (N + kGrid - 1) / kGrid);
+  // Ranges: of a small batch each list's CTAs are its own (attn of 8 x 16 rows on 1,024 keys
+  // KAPART); else each CTA has its part of both, so that the balance does not hang
+  // on how tensor-bound and load-bound tiles compare (64 x 16 rows on 8,192 KMIX).
+  const int N_p = all_c, N_s = all_s[0];
+  const int joint = max(kMinShare, (N_p + N_s + kGrid - 1) / kGrid);
+  const int share_p = joint <= kApart ? joint : max(kMinShare, (N_p + kGrid - 1) / kGrid);
+  const int share_s = joint <= kApart ? joint : max(kMinShare, (N_s + kGrid - 1) / kGrid);
   if (tid >= kThreads - 32) {
     // (the last warp, while the others find their pieces) a group's sequences in ascending order
     for (int k = 0; k < p.B && all_i > 0; k += 32) {
@@ -300,34 +312,41 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     if (blockIdx.x == 0) {
       for (int b = lane; b < p.B; b += 32) {
         const int g = s.grp[b], t = g >= 0 ? s.tiles[g] : 0;
-        p.seqs[b] = PfxSeq{share, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t), t ? s.pos[b] : 0, t ? s.gbase[g] : 0,
+        p.seqs[b] = PfxSeq{share_p, share_s, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t), t ? s.pos[b] : 0, t ? s.gbase[g] : 0,
                            t ? s.gitem[g] : 0, t, t ? s.cnt[g] * p.R : 0};
       }
     }
     return;
   }
-  const int lo = min((long)N, (long)blockIdx.x * share), hi = min((long)N, (long)lo + share);
-  // the item that position x lies in
-  auto item_at = [&](int x) {
-    if (x < all_c) {
-      const int g = pfx_find(s.gbase, p.n_groups, x), rows = s.cnt[g] * p.R;
-      const int rel = x - s.gbase[g], full = p.Hkv * cost(false, kTwo) * s.tiles[g];
-      const int k = min(rel / full, pfx_blocks(rows) - 1), in = rel - k * full;
-      return s.gitem[g] + k * p.Hkv + in / (pfx_weight<false>(pfx_kind(rows, k, p.Hkv)) * s.tiles[g]);
-    }
-    const int b = pfx_find(s.sbase, p.B, x), nt = pfx_own_tiles(p, s.ctx[b], s.grp[b] >= 0 ? s.tiles[s.grp[b]] : 0);
-    const int rel = x - s.sbase[b], full = p.Hkv * (cost(true, kTwo) * nt + kItemCost);
-    const int k = min(rel / full, p.sblk - 1), in = rel - k * full;
-    return all_i + b * p.sitems + k * p.Hkv + in / (pfx_weight<true>(pfx_kind(p.R, k, p.Hkv)) * nt + kItemCost);
-  };
-  // (two lanes find the two ends at once)
-  const int end = lo < hi ? item_at(lane == 1 ? hi - 1 : lo) : lane == 1 ? -1 : 0;
-  const int i0 = __shfl_sync(0xffffffffu, end, 0), i1 = __shfl_sync(0xffffffffu, end, 1);
-  for (int k = tid; k <= i1 - i0; k += kThreads - 32) {
-    const int it = i0 + k;
+  const int v_p = blockIdx.x, used = (N_p + share_p - 1) / share_p;   // this CTA's range of prefixes
+  const int v_s = (v_p - used % kGrid + kGrid) % kGrid;               // and of own parts, the first behind the prefixes' last
+  const int lo_p = min((long)N_p, (long)v_p * share_p), hi_p = min((long)N_p, (long)lo_p + share_p);
+  const int lo_s = min((long)N_s, (long)v_s * share_s), hi_s = min((long)N_s, (long)lo_s + share_s);
+  // the item that position x of a list lies in; its ends in four lanes at once
+  int end = lane & 1 ? -1 : 0;
+  const bool own = lane >= 2;
+  const int lo_ = own ? lo_s : lo_p, hi_ = own ? hi_s : hi_p;
+  if (lane < 4 && lo_ < hi_) {
+    const int x = lane & 1 ? hi_ - 1 : lo_;
+    const int i = pfx_find(own ? s.sbase : s.gbase, own ? p.B : p.n_groups, x);
+    const int g = own ? s.grp[i] : i, t = g >= 0 ? s.tiles[g] : 0;
+    const int rows = own ? p.R : s.cnt[i] * p.R, nt = own ? pfx_own_tiles(p, s.ctx[i], t) : t;
+    const int rel = x - (own ? s.sbase[i] : s.gbase[i]), ov = own ? kItemCost : 0;
+    const int full = p.Hkv * ((own ? cost(true, kTwo) : cost(false, kTwo)) * nt + ov);
+    const int k = min(rel / full, pfx_blocks(rows) - 1), kind = pfx_kind(rows, k, p.Hkv);
+    end = (own ? i * p.sitems : s.gitem[i]) + k * p.Hkv +
+          (rel - k * full) / ((own ? pfx_weight<true>(kind) : pfx_weight<false>(kind)) * nt + ov);
+  }
+  const int i0 = __shfl_sync(0xffffffffu, end, 0), n_p = __shfl_sync(0xffffffffu, end, 1) - i0 + 1;
+  const int j0 = __shfl_sync(0xffffffffu, end, 2), n_s = __shfl_sync(0xffffffffu, end, 3) - j0 + 1;
+  const int piece0 = i0 + v_p, piece1 = all_i + kGrid + j0 + v_s;
+  for (int k = tid; k < n_p + n_s; k += kThreads - 32) {
     PfxPiece d;
-    int base, ov, w, nt;
-    if (it < all_i) {
+    int base, ov, w, nt, lo, hi;
+    if (k < n_p) {
+      const int it = i0 + k;
+      lo = lo_p;
+      hi = hi_p;
       const int g = pfx_find(s.gitem, p.n_groups, it), rows = s.cnt[g] * p.R;
       const int rel = it - s.gitem[g], blk = min(rel / p.Hkv, pfx_blocks(rows) - 1), i = rel - blk * p.Hkv;
       d.kind = pfx_kind(rows, blk, p.Hkv);
@@ -343,9 +362,11 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       d.blk = -1;
       d.row0 = blk * 2 * kM;
       d.nrows = min(2 * kM, rows - d.row0);
-      d.slot = it + (int)blockIdx.x;
+      d.slot = it + v_p;
     } else {
-      const int j = it - all_i, b = j / p.sitems, rel = j - b * p.sitems;
+      const int j = j0 + k - n_p, b = j / p.sitems, rel = j - b * p.sitems;
+      lo = lo_s;
+      hi = hi_s;
       const int blk = min(rel / p.Hkv, p.sblk - 1), i = rel - blk * p.Hkv;
       d.kind = pfx_kind(p.R, blk, p.Hkv);
       d.head = d.kind == kPair ? 2 * i : i;
@@ -361,16 +382,20 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       d.blk = p.n_kv > 0 ? nt - 1 : -1;
       d.row0 = blk * 2 * kM;
       d.nrows = min(2 * kM, p.R - d.row0);
-      d.slot = j + (int)blockIdx.x;
+      d.slot = j + v_s;
     }
     d.t0 = pfx_first_tile(base, ov, w, nt, lo);
     d.nt = pfx_first_tile(base, ov, w, nt, hi) - d.t0;
-    p.pieces[it + (int)blockIdx.x] = d;
-    if (k < kKept) sh.kept[k] = d;
+    if (k < kKept)
+      sh.kept[k] = d;
+    else
+      p.pieces[k < n_p ? piece0 + k : piece1 + (k - n_p)] = d;
   }
   if (tid == 0) {
-    sh.n_pieces = i1 - i0 + 1;
-    sh.piece0 = i0 + (int)blockIdx.x;
+    sh.n_pieces = n_p + n_s;
+    sh.n_shared = n_p;
+    sh.piece0 = piece0;
+    sh.piece1 = piece1;
   }
 }
 
@@ -438,7 +463,7 @@ struct PfxWalk {
   __device__ __forceinline__ void open(const PfxParams& P, const PfxShared& S) {
     p = nullptr;
     for (; k < S.n_pieces; ++k) {
-      const PfxPiece* d = k < pfx::kKept ? &S.kept[k] : P.pieces + S.piece0 + k;
+      const PfxPiece* d = S.piece(P.pieces, k);
       const int nt = d->nt;
       if (nt > 0) {
         kind = d->kind;
@@ -501,6 +526,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     sh.abort_flag = 0;
     fence_barrier_init();
   }
+  if (warp == kWarpK) {
+    const CUtensorMap* maps[5] = {&kmap, &vmap, &kbmap, &vbmap, &qmap};
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (lane == i) prefetch_tensor_map(maps[i]);
+  }
   if (warp == kWarpMma) tmem_alloc(&sh.tmem_base, kTmemCols);
   dependents_may_launch();
   pfx_plan(p, *reinterpret_cast<PfxPlan*>(pfx_smem), sh);
@@ -524,12 +555,16 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const uint64_t pol_once = l2_policy_evict_first();
     const int bpt = kTK >> p.br_shift;                // boxes of a context tile and d-half
     const int per = 32 / bpt;                         // tiles whose page numbers the warp holds at once
-    // first pool row of box `lane` of the tiles from t on; the lanes' entries fit the context
+    // page of box `lane` of the tiles from t on (the lanes' entries fit the context), asked
+    // for some tiles before it is looked at
     auto fetch = [&](const PfxPiece& d, int t) -> int {
-      const int key = t * kTK + lane * p.br, pos = d.key0 + key, lp = pos >> p.page_shift;
+      const int key = t * kTK + lane * p.br, lp = (d.key0 + key) >> p.page_shift;
       if (t + lane / bpt >= d.t0 + d.nt || key >= d.len || lp >= p.max_pages) return 0;
-      const int page = __ldg(p.page_table + (size_t)d.first * p.max_pages + lp);
-      const int in = pos & ((1 << p.page_shift) - 1);
+      return __ldg(p.page_table + (size_t)d.first * p.max_pages + lp);
+    };
+    // the box's first pool row
+    auto pool_row = [&](const PfxPiece& d, int t, int page) -> int {
+      const int in = (d.key0 + t * kTK + lane * p.br) & ((1 << p.page_shift) - 1);
       if (page >= 0 && page < p.num_pages) return (page << p.page_shift) + in;
       record_dev_error(p.err, kDevErrBadPage);        // page 0 is read instead, never out of bounds
       return in;
@@ -543,12 +578,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       PfxWalk nx = wk;
       nx.next_piece(p, sh);
       int ids_nx = nx.p ? fetch(*nx.p, nx.p->t0) : 0;
-      int ids_on = fetch(d, d.t0 + per);
+      int ids_on = fetch(d, d.t0 + per), rows = pool_row(d, d.t0, ids);
       const int two_heads = wk.kind == kPair ? 1 : 0, n_tiles = wk.tiles();
       for (int j = 0; j < n_tiles; ++j) {
         const int jt = j >> two_heads, t = d.t0 + jt, jj = jt % per;
         if (jt > 0 && jj == 0 && (j & two_heads) == 0) {
-          ids = ids_on;
+          rows = pool_row(d, t, ids_on);
           ids_on = fetch(d, t + per);
         }
         // boxes with a context key in use, then the block's rows
@@ -571,7 +606,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (leader) mbar_arrive_expect_tx(full, bytes);
         ++issued;
         for (int box = 0; box < nb; ++box, dst += p.br * 128) {
-          const int row = __shfl_sync(0xffffffffu, ids, jj * bpt + box);
+          const int row = __shfl_sync(0xffffffffu, rows, jj * bpt + box);
           if (leader) {
             if (once) {
               tma_load_3d_hint(dst, map, full, 0, head, row, pol_once);
@@ -716,7 +751,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       uint32_t ph_both = 0, ph_alone = 0, q_ph = 0;   // parities to wait for, a bit for each slot
       int u0 = 0, tile0 = 0, q0 = 0;       // units, tiles and Q tiles of the pieces before
       for (int k = 0; ok && k < sh.n_pieces; ++k) {
-        const PfxPiece* d = k < kKept ? &sh.kept[k] : p.pieces + sh.piece0 + k;
+        const PfxPiece* d = sh.piece(p.pieces, k);
         const int nt = d->nt;
         if (nt == 0) continue;
         const int kind = d->kind;
@@ -895,9 +930,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       if (!ok) break;
       // the piece's partials of this group
       const int rows = d.member0 < 0 ? p.Rs2 : kM;
-      const size_t at = ((size_t)d.slot * 2 + half) * rows + r;
-      float2* ml = (d.member0 < 0 ? p.ml_s : p.ml_p) + at;
-      float* po = (d.member0 < 0 ? p.po_s : p.po_p) + at * kD;
+      const size_t at = ((size_t)d.slot * 2 + half) * rows;
+      float2* ml = (d.member0 < 0 ? p.ml_s : p.ml_p) + at + r;
+      float* po = (d.member0 < 0 ? p.po_s : p.po_p) + at * kD + r * 8;
       const bool mine = row < d.nrows;
       if (mine) *ml = make_float2(m_run, l_run);
       if (w0 < wk.n) {
@@ -912,7 +947,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             if (mine) {
 #pragma unroll
               for (int i = 0; i < 32; i += 8)     // whole sectors
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + c + i), "r"(o[i]),
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(po + (c + i) * rows), "r"(o[i]),
                              "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
                              "r"(o[i + 7])
                              : "memory");
@@ -953,93 +988,96 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 // The parts of every row joined, in the order own part, prefix, each by range and group.
 // ---------------------------------------------------------------------------
 namespace pfx {
-constexpr int kJoinRows = 32, kJoinCols = 8, kJoinThreads = kJoinRows * (kD / kJoinCols);
-constexpr int kJoinLoads = 4;
+constexpr int kJoinRows = 16, kJoinCols = 8, kJoinThreads = kJoinRows * (kD / kJoinCols);
+// Partials whose loads a thread has in flight. Few rows: each round of loads is a microsecond of
+// the call, so all that a row may have at once; many: registers for more rows.
+constexpr int kJoinFew = 8, kJoinMany = 3;
+constexpr int kJoinManyRows = 16384;
 }
 
-__global__ void __launch_bounds__(pfx::kJoinThreads)
+template <int LOADS>
+__global__ void __launch_bounds__(pfx::kJoinThreads, LOADS == pfx::kJoinMany ? 4 : 1)
 prefix_join_kernel(const __grid_constant__ PfxParams p) {
   using namespace pfx;
   wait_for_prior_grid();
+  // a thread: eight columns of a row
+  const int rows_here = blockDim.x / (kD / kJoinCols), c8 = threadIdx.x / rows_here;
   const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
-  const int r = blockIdx.y * kJoinRows + threadIdx.x / (kD / kJoinCols), c0 = threadIdx.x % (kD / kJoinCols) * kJoinCols;
+  const int r = blockIdx.y * rows_here + (threadIdx.x - c8 * rows_here);
   if (r >= p.R) return;
   const PfxSeq s = p.seqs[b];
   // source 0: the own part, source 1: the prefix: partials, one a range that holds tiles of
   // the item, or two (of each group)
-  int n[2] = {0, 0};
-  bool two[2];
-  const float2* ml[2];
-  const float* po[2];
+  int n[2] = {0, 0}, step[2];                        // partials, and their distance in rows
+  size_t at[2];                                      // the first one's, and the row in it
+  int in_row[2];
   const int hs[2] = {p.Rs2, kM};                     // rows of a half of a slot
-  auto source = [&](int e, int rows, int row, int item0, int base, int ov, int nt, int w, int before) {
+  auto source = [&](int e, int rows, int row, int item0, int base, int ov, int nt, int w, int before, int share) {
     const int blk = row / (2 * kM), in = row - blk * 2 * kM, kind = pfx_kind(rows, blk, p.Hkv);
     base += before + ov;                             // where the first tile's cost begins
-    const int v0 = base / s.share, v1 = (base + (nt - 1) * w) / s.share;
-    n[e] = v1 - v0 + 1;
-    two[e] = kind == kOne;
+    const int v0 = base / share, v1 = (base + (nt - 1) * w) / share;
+    n[e] = kind == kOne ? 2 * (v1 - v0 + 1) : v1 - v0 + 1;
+    step[e] = kind == kOne ? hs[e] : 2 * hs[e];
     const int half = kind == kTwo ? in / kM : kind == kPair ? head & 1 : 0;
     const size_t slot = item0 + blk * p.Hkv + (kind == kPair ? head >> 1 : head) + v0;
-    const size_t at = (slot * 2 + half) * hs[e] + (kind == kTwo ? in % kM : in);
-    ml[e] = (e ? p.ml_p : p.ml_s) + at;
-    po[e] = (e ? p.po_p : p.po_s) + at * kD + c0;
+    at[e] = (slot * 2 + half) * hs[e];
+    in_row[e] = kind == kTwo ? in % kM : in;
   };
   if (s.nt > 0) {
     const int blk = r / (2 * kM), kind = pfx_kind(p.R, blk, p.Hkv);
     source(0, p.R, r, b * p.sitems, s.base, kItemCost, s.nt, pfx_weight<true>(kind),
-           pfx_cost_before<true>(p.R, s.nt, p.Hkv, blk, kind == kPair ? head >> 1 : head));
+           pfx_cost_before<true>(p.R, s.nt, p.Hkv, blk, kind == kPair ? head >> 1 : head), s.share_s);
   }
   if (s.g_tiles > 0) {
     const int row = s.pos * p.R + r, blk = row / (2 * kM), kind = pfx_kind(s.g_rows, blk, p.Hkv);
     source(1, s.g_rows, row, s.g_item, s.g_base, 0, s.g_tiles, pfx_weight<false>(kind),
-           pfx_cost_before<false>(s.g_rows, s.g_tiles, p.Hkv, blk, kind == kPair ? head >> 1 : head));
+           pfx_cost_before<false>(s.g_rows, s.g_tiles, p.Hkv, blk, kind == kPair ? head >> 1 : head), s.share_p);
   }
   float m = -CUDART_INF_F, l = 0.f, acc[kJoinCols];
 #pragma unroll
   for (int q = 0; q < kJoinCols; ++q) acc[q] = 0.f;
+  for (int i0 = 0; i0 < n[0] + n[1]; i0 += LOADS) {   // several partials' loads at once
+    float2 x[LOADS];
+    float4 y[LOADS][kJoinCols / 4];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int cnt = two[e] ? 2 * n[e] : n[e];
-    for (int i0 = 0; n[e] > 0 && i0 < cnt; i0 += kJoinLoads) {   // several partials' loads at once
-      float2 x[kJoinLoads];
-      float4 y[kJoinLoads][kJoinCols / 4];
+    for (int j = 0; j < LOADS; ++j) {
+      const int i = i0 + j;
+      x[j] = make_float2(-CUDART_INF_F, 0.f);
+      if (i >= n[0] + n[1]) continue;
+      const bool own = i < n[0];
+      const size_t part = own ? at[0] + (size_t)i * step[0] : at[1] + (size_t)(i - n[0]) * step[1];
+      const int row = own ? in_row[0] : in_row[1];
+      x[j] = (own ? p.ml_s : p.ml_p)[part + row];
+      const float* src = (own ? p.po_s : p.po_p) + part * kD + (c8 * (own ? hs[0] : hs[1]) + row) * 8;
 #pragma unroll
-      for (int j = 0; j < kJoinLoads; ++j) {
-        const int i = i0 + j;
-        x[j] = make_float2(-CUDART_INF_F, 0.f);
-        if (i >= cnt) continue;
-        const size_t at = two[e] ? (size_t)i * hs[e] : (size_t)i * 2 * hs[e];
-        x[j] = ml[e][at];
+      for (int q = 0; q < kJoinCols / 4; ++q) y[j][q] = reinterpret_cast<const float4*>(src)[q];
+    }
+    float mn = m;
 #pragma unroll
-        for (int q = 0; q < kJoinCols / 4; ++q) y[j][q] = reinterpret_cast<const float4*>(po[e] + at * kD)[q];
-      }
-      float mn = m;
+    for (int j = 0; j < LOADS; ++j) mn = fmaxf(mn, x[j].x);
+    if (mn == -CUDART_INF_F) continue;
+    const float f = exp2f(m - mn);                   // (0 before the first)
+    m = mn;
+    l *= f;
 #pragma unroll
-      for (int j = 0; j < kJoinLoads; ++j) mn = fmaxf(mn, x[j].x);
-      if (mn == -CUDART_INF_F) continue;
-      const float f = exp2f(m - mn);                 // (0 before the first)
-      m = mn;
-      l *= f;
+    for (int q = 0; q < kJoinCols; ++q) acc[q] *= f;
 #pragma unroll
-      for (int q = 0; q < kJoinCols; ++q) acc[q] *= f;
+    for (int j = 0; j < LOADS; ++j) {
+      if (x[j].x == -CUDART_INF_F) continue;         // no key for this row: its O may never have been written
+      const float w = exp2f(x[j].x - m);
+      l = fmaf(x[j].y, w, l);
 #pragma unroll
-      for (int j = 0; j < kJoinLoads; ++j) {
-        if (x[j].x == -CUDART_INF_F) continue;       // no key for this row: its O may never have been written
-        const float w = exp2f(x[j].x - m);
-        l = fmaf(x[j].y, w, l);
-#pragma unroll
-        for (int q = 0; q < kJoinCols / 4; ++q) {
-          acc[4 * q] = fmaf(y[j][q].x, w, acc[4 * q]);
-          acc[4 * q + 1] = fmaf(y[j][q].y, w, acc[4 * q + 1]);
-          acc[4 * q + 2] = fmaf(y[j][q].z, w, acc[4 * q + 2]);
-          acc[4 * q + 3] = fmaf(y[j][q].w, w, acc[4 * q + 3]);
-        }
+      for (int q = 0; q < kJoinCols / 4; ++q) {
+        acc[4 * q] = fmaf(y[j][q].x, w, acc[4 * q]);
+        acc[4 * q + 1] = fmaf(y[j][q].y, w, acc[4 * q + 1]);
+        acc[4 * q + 2] = fmaf(y[j][q].z, w, acc[4 * q + 2]);
+        acc[4 * q + 3] = fmaf(y[j][q].w, w, acc[4 * q + 3]);
       }
     }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no key at all: 0 (and NaN stays NaN)
   const int i = r / p.G, hh = r - i * p.G;
-  bf16* dst = p.out + ((size_t)(b * p.n_q + i) * p.Hq + head * p.G + hh) * kD + c0;
+  bf16* dst = p.out + ((size_t)(b * p.n_q + i) * p.Hq + head * p.G + hh) * kD + c8 * 8;
   *reinterpret_cast<uint4*>(dst) = make_uint4(pfx_pack(acc[0] * inv, acc[1] * inv), pfx_pack(acc[2] * inv, acc[3] * inv),
                                               pfx_pack(acc[4] * inv, acc[5] * inv), pfx_pack(acc[6] * inv, acc[7] * inv));
 }
@@ -1077,7 +1115,7 @@ static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
     at += align_up(bytes);
     return o;
   };
-  l.pieces = take((ip + is + kGrid) * sizeof(PfxPiece));
+  l.pieces = take((ip + is + 2 * kGrid) * sizeof(PfxPiece));
   l.order = take(B * sizeof(uint16_t));
   l.seqs = take(B * sizeof(PfxSeq));
   l.po_p = take(sp * 2 * kM * kD * sizeof(float));
@@ -1161,8 +1199,11 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches = 2;
-  const dim3 grid(a.B * a.Hkv, (p.R + kJoinRows - 1) / kJoinRows);
-  return launch_dependent(prefix_join_kernel, grid, dim3(kJoinThreads), 0, a.stream, p);
+  int rows = 1;
+  while (rows < std::min(p.R, kJoinRows)) rows *= 2;
+  const dim3 grid(a.B * a.Hkv, (p.R + rows - 1) / rows);
+  return launch_dependent((size_t)a.B * a.Hkv * p.R < kJoinManyRows ? prefix_join_kernel<kJoinFew> : prefix_join_kernel<kJoinMany>,
+                          grid, dim3(rows * (kD / kJoinCols)), 0, a.stream, p);
 }
 
 }  // namespace dflash
