@@ -690,7 +690,13 @@ def _pools(pools: Sequence[torch.Tensor], dev: int, num_pages: int, page_size: i
     first = pools[0]
     if not isinstance(first, torch.Tensor) or first.dim() < 2 or tuple(first.shape[:2]) != (num_pages, page_size):
         raise ValueError(f"pools must be tensors [{num_pages}, {page_size}, ...]")
-    ptrs = (c_p * len(pools))(*[_arg(t, f"pools[{i}]", dev, first.dtype, first.shape) for i, t in enumerate(pools)])
+    shape, dt = first.shape, first.dtype
+    at = [t.data_ptr() for t in pools if isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape
+          and t.get_device() == dev and t.is_contiguous()]
+    if len(at) != len(pools):
+        for i, t in enumerate(pools):
+            _arg(t, f"pools[{i}]", dev, dt, shape)
+    ptrs = (c_p * len(at))(*at)
     return len(pools), first.stride(1) * first.element_size(), ctypes.cast(ptrs, c_p)
 
 

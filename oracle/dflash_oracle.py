@@ -814,13 +814,13 @@ def pages_compact(page_table, n_pages, shares, pools=()):
 # ---------------------------------------------------------------------------
 # root-mean-square norm
 # ---------------------------------------------------------------------------
-def rms_norm(x, weight, eps, residual=None):
+def residual_norm(x, weight, eps, residual=None):
     """(s, y, scale): s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight and the
     e4m3 scale of every 128 values of y."""
     s = np.asarray(x, dtype=np.float64)
     if residual is not None:
         s = s + np.asarray(residual, dtype=np.float64)
     d = s.shape[1]
-    y = s / np.sqrt((s * s).mean(1, keepdims=True) + eps) * np.asarray(weight, dtype=np.float64)
+    y = rms_norm(s, weight, eps)
     scale = np.stack([np.abs(y[:, j:j + 128]).max(1) for j in range(0, d, 128)], 1) / 448.0
     return s, y, np.maximum(scale, 2.0 ** -126)

@@ -35,7 +35,7 @@ def _tol(d):
 
 
 def _check(o, x, w, eps, residual, dtype):
-    s, y, scale = O.rms_norm(_f64(x), _f64(w), eps, None if residual is None else _f64(residual))
+    s, y, scale = O.residual_norm(_f64(x), _f64(w), eps, None if residual is None else _f64(residual))
     half = 2.0 ** -8 if dtype == torch.bfloat16 else U
     t = _tol(s.shape[1])
     if residual is not None:
@@ -121,7 +121,7 @@ def test_rows_whose_squares_leave_the_range(d, eps):
     w = _rows(1, d, torch.float32, 30)[0].contiguous()
     o = api.rms_norm(x, w, eps, fp8=True, want_y=True)
     eps32 = float(np.float32(eps))
-    _, y, _ = O.rms_norm(_f64(x), _f64(w), eps32)
+    _, y, _ = O.residual_norm(_f64(x), _f64(w), eps32)
     live = np.abs(y) > 1e-37                       # below it the result itself is subnormal
     assert np.all(np.abs(_f64(o["y"]) - y)[live] <= np.abs(y)[live] * _tol(d) * 1.5)
 

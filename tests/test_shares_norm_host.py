@@ -160,7 +160,7 @@ def test_oracle_fork_release_compact_by_hand():
 
 
 def test_oracle_norm_closed_forms():
-    s, y, scale = O.rms_norm(np.full((1, 256), 3.0), np.full(256, 2.0), 0.0)
+    s, y, scale = O.residual_norm(np.full((1, 256), 3.0), np.full(256, 2.0), 0.0)
     assert np.allclose(y, 2.0) and np.allclose(scale, 2 / 448)
-    s, y, _ = O.rms_norm(np.eye(4), np.ones(4), 0.0, residual=-np.eye(4) + 1)
+    s, y, _ = O.residual_norm(np.eye(4), np.ones(4), 0.0, residual=-np.eye(4) + 1)
     assert np.allclose(s, 1) and np.allclose(y, 1)
