@@ -26,6 +26,7 @@ constexpr int kTK = 64;                     // keys of a tile
 constexpr int kM = 128;                     // packed query rows of a Q tile (TMEM lanes)
 constexpr int kGrid = 152;                  // persistent CTAs: one per SM
 constexpr int kMaxSeqs = 1024;
+constexpr int kWarpLists = 128;             // up to so many sequences one warp makes the lists
 constexpr int kSlots = 5;                   // ring of tiles, K and V
 constexpr int kTileBytes = kTK * kD * 2;    // a K or V tile: two d-halves of 64 rows x 128 bytes
 constexpr int kHalf = kTileBytes / 2;
@@ -134,15 +135,24 @@ __device__ __forceinline__ int pfx_cost_before(int rows, int nt, int Hkv, int k,
   return full * Hkv * (two * nt + ov) + i * (pfx_weight<OWN>(pfx_kind(rows, min(k, n - 1), Hkv)) * nt + ov);
 }
 
-// Exclusive prefixes of K values per thread over the CTA's first nw warps (the others have
-// none), and their totals.
-template <int K>
+// Barrier of the NT threads that make the lists: a warp, or the CTA.
+template <int NT>
+__device__ __forceinline__ void pfx_sync() {
+  if constexpr (NT == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+// Exclusive prefixes of K values per thread over the NT threads, and their totals. Of a CTA
+// the first nw warps have values.
+template <int NT, int K>
 __device__ __forceinline__ void pfx_scan(int (&x)[K], int nw, int* s_w, int (&total)[K]) {
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   int in[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) in[k] = x[k];
-  if (w < nw) {
+  if (NT == 32 || w < nw) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
@@ -150,20 +160,25 @@ __device__ __forceinline__ void pfx_scan(int (&x)[K], int nw, int* s_w, int (&to
         const int y = __shfl_up_sync(0xffffffffu, in[k], o);
         if (l >= o) in[k] += y;
       }
-    if (l == 31)
+  }
+  if constexpr (NT == 32) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) total[k] = __shfl_sync(0xffffffffu, in[k], 31);
+  } else {
+    if (w < nw && l == 31)
 #pragma unroll
       for (int k = 0; k < K; ++k) s_w[k * pfx::kWarps + w] = in[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) total[k] = 0;
+    for (int i = 0; i < nw; ++i)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int v = s_w[k * pfx::kWarps + i];
+        in[k] += i < w ? v : 0;
+        total[k] += v;
+      }
   }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) total[k] = 0;
-  for (int i = 0; i < nw; ++i)
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = s_w[k * pfx::kWarps + i];
-      in[k] += i < w ? v : 0;
-      total[k] += v;
-    }
 #pragma unroll
   for (int k = 0; k < K; ++k) x[k] = in[k] - x[k];
 }
@@ -190,6 +205,7 @@ struct PfxShared {
   uint64_t s_full[2], s_read[2], p_full[2], pv_done[2], o_empty[2], mma_done;
   uint32_t tmem_base;
   int abort_flag;
+  int prefix_items, prefix_cost, own_cost;   // of the lists
   int n_pieces, n_shared;          // this CTA's pieces: so many, those of prefixes first
   int piece0, piece1;              // where those and those of own parts begin in the list
   int scan[4 * pfx::kWarps];       // of the plan: three sums over the groups, one over the sequences
@@ -219,19 +235,22 @@ __device__ __forceinline__ int pfx_own_tiles(const PfxParams& p, int ctx, int pr
   return nct + (boxes * p.br + p.n_kv > pfx::kTK);
 }
 
-__device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShared& sh) {
+// The lists' bases, made by the CTA's first NT threads.
+template <int NT>
+__device__ __forceinline__ void pfx_lists(const PfxParams& p, PfxPlan& s, PfxShared& sh) {
   using namespace pfx;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int per_g = (p.n_groups + kThreads - 1) / kThreads, per_b = (p.B + kThreads - 1) / kThreads;
+  const int tid = threadIdx.x;
+  const int per_g = (p.n_groups + NT - 1) / NT, per_b = (p.B + NT - 1) / NT;
   const int g0 = min(p.n_groups, tid * per_g), g1 = min(p.n_groups, g0 + per_g);
   const int b0 = min(p.B, tid * per_b), b1 = min(p.B, b0 + per_b);
-  for (int g = tid; g < p.n_groups; g += kThreads) {
+  for (int g = tid; g < p.n_groups; g += NT) {
     s.cnt[g] = 0;
-    s.minc[g] = s.first[g] = INT_MAX;
+    s.first[g] = INT_MAX;
+    s.minc[g] = max(0, p.prefix_len[g]);
     s.fill[g] = 0;
   }
-  __syncthreads();
-  for (int b = tid; b < p.B; b += kThreads) {
+  pfx_sync<NT>();
+  for (int b = tid; b < p.B; b += NT) {
     const int raw = p.ctx_len[b], C = max(0, min(raw, p.max_ctx)), g = p.group[b];
     const bool in = g >= 0 && g < p.n_groups;
     s.ctx[b] = C;
@@ -246,12 +265,11 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     if (blockIdx.x == 0 && raw != C) record_dev_error(p.err, kDevErrBadCtxLen);
 #endif
   }
-  __syncthreads();
+  pfx_sync<NT>();
   // groups: the tiles shared (none for a lone sequence), where their sequences, items and costs begin
   int at_g[3] = {0, 0, 0}, all_g[3];
   for (int g = g0; g < g1; ++g) {
-    const int P = max(0, min(p.prefix_len[g], s.minc[g]));
-    const int t = s.cnt[g] >= 2 ? P / kTK : 0;
+    const int t = s.cnt[g] >= 2 ? s.minc[g] / kTK : 0;
     s.tiles[g] = t;
     if (t) {
       at_g[0] += s.cnt[g];
@@ -260,7 +278,7 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     }
   }
   const int nw_g = (p.n_groups + per_g * 32 - 1) / max(1, per_g * 32), nw_b = (p.B + per_b * 32 - 1) / (per_b * 32);
-  pfx_scan(at_g, nw_g, sh.scan, all_g);
+  pfx_scan<NT>(at_g, nw_g, sh.scan, all_g);
   for (int g = g0; g < g1; ++g) {
     s.gstart[g] = at_g[0];
     s.gitem[g] = at_g[1];
@@ -271,8 +289,7 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
       at_g[2] += pfx_cost_before<false>(s.cnt[g] * p.R, s.tiles[g], p.Hkv, pfx_blocks(s.cnt[g] * p.R), 0);
     }
   }
-  const int all_i = all_g[1], all_c = all_g[2];
-  __syncthreads();
+  pfx_sync<NT>();
   // own parts
   int at_s[1] = {0}, all_s[1];
   auto own_cost = [&](int b) {
@@ -280,16 +297,31 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     return nt ? pfx_cost_before<true>(p.R, nt, p.Hkv, p.sblk, 0) : 0;
   };
   for (int b = b0; b < b1; ++b) at_s[0] += own_cost(b);
-  pfx_scan(at_s, nw_b, sh.scan + 3 * kWarps, all_s);
+  pfx_scan<NT>(at_s, nw_b, sh.scan + 3 * kWarps, all_s);
   for (int b = b0; b < b1; ++b) {
     s.sbase[b] = at_s[0];
     at_s[0] += own_cost(b);
   }
+  if (tid == 0) {
+    sh.prefix_items = all_g[1];
+    sh.prefix_cost = all_g[2];
+    sh.own_cost = all_s[0];
+  }
+}
+
+__device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShared& sh) {
+  using namespace pfx;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (p.B > kWarpLists)
+    pfx_lists<kThreads>(p, s, sh);
+  else if (tid < 32)
+    pfx_lists<32>(p, s, sh);
   __syncthreads();
+  const int all_i = sh.prefix_items;
   // Ranges: of a small batch each list's CTAs are its own (attn of 8 x 16 rows on 1,024 keys
   // KAPART); else each CTA has its part of both, so that the balance does not hang
   // on how tensor-bound and load-bound tiles compare (64 x 16 rows on 8,192 KMIX).
-  const int N_p = all_c, N_s = all_s[0];
+  const int N_p = sh.prefix_cost, N_s = sh.own_cost;
   const int joint = max(kMinShare, (N_p + N_s + kGrid - 1) / kGrid);
   const int share_p = joint <= kApart ? joint : max(kMinShare, (N_p + kGrid - 1) / kGrid);
   const int share_s = joint <= kApart ? joint : max(kMinShare, (N_s + kGrid - 1) / kGrid);
@@ -1002,8 +1034,9 @@ prefix_join_kernel(const __grid_constant__ PfxParams p) {
   wait_for_prior_grid();
   // a thread: eight columns of a row
   const int rows_here = blockDim.x / (kD / kJoinCols), c8 = threadIdx.x / rows_here;
-  const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
-  const int r = blockIdx.y * rows_here + (threadIdx.x - c8 * rows_here);
+  const int blocks = (p.R + rows_here - 1) / rows_here, bh = blockIdx.x / blocks;
+  const int b = bh / p.Hkv, head = bh - b * p.Hkv;
+  const int r = (blockIdx.x - bh * blocks) * rows_here + (threadIdx.x - c8 * rows_here);
   if (r >= p.R) return;
   const PfxSeq s = p.seqs[b];
   // source 0: the own part, source 1: the prefix: partials, one a range that holds tiles of
@@ -1126,10 +1159,17 @@ static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
   return l;
 }
 
+// Whether a call's sizes are the shared kernel's: many query rows a sequence would want
+// partials that no one has the memory for.
+static bool pfx_takes(int B, int n_groups, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size, int dtype) {
+  return pfx_dims_ok(B, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype) &&
+         pfx_layout(B, n_groups, n_q, Hq, Hkv).end <= (size_t)4 << 30;
+}
+
 size_t prefix_attn_ws_bytes(int B, int n_groups, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size,
                             int dtype) {
   const size_t plain = attn_ws_bytes(B, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype);   // pointers off a vector
-  if (!pfx_dims_ok(B, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype)) return plain;
+  if (!pfx_takes(B, n_groups, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype)) return plain;
   return std::max(plain, pfx_layout(B, n_groups, n_q, Hq, Hkv).end);
 }
 
@@ -1137,8 +1177,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   using namespace pfx;
   const AttnArgs& a = pa.attn;
   auto al = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
-  if (!pfx_dims_ok(a.B, a.n_q, a.n_kv, a.Hq, a.Hkv, a.D, a.max_ctx, a.page_size, a.dtype) || !al(a.q) || !al(a.k_blk) ||
-      !al(a.v_blk) || !al(a.k_pool) || !al(a.v_pool) || !al(a.out) || !(a.scale > 0.f && a.scale < 3.0e38f) ||
+  if (!pfx_takes(a.B, pa.n_groups, a.n_q, a.n_kv, a.Hq, a.Hkv, a.D, a.max_ctx, a.page_size, a.dtype) || !al(a.q) ||
+      !al(a.k_blk) || !al(a.v_blk) || !al(a.k_pool) || !al(a.v_pool) || !al(a.out) || !(a.scale > 0.f && a.scale < 3.0e38f) ||
       (long)a.num_pages * a.page_size >= 1L << 31)
     return launch_block_attn(a, launches);
   PfxParams p{};
@@ -1201,9 +1241,9 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   *launches = 2;
   int rows = 1;
   while (rows < std::min(p.R, kJoinRows)) rows *= 2;
-  const dim3 grid(a.B * a.Hkv, (p.R + rows - 1) / rows);
-  return launch_dependent((size_t)a.B * a.Hkv * p.R < kJoinManyRows ? prefix_join_kernel<kJoinFew> : prefix_join_kernel<kJoinMany>,
-                          grid, dim3(rows * (kD / kJoinCols)), 0, a.stream, p);
+  const dim3 grid((unsigned)(a.B * a.Hkv * ((p.R + rows - 1) / rows))), block(rows * (kD / kJoinCols));
+  const bool few = (size_t)a.B * a.Hkv * p.R < kJoinManyRows;
+  return launch_dependent(few ? prefix_join_kernel<kJoinFew> : prefix_join_kernel<kJoinMany>, grid, block, 0, a.stream, p);
 }
 
 }  // namespace dflash
