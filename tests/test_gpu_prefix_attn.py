@@ -183,6 +183,23 @@ def test_long_context_of_one_sequence():
     Case([9000, 100, 128, 140], [0] * 4, [100], n_q=16, Hq=32, Hkv=8, seed=10).check()
 
 
+@pytest.mark.parametrize("Hkv", [1, 2, 3, 8])
+@pytest.mark.parametrize("own", [0, 300])
+def test_groups_of_all_sizes(Hkv, own):
+    # groups of 2 to 41 sequences of 16 packed rows: Q tiles alone, two on the same keys, of two
+    # heads, several of each to a CTA, prefixes of an odd number of tiles and of one
+    g = np.random.default_rng(Hkv)
+    sizes, prefix = [2, 3, 8, 9, 16, 17, 41, 2, 3], [1000, 64, 3000, 64, 1500, 832, 3500, 2200, 130]
+    group = [i for i, n in enumerate(sizes) for _ in range(n)]
+    g.shuffle(group)
+    ctx = [prefix[i] + (int(g.integers(0, own)) if own else 0) for i in group]
+    Case(ctx, group, prefix, n_q=4, Hq=4 * Hkv, Hkv=Hkv, seed=Hkv).check()
+
+
+def test_many_query_rows():
+    Case([700, 650, 3], [0, 0, 1], [640, 0], n_q=260, n_kv=60, Hq=8, Hkv=2, seed=20).check()
+
+
 def test_a_thousand_sequences():
     g = np.random.default_rng(4)
     n = [int(x) for x in g.integers(0, 40, 1024)]
