@@ -9,8 +9,20 @@
 //   out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
 // The parts here are the group's prefix (whole tiles of 64 positions), worked on with
 // the queries of all its sequences, and what each sequence has of its own: the rest
-// of its context and the block's rows. Both are pieces of one work list (below); every
+// of its context and the block's rows. Both are pieces of two work lists (below); every
 // piece leaves fp32 partials, which a second kernel joins in a fixed order.
+//
+// Bound. A long prefix under many rows: the tensor cores. 64 keys of two Q tiles take 1280
+// cycles of MMAs (S with both operands in shared memory, 48 cycles a step of N = 64, is
+// held by that memory, not by the pipe) and measure some 1750, the softmax between them:
+// 64 x 16 rows of 32 heads on a prefix of 8,192 150 us (137 GFLOP of the prefix: 73 us
+// at the rate of a large product), of which the plan is 5 and the join 16. Own parts: HBM;
+// pages of 16 positions bring 256 bytes in a row for a head, which loads of any kind
+// read at 4.7 TB/s here, this kernel at 4.1 and more. A small batch: the chain of launch,
+// plan, first page, first tile and join, 18 us for 4 rows of a token each.
+//
+// Roundings: P meets V in bf16 (as the matrix instructions take it) under a maximum that lags
+// by at most 2^8; scores, maxima, sums, O and all partials are fp32; out is rounded once.
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,7 +38,7 @@ constexpr int kTK = 64;                     // keys of a tile
 constexpr int kM = 128;                     // packed query rows of a Q tile (TMEM lanes)
 constexpr int kGrid = 152;                  // persistent CTAs: one per SM
 constexpr int kMaxSeqs = 1024;
-constexpr int kWarpLists = 128;             // up to so many sequences one warp makes the lists
+constexpr int kWarpLists = 128;             // up to so many sequences one warp makes the lists (of 4: 0.6 us less)
 constexpr int kSlots = 5;                   // ring of tiles, K and V
 constexpr int kTileBytes = kTK * kD * 2;    // a K or V tile: two d-halves of 64 rows x 128 bytes
 constexpr int kHalf = kTileBytes / 2;
@@ -38,7 +50,9 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kKept = 36;                   // piece descriptors kept in shared memory
 // What an item is: one Q tile and kv head, two Q tiles (more than 128 rows) that share the
-// K/V tiles, or the Q tiles of two kv heads with K/V tiles of their own.
+// K/V tiles, or the Q tiles of two kv heads with K/V tiles of their own. A Q tile alone keeps
+// one softmax group busy with every other K/V tile, and leaves two partials: 32 x 8 rows
+// under seven prefixes 57 us with single heads, 54 with pairs.
 enum Kind { kOne = 0, kTwo = 1, kPair = 2 };
 // Costs of the work list, in quarters of a microsecond: 64 keys of an item, of a prefix or of
 // an own part (whose K/V come from HBM), and an own part's start and end.
@@ -345,14 +359,14 @@ __device__ __forceinline__ void pfx_plan(const PfxParams& p, PfxPlan& s, PfxShar
     if (blockIdx.x == 0) {
       for (int b = lane; b < p.B; b += 32) {
         const int g = s.grp[b], t = g >= 0 ? s.tiles[g] : 0;
-        p.seqs[b] = PfxSeq{share_p, share_s, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t), t ? s.pos[b] : 0, t ? s.gbase[g] : 0,
-                           t ? s.gitem[g] : 0, t, t ? s.cnt[g] * p.R : 0};
+        p.seqs[b] = PfxSeq{share_p, share_s, s.sbase[b], pfx_own_tiles(p, s.ctx[b], t), t ? s.pos[b] : 0,
+                           t ? s.gbase[g] : 0, t ? s.gitem[g] : 0, t, t ? s.cnt[g] * p.R : 0};
       }
     }
     return;
   }
   const int v_p = blockIdx.x, used = (N_p + share_p - 1) / share_p;   // this CTA's range of prefixes
-  const int v_s = (v_p - used % kGrid + kGrid) % kGrid;               // and of own parts, the first behind the prefixes' last
+  const int v_s = (v_p - used % kGrid + kGrid) % kGrid;               // and of own parts, behind them
   const int lo_p = min((long)N_p, (long)v_p * share_p), hi_p = min((long)N_p, (long)lo_p + share_p);
   const int lo_s = min((long)N_s, (long)v_s * share_s), hi_s = min((long)N_s, (long)lo_s + share_s);
   // the item that position x of a list lies in; its ends in four lanes at once
@@ -576,7 +590,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   PfxWalk wk;
   int q_boxes = 0;                 // one past the last Q tile that came as boxes
   int issued = 0;                  // tiles that this warp has asked for
-  uint32_t last = 0, phases = 0;   // by which of a slot's barriers its last tile goes, and which of them have had an odd number
+  // by which of a slot's barriers its last tile goes, and which of them have had an odd number
+  uint32_t last = 0, phases = 0;
 
   if (warp == kWarpK || warp == kWarpV) {
     // ------------------------------ K loads, V loads ------------------------------
@@ -823,7 +838,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           for (int i = 0; i < mine; ++i, ++units) {
             // (the group's first unit of a piece: its O has been read out)
             if (i == 0 && !wait(&sh.o_empty[x], (pieces++ & 1) ^ 1, 46)) { ok = false; break; }
-            if (!wait(&sh.v_full[by][slot], ph >> slot & 1u, 47) || !wait(&sh.p_full[x], units & 1, 48)) { ok = false; break; }
+            if (!wait(&sh.v_full[by][slot], ph >> slot & 1u, 47)) { ok = false; break; }
+            if (!wait(&sh.p_full[x], units & 1, 48)) { ok = false; break; }
             ph ^= 1u << slot;
             tc_fence_after();
             const uint64_t vd = v_desc + (uint64_t)(slot * (kTileBytes / 16));
@@ -851,7 +867,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // ------------------------------ softmax ------------------------------
     const int x = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;   // a thread: one row, TMEM lane r
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_t = tmem + lane_off + kSCol + (uint32_t)(x * kTK), o_t = tmem + lane_off + kOCol + (uint32_t)(x * kD);
+    const uint32_t s_t = tmem + lane_off + kSCol + (uint32_t)(x * kTK);
+    const uint32_t o_t = tmem + lane_off + kOCol + (uint32_t)(x * kD);
     const uint32_t p_t = tmem + lane_off + kPCol + (uint32_t)(x * kTK / 2);
     auto wait = [&](uint64_t* bar, uint32_t par, int code) {
       return pfx_wait(bar, par, abort_flag, p.err, code, p.wait_ns);
@@ -1023,7 +1040,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 namespace pfx {
 constexpr int kJoinRows = 16, kJoinCols = 8, kJoinThreads = kJoinRows * (kD / kJoinCols);
 // Partials whose loads a thread has in flight. Few rows: each round of loads is a microsecond of
-// the call, so all that a row may have at once; many: registers for more rows.
+// the call (8 x 16 rows 22.8 us, three at a time 25.0); many: registers for more rows (64 x 16
+// rows 148, eight at a time 154).
 constexpr int kJoinFew = 8, kJoinMany = 3;
 constexpr int kJoinManyRows = 16384;
 }
@@ -1162,7 +1180,8 @@ static PfxLayout pfx_layout(int B, int n_groups, int n_q, int Hq, int Hkv) {
 
 // Whether a call's sizes are the shared kernel's: many query rows a sequence would want
 // partials that no one has the memory for.
-static bool pfx_takes(int B, int n_groups, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size, int dtype) {
+static bool pfx_takes(int B, int n_groups, int n_q, int n_kv, int Hq, int Hkv, int D, int max_ctx, int page_size,
+                      int dtype) {
   return pfx_dims_ok(B, n_q, n_kv, Hq, Hkv, D, max_ctx, page_size, dtype) &&
          pfx_layout(B, n_groups, n_q, Hq, Hkv).end <= (size_t)4 << 30;
 }
@@ -1179,8 +1198,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   const AttnArgs& a = pa.attn;
   auto al = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
   if (!pfx_takes(a.B, pa.n_groups, a.n_q, a.n_kv, a.Hq, a.Hkv, a.D, a.max_ctx, a.page_size, a.dtype) || !al(a.q) ||
-      !al(a.k_blk) || !al(a.v_blk) || !al(a.k_pool) || !al(a.v_pool) || !al(a.out) || !(a.scale > 0.f && a.scale < 3.0e38f) ||
-      (long)a.num_pages * a.page_size >= 1L << 31)
+      !al(a.k_blk) || !al(a.v_blk) || !al(a.k_pool) || !al(a.v_pool) || !al(a.out) ||
+      !(a.scale > 0.f && a.scale < 3.0e38f) || (long)a.num_pages * a.page_size >= 1L << 31)
     return launch_block_attn(a, launches);
   PfxParams p{};
   const PfxLayout l = pfx_layout(a.B, pa.n_groups, a.n_q, a.Hq, a.Hkv);
@@ -1244,7 +1263,8 @@ cudaError_t launch_prefix_attn(const PrefixArgs& pa, int* launches) {
   while (rows < std::min(p.R, kJoinRows)) rows *= 2;
   const dim3 grid((unsigned)(a.B * a.Hkv * ((p.R + rows - 1) / rows))), block(rows * (kD / kJoinCols));
   const bool few = (size_t)a.B * a.Hkv * p.R < kJoinManyRows;
-  return launch_dependent(few ? prefix_join_kernel<kJoinFew> : prefix_join_kernel<kJoinMany>, grid, block, 0, a.stream, p);
+  return launch_dependent(few ? prefix_join_kernel<kJoinFew> : prefix_join_kernel<kJoinMany>, grid, block, 0, a.stream,
+                          p);
 }
 
 }  // namespace dflash

@@ -104,8 +104,9 @@ enum { DFLASH_FLAG_GATE_BOUNDARY = 1 };
  *                            invalid and completion counters of the workspace
  *                            may be left part-counted, so zero the whole counter
  *                            region (DFLASH_WS_COUNTER_BYTES) before the next call.
- *   DFLASH_DEVERR_BAD_PAGE   dflash_block_attn met a page-table entry outside
- *                            [0, num_pages) for a position inside a context; it
+ *   DFLASH_DEVERR_BAD_PAGE   dflash_block_attn or dflash_prefix_attn met a page-table
+ *                            entry outside [0, num_pages) for a position inside a
+ *                            context; it
  *                            read page 0 for that position (never out of bounds),
  *                            so that call's output is invalid. Counters stay
  *                            consistent; clear the word to reuse the workspace.
@@ -115,8 +116,8 @@ enum { DFLASH_FLAG_GATE_BOUNDARY = 1 };
  *                            outputs are those of the clamped count.
  * Only in a library built with DFLASH_DEBUG defined (the Python build's
  * debug library); release builds clamp these inputs without a record:
- *   DFLASH_DEVERR_BAD_CTX_LEN    dflash_block_attn met a ctx_len[b] outside
- *                            [0, max_ctx] (clamped to that range).
+ *   DFLASH_DEVERR_BAD_CTX_LEN    dflash_block_attn or dflash_prefix_attn met a
+ *                            ctx_len[b] outside [0, max_ctx] (clamped to that range).
  *   DFLASH_DEVERR_BAD_COMMIT_LEN dflash_materialize_ctx_kv met a commit_len[b]
  *                            outside [0, rows_max] (clamped to that range).
  *   DFLASH_DEVERR_BAD_POSITION   dflash_materialize_ctx_kv met a committed row
@@ -124,7 +125,8 @@ enum { DFLASH_FLAG_GATE_BOUNDARY = 1 };
  *                            position, a page past max_pages, or a page-table
  *                            entry outside [0, num_pages)); the row is not
  *                            written.
- * Calls that can set it: dflash_block_attn, dflash_materialize_ctx_kv, the
+ * Calls that can set it: dflash_block_attn, dflash_prefix_attn,
+ * dflash_materialize_ctx_kv, the
  * verify calls (greedy, sampled, sampled with LSEs) and
  * dflash_draft_select. The gate and DDTree kernels never set it.
  */
@@ -272,8 +274,9 @@ int dflash_block_attn_active(const dflash_attn_dims* dims,
  *   ctx_len of the group counts (negative: 0).
  * Every other argument as dflash_block_attn, whose checks and error words apply.
  * n_groups in [0, B]. The shared kernel takes bf16, D = 128, pages of 8, 16, 32, 64
- * or 128 positions, B <= 1024, n_kv_blk <= 64 and pointers aligned to 16 bytes;
- * for other calls the prefix is read once a sequence, as by dflash_block_attn.
+ * or 128 positions, B <= 1024, n_kv_blk <= 64, scale > 0, a workspace of up to 4 GiB
+ * and pointers aligned to 16 bytes; for other calls the prefix is read once a
+ * sequence, as by dflash_block_attn.
  * Repeated calls on the same inputs return identical bits.
  */
 size_t dflash_prefix_attn_workspace_size(const dflash_attn_dims* dims, int32_t n_groups);
@@ -853,7 +856,7 @@ int dflash_pages_compact(const dflash_pages_dims* dims, const int32_t* page_tabl
 /* ------------------------------------------------------------------------- */
 /*
  * Limit, in nanoseconds, of every bounded wait of the tensor-core kernels
- * (dflash_block_attn for bf16, dflash_materialize_ctx_kv for bf16) on the
+ * (dflash_block_attn, dflash_prefix_attn and dflash_materialize_ctx_kv for bf16) on the
  * barriers between their roles (copy landed, MMA done, buffer free). A wait
  * that runs out sets the error word (see DFLASH_WS_ERROR_WORD_OFFSET) and the
  * kernel returns early after draining its own copies and MMAs under a fixed
