@@ -695,6 +695,8 @@ def _pools(pools: Sequence[torch.Tensor], dev: int, num_pages: int, page_size: i
           and t.get_device() == dev and t.is_contiguous()]
     if len(at) != len(pools):
         for i, t in enumerate(pools):
+            if t is None:
+                raise ValueError(f"pools[{i}] is None")
             _arg(t, f"pools[{i}]", dev, dt, shape)
     ptrs = (c_p * len(at))(*at)
     return len(pools), first.stride(1) * first.element_size(), ctypes.cast(ptrs, c_p)

@@ -144,6 +144,17 @@ def test_prefix_attention_refusals(L):
     assert L.dflash_prefix_attn_workspace_size(ctypes.byref(d), 5) == 0
 
 
+def test_a_pool_that_is_missing_or_unlike_the_first_is_refused():
+    import torch
+
+    good = torch.zeros((4, 2, 8))
+    for bad in (None, torch.zeros((4, 2, 9)), torch.zeros((4, 2, 8), dtype=torch.bfloat16),
+                torch.zeros((4, 2, 16))[:, :, ::2], 7):
+        for pools in ([good, bad], [bad, good]):
+            with pytest.raises((ValueError, TypeError)):
+                api._pools(pools, good.get_device(), 4, 2)
+
+
 def test_oracle_fork_release_compact_by_hand():
     table = np.array([[4, 2, 7], [-1, -1, -1], [-1, -1, -1]])
     pool = np.arange(8 * 4, dtype=np.float64).reshape(8, 4, 1)
