@@ -217,9 +217,6 @@ __device__ __forceinline__ uint32_t ctarank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
   float4 v;
   asm volatile(
