@@ -15,7 +15,7 @@
 // Bound. A long prefix under many rows: the tensor cores. 64 keys of two Q tiles take 1280
 // cycles of MMAs (S with both operands in shared memory, 48 cycles a step of N = 64, is
 // held by that memory, not by the pipe) and measure some 1750, the softmax between them:
-// 64 x 16 rows of 32 heads on a prefix of 8,192 150 us (137 GFLOP of the prefix: 73 us
+// 64 x 16 rows of 32 heads on a prefix of 8,192 145 us (137 GFLOP of the prefix: 73 us
 // at the rate of a large product), of which the plan is 5 and the join 16. Own parts: HBM;
 // pages of 16 positions bring 256 bytes in a row for a head, which loads of any kind
 // read at 4.7 TB/s here, this kernel at 4.1 and more. A small batch: the chain of launch,
@@ -944,6 +944,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
           }
           l_run *= alpha;
         }
+        // (asked here, looked at behind the exponentials: P V is done by now, but a barrier's
+        // answer takes 150 cycles; 64 x 16 rows on 8,192 keys 145 us, asked there 150)
+        const bool pv_ready = w == w0 || mbar_test(&sh.pv_done[x], (units - 1) & 1);
         if (raise) m_run = mt;
         const float base = m_run == -CUDART_INF_F ? 0.f : m_run;
         float2 rs[2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -959,7 +962,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         l_run += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
         // P V of the group's last unit has read P
-        if (w > w0 && !wait(&sh.pv_done[x], (units - 1) & 1, 53)) {
+        if (!__all_sync(0xffffffffu, pv_ready) && !wait(&sh.pv_done[x], (units - 1) & 1, 53)) {
           ok = false;
           break;
         }
