@@ -12,14 +12,15 @@
 // of its context and the block's rows. Both are pieces of two work lists (below); every
 // piece leaves fp32 partials, which a second kernel joins in a fixed order.
 //
-// Bound. A long prefix under many rows: the tensor cores. 64 keys of two Q tiles take 1280
-// cycles of MMAs (S with both operands in shared memory, 48 cycles a step of N = 64, is
-// held by that memory, not by the pipe) and measure some 1750, the softmax between them:
-// 64 x 16 rows of 32 heads on a prefix of 8,192 145 us (137 GFLOP of the prefix: 73 us
-// at the rate of a large product), of which the plan is 5 and the join 16. Own parts: HBM;
-// pages of 16 positions bring 256 bytes in a row for a head, which loads of any kind
-// read at 4.7 TB/s here, this kernel at 4.1 and more. A small batch: the chain of launch,
-// plan, first page, first tile and join, 18 us for 4 rows of a token each.
+// Bound. A long prefix under many rows: the chain of a softmax group (S to registers,
+// maximum, exponentials, P to TMEM, the barriers' answers between), some 1700 cycles for 64
+// keys while the other group's runs beside it, with the MMAs of both close behind: 1280
+// (S with both operands in shared memory, 48 cycles a step of N = 64, is held by that
+// memory, not by the pipe). 64 x 16 rows of 32 heads on a prefix of 8,192: 145 us (137
+// GFLOP of the prefix, 73 us at the rate of a large product), of which the plan is 5 and the
+// join 16. Own parts: HBM; pages of 16 positions bring 256 bytes in a row for a head, which
+// loads of any kind read at 4.7 TB/s here, this kernel at 4.1 and more. A small batch: the
+// chain of launch, plan, first page, first tile and join, 18 us for 4 rows of a token each.
 //
 // Roundings: P meets V in bf16 (as the matrix instructions take it) under a maximum that lags
 // by at most 2^8; scores, maxima, sums, O and all partials are fp32; out is rounded once.
