@@ -198,3 +198,14 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     for k in want:
         assert torch.equal(out[k].view(torch.uint8), want[k].view(torch.uint8)), k
+
+
+def test_elements_past_two_to_the_31():
+    T, d = 530000, 4096
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device=DEV)
+    tail, w = _rows(40, d, torch.bfloat16, 16), _rows(1, d, torch.bfloat16, 17)[0].contiguous()
+    x[-40:] = tail
+    o = api.rms_norm(x, w, 1e-6, residual=x, fp8=True, want_y=True, out={"sum": x})
+    # (against the definition: how a row's squares are added depends on the number of rows)
+    _check({k: o[k][-40:] for k in ("sum", "y", "q", "scale")}, tail, w, 1e-6, tail, torch.bfloat16)
+    assert not bool(o["y"][:-40].any())

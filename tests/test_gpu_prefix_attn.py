@@ -292,3 +292,17 @@ def test_a_wait_that_runs_out_ends_the_call():
     assert 1 <= api.device_error_word(ws) <= 99
     api.clear_counters(ws)
     assert torch.equal(c.run(ws=ws), want) and api.device_error_word(ws) == 0
+
+
+def test_pages_past_four_gigabytes():
+    # the same rows in pages at the end of pools of 140,000 (4.6 GB each)
+    c = Case([700, 650, 641], [0] * 3, [640], n_q=16, Hq=32, Hkv=8, seed=21)
+    want = c.check()
+    num = 140000
+    first = num - c.k.shape[0]
+    big = [torch.empty((num, *c.k.shape[1:]), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for pool, old in zip(big, (c.k, c.v)):
+        pool[first:] = old
+    table = torch.where(c.table >= 0, c.table + first, c.table)
+    got = api.prefix_attn(c.q, c.kb, c.vb, *big, table, c.i32(c.ctx), c.i32(c.group), c.i32(c.prefix))
+    assert torch.equal(got, want)

@@ -273,3 +273,21 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         for a, b in zip([t for x in out for t in x.values()] + pools, want):
             assert torch.equal(a, b)
+
+
+def test_pages_past_four_gigabytes():
+    # pools of 140,000 pages of 32 KB: a begun page copied from the last one to one near it, then
+    # the pages in use moved from there to the pool's start
+    num, page = 140000, 16
+    pool = torch.zeros((num, page, 1024), dtype=torch.bfloat16, device=DEV)
+    pool[num - 3:] = torch.arange(3 * page, device=DEV).view(3, page, 1) + 1
+    table = _dev([[num - 3, num - 1], [-1, -1]])
+    n_pages, shares, n_free = _dev([2, 0]), _dev(np.zeros(num)), _dev([1])
+    free = _dev(np.full(num, num - 2))
+    o = api.pages_fork(_dev([-1, 0]), _dev([21, 0]), table, n_pages, shares, free, n_free, page, [pool])
+    assert table.tolist() == [[num - 3, num - 1], [num - 3, num - 2]] and o["n_pages"].tolist() == [2, 2]
+    want = [pool[num - 3].clone(), pool[num - 2].clone(), pool[num - 1].clone()]
+    assert torch.equal(want[1][:5], want[2][:5]) and int(want[1][5, 0]) == 16 + 6
+    c = api.pages_compact(table, o["n_pages"], o["shares"], page, [pool])
+    assert c["page_table"].tolist() == [[0, 2], [0, 1]] and int(c["n_free"]) == num - 3
+    assert all(torch.equal(pool[i], w) for i, w in enumerate(want)) and c["shares"][:3].tolist() == [1, 0, 0]
