@@ -595,7 +595,8 @@ typedef struct {
  * aligned. Every other tensor is aligned to its type; rows are taken by vectors
  * where all of them start at multiples of 16 bytes, d is a multiple of 16 bytes'
  * elements and a row is at most 65536 bytes (an element at a time otherwise).
- * No workspace; repeated calls give identical bits.
+ * No workspace; repeated calls give identical bits (the order in which a row's
+ * squares are added depends on T and d).
  */
 int dflash_rms_norm(const dflash_rms_norm_dims* dims, const void* x, const void* residual, const void* weight,
                     float eps, void* sum, void* y, void* q, float* scale, dflash_stream_t stream);
