@@ -258,15 +258,30 @@ __device__ __forceinline__ void pfx_lists(const PfxParams& p, PfxPlan& s, PfxSha
   const int per_g = (p.n_groups + NT - 1) / NT, per_b = (p.B + NT - 1) / NT;
   const int g0 = min(p.n_groups, tid * per_g), g1 = min(p.n_groups, g0 + per_g);
   const int b0 = min(p.B, tid * per_b), b1 = min(p.B, b0 + per_b);
-  for (int g = tid; g < p.n_groups; g += NT) {
+  constexpr int kPer = NT == 32 ? kWarpLists / 32 : kMaxSeqs / NT;
+  int raws[kPer], groups[kPer], lens[kPer];          // all loads at once
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = tid + k * NT;
+    raws[k] = i < p.B ? p.ctx_len[i] : 0;
+    groups[k] = i < p.B ? p.group[i] : -1;
+    lens[k] = i < p.n_groups ? p.prefix_len[i] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int g = tid + k * NT;
+    if (g >= p.n_groups) break;
     s.cnt[g] = 0;
     s.first[g] = INT_MAX;
-    s.minc[g] = max(0, p.prefix_len[g]);
+    s.minc[g] = max(0, lens[k]);
     s.fill[g] = 0;
   }
   pfx_sync<NT>();
-  for (int b = tid; b < p.B; b += NT) {
-    const int raw = p.ctx_len[b], C = max(0, min(raw, p.max_ctx)), g = p.group[b];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int b = tid + k * NT;
+    if (b >= p.B) break;
+    const int raw = raws[k], C = max(0, min(raw, p.max_ctx)), g = groups[k];
     const bool in = g >= 0 && g < p.n_groups;
     s.ctx[b] = C;
     s.grp[b] = in ? g : -1;
@@ -551,17 +566,17 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
   PfxShared& sh = *reinterpret_cast<PfxShared*>(v_s + kSlots * kTileBytes);
   volatile int* abort_flag = &sh.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+  if (warp == kWarpClean) {        // (not the warp that makes the lists meanwhile)
+    if (lane < kSlots) {
       for (int by = 0; by < 3; ++by) {
-        mbar_init(&sh.k_full[by][i], 1);
-        mbar_init(&sh.v_full[by][i], 1);
+        mbar_init(&sh.k_full[by][lane], 1);
+        mbar_init(&sh.v_full[by][lane], 1);
       }
-      mbar_init(&sh.k_empty[i], 2);        // both groups, or one for both
-      mbar_init(&sh.v_empty[i], 2);
-      mbar_init(&sh.v_land[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_empty[lane], 2);     // both groups, or one for both
+      mbar_init(&sh.v_empty[lane], 2);
+      mbar_init(&sh.v_land[lane], 1);
+    } else if (lane >= 30) {
+      const int i = lane - 30;
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_read[i], 4);
       mbar_init(&sh.p_full[i], 4);
@@ -569,10 +584,12 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
       mbar_init(&sh.o_empty[i], 4);
       for (int by = 0; by < 3; ++by) mbar_init(&sh.q_full[by][i], 1);
       mbar_init(&sh.q_empty[i], 2);
+    } else if (lane == 29) {
+      mbar_init(&sh.mma_done, 4);
+      sh.abort_flag = 0;
     }
-    mbar_init(&sh.mma_done, 4);
-    sh.abort_flag = 0;
     fence_barrier_init();
+    __syncwarp();
   }
   if (warp == kWarpK) {
     const CUtensorMap* maps[5] = {&kmap, &vmap, &kbmap, &vbmap, &qmap};
