@@ -101,7 +101,9 @@ static cudaError_t launch_shares_copy(const int32_t* from, int32_t* to, int n, i
 // Fork. Every CTA forms the prefix of the pages asked for (one a child whose parent
 // has begun a page), as pages_resize does. Then warps take units: a segment of a
 // child's row, a segment of a parent's pages (one atomic for all its children), or
-// the rows of a begun page in one pool.
+// the rows of a begun page in one pool. 896 forks of 1,024 rows in 10 pools: 46 us, the begun
+// pages' 294 MB at 6.4 TB/s; 7 of 8 rows: 6.5 us, two launches and one round trip each to the
+// table, the list and the page.
 // ---------------------------------------------------------------------------
 template <typename V>
 __global__ void __launch_bounds__(pages::kThreads, 2)
@@ -220,7 +222,8 @@ cudaError_t launch_pages_fork(const ForkArgs& a, int num_sms, int* launches) {
 // ---------------------------------------------------------------------------
 // Release. A page's count goes down by one for every row that lets it go; who takes
 // it from 0 to -1 frees it and counts it for its segment of the pool, so that the
-// last kernel lists the freed pages by their number with one prefix sum a segment.
+// last kernel lists the freed pages by their number with one prefix sum a segment. 64 rows
+// of up to 512 pages 8 us, 1,024 of up to 256 13 us: three launches, the atomics of shared pages.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pages_let_go(const ReleaseArgs& a, int cta, int ctas) {
   using namespace pages;
@@ -322,7 +325,8 @@ cudaError_t launch_pages_release(const ReleaseArgs& a, int num_sms, int* launche
 // ---------------------------------------------------------------------------
 // Compact. A bit for every page that a row holds, and their number per segment; with
 // U(p) the pages in use below p and n those in use in all, page p < n not in use is
-// the (p - U(p))-th hole and page p >= n in use the (U(p) - U(n))-th to move.
+// the (p - U(p))-th hole and page p >= n in use the (U(p) - U(n))-th to move. 64 sequences'
+// pages in 10 pools after half have ended: 445 us, 2.8 GB at 6.3 TB/s; 8 rows' in 2: 12 us.
 // ---------------------------------------------------------------------------
 struct CompactScratch {
   int32_t *seg, *bits, *hole, *mover, *rank, *n_moves;
