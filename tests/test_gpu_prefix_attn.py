@@ -306,3 +306,26 @@ def test_pages_past_four_gigabytes():
     table = torch.where(c.table >= 0, c.table + first, c.table)
     got = api.prefix_attn(c.q, c.kb, c.vb, *big, table, c.i32(c.ctx), c.i32(c.group), c.i32(c.prefix))
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("debug", [False, True], ids=["release", "debug"])
+def test_lengths_out_of_range_are_clamped(debug):
+    # above max_ctx: max_ctx; below zero: none; only the debug library records them
+    from block_diffusion_speculative_fusion_gb300 import build
+    build.build(debug=True)
+    c = Case([700, 650, 648, 0], [0, 0, 0, 0], [640], n_q=4, Hq=8, seed=22)
+    top = 640
+    api.select_library(debug=debug)
+    try:
+        ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+        args = (c.q, c.kb, c.vb, c.k, c.v, c.table)
+        rest = (c.i32(c.group), c.i32(c.prefix))
+        for lens, bad in (([top] * 3 + [0], [700, 650, 1 << 30, 0]), ([top] * 3 + [0], [top] * 3 + [-9])):
+            want = api.prefix_attn(*args, c.i32(lens), *rest, max_ctx=top, ws=ws)
+            ws.zero_()
+            got = api.prefix_attn(*args, c.i32(bad), *rest, max_ctx=top, ws=ws)
+            assert torch.equal(got, want)
+            assert api.device_error_word(ws) == (api.DEVERR_BAD_CTX_LEN if debug else 0)
+            ws.zero_()
+    finally:
+        api.select_library(debug=False)
